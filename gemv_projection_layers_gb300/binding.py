@@ -19,7 +19,7 @@ LIB_PATH = os.path.join(_PKG, "libproj.so")
 HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "proj.h")
 
 PROJ_QKV_GATE, PROJ_O, PROJ_POOLER, PROJ_UNPOOLER, PROJ_ROUTER = range(5)
-PROJ_BF16, PROJ_FP32 = 0, 1
+PROJ_BF16, PROJ_FP32, PROJ_FP16 = 0, 1, 2
 PROJ_ENCODE_EXPWIN12 = 1
 (PROJ_OK, PROJ_EINVAL, PROJ_EUNSUPPORTED, PROJ_EALIGN, PROJ_ENOMEM, PROJ_ECUDA,
  PROJ_EDEVICE) = range(7)
@@ -33,6 +33,10 @@ PROJ_UNPACK_FRAG12 = 64  # proj_unpack_weights: the warp-MMA GEMV's 12-bit fragm
 PROJ_UNPACK_RUNS = 128  # proj_unpack_weights: the row-run GEMV's copy (all N rows)
 PROJ_UNPACK_RUNS_SLICE = 256  # proj_unpack_weights: the unpooler's row-run copy of its slice
 PROJ_READ_PDL = 4  # proj_read_floor mode flag: launched as a programmatic dependent launch
+
+PROJ_ROUTE_CHOSEN, PROJ_ROUTE_ALL = 0, 1  # proj_moe_route: softmax over the chosen / all logits
+PROJ_GATE_NONE, PROJ_GATE_CHANNEL, PROJ_GATE_ELEMENT, PROJ_GATE_TOKEN = range(4)
+PROJ_GATE_LINEAR, PROJ_GATE_SIGMOID = 0, 1
 
 LAYER_INDEX = {"qkv_gate": 0, "o": 1, "pooler": 2, "unpooler": 3, "router": 4}
 
@@ -62,6 +66,32 @@ class proj_info_t(ctypes.Structure):
                 ("expwin12_escapes", ctypes.c_int64), ("expwin12_bytes", ctypes.c_int64),
                 ("dense_bytes", ctypes.c_int64), ("workspace_bytes", ctypes.c_int64),
                 ("num_sms", ctypes.c_int), ("reserved", ctypes.c_int * 7)]
+
+
+_NORM_HEAD = [("m", ctypes.c_int64), ("D", ctypes.c_int64), ("dtype", ctypes.c_int),
+              ("gate_mode", ctypes.c_int), ("gate_act", ctypes.c_int), ("y_plain", ctypes.c_int),
+              ("eps", ctypes.c_float), ("alpha", ctypes.c_float), ("beta", ctypes.c_float),
+              ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64),
+              ("residual", ctypes.c_void_p), ("ldr", ctypes.c_int64),
+              ("gate", ctypes.c_void_p), ("ldg", ctypes.c_int64),
+              ("w_post", ctypes.c_void_p), ("w_pre", ctypes.c_void_p)]
+
+
+class proj_norm_args(ctypes.Structure):
+    _fields_ = _NORM_HEAD + [("out", ctypes.c_void_p), ("ldo", ctypes.c_int64),
+                             ("normed", ctypes.c_void_p), ("ldn", ctypes.c_int64),
+                             ("rstd_post", ctypes.c_void_p), ("rstd_pre", ctypes.c_void_p)]
+
+
+class proj_norm_grad_args(ctypes.Structure):
+    _fields_ = _NORM_HEAD + [("rstd_post", ctypes.c_void_p), ("rstd_pre", ctypes.c_void_p),
+                             ("dout", ctypes.c_void_p), ("lddo", ctypes.c_int64),
+                             ("dnormed", ctypes.c_void_p), ("lddn", ctypes.c_int64),
+                             ("dy", ctypes.c_void_p), ("lddy", ctypes.c_int64),
+                             ("dresidual", ctypes.c_void_p), ("lddr", ctypes.c_int64),
+                             ("dgate", ctypes.c_void_p), ("lddg", ctypes.c_int64),
+                             ("dw_post", ctypes.c_void_p), ("dw_pre", ctypes.c_void_p),
+                             ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)]
 
 
 _lib = None
@@ -118,6 +148,39 @@ def load() -> ctypes.CDLL:
     lib.proj_gemv_static.restype = i32
     lib.proj_gemv_static_status.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32)]
     lib.proj_gemv_static_status.restype = i32
+    lib.proj_w4_prepare.argtypes = [vp, vp, vp, i64, i64, i64, i64, i32, ctypes.POINTER(i32)]
+    lib.proj_w4_prepare.restype = vp
+    lib.proj_w4_run.argtypes = [vp, vp, i64, i64, vp, i64, vp]
+    lib.proj_w4_run.restype = i32
+    lib.proj_w4_run_experts.argtypes = [vp, vp, i64, i64, vp, vp, i64, vp]
+    lib.proj_w4_run_experts.restype = i32
+    lib.proj_w4_describe.argtypes = [vp, i64, ctypes.c_char_p, ctypes.c_size_t]
+    lib.proj_w4_describe.restype = i32
+    lib.proj_w4_device_status.argtypes = [vp, vp, ctypes.POINTER(u32)]
+    lib.proj_w4_device_status.restype = i32
+    lib.proj_w4_destroy.argtypes = [vp]
+    lib.proj_w4_destroy.restype = None
+    lib.proj_moe_workspace.argtypes = [i64, i64, i64]
+    lib.proj_moe_workspace.restype = i64
+    lib.proj_moe_route.argtypes = [vp, i64, i64, i64, i64, i32, vp, vp, vp, vp, vp, vp, i64, vp]
+    lib.proj_moe_route.restype = i32
+    lib.proj_moe_sort.argtypes = [vp, i64, i64, i64, vp, vp, vp, vp, i64, vp]
+    lib.proj_moe_sort.restype = i32
+    lib.proj_moe_gather.argtypes = [vp, i64, vp, i64, i64, i64, i32, vp, i64, vp]
+    lib.proj_moe_gather.restype = i32
+    lib.proj_moe_combine.argtypes = [vp, i64, vp, vp, i64, i64, i64, i32, vp, i64, vp]
+    lib.proj_moe_combine.restype = i32
+    lib.proj_moe_combine_backward.argtypes = [vp, i64, vp, i64, vp, vp, i64, i64, i64, i32, vp, i64,
+                                              vp, vp]
+    lib.proj_moe_combine_backward.restype = i32
+    lib.proj_moe_route_backward.argtypes = [vp, i64, i64, i64, i64, i32, vp, vp, vp, vp, i64, vp]
+    lib.proj_moe_route_backward.restype = i32
+    lib.proj_norm.argtypes = [ctypes.POINTER(proj_norm_args), vp]
+    lib.proj_norm.restype = i32
+    lib.proj_norm_workspace.argtypes = [i64, i64]
+    lib.proj_norm_workspace.restype = i64
+    lib.proj_norm_backward.argtypes = [ctypes.POINTER(proj_norm_grad_args), vp]
+    lib.proj_norm_backward.restype = i32
     _lib = lib
     return lib
 
@@ -292,3 +355,136 @@ def proj_gemv_static_status(stream=None) -> int:
     if st not in (PROJ_OK, PROJ_EDEVICE):
         raise ProjError(st, f"proj_gemv_static_status ({last_cuda_error()})")
     return int(code.value)
+
+
+# ------------------------------------------ operators around the projections --
+
+def proj_w4_prepare(codes, scales, zeros, experts: int, N: int, K: int, group: int,
+                    dtype: int) -> int:
+    st = ctypes.c_int(0)
+    h = load().proj_w4_prepare(_addr(codes), _addr(scales), _addr(zeros), int(experts), int(N),
+                               int(K), int(group), int(dtype), ctypes.byref(st))
+    if not h:
+        raise ProjError(st.value, f"proj_w4_prepare ({last_cuda_error()})")
+    return h
+
+
+def _checked(status: int, what: str) -> None:
+    if status != PROJ_OK:
+        raise ProjError(status, f"{what} ({last_cuda_error()})")
+
+
+def proj_w4_run(h: int, x, ldx: int, m: int, out, ldo: int, stream=None) -> None:
+    _checked(load().proj_w4_run(h, _addr(x), ldx, m, _addr(out), ldo, _stream(stream)),
+             "proj_w4_run")
+
+
+def proj_w4_run_experts(h: int, x, ldx: int, m: int, offsets, out, ldo: int, stream=None) -> None:
+    _checked(load().proj_w4_run_experts(h, _addr(x), ldx, m, _addr(offsets), _addr(out), ldo,
+                                        _stream(stream)), "proj_w4_run_experts")
+
+
+def proj_w4_describe(h: int, m: int) -> str:
+    buf = ctypes.create_string_buffer(256)
+    _checked(load().proj_w4_describe(h, int(m), buf, 256), "proj_w4_describe")
+    return buf.value.decode()
+
+
+def proj_w4_device_status(h: int, stream=None) -> int:
+    code = ctypes.c_uint32(0)
+    st = load().proj_w4_device_status(h, _stream(stream), ctypes.byref(code))
+    if st not in (PROJ_OK, PROJ_EDEVICE):
+        raise ProjError(st, "proj_w4_device_status")
+    return int(code.value)
+
+
+def proj_w4_destroy(h: int) -> None:
+    if h:
+        load().proj_w4_destroy(h)
+
+
+def proj_moe_workspace(m: int, experts: int, k: int) -> int:
+    n = int(load().proj_moe_workspace(int(m), int(experts), int(k)))
+    if n < 0:
+        raise ProjError(proj_last_status(), f"proj_moe_workspace ({last_cuda_error()})")
+    return n
+
+
+def proj_moe_route(logits, ldl: int, m: int, experts: int, k: int, mode: int, expert, weight,
+                   offsets=None, order=None, slot=None, workspace=None, workspace_bytes: int = 0,
+                   stream=None) -> None:
+    _checked(load().proj_moe_route(_addr(logits), ldl, m, experts, k, mode, _addr(expert),
+                                   _addr(weight), _addr(offsets), _addr(order), _addr(slot),
+                                   _addr(workspace), workspace_bytes, _stream(stream)),
+             "proj_moe_route")
+
+
+def proj_moe_sort(expert, m: int, experts: int, k: int, offsets, order, slot, workspace=None,
+                  workspace_bytes: int = 0, stream=None) -> None:
+    _checked(load().proj_moe_sort(_addr(expert), m, experts, k, _addr(offsets), _addr(order),
+                                  _addr(slot), _addr(workspace), workspace_bytes,
+                                  _stream(stream)), "proj_moe_sort")
+
+
+def proj_moe_gather(x, ldx: int, slot, m: int, D: int, k: int, dtype: int, xs, ldxs: int,
+                    stream=None) -> None:
+    _checked(load().proj_moe_gather(_addr(x), ldx, _addr(slot), m, D, k, dtype, _addr(xs), ldxs,
+                                    _stream(stream)), "proj_moe_gather")
+
+
+def proj_moe_combine(ys, ldys: int, slot, weight, m: int, D: int, k: int, dtype: int, out,
+                     ldo: int, stream=None) -> None:
+    _checked(load().proj_moe_combine(_addr(ys), ldys, _addr(slot), _addr(weight), m, D, k, dtype,
+                                     _addr(out), ldo, _stream(stream)), "proj_moe_combine")
+
+
+def proj_moe_combine_backward(dout, lddo: int, ys, ldys: int, slot, weight, m: int, D: int,
+                              k: int, dtype: int, dys, lddys: int, dweight, stream=None) -> None:
+    _checked(load().proj_moe_combine_backward(_addr(dout), lddo, _addr(ys), ldys, _addr(slot),
+                                              _addr(weight), m, D, k, dtype, _addr(dys), lddys,
+                                              _addr(dweight), _stream(stream)),
+             "proj_moe_combine_backward")
+
+
+def proj_moe_route_backward(logits, ldl: int, m: int, experts: int, k: int, mode: int, expert,
+                            weight, dweight, dlogits, lddl: int, stream=None) -> None:
+    _checked(load().proj_moe_route_backward(_addr(logits), ldl, m, experts, k, mode,
+                                            _addr(expert), _addr(weight), _addr(dweight),
+                                            _addr(dlogits), lddl, _stream(stream)),
+             "proj_moe_route_backward")
+
+
+def _fill(args, named):
+    pointers = {n for n, t in args._fields_ if t is ctypes.c_void_p}
+    args.held = named  # the tensors live as long as the struct that names them
+    for name, value in named.items():
+        if name not in {n for n, _ in args._fields_}:
+            raise TypeError(f"{type(args).__name__} has no field {name!r}")
+        setattr(args, name, _addr(value) if name in pointers else value)
+    return args
+
+
+def norm_args(**named) -> proj_norm_args:
+    """A proj_norm_args from its fields by name (tensors, addresses or numbers;
+    what is left out is 0 or NULL, and eps, alpha, beta are 0, 1, 1)."""
+    return _fill(proj_norm_args(alpha=1.0, beta=1.0), named)
+
+
+def norm_grad_args(**named) -> proj_norm_grad_args:
+    """The same for proj_norm_grad_args."""
+    return _fill(proj_norm_grad_args(alpha=1.0, beta=1.0), named)
+
+
+def proj_norm(args: proj_norm_args, stream=None) -> None:
+    _checked(load().proj_norm(ctypes.byref(args), _stream(stream)), "proj_norm")
+
+
+def proj_norm_workspace(m: int, D: int) -> int:
+    n = int(load().proj_norm_workspace(int(m), int(D)))
+    if n < 0:
+        raise ProjError(proj_last_status(), f"proj_norm_workspace ({last_cuda_error()})")
+    return n
+
+
+def proj_norm_backward(args: proj_norm_grad_args, stream=None) -> None:
+    _checked(load().proj_norm_backward(ctypes.byref(args), _stream(stream)), "proj_norm_backward")

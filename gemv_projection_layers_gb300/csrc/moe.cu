@@ -1,0 +1,851 @@
+// moe.cu -- tokens to their experts and back: choice of the k largest router
+// logits, stable counting sort by expert, gather, weighted combine, and the
+// gradients.
+//
+// The sort.  Entries (t, j) in flat order are cut into blocks, one per CTA,
+// and a block into chunks of 32, one per warp.  In a chunk a lane's rank among
+// equal experts comes from a match over the warp; per expert, chunk counts are
+// summed over the chunks before it, block counts (the workspace table, [block]
+// [expert]) over the blocks before it, and totals over the experts before it.
+// All of it is whole-number arithmetic in a fixed order: no atomics, stable.
+// One block: one launch does everything.  More: a first launch chooses and
+// counts, a second places.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdio>
+
+#include "../../include/proj.h"
+#include "kernels.h"
+#include "ptx.cuh"
+#include "vec.cuh"
+
+namespace proj {
+namespace {
+
+constexpr int kMaxExperts = 1024;
+constexpr int kMaxK = 32;
+constexpr int kSortThreads = 1024;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kTableBytes = 96 * 1024;  // shared chunk table: [chunks][E] of 16 bits, at most
+
+// ------------------------------------------------------------------ choice --
+
+// A key that orders like the float, equal for +0 and -0; 0 for what is never
+// chosen (NaN and -infinity).
+__device__ __forceinline__ uint32_t order_key(float v) {
+  if (!(v > -INFINITY)) return 0u;
+  const uint32_t u = __float_as_uint(v + 0.f);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
+}
+// exp(v - top) with the limit 1 at v == top, also where both are infinite.
+__device__ __forceinline__ float exp_below(float v, float top) {
+  return v == top ? 1.f : expf(v - top);
+}
+
+// One warp chooses for one token; EPL = experts a lane holds (expert
+// i 32 + lane).  Lane j < k returns choice j (-1: none left) and its weight.
+template <int EPL>
+__device__ __forceinline__ void choose(const float* __restrict__ logits, int E, int k, int mode,
+                                       int lane, int& expert, float& weight) {
+  uint32_t key[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const int e = i * 32 + lane;
+    key[i] = e < E ? order_key(__ldg(logits + e)) : 0u;
+  }
+  float all = 0.f;
+  uint32_t top = 0u;
+  if (mode == PROJ_ROUTE_ALL) {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) top = max(top, key[i]);
+    top = __reduce_max_sync(0xFFFFFFFFu, top);
+    const float tv = key_value(top);
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      if (key[i]) all += exp_below(key_value(key[i]), tv);
+    all = warp_sum(all);
+  }
+  expert = -1;
+  uint32_t mine = 0u;
+  for (int j = 0; j < k; ++j) {
+    uint32_t best = 0u;
+    int at = 0;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      if (key[i] > best) {  // the first of equal ones: the lowest index of this lane
+        best = key[i];
+        at = i;
+      }
+    const uint32_t win = __reduce_max_sync(0xFFFFFFFFu, best);
+    if (!win) break;  // nothing left to choose
+    if (j == 0) top = win;
+    const uint32_t idx = __reduce_min_sync(
+        0xFFFFFFFFu, best == win ? static_cast<uint32_t>(at * 32 + lane) : 0xFFFFFFFFu);
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      if (static_cast<uint32_t>(i * 32 + lane) == idx) key[i] = 0u;
+    if (lane == j) {
+      expert = static_cast<int>(idx);
+      mine = win;
+    }
+  }
+  const float part = expert >= 0 ? exp_below(key_value(mine), key_value(top)) : 0.f;
+  const float total = mode == PROJ_ROUTE_ALL ? all : warp_sum(part);
+  weight = expert >= 0 ? part / total : 0.f;
+}
+
+// ------------------------------------------------------------------- sort --
+
+struct SortParams {
+  const float* logits;  // null: expert is an input
+  int64_t ldl;
+  int32_t* expert;
+  float* weight;
+  int32_t* offsets;  // null: choose only
+  int32_t* order;
+  int32_t* slot;
+  int32_t* table;  // [blocks][E]
+  int64_t m;
+  int E, k, mode;
+  int tokens;  // per block
+  int blocks;
+};
+
+// Counts of each expert in the chunks of this block, from its entries'
+// experts: table[chunk][e], and each entry's rank in its chunk left to the
+// caller (recomputed from the same match).
+__device__ __forceinline__ int chunk_rank(int e, bool real, int lane, int& count, bool& last) {
+  const uint32_t same = __match_any_sync(0xFFFFFFFFu, real ? e : -1);
+  count = __popc(same);
+  const uint32_t below = same & ((1u << lane) - 1u);
+  last = (same >> lane) == 1u;  // the highest lane of its expert writes the count
+  return __popc(below);
+}
+
+// Exclusive sums over the E totals in s_total (E <= 1024), by the whole block;
+// s_total becomes the exclusive sums, the grand total is returned.
+__device__ __forceinline__ int scan_experts(int* s_total, int* s_warp, int E) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int v = tid < E ? s_total[tid] : 0;
+  int inc = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+    if (lane >= o) inc += t;
+  }
+  if (lane == 31) s_warp[warp] = inc;
+  __syncthreads();
+  int w = s_warp[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(0xFFFFFFFFu, w, o);
+    if (lane >= o) w += t;
+  }
+  const int before = warp ? __shfl_sync(0xFFFFFFFFu, w, warp - 1) : 0;
+  const int total = __shfl_sync(0xFFFFFFFFu, w, 31);
+  if (tid < E) s_total[tid] = before + inc - v;
+  __syncthreads();
+  return total;
+}
+
+__device__ __forceinline__ bool is_expert(int e, int E) { return e >= 0 && e < E; }
+
+// Chooses (with logits) and counts; with one block also places.
+template <int EPL>
+__global__ void __launch_bounds__(kSortThreads) choose_count_kernel(const SortParams p) {
+  extern __shared__ __align__(16) uint16_t s_table[];  // [chunks][E]
+  __shared__ int s_total[kMaxExperts];
+  __shared__ int s_warp[kSortWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  griddep_launch_dependents();
+  griddep_wait();
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.tokens;
+  const int nt = static_cast<int>(min(static_cast<int64_t>(p.tokens), p.m - t0));
+  if (p.logits) {
+    for (int t = warp; t < nt; t += kSortWarps) {
+      int e;
+      float w;
+      choose<EPL>(p.logits + (t0 + t) * p.ldl, p.E, p.k, p.mode, lane, e, w);
+      if (lane < p.k) {
+        p.expert[(t0 + t) * p.k + lane] = e;
+        p.weight[(t0 + t) * p.k + lane] = w;
+      }
+    }
+  }
+  if (!p.offsets) return;
+  const int n = nt * p.k;
+  const int chunks = (n + 31) / 32;
+  for (int i = tid; i < (chunks * p.E + 1) / 2; i += kSortThreads)
+    reinterpret_cast<uint32_t*>(s_table)[i] = 0u;
+  __syncthreads();  // also publishes this block's choices to the block
+  const int32_t* expert = p.expert + t0 * p.k;
+  for (int c = warp; c < chunks; c += kSortWarps) {
+    const int i = c * 32 + lane;
+    const int e = i < n ? expert[i] : -1;
+    const bool real = is_expert(e, p.E);
+    int count;
+    bool last;
+    chunk_rank(e, real, lane, count, last);
+    if (real && last) s_table[c * p.E + e] = static_cast<uint16_t>(count);
+  }
+  __syncthreads();
+  // per expert: counts -> exclusive sums over the chunks
+  int total = 0;
+  if (tid < p.E) {
+    for (int c = 0; c < chunks; ++c) {
+      const int v = s_table[c * p.E + tid];
+      s_table[c * p.E + tid] = static_cast<uint16_t>(total);
+      total += v;
+    }
+    if (p.blocks > 1) p.table[static_cast<int64_t>(blockIdx.x) * p.E + tid] = total;
+  }
+  if (p.blocks > 1) return;
+  if (tid < p.E) s_total[tid] = total;
+  __syncthreads();
+  const int kept = scan_experts(s_total, s_warp, p.E);
+  if (tid < p.E) p.offsets[tid] = s_total[tid];
+  if (tid == 0) p.offsets[p.E] = kept;
+  for (int c = warp; c < chunks; c += kSortWarps) {
+    const int i = c * 32 + lane;
+    const int e = i < n ? expert[i] : -1;
+    const bool real = is_expert(e, p.E);
+    int count;
+    bool last;
+    const int rank = chunk_rank(e, real, lane, count, last);
+    if (i < n) {
+      const int at = real ? s_total[e] + s_table[c * p.E + e] + rank : -1;
+      p.slot[i] = at;
+      if (real) p.order[at] = i;
+    }
+  }
+  for (int i = kept + tid; i < n; i += kSortThreads) p.order[i] = -1;
+}
+
+// Places the entries of one block, from every block's counts.
+__global__ void __launch_bounds__(kSortThreads) place_kernel(const SortParams p) {
+  extern __shared__ __align__(16) uint16_t s_table[];
+  __shared__ int s_total[kMaxExperts];
+  __shared__ int s_base[kMaxExperts];
+  __shared__ int s_warp[kSortWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  griddep_launch_dependents();
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.tokens;
+  const int nt = static_cast<int>(min(static_cast<int64_t>(p.tokens), p.m - t0));
+  const int n = nt * p.k;
+  const int chunks = (n + 31) / 32;
+  for (int i = tid; i < (chunks * p.E + 1) / 2; i += kSortThreads)
+    reinterpret_cast<uint32_t*>(s_table)[i] = 0u;
+  __syncthreads();
+  griddep_wait();
+  const int32_t* expert = p.expert + t0 * p.k;
+  for (int c = warp; c < chunks; c += kSortWarps) {
+    const int i = c * 32 + lane;
+    const int e = i < n ? expert[i] : -1;
+    const bool real = is_expert(e, p.E);
+    int count;
+    bool last;
+    chunk_rank(e, real, lane, count, last);
+    if (real && last) s_table[c * p.E + e] = static_cast<uint16_t>(count);
+  }
+  int before = 0;
+  if (tid < p.E) {
+    int total = 0;
+#pragma unroll 8
+    for (int b = 0; b < p.blocks; ++b) {
+      const int v = p.table[static_cast<int64_t>(b) * p.E + tid];
+      if (b < static_cast<int>(blockIdx.x)) before += v;
+      total += v;
+    }
+    s_total[tid] = total;
+  }
+  __syncthreads();
+  if (tid < p.E) {
+    int run = 0;
+    for (int c = 0; c < chunks; ++c) {
+      const int v = s_table[c * p.E + tid];
+      s_table[c * p.E + tid] = static_cast<uint16_t>(run);
+      run += v;
+    }
+  }
+  const int kept = scan_experts(s_total, s_warp, p.E);
+  if (tid < p.E) s_base[tid] = s_total[tid] + before;
+  if (blockIdx.x == 0) {
+    if (tid < p.E) p.offsets[tid] = s_total[tid];
+    if (tid == 0) p.offsets[p.E] = kept;
+  }
+  __syncthreads();
+  for (int c = warp; c < chunks; c += kSortWarps) {
+    const int i = c * 32 + lane;
+    const int e = i < n ? expert[i] : -1;
+    const bool real = is_expert(e, p.E);
+    int count;
+    bool last;
+    const int rank = chunk_rank(e, real, lane, count, last);
+    if (i < n) {
+      const int at = real ? s_base[e] + s_table[c * p.E + e] + rank : -1;
+      p.slot[t0 * p.k + i] = at;
+      if (real) p.order[at] = static_cast<int32_t>(t0 * p.k + i);
+    }
+  }
+  const int64_t all = p.m * p.k;
+  for (int64_t i = kept + static_cast<int64_t>(blockIdx.x) * kSortThreads + tid; i < all;
+       i += static_cast<int64_t>(gridDim.x) * kSortThreads)
+    p.order[i] = -1;
+}
+
+// ------------------------------------------------------- gather, combine --
+
+struct RowsParams {
+  const void* a;  // gather: x; combine: ys; backward: dout
+  int64_t lda;
+  const void* b;  // backward: ys
+  int64_t ldb;
+  const int32_t* slot;
+  const float* weight;
+  void* out;  // gather: xs; combine: out; backward: dys
+  int64_t ldo;
+  float* dweight;
+  int64_t m;
+  int64_t D;
+  int k;
+};
+
+constexpr int kRowThreads = 256;
+
+__device__ __forceinline__ bool is_slot(int s, int64_t rows) { return s >= 0 && s < rows; }
+
+template <typename T, int V>
+__global__ void __launch_bounds__(kRowThreads) gather_kernel(const RowsParams p) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int64_t t = blockIdx.x;
+  const int64_t nvec = p.D / V, rows = p.m * p.k;
+  const T* x = static_cast<const T*>(p.a) + t * p.lda;
+  const int32_t* slot = p.slot + t * p.k;
+  T* xs = static_cast<T*>(p.out);
+  for (int64_t v = static_cast<int64_t>(blockIdx.y) * kRowThreads + threadIdx.x; v < nvec;
+       v += static_cast<int64_t>(gridDim.y) * kRowThreads) {
+    const Vec<T, V> val = load_vec<T, V>(x + v * V);
+    for (int j = 0; j < p.k; ++j) {
+      const int s = __ldg(slot + j);
+      if (is_slot(s, rows)) *reinterpret_cast<Vec<T, V>*>(xs + s * p.ldo + v * V) = val;
+    }
+  }
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(kRowThreads) combine_kernel(const RowsParams p) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int64_t t = blockIdx.x;
+  const int64_t nvec = p.D / V, rows = p.m * p.k;
+  const T* ys = static_cast<const T*>(p.a);
+  const int32_t* slot = p.slot + t * p.k;
+  const float* weight = p.weight ? p.weight + t * p.k : nullptr;
+  T* out = static_cast<T*>(p.out) + t * p.ldo;
+  for (int64_t v = static_cast<int64_t>(blockIdx.y) * kRowThreads + threadIdx.x; v < nvec;
+       v += static_cast<int64_t>(gridDim.y) * kRowThreads) {
+    float acc[V] = {};
+    for (int j0 = 0; j0 < p.k; j0 += 8) {
+      Vec<T, V> val[8];
+      float w[8];
+      bool ok[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int s = j0 + j < p.k ? __ldg(slot + j0 + j) : -1;
+        ok[j] = is_slot(s, rows);
+        if (ok[j]) {
+          val[j] = load_vec<T, V>(ys + s * p.lda + v * V);
+          w[j] = weight ? __ldg(weight + j0 + j) : 1.f;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (ok[j]) {
+          float f[V];
+          widen(val[j], f);
+#pragma unroll
+          for (int i = 0; i < V; ++i) acc[i] = fmaf(w[j], f[i], acc[i]);
+        }
+    }
+    store_vec<T, V>(out + v * V, acc);
+  }
+}
+
+// One token per CTA: the k dot products run over the whole row, eight
+// entries at a time.
+template <typename T, int V>
+__global__ void __launch_bounds__(kRowThreads) combine_grad_kernel(const RowsParams p) {
+  __shared__ float room[2 * 8 * 32];
+  int turn = 0;
+  griddep_launch_dependents();
+  griddep_wait();
+  const int64_t t = blockIdx.x;
+  const int64_t nvec = p.D / V, rows = p.m * p.k;
+  const T* dout = static_cast<const T*>(p.a) + t * p.lda;
+  const T* ys = static_cast<const T*>(p.b);
+  const int32_t* slot = p.slot + t * p.k;
+  T* dys = static_cast<T*>(p.out);
+  for (int j0 = 0; j0 < p.k; j0 += 8) {
+    int s[8];
+    float w[8], dot[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      s[j] = j0 + j < p.k ? __ldg(slot + j0 + j) : -1;
+      if (!is_slot(s[j], rows)) s[j] = -1;
+      w[j] = s[j] >= 0 && p.out ? (p.weight ? __ldg(p.weight + t * p.k + j0 + j) : 1.f) : 0.f;
+      dot[j] = 0.f;
+    }
+    for (int64_t v = threadIdx.x; v < nvec; v += kRowThreads) {
+      float d[V];
+      widen(load_vec<T, V>(dout + v * V), d);
+      Vec<T, V> val[8];
+      if (p.dweight) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (s[j] >= 0) val[j] = load_vec<T, V>(ys + s[j] * p.ldb + v * V);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (s[j] >= 0) {
+          if (p.dweight) {
+            float f[V];
+            widen(val[j], f);
+#pragma unroll
+            for (int i = 0; i < V; ++i) dot[j] = fmaf(d[i], f[i], dot[j]);
+          }
+          if (p.out) {
+            float o[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) o[i] = w[j] * d[i];
+            store_vec<T, V>(dys + s[j] * p.ldo + v * V, o);
+          }
+        }
+    }
+    if (p.dweight) {
+      row_sums<kRowThreads, 8>(dot, room, turn);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (threadIdx.x == j && j0 + j < p.k) p.dweight[t * p.k + j0 + j] = dot[j];
+    }
+  }
+}
+
+// ------------------------------------------------------- route, backward --
+
+struct RouteGradParams {
+  const float* logits;
+  int64_t ldl;
+  const int32_t* expert;
+  const float* weight;
+  const float* dweight;
+  float* dlogits;
+  int64_t lddl;
+  int64_t m;
+  int E, k, mode;
+};
+
+constexpr int kGradWarps = 8;
+
+// One warp per token.  Lane j holds choice j; the choices are handed to the
+// lane that holds their expert by a pass over the k of them.
+template <int EPL>
+__global__ void __launch_bounds__(32 * kGradWarps) route_grad_kernel(const RouteGradParams p) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kGradWarps + (threadIdx.x >> 5);
+  if (t >= p.m) return;
+  int e = -1;
+  float w = 0.f, dw = 0.f;
+  if (lane < p.k) {
+    e = p.expert[t * p.k + lane];
+    if (is_expert(e, p.E)) {
+      w = p.weight[t * p.k + lane];
+      dw = p.dweight[t * p.k + lane];
+    } else {
+      e = -1;
+    }
+  }
+  const float inner = warp_sum(w * dw);
+  float g[EPL];
+  if (p.mode == PROJ_ROUTE_ALL) {
+    uint32_t key[EPL], top = 0u;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const int x = i * 32 + lane;
+      key[i] = x < p.E ? order_key(__ldg(p.logits + t * p.ldl + x)) : 0u;
+      top = max(top, key[i]);
+    }
+    top = __reduce_max_sync(0xFFFFFFFFu, top);
+    const float tv = key_value(top);
+    float all = 0.f;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      g[i] = key[i] ? exp_below(key_value(key[i]), tv) : 0.f;
+      all += g[i];
+    }
+    all = warp_sum(all);
+    const float scale = all > 0.f ? 1.f / all : 0.f;
+    float take[EPL] = {};
+    for (int j = 0; j < p.k; ++j) {
+      const int ej = __shfl_sync(0xFFFFFFFFu, e, j);
+      const float dj = __shfl_sync(0xFFFFFFFFu, dw, j);
+#pragma unroll
+      for (int i = 0; i < EPL; ++i)
+        if (ej == i * 32 + lane) take[i] += dj;
+    }
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) g[i] = g[i] * scale * (take[i] - inner);
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) g[i] = 0.f;
+    const float own = w * (dw - inner);
+    for (int j = 0; j < p.k; ++j) {
+      const int ej = __shfl_sync(0xFFFFFFFFu, e, j);
+      const float oj = __shfl_sync(0xFFFFFFFFu, own, j);
+#pragma unroll
+      for (int i = 0; i < EPL; ++i)
+        if (ej == i * 32 + lane) g[i] += oj;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const int x = i * 32 + lane;
+    if (x < p.E) p.dlogits[t * p.lddl + x] = g[i];
+  }
+}
+
+// --------------------------------------------------------------- launches --
+
+cudaLaunchConfig_t config(int64_t grid_x, int64_t grid_y, unsigned threads, size_t smem,
+                          cudaStream_t s, cudaLaunchAttribute* attr) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid_x), static_cast<unsigned>(grid_y));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
+// Tokens per block of the sort: one block while its warps choose for at most
+// two tokens each; more tokens are spread over blocks of 64 tokens, longer
+// ones from 64 K entries on (the table of counts that every block reads grows
+// with their number), as far as the chunk table fits shared memory.
+int sort_tokens(int64_t m, int E, int k) {
+  int64_t tokens = 64;
+  while (tokens * 256 < m) tokens *= 2;
+  // chunk table in shared memory, counts in 16 bits
+  const int64_t most = std::min<int64_t>(kTableBytes / (2 * E) * 32, 32768) / k;
+  return static_cast<int>(std::max<int64_t>(1, std::min(tokens, most)));
+}
+int64_t sort_blocks(int64_t m, int E, int k) {
+  const int tokens = sort_tokens(m, E, k);
+  return (m + tokens - 1) / tokens;
+}
+size_t sort_smem(int tokens, int E, int k) {
+  const int chunks = (tokens * k + 31) / 32;
+  return (static_cast<size_t>(chunks) * E * 2 + 15) & ~static_cast<size_t>(15);
+}
+
+template <int EPL>
+cudaError_t choose_count(const SortParams& p, size_t smem, cudaStream_t s) {
+  if (smem > 48 * 1024) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(choose_count_kernel<EPL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kTableBytes + 16);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg = config(p.blocks, 1, kSortThreads, smem, s, attr);
+  return cudaLaunchKernelEx(&cfg, choose_count_kernel<EPL>, p);
+}
+
+cudaError_t sort_launch(const SortParams& p, cudaStream_t s) {
+  const size_t smem = p.offsets ? sort_smem(p.tokens, p.E, p.k) : 0;
+  cudaError_t e;
+  if (!p.logits || p.E <= 64)
+    e = choose_count<2>(p, smem, s);
+  else if (p.E <= 256)
+    e = choose_count<8>(p, smem, s);
+  else
+    e = choose_count<32>(p, smem, s);
+  if (e != cudaSuccess || !p.offsets || p.blocks <= 1) return e;
+  if (smem > 48 * 1024) {
+    e = cudaFuncSetAttribute(place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kTableBytes + 16);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg = config(p.blocks, 1, kSortThreads, smem, s, attr);
+  return cudaLaunchKernelEx(&cfg, place_kernel, p);
+}
+
+int refuse(int status, const char* call, const char* why) {
+  char text[160];
+  std::snprintf(text, sizeof text, "%s: %s", call, why);
+  return record_status(status, text);
+}
+
+bool aligned_to(const void* p, int n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+// Sizes that every call shares; nullptr if they are fine.
+const char* refuse_sizes(int64_t m, int64_t E, int64_t k, int* status) {
+  *status = PROJ_EINVAL;
+  if (m < 0 || E < 1 || k < 1 || k > E) return "m < 0, E < 1, or k outside 1 .. E";
+  *status = PROJ_EUNSUPPORTED;
+  if (E > kMaxExperts) return "more than 1024 experts";
+  if (k > kMaxK) return "k > 32";
+  if (m >= (int64_t{1} << 31) / k) return "m * k >= 2^31";
+  *status = PROJ_OK;
+  return nullptr;
+}
+
+int sort_call(const char* call, SortParams p, void* workspace, int64_t workspace_bytes,
+              cudaStream_t s) {
+  if (p.m == 0) {
+    if (!p.offsets) return PROJ_OK;
+    const cudaError_t e = cudaMemsetAsync(p.offsets, 0, sizeof(int32_t) * (p.E + 1), s);
+    return e == cudaSuccess ? PROJ_OK : record_cuda(e, call);
+  }
+  p.tokens = sort_tokens(p.m, p.E, p.k);
+  p.blocks = static_cast<int>(sort_blocks(p.m, p.E, p.k));
+  if (p.offsets && p.blocks > 1) {
+    const int64_t want = static_cast<int64_t>(p.blocks) * p.E * 4;
+    if (!workspace || workspace_bytes < want)
+      return refuse(PROJ_EINVAL, call, "workspace is NULL or too small");
+    if (!aligned_to(workspace, 16))
+      return refuse(PROJ_EALIGN, call, "workspace is not 16-byte aligned");
+    p.table = static_cast<int32_t*>(workspace);
+  }
+  const cudaError_t e = sort_launch(p, s);
+  return e == cudaSuccess ? PROJ_OK : record_cuda(e, call);
+}
+
+// Common to gather and combine; nullptr if fine.
+const char* refuse_rows(const RowsParams& p, int64_t k, int dtype, int* status) {
+  *status = PROJ_EINVAL;
+  if (p.m < 0 || p.D < 1 || k < 1) return "m < 0, D < 1 or k < 1";
+  if (dtype != PROJ_BF16 && dtype != PROJ_FP16 && dtype != PROJ_FP32) return "unknown dtype";
+  if (p.m > 0 && (!p.a || !p.slot)) return "a NULL pointer";
+  if (p.lda < p.D || (p.b && p.ldb < p.D) || (p.out && p.ldo < p.D)) return "a row stride is below D";
+  *status = PROJ_EUNSUPPORTED;
+  if (k > kMaxK) return "k > 32";
+  if (p.m >= (int64_t{1} << 31) / k) return "m * k >= 2^31";
+  const int el = dtype == PROJ_FP32 ? 4 : 2;
+  *status = PROJ_EALIGN;
+  if (!aligned_to(p.a, el) || !aligned_to(p.b, el) || !aligned_to(p.out, el) ||
+      !aligned_to(p.slot, 4) || !aligned_to(p.weight, 4) || !aligned_to(p.dweight, 4))
+    return "a pointer is not aligned to an element";
+  *status = PROJ_OK;
+  return nullptr;
+}
+
+bool rows16(const void* p, int64_t ld, int el) {
+  return !p || (aligned_to(p, 16) && (ld * el) % 16 == 0);
+}
+
+enum class Op { kGather, kCombine, kGrad };
+
+template <typename T, int V>
+cudaError_t rows_launch(Op op, const RowsParams& p, cudaStream_t s) {
+  const int64_t nvec = p.D / V;
+  const int64_t ny = std::min<int64_t>(64, (nvec + kRowThreads - 1) / kRowThreads);
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg =
+      config(p.m, op == Op::kGrad ? 1 : ny, kRowThreads, 0, s, attr);
+  switch (op) {
+    case Op::kGather: return cudaLaunchKernelEx(&cfg, gather_kernel<T, V>, p);
+    case Op::kCombine: return cudaLaunchKernelEx(&cfg, combine_kernel<T, V>, p);
+    case Op::kGrad: return cudaLaunchKernelEx(&cfg, combine_grad_kernel<T, V>, p);
+  }
+  return cudaErrorInvalidValue;
+}
+
+template <typename T>
+cudaError_t rows_any(Op op, const RowsParams& p, cudaStream_t s) {
+  constexpr int el = sizeof(T);
+  const bool vec = (p.D * el) % 16 == 0 && rows16(p.a, p.lda, el) && rows16(p.b, p.ldb, el) &&
+                   rows16(p.out, p.ldo, el);
+  return vec ? rows_launch<T, kFullVec<T>>(op, p, s) : rows_launch<T, 1>(op, p, s);
+}
+
+int rows_call(const char* call, Op op, const RowsParams& p, int dtype, proj_stream stream) {
+  if (p.m == 0) return PROJ_OK;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = dtype == PROJ_BF16   ? rows_any<__nv_bfloat16>(op, p, s)
+                        : dtype == PROJ_FP16 ? rows_any<__half>(op, p, s)
+                                             : rows_any<float>(op, p, s);
+  return e == cudaSuccess ? PROJ_OK : record_cuda(e, call);
+}
+
+}  // namespace
+}  // namespace proj
+
+using namespace proj;
+
+extern "C" int64_t proj_moe_workspace(int64_t m, int64_t experts, int64_t k) {
+  int status = PROJ_OK;
+  if (const char* why = refuse_sizes(m, experts, k, &status)) {
+    refuse(status, "proj_moe_workspace", why);
+    return -1;
+  }
+  const int64_t blocks = sort_blocks(m, static_cast<int>(experts), static_cast<int>(k));
+  return blocks > 1 ? blocks * experts * 4 : 0;
+}
+
+extern "C" int proj_moe_route(const float* logits, int64_t ldl, int64_t m, int64_t experts,
+                              int64_t k, int mode, int32_t* expert, float* weight,
+                              int32_t* offsets, int32_t* order, int32_t* slot, void* workspace,
+                              int64_t workspace_bytes, proj_stream stream) {
+  const char* const call = "proj_moe_route";
+  int status = PROJ_OK;
+  if (const char* why = refuse_sizes(m, experts, k, &status)) return refuse(status, call, why);
+  if (mode != PROJ_ROUTE_CHOSEN && mode != PROJ_ROUTE_ALL)
+    return refuse(PROJ_EINVAL, call, "unknown mode");
+  if (m > 0 && (!logits || !expert || !weight))
+    return refuse(PROJ_EINVAL, call, "logits, expert or weight is NULL");
+  if (ldl < experts) return refuse(PROJ_EINVAL, call, "ldl is below the number of experts");
+  if ((offsets != nullptr) != (order != nullptr) || (offsets != nullptr) != (slot != nullptr))
+    return refuse(PROJ_EINVAL, call, "offsets, order and slot are not all given or all NULL");
+  if (!aligned_to(logits, 4) || !aligned_to(expert, 4) || !aligned_to(weight, 4) ||
+      !aligned_to(offsets, 4) || !aligned_to(order, 4) || !aligned_to(slot, 4))
+    return refuse(PROJ_EALIGN, call, "a pointer is not aligned to 4 bytes");
+  SortParams p = {};
+  p.logits = logits;
+  p.ldl = ldl;
+  p.expert = expert;
+  p.weight = weight;
+  p.offsets = offsets;
+  p.order = order;
+  p.slot = slot;
+  p.m = m;
+  p.E = static_cast<int>(experts);
+  p.k = static_cast<int>(k);
+  p.mode = mode;
+  return sort_call(call, p, workspace, workspace_bytes, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" int proj_moe_sort(const int32_t* expert, int64_t m, int64_t experts, int64_t k,
+                             int32_t* offsets, int32_t* order, int32_t* slot, void* workspace,
+                             int64_t workspace_bytes, proj_stream stream) {
+  const char* const call = "proj_moe_sort";
+  int status = PROJ_OK;
+  if (const char* why = refuse_sizes(m, experts, k, &status)) return refuse(status, call, why);
+  if (!offsets || (m > 0 && (!expert || !order || !slot)))
+    return refuse(PROJ_EINVAL, call, "a NULL pointer");
+  if (!aligned_to(expert, 4) || !aligned_to(offsets, 4) || !aligned_to(order, 4) ||
+      !aligned_to(slot, 4))
+    return refuse(PROJ_EALIGN, call, "a pointer is not aligned to 4 bytes");
+  SortParams p = {};
+  p.expert = const_cast<int32_t*>(expert);  // read only: there are no logits
+  p.offsets = offsets;
+  p.order = order;
+  p.slot = slot;
+  p.m = m;
+  p.E = static_cast<int>(experts);
+  p.k = static_cast<int>(k);
+  return sort_call(call, p, workspace, workspace_bytes, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" int proj_moe_gather(const void* x, int64_t ldx, const int32_t* slot, int64_t m,
+                               int64_t D, int64_t k, int dtype, void* xs, int64_t ldxs,
+                               proj_stream stream) {
+  RowsParams p = {};
+  p.a = x;
+  p.lda = ldx;
+  p.slot = slot;
+  p.out = xs;
+  p.ldo = ldxs;
+  p.m = m;
+  p.D = D;
+  p.k = static_cast<int>(k);
+  int status = PROJ_OK;
+  if (const char* why = refuse_rows(p, k, dtype, &status))
+    return refuse(status, "proj_moe_gather", why);
+  if (m > 0 && !xs) return refuse(PROJ_EINVAL, "proj_moe_gather", "xs is NULL");
+  return rows_call("proj_moe_gather", Op::kGather, p, dtype, stream);
+}
+
+extern "C" int proj_moe_combine(const void* ys, int64_t ldys, const int32_t* slot,
+                                const float* weight, int64_t m, int64_t D, int64_t k, int dtype,
+                                void* out, int64_t ldo, proj_stream stream) {
+  RowsParams p = {};
+  p.a = ys;
+  p.lda = ldys;
+  p.slot = slot;
+  p.weight = weight;
+  p.out = out;
+  p.ldo = ldo;
+  p.m = m;
+  p.D = D;
+  p.k = static_cast<int>(k);
+  int status = PROJ_OK;
+  if (const char* why = refuse_rows(p, k, dtype, &status))
+    return refuse(status, "proj_moe_combine", why);
+  if (m > 0 && !out) return refuse(PROJ_EINVAL, "proj_moe_combine", "out is NULL");
+  return rows_call("proj_moe_combine", Op::kCombine, p, dtype, stream);
+}
+
+extern "C" int proj_moe_combine_backward(const void* dout, int64_t lddo, const void* ys,
+                                         int64_t ldys, const int32_t* slot, const float* weight,
+                                         int64_t m, int64_t D, int64_t k, int dtype, void* dys,
+                                         int64_t lddys, float* dweight, proj_stream stream) {
+  const char* const call = "proj_moe_combine_backward";
+  RowsParams p = {};
+  p.a = dout;
+  p.lda = lddo;
+  p.b = dweight ? ys : nullptr;
+  p.ldb = ldys;
+  p.slot = slot;
+  p.weight = weight;
+  p.out = dys;
+  p.ldo = lddys;
+  p.dweight = dweight;
+  p.m = m;
+  p.D = D;
+  p.k = static_cast<int>(k);
+  int status = PROJ_OK;
+  if (const char* why = refuse_rows(p, k, dtype, &status)) return refuse(status, call, why);
+  if (m > 0 && !dys && !dweight) return refuse(PROJ_EINVAL, call, "dys and dweight are both NULL");
+  if (m > 0 && dweight && !ys) return refuse(PROJ_EINVAL, call, "dweight is wanted, but ys is NULL");
+  return rows_call(call, Op::kGrad, p, dtype, stream);
+}
+
+extern "C" int proj_moe_route_backward(const float* logits, int64_t ldl, int64_t m,
+                                       int64_t experts, int64_t k, int mode,
+                                       const int32_t* expert, const float* weight,
+                                       const float* dweight, float* dlogits, int64_t lddl,
+                                       proj_stream stream) {
+  const char* const call = "proj_moe_route_backward";
+  int status = PROJ_OK;
+  if (const char* why = refuse_sizes(m, experts, k, &status)) return refuse(status, call, why);
+  if (mode != PROJ_ROUTE_CHOSEN && mode != PROJ_ROUTE_ALL)
+    return refuse(PROJ_EINVAL, call, "unknown mode");
+  if (m > 0 && (!expert || !weight || !dweight || !dlogits || (mode == PROJ_ROUTE_ALL && !logits)))
+    return refuse(PROJ_EINVAL, call, "a NULL pointer");
+  if ((mode == PROJ_ROUTE_ALL && ldl < experts) || lddl < experts)
+    return refuse(PROJ_EINVAL, call, "a row stride is below the number of experts");
+  if (!aligned_to(logits, 4) || !aligned_to(expert, 4) || !aligned_to(weight, 4) ||
+      !aligned_to(dweight, 4) || !aligned_to(dlogits, 4))
+    return refuse(PROJ_EALIGN, call, "a pointer is not aligned to 4 bytes");
+  if (m == 0) return PROJ_OK;
+  RouteGradParams p = {logits, ldl, expert, weight, dweight, dlogits, lddl, m,
+                       static_cast<int>(experts), static_cast<int>(k), mode};
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg =
+      config((m + kGradWarps - 1) / kGradWarps, 1, 32 * kGradWarps, 0, s, attr);
+  const cudaError_t e = experts <= 64    ? cudaLaunchKernelEx(&cfg, route_grad_kernel<2>, p)
+                        : experts <= 256 ? cudaLaunchKernelEx(&cfg, route_grad_kernel<8>, p)
+                                         : cudaLaunchKernelEx(&cfg, route_grad_kernel<32>, p);
+  return e == cudaSuccess ? PROJ_OK : record_cuda(e, call);
+}

@@ -65,7 +65,9 @@ enum proj_layer {
     PROJ_ROUTER = 4
 };
 
-enum proj_dtype { PROJ_BF16 = 0, PROJ_FP32 = 1 };
+/* PROJ_FP16 serves the 4-bit products, the expert sort and the norms below; the
+ * five layers keep PROJ_BF16 and PROJ_FP32. */
+enum proj_dtype { PROJ_BF16 = 0, PROJ_FP32 = 1, PROJ_FP16 = 2 };
 
 enum proj_flags {
     /* Also keep a lossless 12-bit exponent-window copy of a bf16 W and use
@@ -410,6 +412,244 @@ int proj_gemv_static(const void *W, int w_dtype, int64_t N, int64_t K, const voi
  * non-NULL.  Returns PROJ_OK (word zero), PROJ_EDEVICE (non-zero) or
  * PROJ_ECUDA; allocates nothing. */
 int proj_gemv_static_status(proj_stream stream, uint32_t *code);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Operators around the projections: products with 4-bit weights, tokens
+ * sorted by expert and back, and the norms at a block's two ends.  They take
+ * any size (no layer table), work on the caller's buffers, enqueue on
+ * `stream` without host synchronisation or allocation, may be captured in a
+ * CUDA graph, and give the same bits for the same inputs on every call.  Row
+ * strides (ld*) count elements.  Data pointers need the alignment stated
+ * with each call; a call that moves nothing (m = 0) returns PROJ_OK.
+ * Indices that a buffer holds on the device (offsets, slots, expert ids) are
+ * checked in the kernels: one out of range is treated as documented and
+ * never read or written through.
+ * ---------------------------------------------------------------------------
+ *
+ * Products with 4-bit weights and group scales.  A handle holds E matrices
+ * [N, K] (E = 1: one layer; E > 1: one matrix per expert) with
+ *
+ *     w[e, n, k] = s[e, n, k / group] * (q[e, n, k] - z[e, n, k / group]),
+ *
+ * q and z whole numbers in 0..15.  proj_w4_run computes out = x w^T, and
+ * proj_w4_run_experts the same for rows sorted by expert.  Products are
+ * summed in fp32 and rounded once, to the type of x.  Up to a few tokens per
+ * matrix, s multiplies the fp32 sum of its group, so the 4-bit numbers enter
+ * exactly; for many tokens s (q - z) is first rounded to the type of x, as in
+ * a checkpoint that was dequantised to it (proj_w4_describe says which).
+ */
+typedef struct proj_w4_ctx *proj_w4_handle;
+
+/*
+ * Repack E matrices (device to device; the sources are consumed before the
+ * call returns, which synchronises the legacy default stream).
+ *   codes  : [E, N, ceil(K / 2)] bytes; column 2 j of a row is the low half of
+ *            its byte j, column 2 j + 1 the high half.
+ *   scales : [E, N, ceil(K / group)] in `dtype`.
+ *   zeros  : the same shape in bytes (the low four bits count), or NULL: all 8.
+ *   group  : columns per scale: 32 or a multiple of 64.
+ *   dtype  : PROJ_BF16 or PROJ_FP16, the type of x, scales and out.
+ * 1 <= E <= 1024, 1 <= N, K <= 2^20.  Returns NULL on error (*status, if
+ * non-NULL, and proj_last_status() say why).
+ */
+proj_w4_handle proj_w4_prepare(const void *codes, const void *scales, const void *zeros,
+                               int64_t experts, int64_t N, int64_t K, int64_t group, int dtype,
+                               int *status);
+
+/*
+ * out[i, n] = sum over k of x[i, k] w[0, n, k], i < m (E must be 1).
+ *   x   : m rows of K values, ldx >= K a multiple of 8, 16-byte aligned; what
+ *         lies between K and ldx is not read.
+ *   out : m rows of N values, ldo >= N, aligned to an element.
+ * x and out must not overlap.  m <= 2^20.
+ */
+int proj_w4_run(proj_w4_handle h, const void *x, int64_t ldx, int64_t m, void *out, int64_t ldo,
+                proj_stream stream);
+
+/*
+ * Rows offsets[e] .. offsets[e + 1] - 1 of x meet matrix e.  offsets: E + 1
+ * int32 on the device, not decreasing, 0 .. m (values outside are moved into
+ * that range).  Rows that belong to no expert are not read, and their rows of
+ * out keep what they held.
+ */
+int proj_w4_run_experts(proj_w4_handle h, const void *x, int64_t ldx, int64_t m,
+                        const int32_t *offsets, void *out, int64_t ldo, proj_stream stream);
+
+/* The kernel and launch shape a call with m rows uses (at most `cap` bytes,
+ * NUL-terminated). */
+int proj_w4_describe(proj_w4_handle h, int64_t m, char *buf, size_t cap);
+
+/* Read and clear the handle's device status word (synchronises `stream`), as
+ * proj_device_status. */
+int proj_w4_device_status(proj_w4_handle h, proj_stream stream, uint32_t *code);
+
+/* Free the handle (synchronises the device first; NULL is ignored). */
+void proj_w4_destroy(proj_w4_handle h);
+
+/*
+ * Tokens sorted by expert and back.  m tokens each choose k of E experts;
+ * entry (t, j) is token t's j-th choice, flat index t k + j.  The sort is
+ * stable: rows of one expert stand in the order of their flat indices.
+ * 1 <= E <= 1024, 1 <= k <= min(E, 32), m * k < 2^31.
+ */
+enum proj_route_mode {
+    PROJ_ROUTE_CHOSEN = 0, /* weights: softmax over the chosen logits */
+    PROJ_ROUTE_ALL = 1     /* weights: softmax over all logits, at the chosen ones */
+};
+
+/* Bytes of workspace that proj_moe_route and proj_moe_sort want (0 is
+ * possible); -1 for arguments they refuse. */
+int64_t proj_moe_workspace(int64_t m, int64_t experts, int64_t k);
+
+/*
+ * Choose and sort.
+ *   logits  : fp32 [m, E], stride ldl >= E, aligned to an element.
+ *   expert  : int32 [m, k], the k largest logits in descending order, equal
+ *             ones by ascending index.  Logits of -infinity and NaN are never
+ *             chosen: where a row has fewer than k others, the rest is -1.
+ *   weight  : fp32 [m, k]; 0 where expert is -1.
+ *   offsets : int32 [E + 1]: rows offsets[e] .. offsets[e + 1] - 1 of the
+ *             sorted order are expert e's.
+ *   order   : int32 [m k]: the flat index of each sorted row; -1 from
+ *             offsets[E] on.
+ *   slot    : int32 [m, k]: the sorted row of each entry; -1 where expert is -1.
+ * offsets, order and slot may be NULL together: then nothing is sorted.  The
+ * workspace (16-byte aligned) is free again when the call's work is done.
+ */
+int proj_moe_route(const float *logits, int64_t ldl, int64_t m, int64_t experts, int64_t k,
+                   int mode, int32_t *expert, float *weight, int32_t *offsets, int32_t *order,
+                   int32_t *slot, void *workspace, int64_t workspace_bytes, proj_stream stream);
+
+/* The sort alone, of the caller's choices (ids outside 0 .. E - 1 are no
+ * expert's: slot -1). */
+int proj_moe_sort(const int32_t *expert, int64_t m, int64_t experts, int64_t k, int32_t *offsets,
+                  int32_t *order, int32_t *slot, void *workspace, int64_t workspace_bytes,
+                  proj_stream stream);
+
+/*
+ * xs[slot[t, j], :] = x[t, :].  x: m rows of D, xs: m k rows of D, both
+ * `dtype` (any of proj_dtype), aligned to an element (16-byte aligned
+ * pointers and strides are faster).  Rows of xs that no entry names keep
+ * what they held; slots outside 0 .. m k - 1 are skipped.
+ */
+int proj_moe_gather(const void *x, int64_t ldx, const int32_t *slot, int64_t m, int64_t D,
+                    int64_t k, int dtype, void *xs, int64_t ldxs, proj_stream stream);
+
+/*
+ * out[t, :] = sum over j of weight[t, j] ys[slot[t, j], :], in fp32 in the
+ * order of j, rounded once; a token without a valid slot gets zeros.  weight
+ * NULL: all ones -- the gradient of proj_moe_gather.
+ */
+int proj_moe_combine(const void *ys, int64_t ldys, const int32_t *slot, const float *weight,
+                     int64_t m, int64_t D, int64_t k, int dtype, void *out, int64_t ldo,
+                     proj_stream stream);
+
+/*
+ * Gradient of proj_moe_combine: dys[slot[t, j], :] = weight[t, j] dout[t, :]
+ * and dweight[t, j] = sum over d of dout[t, d] ys[slot[t, j], d] (0 for a slot
+ * outside 0 .. m k - 1).  dys or dweight may be NULL (then ys may be, with
+ * dweight); rows of dys that no entry names keep what they held.
+ */
+int proj_moe_combine_backward(const void *dout, int64_t lddo, const void *ys, int64_t ldys,
+                              const int32_t *slot, const float *weight, int64_t m, int64_t D,
+                              int64_t k, int dtype, void *dys, int64_t lddys, float *dweight,
+                              proj_stream stream);
+
+/*
+ * Gradient of the weights of proj_moe_route with respect to the logits, with
+ * the choice held fixed.  expert and weight: as proj_moe_route gave them;
+ * logits are read in PROJ_ROUTE_ALL mode only (may be NULL otherwise).
+ * dlogits: fp32 [m, E], every element written.
+ */
+int proj_moe_route_backward(const float *logits, int64_t ldl, int64_t m, int64_t experts,
+                            int64_t k, int mode, const int32_t *expert, const float *weight,
+                            const float *dweight, float *dlogits, int64_t lddl,
+                            proj_stream stream);
+
+/*
+ * The norms after one block and before the next, with the block's gate and
+ * the residual scale, in one pass.  Row by row, in fp32, each output rounded
+ * once:
+ *
+ *     n      = y rsqrt(mean(y^2) + eps) w_post      (y_plain: n = y)
+ *     out    = alpha residual + beta g n,           g = act(gate)
+ *     normed = out' rsqrt(mean(out'^2) + eps) w_pre (out' = out before rounding)
+ */
+enum proj_gate_mode {
+    PROJ_GATE_NONE = 0,    /* g = 1 */
+    PROJ_GATE_CHANNEL = 1, /* gate [D] */
+    PROJ_GATE_ELEMENT = 2, /* gate [m, D], stride ldg */
+    PROJ_GATE_TOKEN = 3    /* gate [m] */
+};
+enum proj_gate_act { PROJ_GATE_LINEAR = 0, PROJ_GATE_SIGMOID = 1 };
+
+typedef struct proj_norm_args {
+    int64_t m, D;          /* 1 <= D <= 16384 */
+    int dtype;             /* of every tensor but the statistics: any of proj_dtype */
+    int gate_mode;         /* enum proj_gate_mode */
+    int gate_act;          /* enum proj_gate_act */
+    int y_plain;           /* 1: no norm after the block (w_post and rstd_post NULL) */
+    float eps, alpha, beta;
+    const void *y;         /* the block's output [m, D]; NULL: no block, out = alpha residual
+                              (then w_post, rstd_post NULL and gate_mode NONE) */
+    int64_t ldy;
+    const void *residual;  /* [m, D] */
+    int64_t ldr;
+    const void *gate;      /* by gate_mode; NULL for NONE */
+    int64_t ldg;
+    const void *w_post;    /* [D], NULL: ones */
+    const void *w_pre;     /* [D], NULL: ones */
+    void *out;             /* [m, D]; may be `residual` itself (same stride), or NULL */
+    int64_t ldo;
+    void *normed;          /* [m, D]; may be `y` itself (same stride), or NULL; one of out
+                              and normed is not NULL, and they do not overlap */
+    int64_t ldn;
+    float *rstd_post;      /* [m], optional: the two rsqrt factors, which the gradient wants */
+    float *rstd_pre;
+} proj_norm_args;
+
+/* Pointers are aligned to an element; rows that all start on 16 bytes, with D
+ * a multiple of 16 bytes, are faster. */
+int proj_norm(const proj_norm_args *args, proj_stream stream);
+
+typedef struct proj_norm_grad_args {
+    int64_t m, D;          /* the forward call's values, down to rstd_pre */
+    int dtype, gate_mode, gate_act, y_plain;
+    float eps, alpha, beta;
+    const void *y;
+    int64_t ldy;
+    const void *residual;
+    int64_t ldr;
+    const void *gate;
+    int64_t ldg;
+    const void *w_post;
+    const void *w_pre;
+    const float *rstd_post; /* as the forward call wrote them (rstd_post: unless y is NULL or */
+    const float *rstd_pre;  /* y_plain; rstd_pre: unless dnormed is NULL) */
+    const void *dout;       /* gradient of out [m, D], NULL: zero */
+    int64_t lddo;
+    const void *dnormed;    /* gradient of normed [m, D], NULL: zero (not both NULL) */
+    int64_t lddn;
+    void *dy;               /* gradients, each optional; none may overlap an input */
+    int64_t lddy;
+    void *dresidual;
+    int64_t lddr;
+    void *dgate;            /* CHANNEL: fp32 [D]; ELEMENT: dtype [m, D], stride lddg;
+                               TOKEN: dtype [m] */
+    int64_t lddg;
+    float *dw_post;         /* fp32 [D] */
+    float *dw_pre;          /* fp32 [D] */
+    void *workspace;        /* proj_norm_workspace(m, D) bytes, 16-byte aligned; wanted for
+                               dw_post, dw_pre and a CHANNEL dgate */
+    int64_t workspace_bytes;
+} proj_norm_grad_args;
+
+/* Bytes of workspace of proj_norm_backward; -1 for m < 0 or a bad D. */
+int64_t proj_norm_workspace(int64_t m, int64_t D);
+
+/* Gradients of proj_norm; sums over tokens are taken in a fixed order. */
+int proj_norm_backward(const proj_norm_grad_args *args, proj_stream stream);
 
 #ifdef __cplusplus
 }

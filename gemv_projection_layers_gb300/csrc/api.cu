@@ -17,6 +17,7 @@
 
 #include "../../include/proj.h"
 #include "kernels.h"
+#include "w4.h"
 
 using namespace proj;
 
@@ -103,6 +104,26 @@ bool make_x_map(CUtensorMap* map, const void* x, int64_t m, int64_t K, int box_r
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
+
+}  // namespace
+
+// Rows of K 16-bit elements at a stride of ld, in boxes of 64 columns x
+// box_rows rows with the 128-byte swizzle; zeros outside.
+bool proj::make_rows_map(CUtensorMap* map, const void* base, int64_t rows, int64_t K, int64_t ld,
+                         bool fp16, int box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
+  const cuuint32_t box[2] = {64u, static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[2] = {1u, 1u};
+  return fn(map, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+            const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+namespace {
 
 // A row-major bf16 [rows, K] matrix viewed as (32 columns, rows, K / 32
 // steps): a box (32, box_rows, box_steps) lands as [step][row][64 bytes].

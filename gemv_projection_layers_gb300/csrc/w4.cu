@@ -9,16 +9,20 @@
 // bits) are exact in bf16 and fp16, so a group's sum is the exact products'
 // fp32 sum, and s multiplies that sum in fp32.
 //
-// Packed layout.  Rows in blocks of 16, columns in units of 64.  Lane
-// l = 4 g + t of the warp that reads unit (rb, u) holds columns
-// 64 u + 32 h + 8 t + 0..7 (h = 0, 1) of rows 16 rb + g and + 8: 16 bytes,
-// [h0 row g][h0 row g + 8][h1 row g][h1 row g + 8], at (rb KU + u) 512 + 16 l.
-// One load of a lane is four A fragments: the order of columns within a unit
-// is free as long as x follows it, and with this one the B fragments of two
-// steps are 16 consecutive bytes of an x row.  In each 32-bit word column
-// 2 i stands at bit 4 i and column 2 i + 1 at bit 16 + 4 i, so one shift and
-// one mask give a pair of 16-bit lanes.  Scales and zeros: [rb][group][g]{row
-// g, row g + 8}.
+// Packed layout.  Rows in blocks of 16, eight blocks a tile, columns in units
+// of 64.  Lane l = 4 g + t of the warp that reads unit u of block b of tile rt
+// holds columns 64 u + 32 h + 16 s + 4 t + 0..3 (h, s = 0, 1) of the block's
+// rows g and g + 8: 16 bytes, [h0 row g][h0 row g + 8][h1 row g][h1 row g + 8],
+// at ((rt KU + u) 8 + b) 512 + 16 l.
+// One load of a lane is four A fragments: the order of columns within a step
+// of 16 is free as long as x follows it, and with this one a lane's B fragment
+// is 8 consecutive bytes of an x row, and its A words are those that a
+// 16-lane store to tensor memory takes (w4_tc.cu).  In each 32-bit word
+// column 2 i stands at bit 4 i and column 2 i + 1 at bit 16 + 4 i, so one
+// shift and one mask give a pair of 16-bit lanes.  Scales and zeros:
+// [rt][group][b][g]{row g, row g + 8}; for groups of 32 [rt][u][b][g][h]{row
+// g, row g + 8}, so that in either case one load of a lane has what a unit
+// needs, and one bulk copy what the 128 rows of a unit need.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -26,10 +30,12 @@
 #include <new>
 
 #include "../../include/proj.h"
+#include "cluster_common.cuh"
 #include "kernels.h"
 #include "ptx.cuh"
 #include "vec.cuh"
 #include "w4.h"
+#include "w4_num.cuh"
 
 namespace proj {
 namespace {
@@ -44,13 +50,13 @@ __device__ __forceinline__ uint32_t code_at(const uint8_t* row, int64_t k, int64
 
 // One thread per 16-byte lane record.
 __global__ void pack_codes_kernel(const uint8_t* __restrict__ codes, uint4* __restrict__ dst,
-                                  int64_t E, int64_t N, int64_t K, int64_t RB, int64_t KU) {
+                                  int64_t E, int64_t N, int64_t K, int64_t RT, int64_t KU) {
   const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (i >= E * RB * KU * 32) return;
-  const int lane = static_cast<int>(i & 31);
-  const int64_t u = (i >> 5) % KU;
-  const int64_t rb = (i >> 5) / KU % RB;
-  const int64_t e = (i >> 5) / KU / RB;
+  if (i >= E * RT * KU * 256) return;
+  const int lane = static_cast<int>(i & 31), b = static_cast<int>((i >> 5) & 7);
+  const int64_t u = (i >> 8) % KU;
+  const int64_t rt = (i >> 8) / KU % RT;
+  const int64_t e = (i >> 8) / KU / RT;
   const int g = lane >> 2, t = lane & 3;
   const int64_t bytes = (K + 1) / 2;
   uint32_t w[4];
@@ -58,14 +64,14 @@ __global__ void pack_codes_kernel(const uint8_t* __restrict__ codes, uint4* __re
   for (int h = 0; h < 2; ++h)
 #pragma unroll
     for (int hi = 0; hi < 2; ++hi) {
-      const int64_t n = rb * 16 + g + 8 * hi;
+      const int64_t n = rt * 128 + b * 16 + g + 8 * hi;
       uint32_t v = 0;
       if (n < N) {
         const uint8_t* row = codes + (e * N + n) * bytes;
-        const int64_t k0 = u * 64 + 32 * h + 8 * t;
+        const int64_t k0 = u * 64 + 32 * h + 4 * t;
 #pragma unroll
         for (int c = 0; c < 8; ++c)
-          v |= code_at(row, k0 + c, K) << ((c & 1) * 16 + (c >> 1) * 4);
+          v |= code_at(row, k0 + 16 * (c >> 2) + (c & 3), K) << ((c & 1) * 16 + (c >> 1) * 4);
       }
       w[2 * h + hi] = v;
     }
@@ -76,14 +82,16 @@ __global__ void pack_codes_kernel(const uint8_t* __restrict__ codes, uint4* __re
 __global__ void pack_scales_kernel(const uint16_t* __restrict__ scales,
                                    const uint8_t* __restrict__ zeros, uint16_t* __restrict__ ds,
                                    uint8_t* __restrict__ dz, int64_t E, int64_t N, int64_t NG,
-                                   int64_t NGp, int64_t RB) {
+                                   int64_t NGp, int64_t RT, bool g32) {
   const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (i >= E * RB * NGp * 16) return;
-  const int r = static_cast<int>(i & 15);
-  const int64_t grp = (i >> 4) % NGp;
-  const int64_t rb = (i >> 4) / NGp % RB;
-  const int64_t e = (i >> 4) / NGp / RB;
-  const int64_t n = rb * 16 + (r >> 1) + 8 * (r & 1);
+  if (i >= E * RT * NGp * 128) return;
+  const int64_t j = i % (NGp * 128);  // within the tile
+  const int64_t rt = i / (NGp * 128) % RT;
+  const int64_t e = i / (NGp * 128) / RT;
+  const int64_t grp = g32 ? 2 * (j >> 8) + ((j >> 1) & 1) : j >> 7;
+  const int b = static_cast<int>(g32 ? (j >> 5) & 7 : (j >> 4) & 7);
+  const int g = static_cast<int>(g32 ? (j >> 2) & 7 : (j >> 1) & 7);
+  const int64_t n = rt * 128 + b * 16 + g + 8 * (j & 1);
   const bool in = n < N && grp < NG;
   const int64_t src = (e * N + n) * NG + grp;
   ds[i] = in ? scales[src] : 0;
@@ -92,59 +100,32 @@ __global__ void pack_scales_kernel(const uint16_t* __restrict__ scales,
 
 // ------------------------------------------------------ streaming kernel --
 
+// Four consecutive x values of a row from column c, which K cuts: zeros from
+// K on.
 template <typename T>
-struct Num;
-template <>
-struct Num<__nv_bfloat16> {
-  static constexpr uint32_t kMagic = 0x43004300u;  // 128 + q in a pair's low mantissa bits
-  static __device__ __forceinline__ uint32_t offset(uint32_t z) {  // 128 + z, twice
-    return (0x4300u + z) * 0x10001u;
-  }
-  static __device__ __forceinline__ uint32_t sub(uint32_t a, uint32_t b) {
-    uint32_t d;
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-  }
-  static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                             uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  }
-};
-template <>
-struct Num<__half> {
-  static constexpr uint32_t kMagic = 0x64006400u;  // 1024 + q
-  static __device__ __forceinline__ uint32_t offset(uint32_t z) {
-    return (0x6400u + z) * 0x10001u;
-  }
-  static __device__ __forceinline__ uint32_t sub(uint32_t a, uint32_t b) {
-    uint32_t d;
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-  }
-  static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                             uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  }
-};
-
-// Eight consecutive x values of a row from column c; zeros from K on.
-template <typename T>
-__device__ __forceinline__ uint4 load_x8(const T* row, int c, int K) {
-  if (c + 8 <= K) return *reinterpret_cast<const uint4*>(row + c);
-  uint4 v = make_uint4(0, 0, 0, 0);
-  uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+__device__ __noinline__ uint2 load_x4_edge(const T* row, int c, int K) {
+  uint2 v = make_uint2(0, 0);
   const uint16_t* r = reinterpret_cast<const uint16_t*>(row);
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (c + i < K) w[i >> 1] |= static_cast<uint32_t>(r[c + i]) << (16 * (i & 1));
+  if (c < K) v.x = r[c];
+  if (c + 1 < K) v.x |= static_cast<uint32_t>(r[c + 1]) << 16;
+  if (c + 2 < K) v.y = r[c + 2];
+  if (c + 3 < K) v.y |= static_cast<uint32_t>(r[c + 3]) << 16;
   return v;
 }
+
+__device__ __forceinline__ float ld_dsmem_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+  return v;
+}
+
+// Launch shape of the streaming kernel: NT tiles of 8 tokens, RB blocks of 16
+// rows a CTA, clusters of C CTAs along K.
+constexpr int kStreamWarps = 8;
+struct StreamShape {
+  int NT, RB, C;
+  int64_t tiles;
+};
 
 struct Tile {
   int expert;
@@ -202,135 +183,225 @@ __device__ __forceinline__ Tile find_tile(const int32_t* __restrict__ offsets, i
   return {s_found[0], s_found[1], s_found[2]};
 }
 
-// A CTA takes one block of 16 weight rows and one tile of 8 NT tokens; its W
-// warps split the units of K (warp w: units w, w + W, ...) and meet in
-// shared memory.
-template <typename T, bool kG32, bool kZeros, int NT, int W>
-__global__ void __launch_bounds__(32 * W) w4_stream_kernel(const W4Params p) {
-  __shared__ alignas(16) float s_red[W][NT][32][4];
+// A CTA takes RB blocks of 16 weight rows and one tile of 8 NT tokens; the
+// warps of the C CTAs of a cluster deal the units of K out in turn and meet
+// in shared memory, CTAs after that through distributed shared memory.  A
+// warp keeps kD units of codes, scales and x in flight, all of them straight
+// to registers: the x of 8 tokens is two bytes per byte of one block's codes,
+// so RB = 2 blocks share it, and it comes from L2.
+template <typename T, bool kG32, bool kZeros, int NT, int RB>
+__global__ void __launch_bounds__(32 * kStreamWarps) w4_stream_kernel(const W4Params p, const int C) {
+  constexpr int W = kStreamWarps;
+  constexpr int kD = NT == 1 ? 4 : 2;
+  using Scale = typename ScaleOf<kG32>::Pair;
+  using Zero = typename ScaleOf<kG32>::Bytes;
+  __shared__ alignas(16) float s_red[W][RB][NT][32][4];
+  __shared__ float s_part[RB * 16 * NT * 8];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
-  const int rb = blockIdx.x;
+  const int rank = static_cast<int>(blockIdx.x) % C;
+  const int rb0 = static_cast<int>(blockIdx.x) / C * RB;
+
+  uint4 code[kD][RB];
+  Scale sc[kD][RB];
+  Zero ze[kD][RB];
+  uint2 xf[kD][NT][4];
+  const uint4* codes[RB];
+  const Scale* scales[RB];
+  const Zero* zeros[RB];
+  const int units = kG32 ? p.KU : p.NGp;  // lines of scales in a tile
+  auto open = [&](int expert) {
+#pragma unroll
+    for (int r = 0; r < RB; ++r) {
+      const int rb = min(rb0 + r, p.RB - 1);
+      const int64_t tile = static_cast<int64_t>(expert) * p.RT + (rb >> 3);
+      codes[r] = p.codes + tile * p.KU * 256 + (rb & 7) * 32 + lane;
+      const int64_t at = tile * units * 64 + (rb & 7) * 8 + g;
+      scales[r] = reinterpret_cast<const Scale*>(p.scales) + at;
+      zeros[r] = reinterpret_cast<const Zero*>(p.zeros) + at;
+    }
+  };
+  auto fetch_w = [&](int d, int u) {
+    if (u >= p.KU) return;
+    const int at = (kG32 ? u : p.group_of(u)) * 64;
+#pragma unroll
+    for (int r = 0; r < RB; ++r) {
+      code[d][r] = ld_stream_v4(codes[r] + u * 256);
+      sc[d][r] = __ldg(scales[r] + at);
+      if (kZeros) ze[d][r] = __ldg(zeros[r] + at);
+    }
+  };
+
+  const int u0 = rank * W + warp, stride = W * C;
   griddep_launch_dependents();
-  griddep_wait();
   Tile tile;
   if (p.offsets) {
+    griddep_wait();
     tile = find_tile<32 * W>(p.offsets, p.E, p.m, 8 * NT, blockIdx.y);
-    if (tile.rows == 0) return;
+    if (tile.rows == 0) return;  // every CTA of the cluster
+    open(tile.expert);
+#pragma unroll
+    for (int d = 0; d < kD; ++d) fetch_w(d, u0 + d * stride);
   } else {
     tile.expert = 0;
     tile.row0 = static_cast<int64_t>(blockIdx.y) * 8 * NT;
     tile.rows = static_cast<int>(min(static_cast<int64_t>(8 * NT), p.m - tile.row0));
+    // the weights are constant: their first loads do not wait for the kernel before
+    open(0);
+#pragma unroll
+    for (int d = 0; d < kD; ++d) fetch_w(d, u0 + d * stride);
+    griddep_wait();
   }
-  const int64_t block = static_cast<int64_t>(tile.expert) * p.RB + rb;
-  const uint4* codes = p.codes + block * p.KU * 32 + lane;
-  const uint32_t* scales = reinterpret_cast<const uint32_t*>(p.scales) + block * p.NGp * 8 + g;
-  const uint16_t* zeros = reinterpret_cast<const uint16_t*>(p.zeros) + block * p.NGp * 8 + g;
-  const T* x = static_cast<const T*>(p.x) + tile.row0 * p.ldx;
+  const T* x[NT];
+  bool live[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    x[j] = static_cast<const T*>(p.x) + (tile.row0 + 8 * j + g) * p.ldx + 4 * t;
+    live[j] = 8 * j + g < tile.rows;
+#pragma unroll
+    for (int d = 0; d < kD; ++d)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) xf[d][j][i] = make_uint2(0, 0);
+  }
+  const int whole = p.K / 64;  // units that K does not cut
+  auto fetch_x = [&](int d, int u) {
+    if (u >= p.KU) return;
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+      if (live[j]) {
+        const T* at = x[j] + u * 64;
+        if (u < whole) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) xf[d][j][i] = *reinterpret_cast<const uint2*>(at + 16 * i);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            xf[d][j][i] = load_x4_edge(at, 16 * i, p.K - u * 64 - 4 * t);
+        }
+      }
+  };
+#pragma unroll
+  for (int d = 0; d < kD; ++d) fetch_x(d, u0 + d * stride);
 
-  float acc[NT][4] = {};
-  const int upg = kG32 ? 1 : p.group / 64;  // units per group
-#pragma unroll 4
-  for (int u = warp; u < p.KU; u += W) {
-    const uint4 q = ld_stream_v4(codes + static_cast<int64_t>(u) * 32);
-    const uint32_t word[4] = {q.x, q.y, q.z, q.w};
-    float part[NT][4];
+  float acc[RB][NT][4] = {};
+  for (int ub = u0; ub < p.KU; ub += kD * stride) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int grp = kG32 ? 2 * u + h : u / upg;
-      uint32_t off[2] = {Num<T>::offset(8), Num<T>::offset(8)};
-      if (kZeros) {
-        const uint32_t z = __ldg(zeros + grp * 8);
-        off[0] = Num<T>::offset(z & 255u);
-        off[1] = Num<T>::offset(z >> 8);
-      }
-      uint32_t a[2][4];
+    for (int d = 0; d < kD; ++d) {
+      const int u = ub + d * stride;
+      if (u < p.KU) {
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
+        for (int r = 0; r < RB; ++r) {
+          const uint32_t word[4] = {code[d][r].x, code[d][r].y, code[d][r].z, code[d][r].w};
+          float part[NT][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int hi = i & 1, pair = 2 * s + (i >> 1);
-          a[s][i] = Num<T>::sub(((word[2 * h + hi] >> (4 * pair)) & 0x000F000Fu) | Num<T>::kMagic,
-                                off[hi]);
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t z = kZeros ? ScaleOf<kG32>::bytes(ze[d][r], h) : 0x0808u;
+            const uint32_t zero[2] = {zero_pair<T>(z, 0), zero_pair<T>(z, 1)};
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+              // rows g, g + 8 of the step's columns 4 t, + 1, then of + 2, + 3
+              const uint32_t a[4] = {code_pair<T>(word[2 * h], 2 * s, zero[0]),
+                                     code_pair<T>(word[2 * h + 1], 2 * s, zero[1]),
+                                     code_pair<T>(word[2 * h], 2 * s + 1, zero[0]),
+                                     code_pair<T>(word[2 * h + 1], 2 * s + 1, zero[1])};
+#pragma unroll
+              for (int j = 0; j < NT; ++j) {
+                const uint2 b = xf[d][j][2 * h + s];
+                if (s == 0 && (kG32 || h == 0))
+                  Num<T>::mma_first(part[j], a, b.x, b.y);
+                else
+                  Num<T>::mma(part[j], a, b.x, b.y);
+              }
+            }
+            if (kG32 || h == 1) {
+              const uint32_t sp = ScaleOf<kG32>::pair(sc[d][r], h);
+              const float s0 = to_f32(reinterpret_cast<const T*>(&sp)[0]);
+              const float s1 = to_f32(reinterpret_cast<const T*>(&sp)[1]);
+#pragma unroll
+              for (int j = 0; j < NT; ++j) {
+                acc[r][j][0] = fmaf(s0, part[j][0], acc[r][j][0]);
+                acc[r][j][1] = fmaf(s0, part[j][1], acc[r][j][1]);
+                acc[r][j][2] = fmaf(s1, part[j][2], acc[r][j][2]);
+                acc[r][j][3] = fmaf(s1, part[j][3], acc[r][j][3]);
+              }
+            }
+          }
         }
-      if (kG32 || h == 0) {
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) part[j][i] = 0.f;
-      }
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        uint4 b = make_uint4(0, 0, 0, 0);
-        if (8 * j + g < tile.rows)
-          b = load_x8(x + static_cast<int64_t>(8 * j + g) * p.ldx, u * 64 + 32 * h + 8 * t, p.K);
-        Num<T>::mma(part[j], a[0], b.x, b.y);
-        Num<T>::mma(part[j], a[1], b.z, b.w);
-      }
-      if (kG32 || h == 1) {
-        const uint32_t sp = __ldg(scales + grp * 8);
-        const float s0 = to_f32(reinterpret_cast<const T*>(&sp)[0]);
-        const float s1 = to_f32(reinterpret_cast<const T*>(&sp)[1]);
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          acc[j][0] = fmaf(s0, part[j][0], acc[j][0]);
-          acc[j][1] = fmaf(s0, part[j][1], acc[j][1]);
-          acc[j][2] = fmaf(s1, part[j][2], acc[j][2]);
-          acc[j][3] = fmaf(s1, part[j][3], acc[j][3]);
-        }
+        fetch_w(d, u + kD * stride);
+        fetch_x(d, u + kD * stride);
       }
     }
   }
 #pragma unroll
-  for (int j = 0; j < NT; ++j)
-    *reinterpret_cast<float4*>(s_red[warp][j][lane]) =
-        make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
+  for (int r = 0; r < RB; ++r)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+      *reinterpret_cast<float4*>(s_red[warp][r][j][lane]) =
+          make_float4(acc[r][j][0], acc[r][j][1], acc[r][j][2], acc[r][j][3]);
   __syncthreads();
-  // sum the warps' partials in order; element i of lane l is row g + 8 (i / 2),
-  // token 2 t + i % 2
-  T* out = static_cast<T*>(p.out);
-  for (int i = threadIdx.x; i < NT * 128; i += 32 * W) {
-    const int n16 = i & 15, tok = i >> 4;
-    const int l = (n16 & 7) * 4 + ((tok & 7) >> 1);
-    const int c = (n16 >> 3) * 2 + (tok & 1);
+  // Sum the warps' partials in order.  Value i of the tile: row i % (16 RB),
+  // token i / (16 RB); element c of lane l is row g + 8 (c / 2), token
+  // 2 t + c % 2.
+  constexpr int kRows = 16 * RB;
+  T* out = static_cast<T*>(p.out) + tile.row0 * p.ldo + static_cast<int64_t>(rb0) * 16;
+  const int n_left = p.N - rb0 * 16;
+  for (int i = threadIdx.x; i < kRows * NT * 8; i += 32 * W) {
+    const int n = i % kRows, tok = i / kRows;
+    const int l = (n & 7) * 4 + ((tok & 7) >> 1);
+    const int c = ((n >> 3) & 1) * 2 + (tok & 1);
     float s = 0.f;
 #pragma unroll
-    for (int w = 0; w < W; ++w) s += s_red[w][tok >> 3][l][c];
-    const int64_t n = static_cast<int64_t>(rb) * 16 + n16;
-    if (tok < tile.rows && n < p.N) out[(tile.row0 + tok) * p.ldo + n] = from_f32<T>(s);
+    for (int w = 0; w < W; ++w) s += s_red[w][n >> 4][tok >> 3][l][c];
+    if (C > 1)
+      s_part[i] = s;
+    else if (tok < tile.rows && n < n_left)
+      out[tok * p.ldo + n] = from_f32<T>(s);
+  }
+  if (C > 1) {
+    cluster_sync_all();
+    const uint32_t base = smem_u32(s_part);
+    for (int i = rank * 32 * W + threadIdx.x; i < kRows * tile.rows; i += 32 * W * C) {
+      const int n = i % kRows, tok = i / kRows;
+      float s = 0.f;
+      for (int r = 0; r < C; ++r)
+        s += ld_dsmem_f32(map_to_rank(base + 4 * i, static_cast<uint32_t>(r)));
+      if (n < n_left) out[tok * p.ldo + n] = from_f32<T>(s);
+    }
+    cluster_sync_all();  // no CTA leaves while another reads its partial sums
   }
 }
 
-template <typename T, bool kG32, bool kZeros, int NT, int W>
-cudaError_t stream_launch(const W4Params& p, int64_t tiles, cudaStream_t s) {
+template <typename T, bool kG32, bool kZeros, int NT, int RB>
+cudaError_t stream_launch(const W4Params& p, const StreamShape& sh, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.RB), static_cast<unsigned>(tiles));
-  cfg.blockDim = dim3(32 * W);
+  cfg.gridDim = dim3(static_cast<unsigned>((p.RB + RB - 1) / RB * sh.C),
+                     static_cast<unsigned>(sh.tiles));
+  cfg.blockDim = dim3(32 * kStreamWarps);
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(sh.C);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, w4_stream_kernel<T, kG32, kZeros, NT, W>, p);
+  cfg.numAttrs = sh.C > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, w4_stream_kernel<T, kG32, kZeros, NT, RB>, p, sh.C);
 }
 
-template <typename T, int NT, int W>
-cudaError_t stream_form(const W4Params& p, int64_t tiles, cudaStream_t s) {
+template <typename T, int NT, int RB>
+cudaError_t stream_form(const W4Params& p, const StreamShape& sh, cudaStream_t s) {
   if (p.group == 32)
-    return p.zeros ? stream_launch<T, true, true, NT, W>(p, tiles, s)
-                   : stream_launch<T, true, false, NT, W>(p, tiles, s);
-  return p.zeros ? stream_launch<T, false, true, NT, W>(p, tiles, s)
-                 : stream_launch<T, false, false, NT, W>(p, tiles, s);
+    return p.zeros ? stream_launch<T, true, true, NT, RB>(p, sh, s)
+                   : stream_launch<T, true, false, NT, RB>(p, sh, s);
+  return p.zeros ? stream_launch<T, false, true, NT, RB>(p, sh, s)
+                 : stream_launch<T, false, false, NT, RB>(p, sh, s);
 }
 
-template <typename T>
-cudaError_t stream_any(int nt, const W4Params& p, int64_t tiles, cudaStream_t s) {
-  switch (nt) {
-    case 1: return stream_form<T, 1, 8>(p, tiles, s);
-    case 2: return stream_form<T, 2, 8>(p, tiles, s);
-    default: return stream_form<T, 4, 8>(p, tiles, s);
-  }
+template <typename T, int NT>
+cudaError_t stream_any(const W4Params& p, const StreamShape& sh, cudaStream_t s) {
+  return sh.RB == 1 ? stream_form<T, NT, 1>(p, sh, s) : stream_form<T, NT, 2>(p, sh, s);
 }
 
 int refuse(int status, const char* call, const char* why) {
@@ -350,15 +421,54 @@ struct proj_w4_ctx {
   W4Params p;       // sizes and the packed weights; x, out, offsets are each call's
   int dtype;
   uint8_t* base;    // one allocation: codes, scales, zeros, status word
+  int sms;
+  int clusters[4];  // of 1, 2, 4, 8 CTAs of the tensor-core kernel that run at once
 };
 
 namespace {
 
-// Token tiles of a call: 8 rows each while a matrix meets few rows, 32 rows
-// at most (the rows an expert meets on average, for a stack of experts).
-int stream_nt(const proj_w4_ctx* h, int64_t m, bool experts) {
-  const int64_t rows = experts ? (m + h->p.E - 1) / h->p.E : m;
-  return rows <= 8 ? 1 : (rows <= 16 ? 2 : 4);
+// What a call with m rows runs.
+struct Plan {
+  bool tc;
+  StreamShape stream;
+  int tn, C;
+  int64_t grid;
+};
+
+// Rows that a matrix meets (on average, for experts) up to which the weights
+// are streamed with exact 4-bit products; above, the tensor-core kernel.
+constexpr int64_t kStreamRows = 16;
+
+Plan make_plan(const proj_w4_ctx* h, int64_t m, bool experts) {
+  const W4Params& p = h->p;
+  Plan pl = {};
+  const int64_t rows = experts ? (m + p.E - 1) / p.E : m;
+  pl.tc = rows > kStreamRows;
+  if (!pl.tc) {
+    StreamShape& s = pl.stream;
+    s.NT = rows <= 8 ? 1 : 2;
+    const int64_t per = 8 * s.NT;
+    // of the experts that have rows, each has at most one part-filled tile
+    s.tiles = experts ? std::min<int64_t>(p.E, m) + m / per : (m + per - 1) / per;
+    // Two blocks of rows share the loads of x where that leaves a CTA per SM
+    // or so; K is split over a cluster while that puts at most two CTAs on an SM.
+    s.RB = experts || p.RB * 3 >= h->sms * 4 ? 2 : 1;
+    s.C = 1;
+    const int64_t groups = (p.RB + s.RB - 1) / s.RB * s.tiles;
+    while (!experts && s.C < 8 && groups * s.C <= h->sms && p.KU >= 2 * kStreamWarps * s.C)
+      s.C *= 2;
+  } else {
+    pl.tn = rows <= 64 ? 64 : experts || m <= 128 ? 128 : 256;
+    const int64_t tiles =
+        experts ? std::min<int64_t>(p.E, m) + m / pl.tn : (m + pl.tn - 1) / pl.tn;
+    const int64_t items = tiles * p.RT;
+    // K is split while the clusters run at once and a CTA keeps two steps
+    pl.C = 1;
+    for (int i = 1; i < 4 && !experts; ++i)
+      if (items <= h->clusters[i] && p.KU >= 4 << i) pl.C = 1 << i;
+    pl.grid = pl.C > 1 ? items * pl.C : std::min<int64_t>(items, h->sms);
+  }
+  return pl;
 }
 
 int run(const char* call, proj_w4_handle h, const void* x, int64_t ldx, int64_t m,
@@ -368,8 +478,8 @@ int run(const char* call, proj_w4_handle h, const void* x, int64_t ldx, int64_t 
     return refuse(PROJ_EINVAL, call, "m < 0, or a row stride below K or N");
   if (!experts && h->p.E != 1)
     return refuse(PROJ_EINVAL, call, "the handle holds several experts");
-  if (m > (int64_t{1} << 20) || ldx >= (int64_t{1} << 38) || ldo >= (int64_t{1} << 38))
-    return refuse(PROJ_EUNSUPPORTED, call, "m > 2^20 or a row stride >= 2^38");
+  if (m > (int64_t{1} << 20) || ldx >= (int64_t{1} << 31) || ldo >= (int64_t{1} << 31))
+    return refuse(PROJ_EUNSUPPORTED, call, "m > 2^20 or a row stride >= 2^31");
   if (m > 0 && (!x || !out || (experts && !offsets)))
     return refuse(PROJ_EINVAL, call, "a NULL pointer");
   if (!aligned_to(x, 16) || ldx % 8)
@@ -384,14 +494,16 @@ int run(const char* call, proj_w4_handle h, const void* x, int64_t ldx, int64_t 
   p.out = out;
   p.ldo = ldo;
   p.offsets = experts ? offsets : nullptr;
-  const int nt = stream_nt(h, m, experts);
-  const int64_t per = 8 * nt;
-  // tiles of the experts: at most one part-filled tile for each that has rows
-  const int64_t tiles =
-      experts ? std::min<int64_t>(p.E, m) + m / per : (m + per - 1) / per;
+  const Plan pl = make_plan(h, m, experts);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = h->dtype == PROJ_BF16 ? stream_any<__nv_bfloat16>(nt, p, tiles, s)
-                                              : stream_any<__half>(nt, p, tiles, s);
+  const bool fp16 = h->dtype == PROJ_FP16;
+  cudaError_t e;
+  if (pl.tc)
+    e = w4_tc_launch(fp16, pl.tn, p, pl.grid, pl.C, s);
+  else if (pl.stream.NT == 1)
+    e = fp16 ? stream_any<__half, 1>(p, pl.stream, s) : stream_any<__nv_bfloat16, 1>(p, pl.stream, s);
+  else
+    e = fp16 ? stream_any<__half, 2>(p, pl.stream, s) : stream_any<__nv_bfloat16, 2>(p, pl.stream, s);
   return e == cudaSuccess ? PROJ_OK : record_cuda(e, call);
 }
 
@@ -424,14 +536,21 @@ extern "C" proj_w4_handle proj_w4_prepare(const void* codes, const void* scales,
   p.K = static_cast<int>(K);
   p.group = static_cast<int>(group);
   p.RB = static_cast<int>((N + 15) / 16);
+  p.RT = static_cast<int>((N + 127) / 128);
   p.KU = static_cast<int>((K + 63) / 64);
   const int64_t NG = (K + group - 1) / group;
+  p.upg = static_cast<int>(group / 64);
+  p.upg_shift = -1;
+  for (int i = 0; i < 16; ++i)
+    if (p.upg == 1 << i) p.upg_shift = i;
+  h->sms = proj_num_sms();
+  for (int i = 0; i < 4; ++i) h->clusters[i] = w4_tc_max_clusters(1 << i);
   p.NGp = static_cast<int>(group == 32 ? 2 * p.KU : NG);  // every unit has its groups
   h->dtype = dtype;
-  const int64_t blocks = experts * p.RB;
-  const int64_t code_bytes = blocks * p.KU * 512;
-  const int64_t scale_bytes = (blocks * p.NGp * 32 + 255) / 256 * 256;
-  const int64_t zero_bytes = zeros ? (blocks * p.NGp * 16 + 255) / 256 * 256 : 0;
+  const int64_t row_tiles = experts * p.RT;
+  const int64_t code_bytes = row_tiles * p.KU * kW4UnitBytes;
+  const int64_t scale_bytes = row_tiles * p.NGp * 256;
+  const int64_t zero_bytes = zeros ? (row_tiles * p.NGp * 128 + 255) / 256 * 256 : 0;
   cudaError_t e = cudaMalloc(reinterpret_cast<void**>(&h->base),
                              static_cast<size_t>(code_bytes + scale_bytes + zero_bytes + 256));
   if (e != cudaSuccess) {
@@ -446,12 +565,12 @@ extern "C" proj_w4_handle proj_w4_prepare(const void* codes, const void* scales,
   p.scales = reinterpret_cast<const uint16_t*>(h->base + code_bytes);
   p.zeros = zeros ? h->base + code_bytes + scale_bytes : nullptr;
   p.status = reinterpret_cast<uint32_t*>(h->base + code_bytes + scale_bytes + zero_bytes);
-  const int64_t lanes = blocks * p.KU * 32, cells = blocks * p.NGp * 16;
+  const int64_t lanes = row_tiles * p.KU * 256, cells = row_tiles * p.NGp * 128;
   pack_codes_kernel<<<static_cast<unsigned>((lanes + 255) / 256), 256>>>(
-      static_cast<const uint8_t*>(codes), const_cast<uint4*>(p.codes), experts, N, K, p.RB, p.KU);
+      static_cast<const uint8_t*>(codes), const_cast<uint4*>(p.codes), experts, N, K, p.RT, p.KU);
   pack_scales_kernel<<<static_cast<unsigned>((cells + 255) / 256), 256>>>(
       static_cast<const uint16_t*>(scales), static_cast<const uint8_t*>(zeros),
-      const_cast<uint16_t*>(p.scales), const_cast<uint8_t*>(p.zeros), experts, N, NG, p.NGp, p.RB);
+      const_cast<uint16_t*>(p.scales), const_cast<uint8_t*>(p.zeros), experts, N, NG, p.NGp, p.RT, group == 32);
   e = cudaGetLastError();
   if (e == cudaSuccess) e = cudaMemsetAsync(p.status, 0, 4, nullptr);
   if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
@@ -480,8 +599,14 @@ extern "C" int proj_w4_run_experts(proj_w4_handle h, const void* x, int64_t ldx,
 extern "C" int proj_w4_describe(proj_w4_handle h, int64_t m, char* buf, size_t cap) {
   if (!h || !buf || cap == 0 || m < 0)
     return refuse(PROJ_EINVAL, "proj_w4_describe", "NULL handle or buffer, cap = 0 or m < 0");
-  std::snprintf(buf, cap, "w4 stream, %d tokens a tile, exact 4-bit products",
-                8 * stream_nt(h, m, h->p.E > 1));
+  const Plan pl = make_plan(h, m, h->p.E > 1);
+  if (pl.tc)
+    std::snprintf(buf, cap, "w4 tcgen05, %d-token tiles, grid %lld, cluster %d, weights rounded to %s",
+                  pl.tn, static_cast<long long>(pl.grid), pl.C,
+                  h->dtype == PROJ_FP16 ? "fp16" : "bf16");
+  else
+    std::snprintf(buf, cap, "w4 stream, %d-token tiles, %d rows, cluster %d, exact 4-bit products",
+                  8 * pl.stream.NT, 16 * pl.stream.RB, pl.stream.C);
   return PROJ_OK;
 }
 

@@ -2,15 +2,19 @@
 // layout).
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
 
 namespace proj {
 
+constexpr int kW4MaxExperts = 1024;
+constexpr int kW4UnitBytes = 4096;  // codes of 128 rows x 64 columns
+
 struct W4Params {
-  const uint4* codes;      // [E][RB][KU][32 lanes] of 16 bytes
-  const uint16_t* scales;  // [E][RB][NGp][8]{row g, row g + 8}
+  const uint4* codes;      // [E][RT][KU][8 blocks][32 lanes] of 16 bytes
+  const uint16_t* scales;  // [E][RT][NGp][8 blocks][8]{row g, row g + 8}
   const uint8_t* zeros;    // the same in bytes, or null: all 8
   uint32_t* status;
   const void* x;
@@ -20,8 +24,26 @@ struct W4Params {
   int E, N, K;
   int group;
   int RB;   // blocks of 16 rows
+  int RT;   // tiles of 128 rows
   int KU;   // units of 64 columns
   int NGp;  // groups per row block in the packed scales
+  int upg;        // units per group (group / 64; 0 for groups of 32)
+  int upg_shift;  // its logarithm, -1 where it is no power of two
+  __host__ __device__ int group_of(int u) const {  // groups of 64 columns or more
+    return upg_shift >= 0 ? u >> upg_shift : u / upg;
+  }
 };
+
+// The tensor-core kernel (w4_tc.cu): token tiles of tn = 64, 128 or, for one
+// matrix, 256; clusters of C CTAs along K (C > 1: grid = C times the number of
+// items, one matrix).
+cudaError_t w4_tc_launch(bool fp16, int tn, const W4Params& p, int64_t grid, int C,
+                         cudaStream_t s);
+
+int w4_tc_max_clusters(int C);  // that run at once (occupancy query)
+
+// api.cu
+bool make_rows_map(CUtensorMap* map, const void* base, int64_t rows, int64_t K, int64_t ld,
+                   bool fp16, int box_rows);
 
 }  // namespace proj

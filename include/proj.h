@@ -462,7 +462,7 @@ proj_w4_handle proj_w4_prepare(const void *codes, const void *scales, const void
  *   x   : m rows of K values, ldx >= K a multiple of 8, 16-byte aligned; what
  *         lies between K and ldx is not read.
  *   out : m rows of N values, ldo >= N, aligned to an element.
- * x and out must not overlap.  m <= 2^20.
+ * x and out must not overlap.  m <= 2^20, strides below 2^31.
  */
 int proj_w4_run(proj_w4_handle h, const void *x, int64_t ldx, int64_t m, void *out, int64_t ldo,
                 proj_stream stream);

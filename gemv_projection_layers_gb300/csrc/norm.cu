@@ -15,8 +15,18 @@
 // and one reduction of three sums serves the whole row.  (For a gate per
 // token, dg = beta (A - ru S1 B) with g left out of A and B.)
 //
-// Every row is read once and stays in registers between the reductions; both
-// kernels are bound by HBM.
+// Both kernels are bound by HBM: a row of D = 8192 in 16 bits moves 64 KB
+// forward and 128 KB backward.  A CTA takes rows in turn and has the next rows'
+// tensors on their way to shared memory (16-byte asynchronous copies) while it
+// works on one, so the two reductions of a row hide behind the loads of
+// others, and both passes over a row read shared memory.  The gradient's
+// column sums stay in registers over all of a CTA's rows and meet in a second
+// kernel, in a fixed order.
+//
+// Rows that do not start on 16 bytes (an odd D, say) keep their misalignment
+// in shared memory: whole 16-byte pieces are copied as such, the elements at
+// the two ends one by one, and the threads read and write single elements,
+// neighbours side by side.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -31,234 +41,454 @@ namespace proj {
 namespace {
 
 constexpr int kMaxD = 16384;
-constexpr int kGradCtas = 304;  // rows of the column sums' workspace, at most
 
+// exp(-g) and the quotient: the 16-bit types' outputs are rounded to 2^-8 or
+// 2^-11, so the hardware's approximations (2^-21 or so) do; fp32 takes expf.
+template <typename T>
 __device__ __forceinline__ float act(float g, int kind) {
-  return kind == PROJ_GATE_SIGMOID ? 1.f / (1.f + expf(-g)) : g;
+  if (kind != PROJ_GATE_SIGMOID) return g;
+  return __fdividef(1.f, 1.f + (sizeof(T) == 2 ? __expf(-g) : expf(-g)));
 }
 // d act / d gate from the activated value.
 __device__ __forceinline__ float act_slope(float g, int kind) {
   return kind == PROJ_GATE_SIGMOID ? g * (1.f - g) : 1.f;
 }
 
-// TPR threads share a row of D = up to TPR x NV x V elements; vector j of
-// thread i is j TPR + i, so accesses are contiguous over the threads.
-template <typename T, int V, int TPR, int NV>
-__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
-    norm_kernel(const __grid_constant__ proj_norm_args a) {
-  constexpr int kRows = TPR < 128 ? 128 / TPR : 1;
-  __shared__ float room[2 * 32];
-  int turn = 0;
-  const int tid = static_cast<int>(threadIdx.x) % TPR;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / TPR;
-  griddep_launch_dependents();
-  griddep_wait();
-  if (row >= a.m) return;  // whole warps (kRows > 1 has no block barrier)
-  const int D = static_cast<int>(a.D);
-  const int nvec = D / V;
-  const float inv_d = 1.f / static_cast<float>(D);
-  const T* y = static_cast<const T*>(a.y) + row * a.ldy;
-  const T* r = static_cast<const T*>(a.residual) + row * a.ldr;
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all_but(int pending) {
+  if (pending <= 0)
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+  else if (pending == 1)
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else
+    asm volatile("cp.async.wait_group 2;" ::: "memory");
+}
 
-  Vec<T, V> vy[NV], vr[NV];
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int c = (j * TPR + tid) * V;
-    if (j * TPR + tid < nvec) {
-      if (a.y) vy[j] = load_vec<T, V>(y + c);
-      vr[j] = load_vec<T, V>(r + c);
-    }
-  }
-  float rp = 1.f;
-  if (a.y && !a.y_plain) {
-    float s[1] = {0.f};
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-      if (j * TPR + tid < nvec) {
-        float v[V];
-        widen(vy[j], v);
-#pragma unroll
-        for (int i = 0; i < V; ++i) s[0] = fmaf(v[i], v[i], s[0]);
-      }
-    row_sums<TPR, 1>(s, room, turn);
-    rp = 1.f / sqrtf(s[0] * inv_d + a.eps);
-    if (tid == 0 && a.rstd_post) a.rstd_post[row] = rp;
-  }
-  float g_row = 1.f;
-  if (a.gate_mode == PROJ_GATE_TOKEN)
-    g_row = act(to_f32(static_cast<const T*>(a.gate)[row]), a.gate_act);
-  const T* gate = static_cast<const T*>(a.gate);
-  if (a.gate_mode == PROJ_GATE_ELEMENT) gate += row * a.ldg;
-  const bool g_vec = a.gate_mode == PROJ_GATE_CHANNEL || a.gate_mode == PROJ_GATE_ELEMENT;
+// How TPR threads share a row.  kVec: group j of a thread is the 16 bytes at
+// element (j TPR + tid) E; else E elements TPR apart, from j E TPR + tid.
+template <typename T, bool kVec_, int TPR_, int NV_>
+struct Shape {
+  using Type = T;
+  static constexpr bool kVec = kVec_;
+  static constexpr int TPR = TPR_, NV = NV_;
+  static constexpr int E = kVec ? kFullVec<T> : 8;
+  static constexpr int kRows = TPR < 128 ? 128 / TPR : 1;  // rows of a CTA at a time
+  static constexpr int kThreads = TPR < 128 ? 128 : TPR;
+  static constexpr bool kRing = TPR >= 128 && TPR <= 512;  // rows come through shared memory
+};
 
-  float u[NV][V];
-  float s[1] = {0.f};
+// Group j of a row in global memory; 0 beyond D.
+template <typename S>
+__device__ __forceinline__ void load_global(const typename S::Type* row, int j, int tid, int D,
+                                            float (&v)[S::E]) {
+  using T = typename S::Type;
+  if constexpr (S::kVec) {
+    const int c = (j * S::TPR + tid) * S::E;
+    if (c < D) {
+      widen(load_vec<T, S::E>(row + c), v);
+    } else {
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int c = (j * TPR + tid) * V;
-    if (j * TPR + tid < nvec) {
-      float rv[V];
-      widen(vr[j], rv);
-#pragma unroll
-      for (int i = 0; i < V; ++i) u[j][i] = a.alpha * rv[i];
-      if (a.y) {
-        float yv[V], gv[V], wv[V];
-        widen(vy[j], yv);
-        if (g_vec) {
-          widen(load_vec<T, V>(gate + c), gv);
-        }
-        if (a.w_post) widen(load_vec<T, V>(static_cast<const T*>(a.w_post) + c), wv);
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          float n = yv[i] * rp;
-          if (a.w_post) n *= wv[i];
-          const float g = g_vec ? act(gv[i], a.gate_act) : g_row;
-          u[j][i] = fmaf(a.beta * g, n, u[j][i]);
-        }
-      }
-      if (a.out) store_vec<T, V>(static_cast<T*>(a.out) + row * a.ldo + c, u[j]);
-#pragma unroll
-      for (int i = 0; i < V; ++i) s[0] = fmaf(u[j][i], u[j][i], s[0]);
+      for (int i = 0; i < S::E; ++i) v[i] = 0.f;
     }
-  }
-  if (!a.normed && !a.rstd_pre) return;
-  row_sums<TPR, 1>(s, room, turn);
-  const float ru = 1.f / sqrtf(s[0] * inv_d + a.eps);
-  if (tid == 0 && a.rstd_pre) a.rstd_pre[row] = ru;
-  if (!a.normed) return;
-  T* h = static_cast<T*>(a.normed) + row * a.ldn;
+  } else {
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int c = (j * TPR + tid) * V;
-    if (j * TPR + tid < nvec) {
-      float wv[V], o[V];
-      if (a.w_pre) widen(load_vec<T, V>(static_cast<const T*>(a.w_pre) + c), wv);
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        o[i] = u[j][i] * ru;
-        if (a.w_pre) o[i] *= wv[i];
-      }
-      store_vec<T, V>(h + c, o);
+    for (int i = 0; i < S::E; ++i) {
+      const int c = (j * S::E + i) * S::TPR + tid;
+      v[i] = c < D ? to_f32(row[c]) : 0.f;
     }
   }
 }
 
-// Column sums: part[cta][which][D] (which: 0 dw_post, 1 dw_pre, 2 dgate).
-template <typename T, int V, int TPR, int NV>
-__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
-    norm_grad_kernel(const __grid_constant__ proj_norm_grad_args a) {
-  constexpr int kRows = TPR < 128 ? 128 / TPR : 1;
-  __shared__ float room[2 * 3 * 32];
+template <typename S>
+__device__ __forceinline__ void store_global(typename S::Type* row, int j, int tid, int D,
+                                             const float (&v)[S::E]) {
+  using T = typename S::Type;
+  if constexpr (S::kVec) {
+    const int c = (j * S::TPR + tid) * S::E;
+    if (c < D) store_vec<T, S::E>(row + c, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < S::E; ++i) {
+      const int c = (j * S::E + i) * S::TPR + tid;
+      if (c < D) row[c] = from_f32<T>(v[i]);
+    }
+  }
+}
+
+// Up to five row tensors and their ring in shared memory.
+template <typename S, int NT>
+struct Rows {
+  using T = typename S::Type;
+  const T* base[NT];  // null: not there
+  int64_t ld[NT];
+  uint8_t* smem;
+  int D, slot, stages;  // bytes of a row's place, stages of NT places
+
+  __device__ __forceinline__ static int skew(const T* p) {
+    return S::kVec ? 0 : static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15);
+  }
+  __device__ __forceinline__ uint8_t* place(int stage, int k) const {
+    return smem + (stage * NT + k) * slot;
+  }
+  // The threads of the CTA start the copies of one row.
+  __device__ __forceinline__ void fetch(int64_t row, int stage, int tid) const {
+#pragma unroll
+    for (int k = 0; k < NT; ++k) {
+      if (!base[k]) continue;
+      const T* src = base[k] + row * ld[k];
+      uint8_t* dst = place(stage, k);
+      if constexpr (S::kVec) {
+        const uint32_t to = smem_u32(dst);
+        // a thread copies the groups that it reads
+#pragma unroll
+        for (int j = 0; j < S::NV; ++j) {
+          const int c = (j * S::TPR + tid) * S::E;
+          if (c < D) cp_async16(to + c * static_cast<int>(sizeof(T)), src + c);
+        }
+      } else {
+        constexpr int el = sizeof(T);
+        const int off = skew(src);
+        const int head = min(D, off ? (16 - off) / el : 0);
+        const int pieces = (D - head) * el / 16;
+        const int tail = D - head - pieces * (16 / el);
+        const uint32_t to = smem_u32(dst) + off;
+        for (int i = tid; i < pieces; i += S::TPR)
+          cp_async16(to + head * el + 16 * i, src + head + i * (16 / el));
+        T* const put = reinterpret_cast<T*>(dst + off);
+        if (tid < head) put[tid] = src[tid];
+        const int t = S::TPR - 1 - tid;
+        if (t < tail) put[D - 1 - t] = src[D - 1 - t];
+      }
+    }
+  }
+  // Group j of tensor k of the row at hand.
+  __device__ __forceinline__ void load(int k, int64_t row, int stage, int j, int tid,
+                                       float (&v)[S::E]) const {
+    const T* src = base[k] + row * ld[k];
+    if constexpr (!S::kRing) {
+      load_global<S>(src, j, tid, D, v);
+    } else {
+      const T* at = reinterpret_cast<const T*>(place(stage, k) + skew(src));
+      load_global<S>(at, j, tid, D, v);
+    }
+  }
+};
+
+// The loop over a CTA's rows: work(row, stage) for rows first, first + step, ...
+// with the next rows' copies under way.  Work has a block barrier between its
+// two passes or none; without shared columns between threads (kVec) a thread
+// waits for its own copies only.
+template <typename S, typename R, typename F>
+__device__ __forceinline__ void over_rows(const R& rows, int64_t m, int64_t first, int64_t step,
+                                          int tid, F work) {
+  if constexpr (!S::kRing) {
+    for (int64_t row = first; row < m; row += step) work(row, 0);
+  } else {
+    const int ahead = rows.stages - 1;
+    for (int i = 0; i < ahead; ++i) {
+      if (first + i * step < m) rows.fetch(first + i * step, i, tid);
+      cp_async_commit();
+    }
+    int stage = 0;
+    for (int64_t row = first; row < m; row += step) {
+      if (ahead == 0) {
+        if (!S::kVec) __syncthreads();  // the row before has been read
+        rows.fetch(row, 0, tid);
+        cp_async_commit();
+      }
+      cp_async_wait_all_but(ahead - 1);
+      if (!S::kVec) __syncthreads();
+      if (ahead) {
+        const int into = stage == 0 ? ahead : stage - 1;  // the stage of the row before
+        if (row + ahead * step < m) rows.fetch(row + ahead * step, into, tid);
+        cp_async_commit();
+      }
+      work(row, stage);
+      if (++stage == rows.stages) stage = 0;
+    }
+  }
+}
+
+template <typename S>
+__global__ void __launch_bounds__(S::kThreads)
+    norm_kernel(const __grid_constant__ proj_norm_args a, const int slot, const int stages) {
+  using T = typename S::Type;
+  constexpr int NV = S::NV, E = S::E, TPR = S::TPR;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float room[2 * 32];
   int turn = 0;
   const int tid = static_cast<int>(threadIdx.x) % TPR;
-  const int part_row = static_cast<int>(blockIdx.x) * kRows + threadIdx.x / TPR;
   griddep_launch_dependents();
   griddep_wait();
   const int D = static_cast<int>(a.D);
-  const int nvec = D / V;
+  const float inv_d = 1.f / static_cast<float>(D);
+  const bool g_vec = a.gate_mode == PROJ_GATE_CHANNEL || a.gate_mode == PROJ_GATE_ELEMENT;
+  Rows<S, 3> rows;
+  rows.base[0] = static_cast<const T*>(a.residual);
+  rows.ld[0] = a.ldr;
+  rows.base[1] = static_cast<const T*>(a.y);
+  rows.ld[1] = a.ldy;
+  rows.base[2] = a.gate_mode == PROJ_GATE_ELEMENT ? static_cast<const T*>(a.gate) : nullptr;
+  rows.ld[2] = a.ldg;
+  rows.smem = smem;
+  rows.D = D;
+  rows.slot = slot;
+  rows.stages = stages;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * S::kRows + threadIdx.x / TPR;
+
+  over_rows<S>(rows, a.m, first, static_cast<int64_t>(gridDim.x) * S::kRows, tid,
+               [&](int64_t row, int stage) {
+    float rp = 1.f;
+    if (a.y && !a.y_plain) {
+      float s[1] = {0.f};
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        float v[E];
+        rows.load(1, row, stage, j, tid, v);
+#pragma unroll
+        for (int i = 0; i < E; ++i) s[0] = fmaf(v[i], v[i], s[0]);
+      }
+      row_sums<TPR, 1>(s, room, turn);
+      rp = 1.f / sqrtf(s[0] * inv_d + a.eps);
+      if (tid == 0 && a.rstd_post) a.rstd_post[row] = rp;
+    }
+    float g_row = 1.f;
+    if (a.gate_mode == PROJ_GATE_TOKEN)
+      g_row = act<T>(to_f32(static_cast<const T*>(a.gate)[row]), a.gate_act);
+    float u[NV][E];
+    float s[1] = {0.f};
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      rows.load(0, row, stage, j, tid, u[j]);
+#pragma unroll
+      for (int i = 0; i < E; ++i) u[j][i] *= a.alpha;
+      if (a.y) {
+        float n[E], w[E];
+        rows.load(1, row, stage, j, tid, n);
+#pragma unroll
+        for (int i = 0; i < E; ++i) n[i] *= rp;
+        if (a.w_post) {
+          load_global<S>(static_cast<const T*>(a.w_post), j, tid, D, w);
+#pragma unroll
+          for (int i = 0; i < E; ++i) n[i] *= w[i];
+        }
+        if (g_vec) {
+          if (a.gate_mode == PROJ_GATE_ELEMENT)
+            rows.load(2, row, stage, j, tid, w);
+          else
+            load_global<S>(static_cast<const T*>(a.gate), j, tid, D, w);
+#pragma unroll
+          for (int i = 0; i < E; ++i) w[i] = act<T>(w[i], a.gate_act);
+        } else {
+#pragma unroll
+          for (int i = 0; i < E; ++i) w[i] = g_row;
+        }
+#pragma unroll
+        for (int i = 0; i < E; ++i) u[j][i] = fmaf(a.beta * w[i], n[i], u[j][i]);
+      }
+      if (a.out) store_global<S>(static_cast<T*>(a.out) + row * a.ldo, j, tid, D, u[j]);
+#pragma unroll
+      for (int i = 0; i < E; ++i) s[0] = fmaf(u[j][i], u[j][i], s[0]);
+    }
+    if (!a.normed && !a.rstd_pre) return;
+    row_sums<TPR, 1>(s, room, turn);
+    const float ru = 1.f / sqrtf(s[0] * inv_d + a.eps);
+    if (tid == 0 && a.rstd_pre) a.rstd_pre[row] = ru;
+    if (!a.normed) return;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (a.w_pre) {
+        float w[E];
+        load_global<S>(static_cast<const T*>(a.w_pre), j, tid, D, w);
+#pragma unroll
+        for (int i = 0; i < E; ++i) u[j][i] *= ru * w[i];
+      } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i) u[j][i] *= ru;
+      }
+      store_global<S>(static_cast<T*>(a.normed) + row * a.ldn, j, tid, D, u[j]);
+    }
+  });
+}
+
+// Column sums: part[CTA row][which][D] (which: 0 dw_post, 1 dw_pre, 2 dgate).
+template <typename S>
+__global__ void __launch_bounds__(S::kThreads, S::kThreads < 512 ? 512 / S::kThreads : 1)
+    norm_grad_kernel(const __grid_constant__ proj_norm_grad_args a, const int slot,
+                     const int stages) {
+  using T = typename S::Type;
+  constexpr int NV = S::NV, E = S::E, TPR = S::TPR;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float room[2 * 3 * 32];
+  int turn = 0;
+  const int tid = static_cast<int>(threadIdx.x) % TPR;
+  const int part_row = static_cast<int>(blockIdx.x) * S::kRows + threadIdx.x / TPR;
+  griddep_launch_dependents();
+  griddep_wait();
+  const int D = static_cast<int>(a.D);
   const float inv_d = 1.f / static_cast<float>(D);
   const bool normed = a.y && !a.y_plain;
   const bool g_vec = a.gate_mode == PROJ_GATE_CHANNEL || a.gate_mode == PROJ_GATE_ELEMENT;
   const bool g_token = a.gate_mode == PROJ_GATE_TOKEN;
   const bool col_gate = a.gate_mode == PROJ_GATE_CHANNEL && a.dgate;
+  Rows<S, 5> rows;
+  rows.base[0] = static_cast<const T*>(a.residual);
+  rows.ld[0] = a.ldr;
+  rows.base[1] = static_cast<const T*>(a.y);
+  rows.ld[1] = a.ldy;
+  rows.base[2] = a.gate_mode == PROJ_GATE_ELEMENT ? static_cast<const T*>(a.gate) : nullptr;
+  rows.ld[2] = a.ldg;
+  rows.base[3] = static_cast<const T*>(a.dout);
+  rows.ld[3] = a.lddo;
+  rows.base[4] = static_cast<const T*>(a.dnormed);
+  rows.ld[4] = a.lddn;
+  rows.smem = smem;
+  rows.D = D;
+  rows.slot = slot;
+  rows.stages = stages;
 
-  float acc_post[NV][V] = {}, acc_pre[NV][V] = {}, acc_gate[NV][V] = {};
+  float acc_post[NV][E] = {}, acc_pre[NV][E] = {}, acc_gate[NV][E] = {};
 
-  for (int64_t row = part_row; row < a.m; row += static_cast<int64_t>(gridDim.x) * kRows) {
-    const T* gate = static_cast<const T*>(a.gate);
-    if (a.gate_mode == PROJ_GATE_ELEMENT) gate += row * a.ldg;
+  over_rows<S>(rows, a.m, part_row, static_cast<int64_t>(gridDim.x) * S::kRows, tid,
+               [&](int64_t row, int stage) {
     const float rp = normed ? a.rstd_post[row] : 1.f;
     const float ru = a.dnormed ? a.rstd_pre[row] : 1.f;
-    const float g_row = g_token ? act(to_f32(gate[row]), a.gate_act) : 1.f;
-    // per element: yn, g (activated), un, e
-    Vec<T, V> vy[NV], vr[NV], vg[NV], vo[NV], vh[NV];
+    const float g_row =
+        g_token ? act<T>(to_f32(static_cast<const T*>(a.gate)[row]), a.gate_act) : 1.f;
+    // group j's yn, n, un, dh, t = dh w_pre and e = du' + ru t, and w_post, with the
+    // activated gate in g
+    float yn[E], n[E], un[E], dh[E], t[E], e[E], wpo[E];
+    auto group = [&](int j, const float (&g)[E]) {
+      float v[E];
+      rows.load(0, row, stage, j, tid, un);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = (j * TPR + tid) * V;
-      if (j * TPR + tid < nvec) {
-        if (a.y) vy[j] = load_vec<T, V>(static_cast<const T*>(a.y) + row * a.ldy + c);
-        vr[j] = load_vec<T, V>(static_cast<const T*>(a.residual) + row * a.ldr + c);
-        if (g_vec) vg[j] = load_vec<T, V>(gate + c);
-        if (a.dout) vo[j] = load_vec<T, V>(static_cast<const T*>(a.dout) + row * a.lddo + c);
-        if (a.dnormed)
-          vh[j] = load_vec<T, V>(static_cast<const T*>(a.dnormed) + row * a.lddn + c);
+      for (int i = 0; i < E; ++i) un[i] *= a.alpha;
+      if (a.w_post) {
+        load_global<S>(static_cast<const T*>(a.w_post), j, tid, D, wpo);
+      } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i) wpo[i] = 1.f;
       }
-    }
-    auto element = [&](int j, int i, float wpo, float wpr, float& yn, float& n, float& g,
-                       float& un, float& dh, float& e) {
-      yn = a.y ? to_f32(vy[j].e[i]) * rp : 0.f;
-      n = yn * wpo;
-      g = g_vec ? act(to_f32(vg[j].e[i]), a.gate_act) : g_row;
-      const float u = fmaf(a.beta * g, n, a.alpha * to_f32(vr[j].e[i]));
-      un = u * ru;
-      dh = a.dnormed ? to_f32(vh[j].e[i]) : 0.f;
-      e = fmaf(ru, dh * wpr, a.dout ? to_f32(vo[j].e[i]) : 0.f);
+      if (a.y) {
+        rows.load(1, row, stage, j, tid, yn);
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+          yn[i] *= rp;
+          n[i] = yn[i] * wpo[i];
+          un[i] = fmaf(a.beta * g[i], n[i], un[i]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i) yn[i] = n[i] = 0.f;
+      }
+      if (a.dout) {
+        rows.load(3, row, stage, j, tid, e);
+      } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i) e[i] = 0.f;
+      }
+      if (a.dnormed) {
+        rows.load(4, row, stage, j, tid, dh);
+        if (a.w_pre) {
+          load_global<S>(static_cast<const T*>(a.w_pre), j, tid, D, v);
+#pragma unroll
+          for (int i = 0; i < E; ++i) t[i] = dh[i] * v[i];
+        } else {
+#pragma unroll
+          for (int i = 0; i < E; ++i) t[i] = dh[i];
+        }
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+          un[i] *= ru;
+          e[i] = fmaf(ru, t[i], e[i]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i) dh[i] = t[i] = 0.f;
+      }
     };
+    float g[NV][E];
     float s[3] = {0.f, 0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (j * TPR + tid) * V;
-      if (j * TPR + tid < nvec) {
-        float wpo[V], wpr[V];
-        if (a.w_post) widen(load_vec<T, V>(static_cast<const T*>(a.w_post) + c), wpo);
-        if (a.w_pre) widen(load_vec<T, V>(static_cast<const T*>(a.w_pre) + c), wpr);
+      if (g_vec) {
+        if (a.gate_mode == PROJ_GATE_ELEMENT)
+          rows.load(2, row, stage, j, tid, g[j]);
+        else
+          load_global<S>(static_cast<const T*>(a.gate), j, tid, D, g[j]);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float wo = a.w_post ? wpo[i] : 1.f, wr = a.w_pre ? wpr[i] : 1.f;
-          float yn, n, g, un, dh, e;
-          element(j, i, wo, wr, yn, n, g, un, dh, e);
-          s[0] = fmaf(dh * wr, un, s[0]);
-          const float gn = g_token ? n : g * n;
-          s[1] = fmaf(gn, e, s[1]);
-          s[2] = fmaf(gn, un, s[2]);
-        }
+        for (int i = 0; i < E; ++i) g[j][i] = act<T>(g[j][i], a.gate_act);
+      } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i) g[j][i] = g_row;
+      }
+      group(j, g[j]);
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        s[0] = fmaf(t[i], un[i], s[0]);
+        const float gn = g_token ? n[i] : g[j][i] * n[i];
+        s[1] = fmaf(gn, e[i], s[1]);
+        s[2] = fmaf(gn, un[i], s[2]);
       }
     }
     row_sums<TPR, 3>(s, room, turn);
-    const float s1 = a.dnormed ? s[0] * inv_d : 0.f;
-    const float ab = a.beta * (s[1] - ru * s1 * s[2]);  // sum of beta [g] n du
+    const float s1 = a.dnormed ? ru * s[0] * inv_d : 0.f;
+    const float ab = a.beta * (s[1] - s1 * s[2]);  // sum of beta [g] n du
     const float s2 = normed ? (g_token ? g_row * ab : ab) * inv_d : 0.f;
     if (g_token && a.dgate && tid == 0)
       static_cast<T*>(a.dgate)[row] = from_f32<T>(ab * act_slope(g_row, a.gate_act));
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (j * TPR + tid) * V;
-      if (j * TPR + tid < nvec) {
-        float wpo[V], wpr[V], dy[V], dr[V], dg[V];
-        if (a.w_post) widen(load_vec<T, V>(static_cast<const T*>(a.w_post) + c), wpo);
-        if (a.w_pre) widen(load_vec<T, V>(static_cast<const T*>(a.w_pre) + c), wpr);
+      group(j, g[j]);
+      float out[E];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float wo = a.w_post ? wpo[i] : 1.f, wr = a.w_pre ? wpr[i] : 1.f;
-          float yn, n, g, un, dh, e;
-          element(j, i, wo, wr, yn, n, g, un, dh, e);
-          const float du = e - ru * un * s1;
-          const float cc = a.beta * g * du;
-          dr[i] = a.alpha * du;
-          dy[i] = normed ? rp * (cc * wo - yn * s2) : cc;
-          dg[i] = a.beta * n * du * act_slope(g, a.gate_act);
-          acc_post[j][i] = fmaf(cc, yn, acc_post[j][i]);
-          acc_pre[j][i] = fmaf(dh, un, acc_pre[j][i]);
-          acc_gate[j][i] += dg[i];
+      for (int i = 0; i < E; ++i) {
+        e[i] = a.dnormed ? fmaf(-un[i], s1, e[i]) : e[i];  // du
+        out[i] = a.alpha * e[i];
+      }
+      if (a.dresidual)
+        store_global<S>(static_cast<T*>(a.dresidual) + row * a.lddr, j, tid, D, out);
+      if (a.dw_pre) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) acc_pre[j][i] = fmaf(dh[i], un[i], acc_pre[j][i]);
+      }
+      if (!a.y) continue;
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        e[i] *= a.beta;
+        const float c = g[j][i] * e[i];
+        acc_post[j][i] = fmaf(c, yn[i], acc_post[j][i]);
+        out[i] = normed ? rp * fmaf(c, wpo[i], -yn[i] * s2) : c;
+      }
+      if (a.dy) store_global<S>(static_cast<T*>(a.dy) + row * a.lddy, j, tid, D, out);
+      if (g_vec && a.dgate) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) out[i] = n[i] * e[i] * act_slope(g[j][i], a.gate_act);
+        if (col_gate) {
+#pragma unroll
+          for (int i = 0; i < E; ++i) acc_gate[j][i] += out[i];
+        } else {
+          store_global<S>(static_cast<T*>(a.dgate) + row * a.lddg, j, tid, D, out);
         }
-        if (a.dy) store_vec<T, V>(static_cast<T*>(a.dy) + row * a.lddy + c, dy);
-        if (a.dresidual) store_vec<T, V>(static_cast<T*>(a.dresidual) + row * a.lddr + c, dr);
-        if (a.gate_mode == PROJ_GATE_ELEMENT && a.dgate)
-          store_vec<T, V>(static_cast<T*>(a.dgate) + row * a.lddg + c, dg);
       }
     }
-  }
+  });
   if (!a.dw_post && !a.dw_pre && !col_gate) return;
   float* part = static_cast<float*>(a.workspace) + static_cast<size_t>(part_row) * 3 * D;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int c = (j * TPR + tid) * V;
-    if (j * TPR + tid < nvec) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        if (a.dw_post) part[c + i] = acc_post[j][i];
-        if (a.dw_pre) part[D + c + i] = acc_pre[j][i];
-        if (col_gate) part[2 * D + c + i] = acc_gate[j][i];
+    for (int i = 0; i < E; ++i) {
+      const int c = S::kVec ? (j * TPR + tid) * E + i : (j * E + i) * TPR + tid;
+      if (c < D) {
+        if (a.dw_post) part[c] = acc_post[j][i];
+        if (a.dw_pre) part[D + c] = acc_pre[j][i];
+        if (col_gate) part[2 * D + c] = acc_gate[j][i];
       }
     }
   }
@@ -294,11 +524,12 @@ __global__ void __launch_bounds__(32 * kSumWarps)
   }
 }
 
-cudaLaunchConfig_t config(unsigned grid_x, unsigned grid_y, unsigned threads, cudaStream_t s,
-                          cudaLaunchAttribute* attr) {
+cudaLaunchConfig_t config(unsigned grid_x, unsigned grid_y, unsigned threads, size_t smem,
+                          cudaStream_t s, cudaLaunchAttribute* attr) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid_x, grid_y);
   cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -307,53 +538,89 @@ cudaLaunchConfig_t config(unsigned grid_x, unsigned grid_y, unsigned threads, cu
   return cfg;
 }
 
-template <typename T, int V, int TPR, int NV>
-cudaError_t forward(const proj_norm_args& a, cudaStream_t s) {
-  constexpr int kRows = TPR < 128 ? 128 / TPR : 1;
-  cudaLaunchAttribute attr[1];
-  const cudaLaunchConfig_t cfg =
-      config(static_cast<unsigned>((a.m + kRows - 1) / kRows), 1, TPR < 128 ? 128 : TPR, s, attr);
-  return cudaLaunchKernelEx(&cfg, norm_kernel<T, V, TPR, NV>, a);
+// CTAs of the gradient, and with it rows of the column sums' workspace, at
+// most: longer rows have more threads and fewer CTAs fit an SM.
+int grad_ctas(int64_t D) { return D > 4096 ? 152 : D > 2048 ? 304 : 608; }
+int grad_parts(int64_t m, int64_t D) {
+  return static_cast<int>(std::min<int64_t>(m, grad_ctas(D)));
 }
 
-int grad_parts(int64_t m) { return static_cast<int>(std::min<int64_t>(m, kGradCtas)); }
+constexpr int kSmemMost = 220 * 1024;
 
-template <typename T, int V, int TPR, int NV>
-cudaError_t backward(const proj_norm_grad_args& a, cudaStream_t s) {
-  constexpr int kRows = TPR < 128 ? 128 / TPR : 1;
-  const int grid = (grad_parts(a.m) + kRows - 1) / kRows;
+// A row's place in shared memory (with room for its misalignment) and the
+// stages of `tensors` places that fit `budget` (0 to `most`).
+template <typename S>
+void ring_shape(int64_t D, int tensors, int budget, int most, int* slot, int* stages) {
+  *slot = static_cast<int>((D * sizeof(typename S::Type) + 15) / 16 * 16 + 16);
+  *stages = S::kRing ? std::max(1, std::min(most, budget / (tensors * *slot))) : 0;
+}
+
+template <typename S>
+cudaError_t forward(const proj_norm_args& a, cudaStream_t s) {
+  // Two CTAs an SM where two stages of the rows fit half of it.
+  int slot, stages;
+  ring_shape<S>(a.D, 3, kSmemMost / 2, 3, &slot, &stages);
+  if (S::kRing && stages < 2) ring_shape<S>(a.D, 3, kSmemMost, 3, &slot, &stages);
+  const size_t smem = static_cast<size_t>(3) * slot * stages;
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        norm_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  int64_t grid = (a.m + S::kRows - 1) / S::kRows;
+  if (S::kRing) {
+    const int per_sm = std::max(1, std::min(static_cast<int>(kSmemMost / smem), 1024 / S::kThreads));
+    grid = std::min<int64_t>(grid, static_cast<int64_t>(per_sm) * std::max(1, proj_num_sms()));
+  }
   cudaLaunchAttribute attr[1];
-  cudaLaunchConfig_t cfg =
-      config(static_cast<unsigned>(grid), 1, TPR < 128 ? 128 : TPR, s, attr);
-  cudaError_t e = cudaLaunchKernelEx(&cfg, norm_grad_kernel<T, V, TPR, NV>, a);
+  const cudaLaunchConfig_t cfg = config(static_cast<unsigned>(grid), 1, S::kThreads, smem, s, attr);
+  return cudaLaunchKernelEx(&cfg, norm_kernel<S>, a, slot, stages);
+}
+
+template <typename S>
+cudaError_t backward(const proj_norm_grad_args& a, cudaStream_t s) {
+  const int grid = (grad_parts(a.m, a.D) + S::kRows - 1) / S::kRows;
+  int slot, stages;
+  // as many CTAs an SM as the grid has for it
+  const int per_sm = std::max(1, grad_ctas(a.D) / 152);
+  ring_shape<S>(a.D, 5, kSmemMost / per_sm, 3, &slot, &stages);
+  const size_t smem = static_cast<size_t>(5) * slot * stages;
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        norm_grad_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = config(static_cast<unsigned>(grid), 1, S::kThreads, smem, s, attr);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, norm_grad_kernel<S>, a, slot, stages);
   if (e != cudaSuccess) return e;
   float* dgate = a.gate_mode == PROJ_GATE_CHANNEL ? static_cast<float*>(a.dgate) : nullptr;
   if (!a.dw_post && !a.dw_pre && !dgate) return cudaSuccess;
-  cfg = config(static_cast<unsigned>((a.D + 31) / 32), 3, 32 * kSumWarps, s, attr);
+  cfg = config(static_cast<unsigned>((a.D + 31) / 32), 3, 32 * kSumWarps, 0, s, attr);
   return cudaLaunchKernelEx(&cfg, norm_grad_sum_kernel,
                             static_cast<const float*>(static_cast<float*>(a.workspace)),
-                            grid * kRows, static_cast<int>(a.D), a.dw_post, a.dw_pre, dgate);
+                            grid * S::kRows, static_cast<int>(a.D), a.dw_post, a.dw_pre, dgate);
 }
 
-// Threads per row and vectors per thread by the row's vectors: the smallest
-// block that holds the row with two vectors a thread (four for the longest
-// rows of fp32, eight or sixteen single elements where rows do not start on
-// 16 bytes).
-#define PROJ_NORM_PICK(FN, T, a, s)                                          \
-  if (vec) {                                                                 \
-    constexpr int V = kFullVec<T>;                                           \
-    const int64_t n = (a).D / V;                                             \
-    if (n <= 64) return FN<T, V, 32, 2>(a, s);                               \
-    if (n <= 256) return FN<T, V, 128, 2>(a, s);                             \
-    if (n <= 512) return FN<T, V, 256, 2>(a, s);                             \
-    if (n <= 1024) return FN<T, V, 512, 2>(a, s);                            \
-    if (V == 4 && n > 2048) return FN<T, V, 1024, 4>(a, s);                  \
-    return FN<T, V, 1024, 2>(a, s);                                          \
-  } else {                                                                   \
-    if ((a).D <= 256) return FN<T, 1, 32, 8>(a, s);                          \
-    if ((a).D <= 2048) return FN<T, 1, 256, 8>(a, s);                        \
-    if ((a).D <= 8192) return FN<T, 1, 1024, 8>(a, s);                       \
-    return FN<T, 1, 1024, 16>(a, s);                                         \
+// Threads per row by its length: 16 elements of 16 bits a thread (8 or 16 of
+// fp32), a warp for the shortest rows.  Beyond 512 threads a row (D > 8192 in
+// 16 bits) there is no ring, and both passes read global memory.
+#define PROJ_NORM_PICK(FN, T, a, s)                                      \
+  if (vec) {                                                             \
+    const int64_t n = (a).D / kFullVec<T>;                               \
+    if (n <= 64) return FN<Shape<T, true, 32, 2>>(a, s);                 \
+    if (n <= 256) return FN<Shape<T, true, 128, 2>>(a, s);               \
+    if (n <= 512) return FN<Shape<T, true, 256, 2>>(a, s);               \
+    if (n <= 1024) return FN<Shape<T, true, 512, 2>>(a, s);              \
+    if constexpr (kFullVec<T> == 4)                                      \
+      if (n > 2048) return FN<Shape<T, true, 1024, 4>>(a, s);            \
+    return FN<Shape<T, true, 1024, 2>>(a, s);                            \
+  } else {                                                               \
+    if ((a).D <= 512) return FN<Shape<T, false, 32, 2>>(a, s);           \
+    if ((a).D <= 2048) return FN<Shape<T, false, 128, 2>>(a, s);         \
+    if ((a).D <= 4096) return FN<Shape<T, false, 256, 2>>(a, s);         \
+    if ((a).D <= 8192) return FN<Shape<T, false, 512, 2>>(a, s);         \
+    return FN<Shape<T, false, 1024, 2>>(a, s);                           \
   }
 
 template <typename T>
@@ -453,7 +720,7 @@ extern "C" int64_t proj_norm_workspace(int64_t m, int64_t D) {
     return -1;
   }
   // rows are rounded up to the four that a block of warps holds
-  return static_cast<int64_t>((grad_parts(m) + 3) / 4 * 4) * 3 * D * 4;
+  return static_cast<int64_t>((grad_parts(m, D) + 3) / 4 * 4) * 3 * D * 4;
 }
 
 extern "C" int proj_norm_backward(const proj_norm_grad_args* args, proj_stream stream) {

@@ -239,6 +239,7 @@ __global__ void __launch_bounds__(kSortThreads) place_kernel(const SortParams p)
   const int chunks = (n + 31) / 32;
   for (int i = tid; i < (chunks * p.E + 1) / 2; i += kSortThreads)
     reinterpret_cast<uint32_t*>(s_table)[i] = 0u;
+  if (tid < p.E) s_total[tid] = s_base[tid] = 0;
   __syncthreads();
   griddep_wait();
   const int32_t* expert = p.expert + t0 * p.k;
@@ -251,16 +252,20 @@ __global__ void __launch_bounds__(kSortThreads) place_kernel(const SortParams p)
     chunk_rank(e, real, lane, count, last);
     if (real && last) s_table[c * p.E + e] = static_cast<uint16_t>(count);
   }
-  int before = 0;
-  if (tid < p.E) {
-    int total = 0;
+  // Every block's counts, by as many threads per expert as there are (sums of
+  // whole numbers: their order does not matter).
+  const int parts = kSortThreads / p.E;
+  if (tid < parts * p.E) {
+    const int e = tid % p.E;
+    int before = 0, total = 0;
 #pragma unroll 8
-    for (int b = 0; b < p.blocks; ++b) {
-      const int v = p.table[static_cast<int64_t>(b) * p.E + tid];
+    for (int b = tid / p.E; b < p.blocks; b += parts) {
+      const int v = p.table[static_cast<int64_t>(b) * p.E + e];
       if (b < static_cast<int>(blockIdx.x)) before += v;
       total += v;
     }
-    s_total[tid] = total;
+    atomicAdd(s_total + e, total);
+    atomicAdd(s_base + e, before);
   }
   __syncthreads();
   if (tid < p.E) {
@@ -272,7 +277,7 @@ __global__ void __launch_bounds__(kSortThreads) place_kernel(const SortParams p)
     }
   }
   const int kept = scan_experts(s_total, s_warp, p.E);
-  if (tid < p.E) s_base[tid] = s_total[tid] + before;
+  if (tid < p.E) s_base[tid] += s_total[tid];
   if (blockIdx.x == 0) {
     if (tid < p.E) p.offsets[tid] = s_total[tid];
     if (tid == 0) p.offsets[p.E] = kept;
@@ -318,8 +323,18 @@ constexpr int kRowThreads = 256;
 
 __device__ __forceinline__ bool is_slot(int s, int64_t rows) { return s >= 0 && s < rows; }
 
+// Rows are read and written V elements at a time, as wide as every row's
+// alignment allows (16, 8 or 4 bytes, or single elements for an odd width);
+// a thread has U of them under way, so that narrow accesses keep about as
+// many bytes in flight as wide ones.
+template <typename T, int V>
+constexpr int kAhead = 16 / (V * static_cast<int>(sizeof(T))) < 8
+                           ? 16 / (V * static_cast<int>(sizeof(T)))
+                           : 8;
+
 template <typename T, int V>
 __global__ void __launch_bounds__(kRowThreads) gather_kernel(const RowsParams p) {
+  constexpr int U = kAhead<T, V>;
   griddep_launch_dependents();
   griddep_wait();
   const int64_t t = blockIdx.x;
@@ -327,18 +342,29 @@ __global__ void __launch_bounds__(kRowThreads) gather_kernel(const RowsParams p)
   const T* x = static_cast<const T*>(p.a) + t * p.lda;
   const int32_t* slot = p.slot + t * p.k;
   T* xs = static_cast<T*>(p.out);
-  for (int64_t v = static_cast<int64_t>(blockIdx.y) * kRowThreads + threadIdx.x; v < nvec;
-       v += static_cast<int64_t>(gridDim.y) * kRowThreads) {
-    const Vec<T, V> val = load_vec<T, V>(x + v * V);
+  for (int64_t v0 = static_cast<int64_t>(blockIdx.y) * kRowThreads * U + threadIdx.x; v0 < nvec;
+       v0 += static_cast<int64_t>(gridDim.y) * kRowThreads * U) {
+    Vec<T, V> val[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (v0 + u * kRowThreads < nvec) val[u] = load_vec<T, V>(x + (v0 + u * kRowThreads) * V);
     for (int j = 0; j < p.k; ++j) {
       const int s = __ldg(slot + j);
-      if (is_slot(s, rows)) *reinterpret_cast<Vec<T, V>*>(xs + s * p.ldo + v * V) = val;
+      if (!is_slot(s, rows)) continue;
+      T* to = xs + s * p.ldo + v0 * V;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (v0 + u * kRowThreads < nvec)
+          *reinterpret_cast<Vec<T, V>*>(to + u * kRowThreads * V) = val[u];
     }
   }
 }
 
+// Single elements of 16 bits (an odd width): the rows' values go through
+// registers.
 template <typename T, int V>
 __global__ void __launch_bounds__(kRowThreads) combine_kernel(const RowsParams p) {
+  constexpr int U = kAhead<T, V>;
   griddep_launch_dependents();
   griddep_wait();
   const int64_t t = blockIdx.x;
@@ -347,11 +373,11 @@ __global__ void __launch_bounds__(kRowThreads) combine_kernel(const RowsParams p
   const int32_t* slot = p.slot + t * p.k;
   const float* weight = p.weight ? p.weight + t * p.k : nullptr;
   T* out = static_cast<T*>(p.out) + t * p.ldo;
-  for (int64_t v = static_cast<int64_t>(blockIdx.y) * kRowThreads + threadIdx.x; v < nvec;
-       v += static_cast<int64_t>(gridDim.y) * kRowThreads) {
-    float acc[V] = {};
+  for (int64_t v0 = static_cast<int64_t>(blockIdx.y) * kRowThreads * U + threadIdx.x; v0 < nvec;
+       v0 += static_cast<int64_t>(gridDim.y) * kRowThreads * U) {
+    float acc[U][V] = {};
     for (int j0 = 0; j0 < p.k; j0 += 8) {
-      Vec<T, V> val[8];
+      Vec<T, V> val[8][U];
       float w[8];
       bool ok[8];
 #pragma unroll
@@ -359,28 +385,169 @@ __global__ void __launch_bounds__(kRowThreads) combine_kernel(const RowsParams p
         const int s = j0 + j < p.k ? __ldg(slot + j0 + j) : -1;
         ok[j] = is_slot(s, rows);
         if (ok[j]) {
-          val[j] = load_vec<T, V>(ys + s * p.lda + v * V);
           w[j] = weight ? __ldg(weight + j0 + j) : 1.f;
+          const T* from = ys + s * p.lda + v0 * V;
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            if (v0 + u * kRowThreads < nvec) val[j][u] = load_vec<T, V>(from + u * kRowThreads * V);
         }
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         if (ok[j]) {
-          float f[V];
-          widen(val[j], f);
 #pragma unroll
-          for (int i = 0; i < V; ++i) acc[i] = fmaf(w[j], f[i], acc[i]);
+          for (int u = 0; u < U; ++u) {
+            float f[V];
+            widen(val[j][u], f);
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[u][i] = fmaf(w[j], f[i], acc[u][i]);
+          }
         }
     }
-    store_vec<T, V>(out + v * V, acc);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (v0 + u * kRowThreads < nvec) store_vec<T, V>(out + (v0 + u * kRowThreads) * V, acc[u]);
   }
 }
 
-// One token per CTA: the k dot products run over the whole row, eight
-// entries at a time.
+template <int kBytes>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
+  if constexpr (kBytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(kBytes)
+                 : "memory");
+}
+
+// The slots and weights of eight entries of a token from j0 on (-1: no row).
+struct Eight {
+  int s[8];
+  float w[8];
+  __device__ __forceinline__ void slots(const RowsParams& p, int64_t t, int j0) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s[j] = j0 + j < p.k ? __ldg(p.slot + t * p.k + j0 + j) : -1;
+  }
+  __device__ __forceinline__ void weights(const RowsParams& p, int64_t t, int j0) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      w[j] = p.weight && j0 + j < p.k ? __ldg(p.weight + t * p.k + j0 + j) : 1.f;
+  }
+};
+
+// The combine is bound by the loads of k rows per token from anywhere.  A CTA
+// takes pieces (token, columns, eight entries) in turn and has the rows of the
+// next kDeep - 1 on their way to shared memory, where a thread reads back what
+// it copied itself: no barriers, no registers held by loads in flight, and the
+// slots of a piece are read one piece before its copies start.
+constexpr int kDeep = 3;
+constexpr int kDeepBytes = kDeep * 8 * kRowThreads * 16;
+
+template <typename T, int V>
+__global__ void __launch_bounds__(kRowThreads, 2)
+    combine_deep_kernel(const RowsParams p, const int pieces_per_token) {
+  constexpr int U = kAhead<T, V>, kBytes = V * static_cast<int>(sizeof(T));
+  extern __shared__ __align__(16) uint8_t s_rows[];  // [kDeep][8][U][kRowThreads] of kBytes
+  griddep_launch_dependents();
+  griddep_wait();
+  const int nvec = static_cast<int>(p.D / V);
+  const int64_t rows = p.m * p.k;
+  const T* ys = static_cast<const T*>(p.a);
+  const int jgroups = (p.k + 7) / 8;  // the entries of a piece's token, eight at a time, fastest
+  const int columns = pieces_per_token / jgroups;
+  const int64_t total = p.m * columns;  // pieces but for the entries
+  const uint32_t mine = smem_u32(s_rows) + threadIdx.x * kBytes;
+
+  struct At {
+    int64_t t;
+    int col, j0;
+  };
+  auto where = [&](int64_t n) {  // this CTA's n-th piece
+    const int64_t i = blockIdx.x + n / jgroups * gridDim.x;
+    At at;
+    at.t = i < total ? i / columns : -1;
+    at.col = static_cast<int>(i % columns) * kRowThreads * U + threadIdx.x;
+    at.j0 = static_cast<int>(n % jgroups) * 8;
+    return at;
+  };
+  auto start = [&](const At& at, const int (&s)[8], int stage) {
+    if (at.t < 0) return;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (is_slot(s[j], rows)) {
+        const T* from = ys + s[j] * p.lda + static_cast<int64_t>(at.col) * V;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (at.col + u * kRowThreads < nvec)
+            cp_async<kBytes>(mine + ((stage * 8 + j) * U + u) * kRowThreads * kBytes,
+                             from + u * kRowThreads * V);
+      }
+  };
+
+  Eight ahead, cur;
+  for (int d = 0; d < kDeep - 1; ++d) {
+    const At at = where(d);
+    if (at.t >= 0) ahead.slots(p, at.t, at.j0);
+    start(at, ahead.s, d);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  At next = where(kDeep - 1);
+  if (next.t >= 0) ahead.slots(p, next.t, next.j0);
+  At at = where(0);
+  if (at.t >= 0) {
+    cur.slots(p, at.t, at.j0);
+    cur.weights(p, at.t, at.j0);
+  }
+  float acc[U][V] = {};
+  int stage = 0;
+  for (int64_t n = 0; at.t >= 0; ++n) {
+    // start the piece kDeep - 1 ahead in the stage that the last one left
+    start(next, ahead.s, stage == 0 ? kDeep - 1 : stage - 1);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    next = where(n + kDeep);
+    if (next.t >= 0) ahead.slots(p, next.t, next.j0);
+    const At after = where(n + 1);
+    Eight then;
+    if (after.t >= 0) {
+      then.slots(p, after.t, after.j0);
+      then.weights(p, after.t, after.j0);
+    }
+    asm volatile("cp.async.wait_group %0;" ::"n"(kDeep - 1) : "memory");
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (is_slot(cur.s[j], rows)) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          float f[V];
+          widen(*reinterpret_cast<const Vec<T, V>*>(
+                    s_rows + (static_cast<size_t>((stage * 8 + j) * U + u) * kRowThreads +
+                              threadIdx.x) * kBytes),
+                f);
+#pragma unroll
+          for (int i = 0; i < V; ++i) acc[u][i] = fmaf(cur.w[j], f[i], acc[u][i]);
+        }
+      }
+    if (at.j0 + 8 >= p.k) {
+      T* out = static_cast<T*>(p.out) + at.t * p.ldo;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (at.col + u * kRowThreads < nvec)
+          store_vec<T, V>(out + (at.col + u * kRowThreads) * V, acc[u]);
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[u][i] = 0.f;
+      }
+    }
+    at = after;
+    cur = then;
+    if (++stage == kDeep) stage = 0;
+  }
+}
+
+// One token per CTA: the k dot products run over the whole row, KJ entries at
+// a time.
 template <typename T, int V>
 __global__ void __launch_bounds__(kRowThreads) combine_grad_kernel(const RowsParams p) {
-  __shared__ float room[2 * 8 * 32];
+  constexpr int U = kAhead<T, V>, KJ = 8;
+  __shared__ float room[2 * KJ * 32];
   int turn = 0;
   griddep_launch_dependents();
   griddep_wait();
@@ -390,46 +557,59 @@ __global__ void __launch_bounds__(kRowThreads) combine_grad_kernel(const RowsPar
   const T* ys = static_cast<const T*>(p.b);
   const int32_t* slot = p.slot + t * p.k;
   T* dys = static_cast<T*>(p.out);
-  for (int j0 = 0; j0 < p.k; j0 += 8) {
-    int s[8];
-    float w[8], dot[8];
+  for (int j0 = 0; j0 < p.k; j0 += KJ) {
+    int s[KJ];
+    float w[KJ], dot[KJ];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < KJ; ++j) {
       s[j] = j0 + j < p.k ? __ldg(slot + j0 + j) : -1;
       if (!is_slot(s[j], rows)) s[j] = -1;
       w[j] = s[j] >= 0 && p.out ? (p.weight ? __ldg(p.weight + t * p.k + j0 + j) : 1.f) : 0.f;
       dot[j] = 0.f;
     }
-    for (int64_t v = threadIdx.x; v < nvec; v += kRowThreads) {
-      float d[V];
-      widen(load_vec<T, V>(dout + v * V), d);
-      Vec<T, V> val[8];
+    for (int64_t v0 = threadIdx.x; v0 < nvec; v0 += kRowThreads * U) {
+      Vec<T, V> dv[U], val[KJ][U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (v0 + u * kRowThreads < nvec) dv[u] = load_vec<T, V>(dout + (v0 + u * kRowThreads) * V);
       if (p.dweight) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (s[j] >= 0) val[j] = load_vec<T, V>(ys + s[j] * p.ldb + v * V);
+        for (int j = 0; j < KJ; ++j)
+          if (s[j] >= 0) {
+            const T* from = ys + s[j] * p.ldb + v0 * V;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+              if (v0 + u * kRowThreads < nvec)
+                val[j][u] = load_vec<T, V>(from + u * kRowThreads * V);
+          }
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (s[j] >= 0) {
-          if (p.dweight) {
-            float f[V];
-            widen(val[j], f);
+      for (int u = 0; u < U; ++u) {
+        if (v0 + u * kRowThreads >= nvec) continue;
+        float d[V];
+        widen(dv[u], d);
 #pragma unroll
-            for (int i = 0; i < V; ++i) dot[j] = fmaf(d[i], f[i], dot[j]);
-          }
-          if (p.out) {
-            float o[V];
+        for (int j = 0; j < KJ; ++j)
+          if (s[j] >= 0) {
+            if (p.dweight) {
+              float f[V];
+              widen(val[j][u], f);
 #pragma unroll
-            for (int i = 0; i < V; ++i) o[i] = w[j] * d[i];
-            store_vec<T, V>(dys + s[j] * p.ldo + v * V, o);
+              for (int i = 0; i < V; ++i) dot[j] = fmaf(d[i], f[i], dot[j]);
+            }
+            if (p.out) {
+              float o[V];
+#pragma unroll
+              for (int i = 0; i < V; ++i) o[i] = w[j] * d[i];
+              store_vec<T, V>(dys + s[j] * p.ldo + (v0 + u * kRowThreads) * V, o);
+            }
           }
-        }
+      }
     }
     if (p.dweight) {
-      row_sums<kRowThreads, 8>(dot, room, turn);
+      row_sums<kRowThreads, KJ>(dot, room, turn);
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+      for (int j = 0; j < KJ; ++j)
         if (threadIdx.x == j && j0 + j < p.k) p.dweight[t * p.k + j0 + j] = dot[j];
     }
   }
@@ -536,13 +716,12 @@ cudaLaunchConfig_t config(int64_t grid_x, int64_t grid_y, unsigned threads, size
   return cfg;
 }
 
-// Tokens per block of the sort: one block while its warps choose for at most
-// two tokens each; more tokens are spread over blocks of 64 tokens, longer
-// ones from 64 K entries on (the table of counts that every block reads grows
-// with their number), as far as the chunk table fits shared memory.
+// Tokens per block of the sort: one block, and with it one launch, up to 64
+// tokens (two a warp); more tokens are spread over as many blocks as there are
+// SMs, a warp choosing for at least one token each, as far as the chunk table
+// fits shared memory.
 int sort_tokens(int64_t m, int E, int k) {
-  int64_t tokens = 64;
-  while (tokens * 256 < m) tokens *= 2;
+  const int64_t tokens = m <= 64 ? 64 : std::max<int64_t>(kSortWarps, (m + 151) / 152);
   // chunk table in shared memory, counts in 16 bits
   const int64_t most = std::min<int64_t>(kTableBytes / (2 * E) * 32, 32768) / k;
   return static_cast<int>(std::max<int64_t>(1, std::min(tokens, most)));
@@ -649,33 +828,56 @@ const char* refuse_rows(const RowsParams& p, int64_t k, int dtype, int* status) 
   return nullptr;
 }
 
-bool rows16(const void* p, int64_t ld, int el) {
-  return !p || (aligned_to(p, 16) && (ld * el) % 16 == 0);
-}
-
 enum class Op { kGather, kCombine, kGrad };
 
 template <typename T, int V>
 cudaError_t rows_launch(Op op, const RowsParams& p, cudaStream_t s) {
   const int64_t nvec = p.D / V;
-  const int64_t ny = std::min<int64_t>(64, (nvec + kRowThreads - 1) / kRowThreads);
+  const int64_t per = kRowThreads * kAhead<T, V>;
+  const int64_t ny = op == Op::kGrad ? 1 : std::min<int64_t>(64, (nvec + per - 1) / per);
   cudaLaunchAttribute attr[1];
-  const cudaLaunchConfig_t cfg =
-      config(p.m, op == Op::kGrad ? 1 : ny, kRowThreads, 0, s, attr);
+  if constexpr (V * sizeof(T) >= 4) {
+    if (op == Op::kCombine) {
+      const int64_t columns = (nvec + per - 1) / per;
+      const int64_t jgroups = (p.k + 7) / 8;
+      const cudaError_t e =
+          cudaFuncSetAttribute(combine_deep_kernel<T, V>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, kDeepBytes);
+      if (e != cudaSuccess) return e;
+      const int64_t grid = std::min<int64_t>(p.m * columns, 2 * std::max(1, proj_num_sms()));
+      const cudaLaunchConfig_t cfg = config(grid, 1, kRowThreads, kDeepBytes, s, attr);
+      return cudaLaunchKernelEx(&cfg, combine_deep_kernel<T, V>, p,
+                                static_cast<int>(columns * jgroups));
+    }
+  }
+  const cudaLaunchConfig_t cfg = config(p.m, ny, kRowThreads, 0, s, attr);
   switch (op) {
     case Op::kGather: return cudaLaunchKernelEx(&cfg, gather_kernel<T, V>, p);
-    case Op::kCombine: return cudaLaunchKernelEx(&cfg, combine_kernel<T, V>, p);
+    case Op::kCombine:
+      if constexpr (V * sizeof(T) < 4) return cudaLaunchKernelEx(&cfg, combine_kernel<T, V>, p);
+      break;
     case Op::kGrad: return cudaLaunchKernelEx(&cfg, combine_grad_kernel<T, V>, p);
   }
   return cudaErrorInvalidValue;
 }
 
+// Whether every row of every tensor starts on a multiple of `bytes`, and so
+// does its end.
+bool rows_on(const RowsParams& p, int el, int bytes) {
+  auto fits = [&](const void* q, int64_t ld) {
+    return !q || (aligned_to(q, bytes) && (ld * el) % bytes == 0);
+  };
+  return (p.D * el) % bytes == 0 && fits(p.a, p.lda) && fits(p.b, p.ldb) && fits(p.out, p.ldo);
+}
+
 template <typename T>
 cudaError_t rows_any(Op op, const RowsParams& p, cudaStream_t s) {
   constexpr int el = sizeof(T);
-  const bool vec = (p.D * el) % 16 == 0 && rows16(p.a, p.lda, el) && rows16(p.b, p.ldb, el) &&
-                   rows16(p.out, p.ldo, el);
-  return vec ? rows_launch<T, kFullVec<T>>(op, p, s) : rows_launch<T, 1>(op, p, s);
+  if (rows_on(p, el, 16)) return rows_launch<T, 16 / el>(op, p, s);
+  if (rows_on(p, el, 8)) return rows_launch<T, 8 / el>(op, p, s);
+  if constexpr (el == 2)
+    if (rows_on(p, el, 4)) return rows_launch<T, 2>(op, p, s);
+  return rows_launch<T, 1>(op, p, s);
 }
 
 int rows_call(const char* call, Op op, const RowsParams& p, int dtype, proj_stream stream) {

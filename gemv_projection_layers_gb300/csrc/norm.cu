@@ -42,12 +42,29 @@ namespace {
 
 constexpr int kMaxD = 16384;
 
-// exp(-g) and the quotient: the 16-bit types' outputs are rounded to 2^-8 or
-// 2^-11, so the hardware's approximations (2^-21 or so) do; fp32 takes expf.
+// The sigmoid's exponential and reciprocal: the 16-bit types' outputs are
+// rounded to 2^-8 or 2^-11, so the hardware's approximations (2^-21 or so) do;
+// fp32 takes expf and a true quotient.
+template <typename T>
+__device__ __forceinline__ float sigmoid(float g) {
+  if constexpr (sizeof(T) == 2) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return r;
+  } else {
+    return 1.f / (1.f + expf(-g));
+  }
+}
 template <typename T>
 __device__ __forceinline__ float act(float g, int kind) {
-  if (kind != PROJ_GATE_SIGMOID) return g;
-  return __fdividef(1.f, 1.f + (sizeof(T) == 2 ? __expf(-g) : expf(-g)));
+  return kind == PROJ_GATE_SIGMOID ? sigmoid<T>(g) : g;
+}
+template <typename T, int E>
+__device__ __forceinline__ void act_all(float (&g)[E], int kind) {
+  if (kind != PROJ_GATE_SIGMOID) return;
+#pragma unroll
+  for (int i = 0; i < E; ++i) g[i] = sigmoid<T>(g[i]);
 }
 // d act / d gate from the activated value.
 __device__ __forceinline__ float act_slope(float g, int kind) {
@@ -96,10 +113,55 @@ __device__ __forceinline__ void load_global(const typename S::Type* row, int j, 
       for (int i = 0; i < S::E; ++i) v[i] = 0.f;
     }
   } else {
+    const int c0 = j * S::E * S::TPR + tid;
+    if ((j + 1) * S::E * S::TPR <= D) {
 #pragma unroll
-    for (int i = 0; i < S::E; ++i) {
-      const int c = (j * S::E + i) * S::TPR + tid;
-      v[i] = c < D ? to_f32(row[c]) : 0.f;
+      for (int i = 0; i < S::E; ++i) v[i] = to_f32(row[c0 + i * S::TPR]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < S::E; ++i)
+        v[i] = c0 + i * S::TPR < D ? to_f32(row[c0 + i * S::TPR]) : 0.f;
+    }
+  }
+}
+
+// The same of a row in shared memory, by its 32-bit address (generic loads
+// are slower).
+template <typename T>
+__device__ __forceinline__ float load_shared_one(uint32_t addr) {
+  if constexpr (sizeof(T) == 4) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+    return v;
+  } else {
+    uint16_t b;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(b) : "r"(addr));
+    return to_f32(*reinterpret_cast<const T*>(&b));
+  }
+}
+template <typename S>
+__device__ __forceinline__ void load_shared(uint32_t row, int j, int tid, int D,
+                                            float (&v)[S::E]) {
+  using T = typename S::Type;
+  constexpr int el = sizeof(T);
+  if constexpr (S::kVec) {
+    const int c = (j * S::TPR + tid) * S::E;
+    if (c < D) {
+      const uint4 b = ld_shared_u4(row + c * el);
+      widen(*reinterpret_cast<const Vec<T, S::E>*>(&b), v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < S::E; ++i) v[i] = 0.f;
+    }
+  } else {
+    const int c0 = j * S::E * S::TPR + tid;
+    if ((j + 1) * S::E * S::TPR <= D) {
+#pragma unroll
+      for (int i = 0; i < S::E; ++i) v[i] = load_shared_one<T>(row + (c0 + i * S::TPR) * el);
+    } else {
+#pragma unroll
+      for (int i = 0; i < S::E; ++i)
+        v[i] = c0 + i * S::TPR < D ? load_shared_one<T>(row + (c0 + i * S::TPR) * el) : 0.f;
     }
   }
 }
@@ -112,10 +174,14 @@ __device__ __forceinline__ void store_global(typename S::Type* row, int j, int t
     const int c = (j * S::TPR + tid) * S::E;
     if (c < D) store_vec<T, S::E>(row + c, v);
   } else {
+    const int c0 = j * S::E * S::TPR + tid;
+    if ((j + 1) * S::E * S::TPR <= D) {
 #pragma unroll
-    for (int i = 0; i < S::E; ++i) {
-      const int c = (j * S::E + i) * S::TPR + tid;
-      if (c < D) row[c] = from_f32<T>(v[i]);
+      for (int i = 0; i < S::E; ++i) row[c0 + i * S::TPR] = from_f32<T>(v[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < S::E; ++i)
+        if (c0 + i * S::TPR < D) row[c0 + i * S::TPR] = from_f32<T>(v[i]);
     }
   }
 }
@@ -170,12 +236,10 @@ struct Rows {
   __device__ __forceinline__ void load(int k, int64_t row, int stage, int j, int tid,
                                        float (&v)[S::E]) const {
     const T* src = base[k] + row * ld[k];
-    if constexpr (!S::kRing) {
+    if constexpr (!S::kRing)
       load_global<S>(src, j, tid, D, v);
-    } else {
-      const T* at = reinterpret_cast<const T*>(place(stage, k) + skew(src));
-      load_global<S>(at, j, tid, D, v);
-    }
+    else
+      load_shared<S>(smem_u32(place(stage, k)) + skew(src), j, tid, D, v);
   }
 };
 
@@ -282,8 +346,7 @@ __global__ void __launch_bounds__(S::kThreads)
             rows.load(2, row, stage, j, tid, w);
           else
             load_global<S>(static_cast<const T*>(a.gate), j, tid, D, w);
-#pragma unroll
-          for (int i = 0; i < E; ++i) w[i] = act<T>(w[i], a.gate_act);
+          act_all<T>(w, a.gate_act);
         } else {
 #pragma unroll
           for (int i = 0; i < E; ++i) w[i] = g_row;
@@ -421,8 +484,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kThreads < 512 ? 512 / S::kThr
           rows.load(2, row, stage, j, tid, g[j]);
         else
           load_global<S>(static_cast<const T*>(a.gate), j, tid, D, g[j]);
-#pragma unroll
-        for (int i = 0; i < E; ++i) g[j][i] = act<T>(g[j][i], a.gate_act);
+        act_all<T>(g[j], a.gate_act);
       } else {
 #pragma unroll
         for (int i = 0; i < E; ++i) g[j][i] = g_row;
@@ -468,7 +530,11 @@ __global__ void __launch_bounds__(S::kThreads, S::kThreads < 512 ? 512 / S::kThr
       if (a.dy) store_global<S>(static_cast<T*>(a.dy) + row * a.lddy, j, tid, D, out);
       if (g_vec && a.dgate) {
 #pragma unroll
-        for (int i = 0; i < E; ++i) out[i] = n[i] * e[i] * act_slope(g[j][i], a.gate_act);
+        for (int i = 0; i < E; ++i) out[i] = n[i] * e[i];
+        if (a.gate_act == PROJ_GATE_SIGMOID) {
+#pragma unroll
+          for (int i = 0; i < E; ++i) out[i] *= g[j][i] * (1.f - g[j][i]);
+        }
         if (col_gate) {
 #pragma unroll
           for (int i = 0; i < E; ++i) acc_gate[j][i] += out[i];

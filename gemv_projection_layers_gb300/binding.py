@@ -197,10 +197,11 @@ def header_functions() -> list[str]:
 def _addr(p) -> int | None:
     if p is None:
         return None
+    data_ptr = getattr(p, "data_ptr", None)
+    if data_ptr is not None:
+        return data_ptr()
     if isinstance(p, int):
         return p
-    if hasattr(p, "data_ptr"):
-        return int(p.data_ptr())
     if hasattr(p, "ctypes"):
         return int(p.ctypes.data)
     raise TypeError(f"cannot take the address of {type(p)!r}")

@@ -2,6 +2,7 @@
 // translation units.  Internal to libproj.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -110,6 +111,9 @@ cudaError_t gemv_reg12_launch(int MT, const GemvParams& p, cudaStream_t s);
 // proj_last_cuda_error; both return the status.
 int record_status(int status, const char* text);
 int record_cuda(cudaError_t e, const char* what);
+// Allow a kernel `bytes` of dynamic shared memory, once per device and kernel
+// (`done` is the kernel's own mask of devices).
+cudaError_t allow_smem(const void* kernel, size_t bytes, std::atomic<uint64_t>& done);
 cudaError_t gemv_launch(bool f32w, int MT, const GemvParams& p, cudaStream_t s);
 
 // Tensor-core path: BN in {16, 32, 64, 128, 256}; expwin12 for BN in {16, 32, 64, 128}.

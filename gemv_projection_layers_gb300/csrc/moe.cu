@@ -738,9 +738,9 @@ size_t sort_smem(int tokens, int E, int k) {
 template <int EPL>
 cudaError_t choose_count(const SortParams& p, size_t smem, cudaStream_t s) {
   if (smem > 48 * 1024) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(choose_count_kernel<EPL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kTableBytes + 16);
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(choose_count_kernel<EPL>),
+                                     kTableBytes + 16, done);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchAttribute attr[1];
@@ -759,8 +759,8 @@ cudaError_t sort_launch(const SortParams& p, cudaStream_t s) {
     e = choose_count<32>(p, smem, s);
   if (e != cudaSuccess || !p.offsets || p.blocks <= 1) return e;
   if (smem > 48 * 1024) {
-    e = cudaFuncSetAttribute(place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kTableBytes + 16);
+    static std::atomic<uint64_t> done{0};
+    e = allow_smem(reinterpret_cast<const void*>(place_kernel), kTableBytes + 16, done);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchAttribute attr[1];
@@ -840,9 +840,9 @@ cudaError_t rows_launch(Op op, const RowsParams& p, cudaStream_t s) {
     if (op == Op::kCombine) {
       const int64_t columns = (nvec + per - 1) / per;
       const int64_t jgroups = (p.k + 7) / 8;
-      const cudaError_t e =
-          cudaFuncSetAttribute(combine_deep_kernel<T, V>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize, kDeepBytes);
+      static std::atomic<uint64_t> done{0};
+      const cudaError_t e = allow_smem(reinterpret_cast<const void*>(combine_deep_kernel<T, V>),
+                                       kDeepBytes, done);
       if (e != cudaSuccess) return e;
       const int64_t grid = std::min<int64_t>(p.m * columns, 2 * std::max(1, proj_num_sms()));
       const cudaLaunchConfig_t cfg = config(grid, 1, kRowThreads, kDeepBytes, s, attr);

@@ -415,130 +415,171 @@ __global__ void __launch_bounds__(S::kThreads, S::kThreads < 512 ? 512 / S::kThr
   rows.slot = slot;
   rows.stages = stages;
 
-  float acc_post[NV][E] = {}, acc_pre[NV][E] = {}, acc_gate[NV][E] = {};
+  constexpr int H = E / 2;  // the arithmetic runs on pairs of elements
+  const F2 zero = f2(0.f), one = f2(1.f), minus = f2(-1.f);
+  const F2 alpha = f2(a.alpha), beta = f2(a.beta);
+  F2 acc_post[NV][H], acc_pre[NV][H], acc_gate[NV][H];
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int i = 0; i < H; ++i) acc_post[j][i] = acc_pre[j][i] = acc_gate[j][i] = zero;
+
+  float rp_next = 1.f, ru_next = 1.f;  // the next row's factors, read a row ahead
+  auto factors = [&](int64_t row) {
+    if (row >= a.m) return;
+    if (normed) rp_next = a.rstd_post[row];
+    if (a.dnormed) ru_next = a.rstd_pre[row];
+  };
+  factors(part_row);
 
   over_rows<S>(rows, a.m, part_row, static_cast<int64_t>(gridDim.x) * S::kRows, tid,
                [&](int64_t row, int stage) {
-    const float rp = normed ? a.rstd_post[row] : 1.f;
-    const float ru = a.dnormed ? a.rstd_pre[row] : 1.f;
+    const F2 rp = f2(rp_next);
+    const float ru_row = ru_next;
+    const F2 ru = f2(ru_row);
+    factors(row + static_cast<int64_t>(gridDim.x) * S::kRows);
     const float g_row =
         g_token ? act<T>(to_f32(static_cast<const T*>(a.gate)[row]), a.gate_act) : 1.f;
     // group j's yn, n, un, dh, t = dh w_pre and e = du' + ru t, and w_post, with the
     // activated gate in g
-    float yn[E], n[E], un[E], dh[E], t[E], e[E], wpo[E];
-    auto group = [&](int j, const float (&g)[E]) {
+    F2 yn[H], n[H], un[H], dh[H], t[H], e[H], wpo[H];
+    auto group = [&](int j, const F2 (&g)[H]) {
       float v[E];
-      rows.load(0, row, stage, j, tid, un);
+      rows.load(0, row, stage, j, tid, v);
+      pairs<E>(v, un);
 #pragma unroll
-      for (int i = 0; i < E; ++i) un[i] *= a.alpha;
+      for (int i = 0; i < H; ++i) un[i] = mul2(un[i], alpha);
       if (a.w_post) {
-        load_global<S>(static_cast<const T*>(a.w_post), j, tid, D, wpo);
+        load_global<S>(static_cast<const T*>(a.w_post), j, tid, D, v);
+        pairs<E>(v, wpo);
       } else {
 #pragma unroll
-        for (int i = 0; i < E; ++i) wpo[i] = 1.f;
+        for (int i = 0; i < H; ++i) wpo[i] = one;
       }
       if (a.y) {
-        rows.load(1, row, stage, j, tid, yn);
+        rows.load(1, row, stage, j, tid, v);
+        pairs<E>(v, yn);
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-          yn[i] *= rp;
-          n[i] = yn[i] * wpo[i];
-          un[i] = fmaf(a.beta * g[i], n[i], un[i]);
+        for (int i = 0; i < H; ++i) {
+          yn[i] = mul2(yn[i], rp);
+          n[i] = mul2(yn[i], wpo[i]);
+          un[i] = fma2(mul2(beta, g[i]), n[i], un[i]);
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < E; ++i) yn[i] = n[i] = 0.f;
+        for (int i = 0; i < H; ++i) yn[i] = n[i] = zero;
       }
       if (a.dout) {
-        rows.load(3, row, stage, j, tid, e);
+        rows.load(3, row, stage, j, tid, v);
+        pairs<E>(v, e);
       } else {
 #pragma unroll
-        for (int i = 0; i < E; ++i) e[i] = 0.f;
+        for (int i = 0; i < H; ++i) e[i] = zero;
       }
       if (a.dnormed) {
-        rows.load(4, row, stage, j, tid, dh);
+        rows.load(4, row, stage, j, tid, v);
+        pairs<E>(v, dh);
         if (a.w_pre) {
           load_global<S>(static_cast<const T*>(a.w_pre), j, tid, D, v);
+          pairs<E>(v, t);
 #pragma unroll
-          for (int i = 0; i < E; ++i) t[i] = dh[i] * v[i];
+          for (int i = 0; i < H; ++i) t[i] = mul2(dh[i], t[i]);
         } else {
 #pragma unroll
-          for (int i = 0; i < E; ++i) t[i] = dh[i];
+          for (int i = 0; i < H; ++i) t[i] = dh[i];
         }
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-          un[i] *= ru;
-          e[i] = fmaf(ru, t[i], e[i]);
+        for (int i = 0; i < H; ++i) {
+          un[i] = mul2(un[i], ru);
+          e[i] = fma2(ru, t[i], e[i]);
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < E; ++i) dh[i] = t[i] = 0.f;
+        for (int i = 0; i < H; ++i) dh[i] = t[i] = zero;
       }
     };
-    float g[NV][E];
-    float s[3] = {0.f, 0.f, 0.f};
+    F2 g[NV][H];
+    F2 s2x[3] = {zero, zero, zero};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       if (g_vec) {
+        float v[E];
         if (a.gate_mode == PROJ_GATE_ELEMENT)
-          rows.load(2, row, stage, j, tid, g[j]);
+          rows.load(2, row, stage, j, tid, v);
         else
-          load_global<S>(static_cast<const T*>(a.gate), j, tid, D, g[j]);
-        act_all<T>(g[j], a.gate_act);
+          load_global<S>(static_cast<const T*>(a.gate), j, tid, D, v);
+        act_all<T>(v, a.gate_act);
+        pairs<E>(v, g[j]);
       } else {
 #pragma unroll
-        for (int i = 0; i < E; ++i) g[j][i] = g_row;
+        for (int i = 0; i < H; ++i) g[j][i] = f2(g_row);
       }
       group(j, g[j]);
 #pragma unroll
-      for (int i = 0; i < E; ++i) {
-        s[0] = fmaf(t[i], un[i], s[0]);
-        const float gn = g_token ? n[i] : g[j][i] * n[i];
-        s[1] = fmaf(gn, e[i], s[1]);
-        s[2] = fmaf(gn, un[i], s[2]);
+      for (int i = 0; i < H; ++i) {
+        s2x[0] = fma2(t[i], un[i], s2x[0]);
+        const F2 gn = g_token ? n[i] : mul2(g[j][i], n[i]);
+        s2x[1] = fma2(gn, e[i], s2x[1]);
+        s2x[2] = fma2(gn, un[i], s2x[2]);
       }
     }
+    float s[3];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      float x, y;
+      parts(s2x[i], x, y);
+      s[i] = x + y;
+    }
     row_sums<TPR, 3>(s, room, turn);
-    const float s1 = a.dnormed ? ru * s[0] * inv_d : 0.f;
+    const float s1 = a.dnormed ? ru_row * s[0] * inv_d : 0.f;
     const float ab = a.beta * (s[1] - s1 * s[2]);  // sum of beta [g] n du
-    const float s2 = normed ? (g_token ? g_row * ab : ab) * inv_d : 0.f;
+    const F2 s2 = f2(normed ? -(g_token ? g_row * ab : ab) * inv_d : 0.f);
+    const F2 minus_s1 = f2(-s1);
     if (g_token && a.dgate && tid == 0)
       static_cast<T*>(a.dgate)[row] = from_f32<T>(ab * act_slope(g_row, a.gate_act));
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       group(j, g[j]);
+      F2 o[H];
       float out[E];
 #pragma unroll
-      for (int i = 0; i < E; ++i) {
-        e[i] = a.dnormed ? fmaf(-un[i], s1, e[i]) : e[i];  // du
-        out[i] = a.alpha * e[i];
+      for (int i = 0; i < H; ++i) {
+        if (a.dnormed) e[i] = fma2(un[i], minus_s1, e[i]);  // du
+        o[i] = mul2(alpha, e[i]);
       }
-      if (a.dresidual)
+      if (a.dresidual) {
+        unpair<E>(o, out);
         store_global<S>(static_cast<T*>(a.dresidual) + row * a.lddr, j, tid, D, out);
+      }
       if (a.dw_pre) {
 #pragma unroll
-        for (int i = 0; i < E; ++i) acc_pre[j][i] = fmaf(dh[i], un[i], acc_pre[j][i]);
+        for (int i = 0; i < H; ++i) acc_pre[j][i] = fma2(dh[i], un[i], acc_pre[j][i]);
       }
       if (!a.y) continue;
 #pragma unroll
-      for (int i = 0; i < E; ++i) {
-        e[i] *= a.beta;
-        const float c = g[j][i] * e[i];
-        acc_post[j][i] = fmaf(c, yn[i], acc_post[j][i]);
-        out[i] = normed ? rp * fmaf(c, wpo[i], -yn[i] * s2) : c;
+      for (int i = 0; i < H; ++i) {
+        e[i] = mul2(e[i], beta);
+        const F2 c = mul2(g[j][i], e[i]);
+        acc_post[j][i] = fma2(c, yn[i], acc_post[j][i]);
+        o[i] = normed ? mul2(rp, fma2(c, wpo[i], mul2(yn[i], s2))) : c;
       }
-      if (a.dy) store_global<S>(static_cast<T*>(a.dy) + row * a.lddy, j, tid, D, out);
+      if (a.dy) {
+        unpair<E>(o, out);
+        store_global<S>(static_cast<T*>(a.dy) + row * a.lddy, j, tid, D, out);
+      }
       if (g_vec && a.dgate) {
 #pragma unroll
-        for (int i = 0; i < E; ++i) out[i] = n[i] * e[i];
+        for (int i = 0; i < H; ++i) o[i] = mul2(n[i], e[i]);
         if (a.gate_act == PROJ_GATE_SIGMOID) {
 #pragma unroll
-          for (int i = 0; i < E; ++i) out[i] *= g[j][i] * (1.f - g[j][i]);
+          for (int i = 0; i < H; ++i)
+            o[i] = mul2(o[i], mul2(g[j][i], fma2(g[j][i], minus, one)));
         }
         if (col_gate) {
 #pragma unroll
-          for (int i = 0; i < E; ++i) acc_gate[j][i] += out[i];
+          for (int i = 0; i < H; ++i) acc_gate[j][i] = add2(acc_gate[j][i], o[i]);
         } else {
+          unpair<E>(o, out);
           store_global<S>(static_cast<T*>(a.dgate) + row * a.lddg, j, tid, D, out);
         }
       }
@@ -548,13 +589,17 @@ __global__ void __launch_bounds__(S::kThreads, S::kThreads < 512 ? 512 / S::kThr
   float* part = static_cast<float*>(a.workspace) + static_cast<size_t>(part_row) * 3 * D;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
+    float post[E], pre[E], gate[E];
+    unpair<E>(acc_post[j], post);
+    unpair<E>(acc_pre[j], pre);
+    unpair<E>(acc_gate[j], gate);
 #pragma unroll
     for (int i = 0; i < E; ++i) {
       const int c = S::kVec ? (j * TPR + tid) * E + i : (j * E + i) * TPR + tid;
       if (c < D) {
-        if (a.dw_post) part[c] = acc_post[j][i];
-        if (a.dw_pre) part[D + c] = acc_pre[j][i];
-        if (col_gate) part[2 * D + c] = acc_gate[j][i];
+        if (a.dw_post) part[c] = post[i];
+        if (a.dw_pre) part[D + c] = pre[i];
+        if (col_gate) part[2 * D + c] = gate[i];
       }
     }
   }
@@ -629,8 +674,9 @@ cudaError_t forward(const proj_norm_args& a, cudaStream_t s) {
   if (S::kRing && stages < 2) ring_shape<S>(a.D, 3, kSmemMost, 3, &slot, &stages);
   const size_t smem = static_cast<size_t>(3) * slot * stages;
   if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        norm_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e =
+        allow_smem(reinterpret_cast<const void*>(norm_kernel<S>), kSmemMost, done);
     if (e != cudaSuccess) return e;
   }
   int64_t grid = (a.m + S::kRows - 1) / S::kRows;
@@ -652,8 +698,9 @@ cudaError_t backward(const proj_norm_grad_args& a, cudaStream_t s) {
   ring_shape<S>(a.D, 5, kSmemMost / per_sm, 3, &slot, &stages);
   const size_t smem = static_cast<size_t>(5) * slot * stages;
   if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        norm_grad_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e =
+        allow_smem(reinterpret_cast<const void*>(norm_grad_kernel<S>), kSmemMost, done);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchAttribute attr[1];

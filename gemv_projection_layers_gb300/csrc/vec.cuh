@@ -39,18 +39,74 @@ __device__ __forceinline__ Vec<T, V> load_vec(const T* p) {
   return *reinterpret_cast<const Vec<T, V>*>(p);
 }
 
+// Two values rounded at once, the first in the low half.
+__device__ __forceinline__ uint32_t pack2(float a, float b, __nv_bfloat16) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b, __half) {
+  const __half2 v = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
 template <typename T, int V>
 __device__ __forceinline__ void store_vec(T* p, const float (&v)[V]) {
-  Vec<T, V> o;
+  if constexpr (sizeof(T) == 2 && V >= 2) {
+    Vec<uint32_t, V / 2> o;
 #pragma unroll
-  for (int i = 0; i < V; ++i) o.e[i] = from_f32<T>(v[i]);
-  *reinterpret_cast<Vec<T, V>*>(p) = o;
+    for (int i = 0; i < V / 2; ++i) o.e[i] = pack2(v[2 * i], v[2 * i + 1], T());
+    *reinterpret_cast<Vec<uint32_t, V / 2>*>(p) = o;
+  } else {
+    Vec<T, V> o;
+#pragma unroll
+    for (int i = 0; i < V; ++i) o.e[i] = from_f32<T>(v[i]);
+    *reinterpret_cast<Vec<T, V>*>(p) = o;
+  }
 }
 
 template <typename T, int V>
 __device__ __forceinline__ void widen(const Vec<T, V>& a, float (&v)[V]) {
 #pragma unroll
   for (int i = 0; i < V; ++i) v[i] = to_f32(a.e[i]);
+}
+
+// A pair of fp32 that one instruction multiplies and adds.
+struct F2 {
+  unsigned long long b;
+};
+__device__ __forceinline__ F2 f2(float x, float y) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.b) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ F2 f2(float x) { return f2(x, x); }
+__device__ __forceinline__ void parts(F2 a, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a.b));
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.b) : "l"(a.b), "l"(b.b));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.b) : "l"(a.b), "l"(b.b));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.b) : "l"(a.b), "l"(b.b), "l"(c.b));
+  return r;
+}
+template <int E>
+__device__ __forceinline__ void pairs(const float (&v)[E], F2 (&p)[E / 2]) {
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) p[i] = f2(v[2 * i], v[2 * i + 1]);
+}
+template <int E>
+__device__ __forceinline__ void unpair(const F2 (&p)[E / 2], float (&v)[E]) {
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) parts(p[i], v[2 * i], v[2 * i + 1]);
 }
 
 __device__ __forceinline__ float warp_sum(float v) {

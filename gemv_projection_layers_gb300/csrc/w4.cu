@@ -188,11 +188,14 @@ __device__ __forceinline__ Tile find_tile(const int32_t* __restrict__ offsets, i
 // in shared memory, CTAs after that through distributed shared memory.  A
 // warp keeps kD units of codes, scales and x in flight, all of them straight
 // to registers: the x of 8 tokens is two bytes per byte of one block's codes,
-// so RB = 2 blocks share it, and it comes from L2.
-template <typename T, bool kG32, bool kZeros, int NT, int RB>
-__global__ void __launch_bounds__(32 * kStreamWarps) w4_stream_kernel(const W4Params p, const int C) {
+// so RB = 2 blocks share it, and it comes from L2.  One matrix is short of
+// warps and takes kD = 4 units; experts, whose CTAs come in several waves, do
+// better with kD = 2 and three CTAs an SM (64 rows over 256 experts of 1024 x
+// 8192: 77 us against 92).
+template <typename T, bool kG32, bool kZeros, int NT, int RB, int kD>
+__global__ void __launch_bounds__(32 * kStreamWarps, kD == 2 && NT == 1 ? 3 : 2)
+    w4_stream_kernel(const W4Params p, const int C) {
   constexpr int W = kStreamWarps;
-  constexpr int kD = NT == 1 ? 4 : 2;
   using Scale = typename ScaleOf<kG32>::Pair;
   using Zero = typename ScaleOf<kG32>::Bytes;
   __shared__ alignas(16) float s_red[W][RB][NT][32][4];
@@ -371,7 +374,7 @@ __global__ void __launch_bounds__(32 * kStreamWarps) w4_stream_kernel(const W4Pa
   }
 }
 
-template <typename T, bool kG32, bool kZeros, int NT, int RB>
+template <typename T, bool kG32, bool kZeros, int NT, int RB, int kD>
 cudaError_t stream_launch(const W4Params& p, const StreamShape& sh, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((p.RB + RB - 1) / RB * sh.C),
@@ -387,21 +390,23 @@ cudaError_t stream_launch(const W4Params& p, const StreamShape& sh, cudaStream_t
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = sh.C > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, w4_stream_kernel<T, kG32, kZeros, NT, RB>, p, sh.C);
+  return cudaLaunchKernelEx(&cfg, w4_stream_kernel<T, kG32, kZeros, NT, RB, kD>, p, sh.C);
 }
 
-template <typename T, int NT, int RB>
+template <typename T, int NT, int RB, int kD>
 cudaError_t stream_form(const W4Params& p, const StreamShape& sh, cudaStream_t s) {
   if (p.group == 32)
-    return p.zeros ? stream_launch<T, true, true, NT, RB>(p, sh, s)
-                   : stream_launch<T, true, false, NT, RB>(p, sh, s);
-  return p.zeros ? stream_launch<T, false, true, NT, RB>(p, sh, s)
-                 : stream_launch<T, false, false, NT, RB>(p, sh, s);
+    return p.zeros ? stream_launch<T, true, true, NT, RB, kD>(p, sh, s)
+                   : stream_launch<T, true, false, NT, RB, kD>(p, sh, s);
+  return p.zeros ? stream_launch<T, false, true, NT, RB, kD>(p, sh, s)
+                 : stream_launch<T, false, false, NT, RB, kD>(p, sh, s);
 }
 
 template <typename T, int NT>
 cudaError_t stream_any(const W4Params& p, const StreamShape& sh, cudaStream_t s) {
-  return sh.RB == 1 ? stream_form<T, NT, 1>(p, sh, s) : stream_form<T, NT, 2>(p, sh, s);
+  if (sh.RB == 1) return stream_form<T, NT, 1, NT == 1 ? 4 : 2>(p, sh, s);
+  if (NT == 2 || p.offsets) return stream_form<T, NT, 2, 2>(p, sh, s);
+  return stream_form<T, NT, 2, NT == 1 ? 4 : 2>(p, sh, s);
 }
 
 int refuse(int status, const char* call, const char* why) {
@@ -422,7 +427,7 @@ struct proj_w4_ctx {
   int dtype;
   uint8_t* base;    // one allocation: codes, scales, zeros, status word
   int sms;
-  int clusters[4];  // of 1, 2, 4, 8 CTAs of the tensor-core kernel that run at once
+  int clusters[9];  // [C]: clusters of C CTAs of the tensor-core kernel that run at once
 };
 
 namespace {
@@ -464,8 +469,8 @@ Plan make_plan(const proj_w4_ctx* h, int64_t m, bool experts) {
     const int64_t items = tiles * p.RT;
     // K is split while the clusters run at once and a CTA keeps two steps
     pl.C = 1;
-    for (int i = 1; i < 4 && !experts; ++i)
-      if (items <= h->clusters[i] && p.KU >= 4 << i) pl.C = 1 << i;
+    for (int c = 2; c <= 8 && !experts; ++c)
+      if (items <= h->clusters[c] && p.KU >= 4 * c) pl.C = c;
     pl.grid = pl.C > 1 ? items * pl.C : std::min<int64_t>(items, h->sms);
   }
   return pl;
@@ -544,7 +549,7 @@ extern "C" proj_w4_handle proj_w4_prepare(const void* codes, const void* scales,
   for (int i = 0; i < 16; ++i)
     if (p.upg == 1 << i) p.upg_shift = i;
   h->sms = proj_num_sms();
-  for (int i = 0; i < 4; ++i) h->clusters[i] = w4_tc_max_clusters(1 << i);
+  for (int c = 1; c <= 8; ++c) h->clusters[c] = w4_tc_max_clusters(c);
   p.NGp = static_cast<int>(group == 32 ? 2 * p.KU : NG);  // every unit has its groups
   h->dtype = dtype;
   const int64_t row_tiles = experts * p.RT;

@@ -661,8 +661,8 @@ template <typename T, bool kG32, bool kZeros, int TN>
 cudaError_t launch(const CUtensorMap& map, const W4Params& p, int grid, int C, int box,
                    cudaStream_t s) {
   auto kernel = w4_tc_kernel<T, kG32, kZeros, TN>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       Cfg<TN>::kSmem);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), Cfg<TN>::kSmem, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));

@@ -183,9 +183,9 @@ __device__ __forceinline__ Tile find_tile(const int32_t* __restrict__ offsets, i
   return {s_found[0], s_found[1], s_found[2]};
 }
 
-// A CTA takes RB blocks of 16 weight rows and one tile of 8 NT tokens; the
-// warps of the C CTAs of a cluster deal the units of K out in turn and meet
-// in shared memory, CTAs after that through distributed shared memory.  A
+// A CTA takes RB blocks of 16 weight rows and one tile of 8 NT tokens; each
+// warp of the C CTAs of a cluster has a run of the units of K; warps meet in
+// shared memory, CTAs after that through distributed shared memory.  A
 // warp keeps kD units of codes, scales and x in flight, all of them straight
 // to registers: the x of 8 tokens is two bytes per byte of one block's codes,
 // so RB = 2 blocks share it, and it comes from L2.  One matrix is short of
@@ -213,29 +213,33 @@ __global__ void __launch_bounds__(32 * kStreamWarps, kD == 2 && NT == 1 ? 3 : 2)
   const Scale* scales[RB];
   const Zero* zeros[RB];
   const int units = kG32 ? p.KU : p.NGp;  // lines of scales in a tile
+  // the warp's run of units
+  const int part = rank * W + warp;
+  const int u0 = static_cast<int>(static_cast<int64_t>(part) * p.KU / (W * C));
+  const int u1 = static_cast<int>(static_cast<int64_t>(part + 1) * p.KU / (W * C));
   auto open = [&](int expert) {
 #pragma unroll
     for (int r = 0; r < RB; ++r) {
       const int rb = min(rb0 + r, p.RB - 1);
       const int64_t tile = static_cast<int64_t>(expert) * p.RT + (rb >> 3);
-      codes[r] = p.codes + tile * p.KU * 256 + (rb & 7) * 32 + lane;
+      codes[r] = p.codes + (tile * p.KU + u0) * 256 + (rb & 7) * 32 + lane;
       const int64_t at = tile * units * 64 + (rb & 7) * 8 + g;
       scales[r] = reinterpret_cast<const Scale*>(p.scales) + at;
       zeros[r] = reinterpret_cast<const Zero*>(p.zeros) + at;
     }
   };
-  auto fetch_w = [&](int d, int u) {
-    if (u >= p.KU) return;
+  // unit `u` to slot d, i units behind the one that the pointers stand at
+  auto fetch_w = [&](int d, int i, int u) {
+    if (u >= u1) return;
     const int at = (kG32 ? u : p.group_of(u)) * 64;
 #pragma unroll
     for (int r = 0; r < RB; ++r) {
-      code[d][r] = ld_stream_v4(codes[r] + u * 256);
+      code[d][r] = ld_stream_v4(codes[r] + i * 256);
       sc[d][r] = __ldg(scales[r] + at);
       if (kZeros) ze[d][r] = __ldg(zeros[r] + at);
     }
   };
 
-  const int u0 = rank * W + warp, stride = W * C;
   griddep_launch_dependents();
   Tile tile;
   if (p.offsets) {
@@ -244,7 +248,7 @@ __global__ void __launch_bounds__(32 * kStreamWarps, kD == 2 && NT == 1 ? 3 : 2)
     if (tile.rows == 0) return;  // every CTA of the cluster
     open(tile.expert);
 #pragma unroll
-    for (int d = 0; d < kD; ++d) fetch_w(d, u0 + d * stride);
+    for (int d = 0; d < kD; ++d) fetch_w(d, d, u0 + d);
   } else {
     tile.expert = 0;
     tile.row0 = static_cast<int64_t>(blockIdx.y) * 8 * NT;
@@ -252,14 +256,14 @@ __global__ void __launch_bounds__(32 * kStreamWarps, kD == 2 && NT == 1 ? 3 : 2)
     // the weights are constant: their first loads do not wait for the kernel before
     open(0);
 #pragma unroll
-    for (int d = 0; d < kD; ++d) fetch_w(d, u0 + d * stride);
+    for (int d = 0; d < kD; ++d) fetch_w(d, d, u0 + d);
     griddep_wait();
   }
   const T* x[NT];
   bool live[NT];
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
-    x[j] = static_cast<const T*>(p.x) + (tile.row0 + 8 * j + g) * p.ldx + 4 * t;
+    x[j] = static_cast<const T*>(p.x) + (tile.row0 + 8 * j + g) * p.ldx + u0 * 64 + 4 * t;
     live[j] = 8 * j + g < tile.rows;
 #pragma unroll
     for (int d = 0; d < kD; ++d)
@@ -267,12 +271,12 @@ __global__ void __launch_bounds__(32 * kStreamWarps, kD == 2 && NT == 1 ? 3 : 2)
       for (int i = 0; i < 4; ++i) xf[d][j][i] = make_uint2(0, 0);
   }
   const int whole = p.K / 64;  // units that K does not cut
-  auto fetch_x = [&](int d, int u) {
-    if (u >= p.KU) return;
+  auto fetch_x = [&](int d, int b, int u) {
+    if (u >= u1) return;
 #pragma unroll
     for (int j = 0; j < NT; ++j)
       if (live[j]) {
-        const T* at = x[j] + u * 64;
+        const T* at = x[j] + b * 64;
         if (u < whole) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) xf[d][j][i] = *reinterpret_cast<const uint2*>(at + 16 * i);
@@ -284,14 +288,18 @@ __global__ void __launch_bounds__(32 * kStreamWarps, kD == 2 && NT == 1 ? 3 : 2)
       }
   };
 #pragma unroll
-  for (int d = 0; d < kD; ++d) fetch_x(d, u0 + d * stride);
+  for (int d = 0; d < kD; ++d) fetch_x(d, d, u0 + d);
 
   float acc[RB][NT][4] = {};
-  for (int ub = u0; ub < p.KU; ub += kD * stride) {
+  for (int ub = u0; ub < u1; ub += kD) {
+#pragma unroll
+    for (int r = 0; r < RB; ++r) codes[r] += kD * 256;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) x[j] += kD * 64;
 #pragma unroll
     for (int d = 0; d < kD; ++d) {
-      const int u = ub + d * stride;
-      if (u < p.KU) {
+      const int u = ub + d;
+      if (u < u1) {
 #pragma unroll
         for (int r = 0; r < RB; ++r) {
           const uint32_t word[4] = {code[d][r].x, code[d][r].y, code[d][r].z, code[d][r].w};
@@ -330,8 +338,8 @@ __global__ void __launch_bounds__(32 * kStreamWarps, kD == 2 && NT == 1 ? 3 : 2)
             }
           }
         }
-        fetch_w(d, u + kD * stride);
-        fetch_x(d, u + kD * stride);
+        fetch_w(d, d, u + kD);
+        fetch_x(d, d, u + kD);
       }
     }
   }
@@ -442,13 +450,16 @@ struct Plan {
 
 // Rows that a matrix meets (on average, for experts) up to which the weights
 // are streamed with exact 4-bit products; above, the tensor-core kernel.
-constexpr int64_t kStreamRows = 16;
+// Measured: 4096 x 8192 at 16 rows 13.1 us streamed, 14.4 on the tensor cores,
+// at 17 rows 17.8 and 14.4; 60 experts of 2048 x 4096, 4.3 rows each, 88 us
+// and 99, at 8.5 rows 121 and 100.
+constexpr int64_t kStreamRows = 16, kStreamRowsExperts = 6;
 
 Plan make_plan(const proj_w4_ctx* h, int64_t m, bool experts) {
   const W4Params& p = h->p;
   Plan pl = {};
   const int64_t rows = experts ? (m + p.E - 1) / p.E : m;
-  pl.tc = rows > kStreamRows;
+  pl.tc = rows > (experts ? kStreamRowsExperts : kStreamRows);
   if (!pl.tc) {
     StreamShape& s = pl.stream;
     s.NT = rows <= 8 ? 1 : 2;

@@ -47,6 +47,7 @@ constexpr int kDecodeWarp = 12;  // first of 4 kGroups
 constexpr int kGroups = 3;
 constexpr int kThreads = 32 * (kDecodeWarp + 4 * kGroups);
 constexpr int kTmemCols = 512;
+constexpr int kTileTable = 1024;  // token tiles of experts that are looked up
 
 // A step is 128 columns (two units): one hand-off each between the producers,
 // the decode warps and the MMA warp, whose loops cost more than the work of
@@ -58,9 +59,15 @@ template <int TN>
 struct Cfg {
   static constexpr int kHalf = TN * 128;          // x of one unit
   static constexpr int kStage = 2 * kHalf;
-  // x in shared memory: its copies take about a microsecond from L2, so few
-  // tokens want many stages
-  static constexpr int S = TN == 64 ? 8 : TN == 128 ? 4 : 3;
+  // Few tokens: the decode warps copy x too, 16 bytes at a time and only the
+  // tile's own rows, in the same stages as their A.  A tensor copy costs an
+  // SM's copy engine some 75 ns per 32 rows of 64 columns, needed or not, and
+  // the warp that issues it a round of waits per step: with it, tiles of a
+  // dozen rows (the experts' down product of 1000 tokens) waited for x in
+  // every step.
+  static constexpr bool kRowCopies = TN == 64;
+  // x in shared memory
+  static constexpr int S = TN == 64 ? 6 : TN == 128 ? 4 : 3;
   static constexpr int SA = TN == 64 ? 6 : 3;     // A in tensor memory, 64 columns each
   static constexpr int SW = TN <= 128 ? 6 : 3;    // weights in shared memory
   // The decode groups take the steps in turn, and each waits for every phase
@@ -74,7 +81,9 @@ struct Cfg {
   // rings, barriers, tensor-memory address, and for experts (TN = 128) the
   // tile and row tables
   static constexpr int kTables = kBarsAt + kBars * 8 + 16;
-  static constexpr int kSmem = 1024 + kTables + (TN <= 128 ? (3 * kW4MaxExperts + 1) * 4 : 0);
+  static constexpr int kSmem =
+      1024 + kTables + (TN <= 128 ? (3 * kW4MaxExperts + 4) * 4 + kTileTable * 8 : 0);
+  static_assert(!kRowCopies || S == SA, "x and A share their stages");
   static_assert(kACol + 64 * SA <= kTmemCols && TN * 512 <= kRing && kSmem <= 232448, "stages");
 };
 
@@ -109,6 +118,12 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
       : "memory");
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// 16 bytes, of which `bytes` are read and the rest zeros.
+__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
 }
 
 __device__ __forceinline__ uint2 ld_shared_u2(uint32_t addr) {
@@ -178,6 +193,7 @@ struct Items {
   const int* pre;   // [E + 1] tiles before each expert (null: one matrix)
   const int* off;   // [E] first row
   const int* end;   // [E] row behind the last
+  const int2* tile;  // by token tile: first row, expert << 9 | rows; or null: too many
   int tt, rt, step_t, step_r, RT, m;
   int e;
   __device__ __forceinline__ void begin(int first, int step) {
@@ -199,7 +215,12 @@ struct Items {
   __device__ __forceinline__ Item get() {
     Item it;
     it.rt = rt;
-    if (pre) {
+    if (tile) {
+      const int2 v = tile[tt];
+      it.row0 = v.x;
+      it.rows = v.y & 511;
+      it.expert = v.y >> 9;
+    } else if (pre) {
       while (pre[e + 1] <= tt) ++e;
       it.expert = e;
       it.row0 = off[e] + (tt - pre[e]) * TN;
@@ -227,6 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* s_pre = reinterpret_cast<int*>(smem + F::kTables);
   int* s_off = s_pre + kW4MaxExperts + 1;
   int* s_end = s_off + kW4MaxExperts;
+  int2* s_tile = reinterpret_cast<int2*>(s_end + kW4MaxExperts + 3);  // 8-byte aligned
   __shared__ int s_warp[kThreads / 32];
 
   const uint32_t ring = smem_u32(smem), wring = ring + F::kRing;
@@ -247,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(xempty + 8 * s, 1);
     }
     for (int s = 0; s < SA; ++s) {
-      mbar_init(afull + 8 * s, 4);
+      mbar_init(afull + 8 * s, 4);  // decode warps
       mbar_init(aempty + 8 * s, 1);
     }
     for (int s = 0; s < SW; ++s) {
@@ -260,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(turn + 8 * s, 1);
     }
     fence_mbar_init();
-    prefetch_tmap(&tmap_x);
+    if (!F::kRowCopies) prefetch_tmap(&tmap_x);
   }
 
   Items items;
@@ -305,6 +327,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int e = threadIdx.x * kPer + i;
       if (e < p.E) {
         s_pre[e] = before;
+        for (int k = 0; k < tiles[i] && before + k < kTileTable; ++k)
+          s_tile[before + k] =
+              make_int2(s_off[e] + k * TN, e << 9 | min(TN, s_end[e] - s_off[e] - k * TN));
         before += tiles[i];
         if (e == p.E - 1) s_pre[p.E] = before;
       }
@@ -313,12 +338,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     items.pre = s_pre;
     items.off = s_off;
     items.end = s_end;
+    items.tile = s_pre[p.E] <= kTileTable ? s_tile : nullptr;
     all_items = s_pre[p.E] * items.RT;
   } else {
     __syncthreads();  // the barriers are initialised
     items.pre = nullptr;
     items.off = nullptr;
     items.end = nullptr;
+    items.tile = nullptr;
     all_items = (items.m + TN - 1) / TN * items.RT;
   }
   const int n_items = first < all_items ? (all_items - first + step - 1) / step : 0;
@@ -334,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     named_bar_sync(1, kThreads);
     int st = 0;
     uint32_t phase = 0;
-    bool ok = true;
+    bool ok = !F::kRowCopies;
     for (int n = 0; n < n_items && ok; ++n, items.next()) {
       const Item im = items.get<TN>();
       const int boxes = (im.rows + box - 1) / box;
@@ -360,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // Every copy issued has to land before its buffer goes to other use: wait
     // until the MMAs have released each stage.
-    for (int j = 0; j < S; ++j) {
+    for (int j = 0; j < S && !F::kRowCopies; ++j) {
       wait_bar(xempty + 8 * st, phase ^ 1u, p.status, kStatusTimeoutDrain);
       if (++st == S) {
         st = 0;
@@ -403,8 +430,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int step = 0; step < steps; ++step, ++it) {
         const int st = it % S, sa = it % SA;
         ok = __all_sync(0xFFFFFFFFu, ok &&
-                            wait_bar(xfull + 8 * st, static_cast<uint32_t>((it / S) & 1), p.status,
-                                     kStatusTimeoutMma) &&
+                            (F::kRowCopies ||
+                             wait_bar(xfull + 8 * st, static_cast<uint32_t>((it / S) & 1),
+                                      p.status, kStatusTimeoutMma)) &&
                             wait_bar(afull + 8 * sa, static_cast<uint32_t>((it / SA) & 1), p.status,
                                      kStatusTimeoutMma));
         if (!ok) break;
@@ -420,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; k < 4; ++k)
               mma_ts(d, a + 32 + 8 * k, b + (F::kHalf >> 4) + 2 * k, idesc, 1u);
           }
-          tc_commit(xempty + 8 * st);
+          if (!F::kRowCopies) tc_commit(xempty + 8 * st);
           tc_commit(aempty + 8 * sa);
           if (step == steps - 1) {
             tc_commit(accf + 8 * set);
@@ -531,13 +559,41 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int q = warp & 3;
     const int g = lane >> 2;
     const int total = n_items * steps;
+    if (F::kRowCopies) griddep_wait();  // these warps read x
     named_bar_sync(1, kThreads);
     tc_fence_after();
     const uint32_t a0 = *tmem_slot + (static_cast<uint32_t>(32 * q) << 16) + F::kACol;
     int step = gi;  // within the item
-    while (step >= steps) step -= steps;
+    while (step >= steps) {
+      step -= steps;
+      items.next();
+    }
+    Item im = {};
+    if (F::kRowCopies && gi < total) im = items.get<TN>();
+    // x: of the two units' 16 pieces of a row the (thread % 16)th, of every
+    // eighth row; what K cuts off is filled with zeros
+    const int piece = threadIdx.x & 15;
+    const int r0 = static_cast<int>(threadIdx.x - 32 * kDecodeWarp) % 128 / 16;
     for (int it = gi; it < total; it += kGroups) {
       const int sa = it % SA, sw = it % SW;
+      if constexpr (F::kRowCopies) {
+        if (!wait_bar(aempty + 8 * sa, static_cast<uint32_t>((it / SA) & 1) ^ 1u, p.status,
+                      kStatusTimeoutDecode))
+          break;
+        const int unit = kb0 + 2 * step + (piece >> 3);
+        const int col = unit * 64 + (piece & 7) * 8;
+        const int bytes = min(16, max(0, 2 * (p.K - col)));
+        const char* from = static_cast<const char*>(p.x) +
+                           2 * ((static_cast<int64_t>(im.row0) + r0) * p.ldx + (bytes ? col : 0));
+        const uint32_t to = ring + sa * F::kStage + (piece >> 3) * F::kHalf;
+        if (unit < kb1) {
+          // rows 8 apart sit alike in the swizzle
+          const uint32_t swizzled = to + r0 * 128 + (((piece ^ r0) & 7) << 4);
+          for (int i = 0; i < im.rows - r0; i += 8, from += 16 * p.ldx)
+            cp_async16_zfill(swizzled + i * 128, from, bytes);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      }
       if (!wait_bar(wfull + 8 * sw, static_cast<uint32_t>((it / SW) & 1), p.status,
                     kStatusTimeoutDecode))
         break;
@@ -569,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               ze[j][0] = ze[j][1] = ld_shared_u16(src + kCodeBytes + kScaleBytes + 2 * at);
           }
         }
-        if (u == 0) {
+        if (u == 0 && !F::kRowCopies) {
           ok = wait_bar(aempty + 8 * sa, static_cast<uint32_t>((it / SA) & 1) ^ 1u, p.status,
                         kStatusTimeoutDecode);
           tc_fence_after();
@@ -593,6 +649,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       tmem_st_wait();
+      if constexpr (F::kRowCopies) {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        fence_proxy_async_smem();
+      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -601,7 +661,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       step += kGroups;
-      while (step >= steps) step -= steps;
+      if (step >= steps) {
+        do {
+          step -= steps;
+          items.next();
+        } while (step >= steps);
+        if (F::kRowCopies && it + kGroups < total) im = items.get<TN>();
+      }
     }
   }
   __syncwarp();
@@ -705,12 +771,13 @@ cudaError_t launch_any(int tn, const CUtensorMap& map, const W4Params& p, int gr
 
 cudaError_t w4_tc_launch(bool fp16, int tn, const W4Params& p, int64_t grid, int C,
                          cudaStream_t s) {
-  CUtensorMap map;
+  CUtensorMap map = {};
   // An expert's rows are few: boxes of 32 keep the rows behind them out.  One
   // matrix has whole tiles, and a copy's issue costs more than its rows.
   int box = 32;
   while (!p.offsets && box < tn && box < p.m) box *= 2;
-  if (!make_rows_map(&map, p.x, p.m, p.K, p.ldx, fp16, box)) return cudaErrorInvalidValue;
+  if (tn != 64 && !make_rows_map(&map, p.x, p.m, p.K, p.ldx, fp16, box))
+    return cudaErrorInvalidValue;
   const int n = static_cast<int>(grid);
   return fp16 ? launch_any<__half>(tn, map, p, n, C, box, s)
               : launch_any<__nv_bfloat16>(tn, map, p, n, C, box, s);

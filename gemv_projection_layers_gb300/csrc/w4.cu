@@ -452,14 +452,18 @@ struct Plan {
 // are streamed with exact 4-bit products; above, the tensor-core kernel.
 // Measured: 4096 x 8192 at 16 rows 13.1 us streamed, 14.4 on the tensor cores,
 // at 17 rows 17.8 and 14.4; 60 experts of 2048 x 4096, 4.3 rows each, 88 us
-// and 99, at 8.5 rows 121 and 100.
+// and 99, at 8.5 rows 121 and 100.  Experts with fewer units of K than
+// kStreamUnits keep a streaming CTA too short for what it takes to start: 104
+// experts of 8192 x 512 take 204 us streamed and 76 on the tensor cores, whose
+// CTAs stay; of 2048 x 4096 both take 83 us.
 constexpr int64_t kStreamRows = 16, kStreamRowsExperts = 6;
+constexpr int kStreamUnits = 64;
 
 Plan make_plan(const proj_w4_ctx* h, int64_t m, bool experts) {
   const W4Params& p = h->p;
   Plan pl = {};
   const int64_t rows = experts ? (m + p.E - 1) / p.E : m;
-  pl.tc = rows > (experts ? kStreamRowsExperts : kStreamRows);
+  pl.tc = p.E > 1 ? rows > kStreamRowsExperts || p.KU < kStreamUnits : rows > kStreamRows;
   if (!pl.tc) {
     StreamShape& s = pl.stream;
     s.NT = rows <= 8 ? 1 : 2;

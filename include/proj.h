@@ -436,8 +436,10 @@ int proj_gemv_static_status(proj_stream stream, uint32_t *code);
  * proj_w4_run_experts the same for rows sorted by expert.  Products are
  * summed in fp32 and rounded once, to the type of x.  Up to a few tokens per
  * matrix, s multiplies the fp32 sum of its group, so the 4-bit numbers enter
- * exactly; for many tokens s (q - z) is first rounded to the type of x, as in
- * a checkpoint that was dequantised to it (proj_w4_describe says which).
+ * exactly.  For more (and for experts with K below 4096) s (q - z) is first
+ * rounded to the type of x, as in a checkpoint that was dequantised to it; it
+ * then has to lie in that type's range.  proj_w4_describe says which of the
+ * two a call does.
  */
 typedef struct proj_w4_ctx *proj_w4_handle;
 

@@ -277,3 +277,61 @@ def test_refusals_before_any_device_call():
     lib.proj_w4_destroy(None)
     with pytest.raises(B.ProjError):
         B.proj_w4_run(0, 16, 64, 1, 16, 16)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,group,zeros,N,K", [("bf16", 128, False, 40, 4200), ("fp16", 32, True, 70, 4096), ("bf16", 64, True, 33, 5001)])
+@pytest.mark.parametrize("counts", [[1], [0, 3, 0, 9, 1, 17, 0], [2, 2, 2, 0, 0, 6], [70, 1, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0]])
+def test_experts_of_long_rows(counts, dtype, group, zeros, N, K):
+    """K long enough that few rows are streamed; some experts have several tiles all the same."""
+    E, m = len(counts), sum(counts)
+    with Weights(E, N, K, group, zeros, dtype, E) as w:
+        x, ld = make_x(m, K, dtype, E)
+        off = offsets_of(counts)
+        out = torch.full((m + 1, N), -7.0, device="cuda", dtype=x.dtype)
+        B.proj_w4_run_experts(w.h, x, ld, m, off, out, N)
+        torch.cuda.synchronize()
+        assert (out[m:] == -7.0).all()
+        o = off.tolist()
+        for e in range(E):
+            if o[e] < o[e + 1]:
+                rows = slice(o[e], o[e + 1])
+                assert_close(out[rows], x[rows, :K].double(), w.w64(e), dtype, is_exact(w.h, m), K)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("counts", [[40000] + [1, 0] * 511 + [3], [70000, 0, 1, 75000]])
+def test_experts_with_more_token_tiles_than_the_table_holds(counts):
+    E, m, N, K = len(counts), sum(counts), 17, 96
+    with Weights(E, N, K, 32, False, "bf16", 6) as w:
+        x, ld = make_x(m, K, "bf16", 6)
+        off = offsets_of(counts)
+        out = torch.full((m, N), -7.0, device="cuda", dtype=x.dtype)
+        B.proj_w4_run_experts(w.h, x, ld, m, off, out, N)
+        torch.cuda.synchronize()
+        o = off.tolist()
+        for e in [i for i in range(E) if counts[i] > 1] + [1, 3, 101]:
+            if e < E and o[e] < o[e + 1]:
+                rows = slice(o[e], o[e + 1])
+                assert_close(out[rows], x[rows, :K].double(), w.w64(e), "bf16", is_exact(w.h, m), K)
+
+
+@pytest.mark.gpu
+def test_dependent_calls_back_to_back():
+    """Each call's x is the call before's out, on one stream, across both kernels: the first loads that do not
+    wait for the kernel before are the weights' only."""
+    m, N = 40, 512
+    with Weights(1, N, N, 64, False, "bf16", 12) as a, Weights(1, N, N, 128, True, "bf16", 13) as b:
+        x = (torch.randn(m, N, device="cuda") * 0.1).bfloat16()
+        bufs = [torch.zeros(m, N, device="cuda", dtype=torch.bfloat16) for _ in range(4)]
+        for rows in (m, 8):  # tensor cores, streamed
+            for _ in range(5):
+                src = x
+                for i, w in enumerate((a, b, a, b)):
+                    B.proj_w4_run(w.h, src, N, rows, bufs[i], N)
+                    src = bufs[i]
+            torch.cuda.synchronize()
+            src = x
+            for i, w in enumerate((a, b, a, b)):
+                assert_close(bufs[i][:rows], src[:rows].double(), w.w64(0), "bf16", is_exact(w.h, rows), N)
+                src = bufs[i]

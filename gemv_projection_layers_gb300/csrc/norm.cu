@@ -99,19 +99,21 @@ struct Shape {
   static constexpr bool kRing = TPR >= 128 && TPR <= 512;  // rows come through shared memory
 };
 
-// Group j of a row in global memory; 0 beyond D.
+// Whether the row reaches group j of a thread (kVec: with all of it, or not at
+// all).  The groups that it does not reach are skipped by the callers of what
+// follows; of the others, elements beyond D are 0.
+template <typename S>
+__device__ __forceinline__ bool reaches(int j, int tid, int D) {
+  return S::kVec ? (j * S::TPR + tid) * S::E < D : j * S::E * S::TPR + tid < D;
+}
+
+// Group j of a row in global memory.
 template <typename S>
 __device__ __forceinline__ void load_global(const typename S::Type* row, int j, int tid, int D,
                                             float (&v)[S::E]) {
   using T = typename S::Type;
   if constexpr (S::kVec) {
-    const int c = (j * S::TPR + tid) * S::E;
-    if (c < D) {
-      widen(load_vec<T, S::E>(row + c), v);
-    } else {
-#pragma unroll
-      for (int i = 0; i < S::E; ++i) v[i] = 0.f;
-    }
+    widen(load_vec<T, S::E>(row + (j * S::TPR + tid) * S::E), v);
   } else {
     const int c0 = j * S::E * S::TPR + tid;
     if ((j + 1) * S::E * S::TPR <= D) {
@@ -145,14 +147,8 @@ __device__ __forceinline__ void load_shared(uint32_t row, int j, int tid, int D,
   using T = typename S::Type;
   constexpr int el = sizeof(T);
   if constexpr (S::kVec) {
-    const int c = (j * S::TPR + tid) * S::E;
-    if (c < D) {
-      const uint4 b = ld_shared_u4(row + c * el);
-      widen(*reinterpret_cast<const Vec<T, S::E>*>(&b), v);
-    } else {
-#pragma unroll
-      for (int i = 0; i < S::E; ++i) v[i] = 0.f;
-    }
+    const uint4 b = ld_shared_u4(row + (j * S::TPR + tid) * S::E * el);
+    widen(*reinterpret_cast<const Vec<T, S::E>*>(&b), v);
   } else {
     const int c0 = j * S::E * S::TPR + tid;
     if ((j + 1) * S::E * S::TPR <= D) {
@@ -171,8 +167,7 @@ __device__ __forceinline__ void store_global(typename S::Type* row, int j, int t
                                              const float (&v)[S::E]) {
   using T = typename S::Type;
   if constexpr (S::kVec) {
-    const int c = (j * S::TPR + tid) * S::E;
-    if (c < D) store_vec<T, S::E>(row + c, v);
+    store_vec<T, S::E>(row + (j * S::TPR + tid) * S::E, v);
   } else {
     const int c0 = j * S::E * S::TPR + tid;
     if ((j + 1) * S::E * S::TPR <= D) {
@@ -312,6 +307,7 @@ __global__ void __launch_bounds__(S::kThreads)
       float s[1] = {0.f};
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
+        if (!reaches<S>(j, tid, D)) break;
         float v[E];
         rows.load(1, row, stage, j, tid, v);
 #pragma unroll
@@ -328,6 +324,7 @@ __global__ void __launch_bounds__(S::kThreads)
     float s[1] = {0.f};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
+      if (!reaches<S>(j, tid, D)) break;
       rows.load(0, row, stage, j, tid, u[j]);
 #pragma unroll
       for (int i = 0; i < E; ++i) u[j][i] *= a.alpha;
@@ -365,6 +362,7 @@ __global__ void __launch_bounds__(S::kThreads)
     if (!a.normed) return;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
+      if (!reaches<S>(j, tid, D)) break;
       if (a.w_pre) {
         float w[E];
         load_global<S>(static_cast<const T*>(a.w_pre), j, tid, D, w);
@@ -502,6 +500,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kThreads < 512 ? 512 / S::kThr
     F2 s2x[3] = {zero, zero, zero};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
+      if (!reaches<S>(j, tid, D)) break;
       if (g_vec) {
         float v[E];
         if (a.gate_mode == PROJ_GATE_ELEMENT)
@@ -539,6 +538,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kThreads < 512 ? 512 / S::kThr
       static_cast<T*>(a.dgate)[row] = from_f32<T>(ab * act_slope(g_row, a.gate_act));
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
+      if (!reaches<S>(j, tid, D)) break;
       group(j, g[j]);
       F2 o[H];
       float out[E];

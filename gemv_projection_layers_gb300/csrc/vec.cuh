@@ -64,10 +64,27 @@ __device__ __forceinline__ void store_vec(T* p, const float (&v)[V]) {
   }
 }
 
+// The two values of a word, the low half first: one instruction each.
+__device__ __forceinline__ void widen2(uint32_t w, float& x, float& y, __nv_bfloat16) {
+  x = __uint_as_float(w << 16);
+  y = __uint_as_float(w & 0xFFFF0000u);
+}
+__device__ __forceinline__ void widen2(uint32_t w, float& x, float& y, __half) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  x = f.x;
+  y = f.y;
+}
+
 template <typename T, int V>
 __device__ __forceinline__ void widen(const Vec<T, V>& a, float (&v)[V]) {
+  if constexpr (sizeof(T) == 2 && V >= 2) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&a);
 #pragma unroll
-  for (int i = 0; i < V; ++i) v[i] = to_f32(a.e[i]);
+    for (int i = 0; i < V / 2; ++i) widen2(w[i], v[2 * i], v[2 * i + 1], T());
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = to_f32(a.e[i]);
+  }
 }
 
 // A pair of fp32 that one instruction multiplies and adds.

@@ -27,10 +27,11 @@ struct W4Params {
   int RT;   // tiles of 128 rows
   int KU;   // units of 64 columns
   int NGp;  // groups per row block in the packed scales
-  int upg;        // units per group (group / 64; 0 for groups of 32)
-  int upg_shift;  // its logarithm, -1 where it is no power of two
-  __host__ __device__ int group_of(int u) const {  // groups of 64 columns or more
-    return upg_shift >= 0 ? u >> upg_shift : u / upg;
+  // Units per group d = group / 64 as ceil(2^32 / d), 0 for d = 1: exact
+  // quotients while u and d are at most 2^14, without a division.
+  uint32_t group_magic;
+  __device__ int group_of(int u) const {  // groups of 64 columns or more
+    return group_magic ? static_cast<int>(__umulhi(static_cast<uint32_t>(u), group_magic)) : u;
   }
 };
 

@@ -7,9 +7,11 @@
 // equal experts comes from a match over the warp; per expert, chunk counts are
 // summed over the chunks before it, block counts (the workspace table, [block]
 // [expert]) over the blocks before it, and totals over the experts before it.
-// All of it is whole-number arithmetic in a fixed order: no atomics, stable.
+// All of it is whole-number arithmetic, stable and the same on every call (the
+// shared atomic additions are of whole numbers, whose order does not matter).
 // One block: one launch does everything.  More: a first launch chooses and
-// counts, a second places.
+// counts, a second places.  (4096 tokens, 8 of 256 experts: 11 and 13 us; the
+// choice is bound by its instructions, some 970 a token and warp.)
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -326,7 +328,10 @@ __device__ __forceinline__ bool is_slot(int s, int64_t rows) { return s >= 0 && 
 // Rows are read and written V elements at a time, as wide as every row's
 // alignment allows (16, 8 or 4 bytes, or single elements for an odd width);
 // a thread has U of them under way, so that narrow accesses keep about as
-// many bytes in flight as wide ones.
+// many bytes in flight as wide ones.  All of this is bound by HBM.  (Gather of
+// 4096 x 8 rows of 8192 bf16: 86 us, 7.0 TB/s; of 2000 x 6 rows of 5001: 33 us,
+// 4.2 TB/s.  Gradient of the combine, 1000 tokens x 6 of 4100 fp16: 29 us, 3.6
+// TB/s.)
 template <typename T, int V>
 constexpr int kAhead = 16 / (V * static_cast<int>(sizeof(T))) < 8
                            ? 16 / (V * static_cast<int>(sizeof(T)))
@@ -819,6 +824,7 @@ const char* refuse_rows(const RowsParams& p, int64_t k, int dtype, int* status) 
   *status = PROJ_EUNSUPPORTED;
   if (k > kMaxK) return "k > 32";
   if (p.m >= (int64_t{1} << 31) / k) return "m * k >= 2^31";
+  if (p.D > (int64_t{1} << 30)) return "D > 2^30";
   const int el = dtype == PROJ_FP32 ? 4 : 2;
   *status = PROJ_EALIGN;
   if (!aligned_to(p.a, el) || !aligned_to(p.b, el) || !aligned_to(p.out, el) ||

@@ -452,7 +452,9 @@ typedef struct proj_w4_ctx *proj_w4_handle;
  *   zeros  : the same shape in bytes (the low four bits count), or NULL: all 8.
  *   group  : columns per scale: 32 or a multiple of 64.
  *   dtype  : PROJ_BF16 or PROJ_FP16, the type of x, scales and out.
- * 1 <= E <= 1024, 1 <= N, K <= 2^20.  Returns NULL on error (*status, if
+ * 1 <= E <= 1024, 1 <= N, K <= 2^20.  A handle holds the packed weights and a
+ * status word, nothing else of a call: calls on several streams may overlap.
+ * Returns NULL on error (*status, if
  * non-NULL, and proj_last_status() say why).
  */
 proj_w4_handle proj_w4_prepare(const void *codes, const void *scales, const void *zeros,
@@ -493,7 +495,7 @@ void proj_w4_destroy(proj_w4_handle h);
  * Tokens sorted by expert and back.  m tokens each choose k of E experts;
  * entry (t, j) is token t's j-th choice, flat index t k + j.  The sort is
  * stable: rows of one expert stand in the order of their flat indices.
- * 1 <= E <= 1024, 1 <= k <= min(E, 32), m * k < 2^31.
+ * 1 <= E <= 1024, 1 <= k <= min(E, 32), m * k < 2^31, D <= 2^30.
  */
 enum proj_route_mode {
     PROJ_ROUTE_CHOSEN = 0, /* weights: softmax over the chosen logits */

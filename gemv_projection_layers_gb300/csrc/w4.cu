@@ -297,7 +297,6 @@ __global__ void __launch_bounds__(32 * kStreamWarps, kD == 2 && NT == 1 ? 3 : 2)
 #pragma unroll
   for (int d = 0; d < kD; ++d) fetch_x(d, d, u0 + d);
 
-  const uint32_t power = power_pair<T>();
   float acc[RB][NT][4] = {};
   for (int ub = u0; ub < u1; ub += kD) {
 #pragma unroll
@@ -319,10 +318,10 @@ __global__ void __launch_bounds__(32 * kStreamWarps, kD == 2 && NT == 1 ? 3 : 2)
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
               // rows g, g + 8 of the step's columns 4 t, + 1, then of + 2, + 3
-              const uint32_t a[4] = {code_pair<T>(word[2 * h], 2 * s, zero[0], power),
-                                     code_pair<T>(word[2 * h + 1], 2 * s, zero[1], power),
-                                     code_pair<T>(word[2 * h], 2 * s + 1, zero[0], power),
-                                     code_pair<T>(word[2 * h + 1], 2 * s + 1, zero[1], power)};
+              const uint32_t a[4] = {code_pair<T>(word[2 * h], 2 * s, zero[0]),
+                                     code_pair<T>(word[2 * h + 1], 2 * s, zero[1]),
+                                     code_pair<T>(word[2 * h], 2 * s + 1, zero[0]),
+                                     code_pair<T>(word[2 * h + 1], 2 * s + 1, zero[1])};
 #pragma unroll
               for (int j = 0; j < NT; ++j) {
                 const uint2 b = xf[d][j][2 * h + s];
@@ -568,7 +567,7 @@ extern "C" proj_w4_handle proj_w4_prepare(const void* codes, const void* scales,
   p.KU = static_cast<int>((K + 63) / 64);
   const int64_t NG = (K + group - 1) / group;
   const uint64_t upg = static_cast<uint64_t>(group) / 64;
-  p.group_magic = upg > 1 ? static_cast<uint32_t>(((uint64_t{1} << 32) + upg - 1) / upg) : 0u;
+  p.group_magic = upg ? static_cast<uint32_t>(((uint64_t{1} << 31) + upg - 1) / upg) : 0u;
   h->sms = proj_num_sms();
   for (int c = 1; c <= 8; ++c) h->clusters[c] = w4_tc_max_clusters(c);
   p.NGp = static_cast<int>(group == 32 ? 2 * p.KU : NG);  // every unit has its groups

@@ -27,11 +27,11 @@ struct W4Params {
   int RT;   // tiles of 128 rows
   int KU;   // units of 64 columns
   int NGp;  // groups per row block in the packed scales
-  // Units per group d = group / 64 as ceil(2^32 / d), 0 for d = 1: exact
-  // quotients while u and d are at most 2^14, without a division.
+  // ceil(2^31 / d) for the d = group / 64 units of a group: exact quotients
+  // while u and d are at most 2^14, without a division.
   uint32_t group_magic;
   __device__ int group_of(int u) const {  // groups of 64 columns or more
-    return group_magic ? static_cast<int>(__umulhi(static_cast<uint32_t>(u), group_magic)) : u;
+    return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(u)) * group_magic) >> 31);
   }
 };
 

@@ -82,18 +82,9 @@ __device__ __forceinline__ uint32_t zero_pair(uint32_t zeros, int which) {
 }
 
 // Columns 2 i and 2 i + 1 of a packed word as the pair q - z.
-// `power` comes from power_pair(): a register that the compiler cannot take
-// for a constant, so that mask and power are one three-input operation.
 template <typename T>
-__device__ __forceinline__ uint32_t code_pair(uint32_t word, int i, uint32_t zero,
-                                              uint32_t power) {
-  return Num<T>::sub(((word >> (4 * i)) & 0x000F000Fu) | power, zero);
-}
-template <typename T>
-__device__ __forceinline__ uint32_t power_pair() {
-  uint32_t p;
-  asm volatile("mov.b32 %0, %1;" : "=r"(p) : "n"(Num<T>::kPower * 0x10001u));
-  return p;
+__device__ __forceinline__ uint32_t code_pair(uint32_t word, int i, uint32_t zero) {
+  return Num<T>::sub(((word >> (4 * i)) & 0x000F000Fu) | (Num<T>::kPower * 0x10001u), zero);
 }
 
 // What a lane loads of the scales and zeros of a unit of 64 columns: one pair

@@ -569,7 +569,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (F::kRowCopies) griddep_wait();  // these warps read x
     named_bar_sync(1, kThreads);
     tc_fence_after();
-    const uint32_t power = power_pair<T>();
     const uint32_t a0 = *tmem_slot + (static_cast<uint32_t>(32 * q) << 16) + F::kACol;
     int step = gi;  // within the item
     while (step >= steps) {
@@ -651,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int i = 0; i < 4; ++i)
                 r[(2 * h + (i >> 1)) * 4 + 2 * hi + (i & 1)] =
-                    Num<T>::mul(code_pair<T>(word[2 * h + hi], i, zero, power), s);
+                    Num<T>::mul(code_pair<T>(word[2 * h + hi], i, zero), s);
             }
           tmem_st_16x256b_x4(a0 + (static_cast<uint32_t>(16 * j) << 16) + sa * 64 + 32 * u, r);
         }

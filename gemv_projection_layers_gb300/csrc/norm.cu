@@ -28,9 +28,8 @@
 // bound it: 315 us for the kernel, 3.4 TB/s.
 //
 // Rows that do not start on 16 bytes (an odd D, say) keep their misalignment
-// in shared memory: whole 16-byte pieces are copied as such, the elements at
-// the two ends one by one, and the threads read and write single elements,
-// neighbours side by side.
+// in shared memory, where the 16-byte words that hold them go, and the threads
+// read and write single elements, neighbours side by side.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -97,7 +96,7 @@ struct Shape {
   using Type = T;
   static constexpr bool kVec = kVec_;
   static constexpr int TPR = TPR_, NV = NV_;
-  static constexpr int E = kVec ? kFullVec<T> : 8;
+  static constexpr int E = kVec ? kFullVec<T> : 4;
   static constexpr int kRows = TPR < 128 ? 128 / TPR : 1;  // rows of a CTA at a time
   static constexpr int kThreads = TPR < 128 ? 128 : TPR;
   static constexpr bool kRing = TPR >= 128 && TPR <= 512;  // rows come through shared memory
@@ -192,6 +191,7 @@ struct Rows {
   const T* base[NT];  // null: not there
   int64_t ld[NT];
   uint8_t* smem;
+  int64_t m;
   int D, slot, stages;  // bytes of a row's place, stages of NT places
 
   __device__ __forceinline__ static int skew(const T* p) {
@@ -216,29 +216,54 @@ struct Rows {
           if (c < D) cp_async16(to + c * static_cast<int>(sizeof(T)), src + c);
         }
       } else {
+        // The 16-byte words that hold the row.  Those at its ends may hold
+        // elements of other rows, or between them, which nobody uses; words
+        // that reach out of the tensor go element by element.
         constexpr int el = sizeof(T);
+        const char* const begin = reinterpret_cast<const char*>(base[k]);
+        const char* const end = reinterpret_cast<const char*>(base[k] + (m - 1) * ld[k] + D);
+        const char* const row_begin = reinterpret_cast<const char*>(src);
+        const char* const row_end = row_begin + D * el;
         const int off = skew(src);
-        const int head = min(D, off ? (16 - off) / el : 0);
-        const int pieces = (D - head) * el / 16;
-        const int tail = D - head - pieces * (16 / el);
-        const uint32_t to = smem_u32(dst) + off;
-        for (int i = tid; i < pieces; i += S::TPR)
-          cp_async16(to + head * el + 16 * i, src + head + i * (16 / el));
-        T* const put = reinterpret_cast<T*>(dst + off);
-        if (tid < head) put[tid] = src[tid];
-        const int t = S::TPR - 1 - tid;
-        if (t < tail) put[D - 1 - t] = src[D - 1 - t];
+        const uint32_t to = smem_u32(dst);
+        const int words = (off + D * el + 15) / 16;
+        for (int i = tid; i < words; i += S::TPR) {
+          const char* const w = row_begin - off + 16 * i;
+          if (w >= begin && w + 16 <= end) {
+            cp_async16(to + 16 * i, w);
+          } else {
+            for (int e = 0; e < 16; e += el)
+              if (w + e >= row_begin && w + e < row_end)
+                *reinterpret_cast<T*>(dst + 16 * i + e) = *reinterpret_cast<const T*>(w + e);
+          }
+        }
       }
     }
   }
-  // Group j of tensor k of the row at hand.
-  __device__ __forceinline__ void load(int k, int64_t row, int stage, int j, int tid,
-                                       float (&v)[S::E]) const {
-    const T* src = base[k] + row * ld[k];
+};
+
+// The tensors of the row at hand: where they stand.
+template <typename S, int NT>
+struct Row {
+  using T = typename S::Type;
+  const T* global[NT];
+  uint32_t shared[NT];
+  int D, tid;
+
+  __device__ __forceinline__ Row(const Rows<S, NT>& rows, int64_t row, int stage, int tid_)
+      : D(rows.D), tid(tid_) {
+#pragma unroll
+    for (int k = 0; k < NT; ++k) {
+      global[k] = rows.base[k] + row * rows.ld[k];
+      shared[k] = smem_u32(rows.place(stage, k)) + Rows<S, NT>::skew(global[k]);
+    }
+  }
+  // Group j of tensor k.
+  __device__ __forceinline__ void load(int k, int j, float (&v)[S::E]) const {
     if constexpr (!S::kRing)
-      load_global<S>(src, j, tid, D, v);
+      load_global<S>(global[k], j, tid, D, v);
     else
-      load_shared<S>(smem_u32(place(stage, k)) + skew(src), j, tid, D, v);
+      load_shared<S>(shared[k], j, tid, D, v);
   }
 };
 
@@ -299,6 +324,7 @@ __global__ void __launch_bounds__(S::kThreads)
   rows.base[2] = a.gate_mode == PROJ_GATE_ELEMENT ? static_cast<const T*>(a.gate) : nullptr;
   rows.ld[2] = a.ldg;
   rows.smem = smem;
+  rows.m = a.m;
   rows.D = D;
   rows.slot = slot;
   rows.stages = stages;
@@ -306,6 +332,7 @@ __global__ void __launch_bounds__(S::kThreads)
 
   over_rows<S>(rows, a.m, first, static_cast<int64_t>(gridDim.x) * S::kRows, tid,
                [&](int64_t row, int stage) {
+    const Row<S, 3> at(rows, row, stage, tid);
     float rp = 1.f;
     if (a.y && !a.y_plain) {
       float s[1] = {0.f};
@@ -313,7 +340,7 @@ __global__ void __launch_bounds__(S::kThreads)
       for (int j = 0; j < NV; ++j) {
         if (!reaches<S>(j, tid, D)) break;
         float v[E];
-        rows.load(1, row, stage, j, tid, v);
+        at.load(1, j, v);
 #pragma unroll
         for (int i = 0; i < E; ++i) s[0] = fmaf(v[i], v[i], s[0]);
       }
@@ -329,12 +356,12 @@ __global__ void __launch_bounds__(S::kThreads)
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       if (!reaches<S>(j, tid, D)) break;
-      rows.load(0, row, stage, j, tid, u[j]);
+      at.load(0, j, u[j]);
 #pragma unroll
       for (int i = 0; i < E; ++i) u[j][i] *= a.alpha;
       if (a.y) {
         float n[E], w[E];
-        rows.load(1, row, stage, j, tid, n);
+        at.load(1, j, n);
 #pragma unroll
         for (int i = 0; i < E; ++i) n[i] *= rp;
         if (a.w_post) {
@@ -344,7 +371,7 @@ __global__ void __launch_bounds__(S::kThreads)
         }
         if (g_vec) {
           if (a.gate_mode == PROJ_GATE_ELEMENT)
-            rows.load(2, row, stage, j, tid, w);
+            at.load(2, j, w);
           else
             load_global<S>(static_cast<const T*>(a.gate), j, tid, D, w);
           act_all<T>(w, a.gate_act);
@@ -413,6 +440,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kThreads < 512 ? 512 / S::kThr
   rows.base[4] = static_cast<const T*>(a.dnormed);
   rows.ld[4] = a.lddn;
   rows.smem = smem;
+  rows.m = a.m;
   rows.D = D;
   rows.slot = slot;
   rows.stages = stages;
@@ -436,6 +464,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kThreads < 512 ? 512 / S::kThr
 
   over_rows<S>(rows, a.m, part_row, static_cast<int64_t>(gridDim.x) * S::kRows, tid,
                [&](int64_t row, int stage) {
+    const Row<S, 5> at(rows, row, stage, tid);
     const F2 rp = f2(rp_next);
     const float ru_row = ru_next;
     const F2 ru = f2(ru_row);
@@ -447,7 +476,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kThreads < 512 ? 512 / S::kThr
     F2 yn[H], n[H], un[H], dh[H], t[H], e[H], wpo[H];
     auto group = [&](int j, const F2 (&g)[H]) {
       float v[E];
-      rows.load(0, row, stage, j, tid, v);
+      at.load(0, j, v);
       pairs<E>(v, un);
 #pragma unroll
       for (int i = 0; i < H; ++i) un[i] = mul2(un[i], alpha);
@@ -459,7 +488,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kThreads < 512 ? 512 / S::kThr
         for (int i = 0; i < H; ++i) wpo[i] = one;
       }
       if (a.y) {
-        rows.load(1, row, stage, j, tid, v);
+        at.load(1, j, v);
         pairs<E>(v, yn);
 #pragma unroll
         for (int i = 0; i < H; ++i) {
@@ -472,14 +501,14 @@ __global__ void __launch_bounds__(S::kThreads, S::kThreads < 512 ? 512 / S::kThr
         for (int i = 0; i < H; ++i) yn[i] = n[i] = zero;
       }
       if (a.dout) {
-        rows.load(3, row, stage, j, tid, v);
+        at.load(3, j, v);
         pairs<E>(v, e);
       } else {
 #pragma unroll
         for (int i = 0; i < H; ++i) e[i] = zero;
       }
       if (a.dnormed) {
-        rows.load(4, row, stage, j, tid, v);
+        at.load(4, j, v);
         pairs<E>(v, dh);
         if (a.w_pre) {
           load_global<S>(static_cast<const T*>(a.w_pre), j, tid, D, v);
@@ -508,7 +537,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kThreads < 512 ? 512 / S::kThr
       if (g_vec) {
         float v[E];
         if (a.gate_mode == PROJ_GATE_ELEMENT)
-          rows.load(2, row, stage, j, tid, v);
+          at.load(2, j, v);
         else
           load_global<S>(static_cast<const T*>(a.gate), j, tid, D, v);
         act_all<T>(v, a.gate_act);
@@ -733,11 +762,11 @@ cudaError_t backward(const proj_norm_grad_args& a, cudaStream_t s) {
       if (n > 2048) return FN<Shape<T, true, 1024, 4>>(a, s);            \
     return FN<Shape<T, true, 1024, 2>>(a, s);                            \
   } else {                                                               \
-    if ((a).D <= 512) return FN<Shape<T, false, 32, 2>>(a, s);           \
-    if ((a).D <= 2048) return FN<Shape<T, false, 128, 2>>(a, s);         \
-    if ((a).D <= 4096) return FN<Shape<T, false, 256, 2>>(a, s);         \
-    if ((a).D <= 8192) return FN<Shape<T, false, 512, 2>>(a, s);         \
-    return FN<Shape<T, false, 1024, 2>>(a, s);                           \
+    if ((a).D <= 512) return FN<Shape<T, false, 32, 4>>(a, s);           \
+    if ((a).D <= 2048) return FN<Shape<T, false, 128, 4>>(a, s);         \
+    if ((a).D <= 4096) return FN<Shape<T, false, 256, 4>>(a, s);         \
+    if ((a).D <= 8192) return FN<Shape<T, false, 512, 4>>(a, s);         \
+    return FN<Shape<T, false, 1024, 4>>(a, s);                           \
   }
 
 template <typename T>

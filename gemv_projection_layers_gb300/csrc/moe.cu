@@ -365,63 +365,8 @@ __global__ void __launch_bounds__(kRowThreads) gather_kernel(const RowsParams p)
   }
 }
 
-// Single elements of 16 bits (an odd width): the rows' values go through
-// registers.
-template <typename T, int V>
-__global__ void __launch_bounds__(kRowThreads) combine_kernel(const RowsParams p) {
-  constexpr int U = kAhead<T, V>;
-  griddep_launch_dependents();
-  griddep_wait();
-  const int64_t t = blockIdx.x;
-  const int64_t nvec = p.D / V, rows = p.m * p.k;
-  const T* ys = static_cast<const T*>(p.a);
-  const int32_t* slot = p.slot + t * p.k;
-  const float* weight = p.weight ? p.weight + t * p.k : nullptr;
-  T* out = static_cast<T*>(p.out) + t * p.ldo;
-  for (int64_t v0 = static_cast<int64_t>(blockIdx.y) * kRowThreads * U + threadIdx.x; v0 < nvec;
-       v0 += static_cast<int64_t>(gridDim.y) * kRowThreads * U) {
-    float acc[U][V] = {};
-    for (int j0 = 0; j0 < p.k; j0 += 8) {
-      Vec<T, V> val[8][U];
-      float w[8];
-      bool ok[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int s = j0 + j < p.k ? __ldg(slot + j0 + j) : -1;
-        ok[j] = is_slot(s, rows);
-        if (ok[j]) {
-          w[j] = weight ? __ldg(weight + j0 + j) : 1.f;
-          const T* from = ys + s * p.lda + v0 * V;
-#pragma unroll
-          for (int u = 0; u < U; ++u)
-            if (v0 + u * kRowThreads < nvec) val[j][u] = load_vec<T, V>(from + u * kRowThreads * V);
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (ok[j]) {
-#pragma unroll
-          for (int u = 0; u < U; ++u) {
-            float f[V];
-            widen(val[j][u], f);
-#pragma unroll
-            for (int i = 0; i < V; ++i) acc[u][i] = fmaf(w[j], f[i], acc[u][i]);
-          }
-        }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (v0 + u * kRowThreads < nvec) store_vec<T, V>(out + (v0 + u * kRowThreads) * V, acc[u]);
-  }
-}
-
-template <int kBytes>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
-  if constexpr (kBytes == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(kBytes)
-                 : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
 // The slots and weights of eight entries of a token from j0 on (-1: no row).
@@ -440,37 +385,49 @@ struct Eight {
 };
 
 // The combine is bound by the loads of k rows per token from anywhere.  A CTA
-// takes pieces (token, columns, eight entries) in turn and has the rows of the
-// next kDeep - 1 on their way to shared memory, where a thread reads back what
-// it copied itself: no barriers, no registers held by loads in flight, and the
-// slots of a piece are read one piece before its copies start.
+// takes pieces (token, 4 KB of columns, eight entries) in turn and has the rows
+// of the next kDeep - 1 on their way to shared memory: no registers are held by
+// loads in flight, and the slots of a piece are read one piece before its copies
+// start.  (4096 tokens x 8 rows of 8192 bf16: 119 us, 289 with the rows loaded
+// to registers.)  Rows that start on 16 bytes, and end so (kUnit = 16): a
+// thread reads back what it copied itself, without barriers.  Any others keep
+// their misalignment in shared memory, where the 16-byte words that hold them
+// go -- with elements of neighbouring rows, which nobody uses, at the ends --
+// and threads read kUnit bytes, 4 or an element as the rows' alignment allows,
+// side by side and behind a barrier.  Words that reach out of ys go element by
+// element.  (2000 tokens x 6 rows of 5001 bf16: 68 us, 107 through registers.)
 constexpr int kDeep = 3;
-constexpr int kDeepBytes = kDeep * 8 * kRowThreads * 16;
+constexpr int kPieceBytes = kRowThreads * 16;
+constexpr int kPlace = kPieceBytes + 32;  // of a row's piece in shared memory
+constexpr int kDeepBytes = kDeep * 8 * kPlace;
 
-template <typename T, int V>
+template <typename T, int kUnit>
 __global__ void __launch_bounds__(kRowThreads, 2)
-    combine_deep_kernel(const RowsParams p, const int pieces_per_token) {
-  constexpr int U = kAhead<T, V>, kBytes = V * static_cast<int>(sizeof(T));
-  extern __shared__ __align__(16) uint8_t s_rows[];  // [kDeep][8][U][kRowThreads] of kBytes
+    combine_kernel(const RowsParams p, const int columns, const int width) {
+  constexpr int V = 16 / static_cast<int>(sizeof(T)), kCols = V * kRowThreads;
+  constexpr int el = sizeof(T);
+  constexpr bool kWhole = kUnit == 16;
+  constexpr int UE = kUnit / el, NU = V / UE;  // elements of a unit, units of a thread
+  extern __shared__ __align__(16) uint8_t s_rows[];  // [kDeep][8] of kPlace
   griddep_launch_dependents();
   griddep_wait();
-  const int nvec = static_cast<int>(p.D / V);
+  const int D = static_cast<int>(p.D), tid = threadIdx.x;
   const int64_t rows = p.m * p.k;
   const T* ys = static_cast<const T*>(p.a);
-  const int jgroups = (p.k + 7) / 8;  // the entries of a piece's token, eight at a time, fastest
-  const int columns = pieces_per_token / jgroups;
-  const int64_t total = p.m * columns;  // pieces but for the entries
-  const uint32_t mine = smem_u32(s_rows) + threadIdx.x * kBytes;
+  const char* const begin = reinterpret_cast<const char*>(ys);
+  const char* const end = reinterpret_cast<const char*>(ys + (rows - 1) * p.lda + p.D);
+  const int jgroups = (p.k + 7) / 8;  // a token's entries, eight at a time, are the fastest
+  const int64_t total = p.m * columns;
 
   struct At {
     int64_t t;
-    int col, j0;
+    int c0, j0;
   };
   auto where = [&](int64_t n) {  // this CTA's n-th piece
     const int64_t i = blockIdx.x + n / jgroups * gridDim.x;
     At at;
     at.t = i < total ? i / columns : -1;
-    at.col = static_cast<int>(i % columns) * kRowThreads * U + threadIdx.x;
+    at.c0 = static_cast<int>(i % columns) * width;
     at.j0 = static_cast<int>(n % jgroups) * 8;
     return at;
   };
@@ -479,12 +436,27 @@ __global__ void __launch_bounds__(kRowThreads, 2)
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       if (is_slot(s[j], rows)) {
-        const T* from = ys + s[j] * p.lda + static_cast<int64_t>(at.col) * V;
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-          if (at.col + u * kRowThreads < nvec)
-            cp_async<kBytes>(mine + ((stage * 8 + j) * U + u) * kRowThreads * kBytes,
-                             from + u * kRowThreads * V);
+        const T* from = ys + s[j] * p.lda + at.c0;
+        uint8_t* const place = s_rows + (stage * 8 + j) * kPlace;
+        if constexpr (kWhole) {
+          if (tid * V < min(width, D - at.c0))
+            cp_async16(smem_u32(place) + tid * 16, from + tid * V);
+        } else {
+          const char* const first = reinterpret_cast<const char*>(from);
+          const int off = static_cast<int>(reinterpret_cast<uintptr_t>(first) & 15);
+          const int bytes = min(width, D - at.c0) * el;
+          const int words = (off + bytes + 15) / 16;
+          for (int i = tid; i < words; i += kRowThreads) {
+            const char* const w = first - off + 16 * i;
+            if (w >= begin && w + 16 <= end) {
+              cp_async16(smem_u32(place) + 16 * i, w);
+            } else {
+              for (int e = 0; e < 16; e += el)
+                if (w + e >= first && w + e < first + bytes)
+                  *reinterpret_cast<T*>(place + 16 * i + e) = *reinterpret_cast<const T*>(w + e);
+            }
+          }
+        }
       }
   };
 
@@ -502,9 +474,12 @@ __global__ void __launch_bounds__(kRowThreads, 2)
     cur.slots(p, at.t, at.j0);
     cur.weights(p, at.t, at.j0);
   }
-  float acc[U][V] = {};
+  float acc[V] = {};
   int stage = 0;
   for (int64_t n = 0; at.t >= 0; ++n) {
+    const int wide = min(width, D - at.c0);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kDeep - 2) : "memory");
+    if (!kWhole) __syncthreads();  // the piece is there, and the one before has been read
     // start the piece kDeep - 1 ahead in the stage that the last one left
     start(next, ahead.s, stage == 0 ? kDeep - 1 : stage - 1);
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -516,30 +491,51 @@ __global__ void __launch_bounds__(kRowThreads, 2)
       then.slots(p, after.t, after.j0);
       then.weights(p, after.t, after.j0);
     }
-    asm volatile("cp.async.wait_group %0;" ::"n"(kDeep - 1) : "memory");
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       if (is_slot(cur.s[j], rows)) {
+        const uint8_t* const place = s_rows + (stage * 8 + j) * kPlace;
+        if constexpr (kWhole) {
+          if (tid * V < wide) {
+            float f[V];
+            widen(*reinterpret_cast<const Vec<T, V>*>(place + tid * 16), f);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          float f[V];
-          widen(*reinterpret_cast<const Vec<T, V>*>(
-                    s_rows + (static_cast<size_t>((stage * 8 + j) * U + u) * kRowThreads +
-                              threadIdx.x) * kBytes),
-                f);
+            for (int i = 0; i < V; ++i) acc[i] = fmaf(cur.w[j], f[i], acc[i]);
+          }
+        } else {
+          const T* const first = ys + cur.s[j] * p.lda + at.c0;
+          const uint8_t* const e = place + (reinterpret_cast<uintptr_t>(first) & 15);
 #pragma unroll
-          for (int i = 0; i < V; ++i) acc[u][i] = fmaf(cur.w[j], f[i], acc[u][i]);
+          for (int i = 0; i < NU; ++i) {
+            const int u = i * kRowThreads + tid;
+            if (u * UE < wide) {
+              float f[UE];
+              widen(*reinterpret_cast<const Vec<T, UE>*>(e + u * kUnit), f);
+#pragma unroll
+              for (int l = 0; l < UE; ++l)
+                acc[i * UE + l] = fmaf(cur.w[j], f[l], acc[i * UE + l]);
+            }
+          }
         }
       }
     if (at.j0 + 8 >= p.k) {
-      T* out = static_cast<T*>(p.out) + at.t * p.ldo;
+      T* out = static_cast<T*>(p.out) + at.t * p.ldo + at.c0;
+      if constexpr (kWhole) {
+        if (tid * V < wide) store_vec<T, V>(out + tid * V, acc);
+      } else {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (at.col + u * kRowThreads < nvec)
-          store_vec<T, V>(out + (at.col + u * kRowThreads) * V, acc[u]);
+        for (int i = 0; i < NU; ++i) {
+          const int u = i * kRowThreads + tid;
+          if (u * UE < wide) {
+            float f[UE];
 #pragma unroll
-        for (int i = 0; i < V; ++i) acc[u][i] = 0.f;
+            for (int l = 0; l < UE; ++l) f[l] = acc[i * UE + l];
+            store_vec<T, UE>(out + u * UE, f);
+          }
+        }
       }
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] = 0.f;
     }
     at = after;
     cur = then;
@@ -842,29 +838,27 @@ cudaError_t rows_launch(Op op, const RowsParams& p, cudaStream_t s) {
   const int64_t per = kRowThreads * kAhead<T, V>;
   const int64_t ny = op == Op::kGrad ? 1 : std::min<int64_t>(64, (nvec + per - 1) / per);
   cudaLaunchAttribute attr[1];
-  if constexpr (V * sizeof(T) >= 4) {
-    if (op == Op::kCombine) {
-      const int64_t columns = (nvec + per - 1) / per;
-      const int64_t jgroups = (p.k + 7) / 8;
-      static std::atomic<uint64_t> done{0};
-      const cudaError_t e = allow_smem(reinterpret_cast<const void*>(combine_deep_kernel<T, V>),
-                                       kDeepBytes, done);
-      if (e != cudaSuccess) return e;
-      const int64_t grid = std::min<int64_t>(p.m * columns, 2 * std::max(1, proj_num_sms()));
-      const cudaLaunchConfig_t cfg = config(grid, 1, kRowThreads, kDeepBytes, s, attr);
-      return cudaLaunchKernelEx(&cfg, combine_deep_kernel<T, V>, p,
-                                static_cast<int>(columns * jgroups));
-    }
-  }
   const cudaLaunchConfig_t cfg = config(p.m, ny, kRowThreads, 0, s, attr);
-  switch (op) {
-    case Op::kGather: return cudaLaunchKernelEx(&cfg, gather_kernel<T, V>, p);
-    case Op::kCombine:
-      if constexpr (V * sizeof(T) < 4) return cudaLaunchKernelEx(&cfg, combine_kernel<T, V>, p);
-      break;
-    case Op::kGrad: return cudaLaunchKernelEx(&cfg, combine_grad_kernel<T, V>, p);
-  }
-  return cudaErrorInvalidValue;
+  return op == Op::kGather ? cudaLaunchKernelEx(&cfg, gather_kernel<T, V>, p)
+                           : cudaLaunchKernelEx(&cfg, combine_grad_kernel<T, V>, p);
+}
+
+template <typename T, int kUnit>
+cudaError_t combine_launch(const RowsParams& p, cudaStream_t s) {
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e =
+      allow_smem(reinterpret_cast<const void*>(combine_kernel<T, kUnit>), kDeepBytes, done);
+  if (e != cudaSuccess) return e;
+  constexpr int kCols = kPieceBytes / static_cast<int>(sizeof(T));
+  // pieces of about equal width, in 16 bytes
+  const int64_t columns = (p.D + kCols - 1) / kCols;
+  constexpr int kStep = 16 / static_cast<int>(sizeof(T));
+  const int64_t width = ((p.D + columns - 1) / columns + kStep - 1) / kStep * kStep;
+  const int64_t grid = std::min<int64_t>(p.m * columns, 2 * std::max(1, proj_num_sms()));
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg = config(grid, 1, kRowThreads, kDeepBytes, s, attr);
+  return cudaLaunchKernelEx(&cfg, combine_kernel<T, kUnit>, p, static_cast<int>(columns),
+                            static_cast<int>(width));
 }
 
 // Whether every row of every tensor starts on a multiple of `bytes`, and so
@@ -879,6 +873,10 @@ bool rows_on(const RowsParams& p, int el, int bytes) {
 template <typename T>
 cudaError_t rows_any(Op op, const RowsParams& p, cudaStream_t s) {
   constexpr int el = sizeof(T);
+  if (op == Op::kCombine)
+    return rows_on(p, el, 16)  ? combine_launch<T, 16>(p, s)
+           : rows_on(p, el, 4) ? combine_launch<T, 4>(p, s)
+                               : combine_launch<T, el>(p, s);
   if (rows_on(p, el, 16)) return rows_launch<T, 16 / el>(op, p, s);
   if (rows_on(p, el, 8)) return rows_launch<T, 8 / el>(op, p, s);
   if constexpr (el == 2)

@@ -424,7 +424,9 @@ int proj_gemv_static_status(proj_stream stream, uint32_t *code);
  * with each call; a call that moves nothing (m = 0) returns PROJ_OK.
  * Indices that a buffer holds on the device (offsets, slots, expert ids) are
  * checked in the kernels: one out of range is treated as documented and
- * never read or written through.
+ * never read or written through.  Between a row's end and the next row's start
+ * (ld > width) nothing is written; what stands there may be read, as part of a
+ * 16-byte word, but does not enter any result.
  * ---------------------------------------------------------------------------
  *
  * Products with 4-bit weights and group scales.  A handle holds E matrices
@@ -463,8 +465,7 @@ proj_w4_handle proj_w4_prepare(const void *codes, const void *scales, const void
 
 /*
  * out[i, n] = sum over k of x[i, k] w[0, n, k], i < m (E must be 1).
- *   x   : m rows of K values, ldx >= K a multiple of 8, 16-byte aligned; what
- *         lies between K and ldx is not read.
+ *   x   : m rows of K values, ldx >= K a multiple of 8, 16-byte aligned.
  *   out : m rows of N values, ldo >= N, aligned to an element.
  * x and out must not overlap.  m <= 2^20, strides below 2^31.
  */

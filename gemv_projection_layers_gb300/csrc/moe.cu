@@ -404,7 +404,7 @@ constexpr int kDeepBytes = kDeep * 8 * kPlace;
 template <typename T, int kUnit>
 __global__ void __launch_bounds__(kRowThreads, 2)
     combine_kernel(const RowsParams p, const int columns, const int width) {
-  constexpr int V = 16 / static_cast<int>(sizeof(T)), kCols = V * kRowThreads;
+  constexpr int V = 16 / static_cast<int>(sizeof(T));
   constexpr int el = sizeof(T);
   constexpr bool kWhole = kUnit == 16;
   constexpr int UE = kUnit / el, NU = V / UE;  // elements of a unit, units of a thread

@@ -99,7 +99,7 @@ struct Shape {
   static constexpr int E = kVec ? kFullVec<T> : 4;
   static constexpr int kRows = TPR < 128 ? 128 / TPR : 1;  // rows of a CTA at a time
   static constexpr int kThreads = TPR < 128 ? 128 : TPR;
-  static constexpr bool kRing = TPR >= 128 && TPR <= 512;  // rows come through shared memory
+  static constexpr bool kRing = TPR <= 512;  // rows come through shared memory
 };
 
 // Whether the row reaches group j of a thread (kVec: with all of it, or not at
@@ -267,6 +267,15 @@ struct Row {
   }
 };
 
+// The threads of a row have come here: a warp, or the CTA.
+template <typename S>
+__device__ __forceinline__ void row_sync() {
+  if constexpr (S::TPR == 32)
+    __syncwarp();
+  else
+    __syncthreads();
+}
+
 // The loop over a CTA's rows: work(row, stage) for rows first, first + step, ...
 // with the next rows' copies under way.  Work has a block barrier between its
 // two passes or none; without shared columns between threads (kVec) a thread
@@ -285,12 +294,12 @@ __device__ __forceinline__ void over_rows(const R& rows, int64_t m, int64_t firs
     int stage = 0;
     for (int64_t row = first; row < m; row += step) {
       if (ahead == 0) {
-        if (!S::kVec) __syncthreads();  // the row before has been read
+        if (!S::kVec) row_sync<S>();  // the row before has been read
         rows.fetch(row, 0, tid);
         cp_async_commit();
       }
       cp_async_wait_all_but(ahead - 1);
-      if (!S::kVec) __syncthreads();
+      if (!S::kVec) row_sync<S>();
       if (ahead) {
         const int into = stage == 0 ? ahead : stage - 1;  // the stage of the row before
         if (row + ahead * step < m) rows.fetch(row + ahead * step, into, tid);
@@ -323,7 +332,7 @@ __global__ void __launch_bounds__(S::kThreads)
   rows.ld[1] = a.ldy;
   rows.base[2] = a.gate_mode == PROJ_GATE_ELEMENT ? static_cast<const T*>(a.gate) : nullptr;
   rows.ld[2] = a.ldg;
-  rows.smem = smem;
+  rows.smem = smem + threadIdx.x / TPR * (stages * 3) * slot;
   rows.m = a.m;
   rows.D = D;
   rows.slot = slot;
@@ -419,7 +428,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kThreads < 512 ? 512 / S::kThr
   __shared__ float room[2 * 3 * 32];
   int turn = 0;
   const int tid = static_cast<int>(threadIdx.x) % TPR;
-  const int part_row = static_cast<int>(blockIdx.x) * S::kRows + threadIdx.x / TPR;
+  const int first = static_cast<int>(blockIdx.x) * S::kRows + threadIdx.x / TPR;
   griddep_launch_dependents();
   griddep_wait();
   const int D = static_cast<int>(a.D);
@@ -427,7 +436,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kThreads < 512 ? 512 / S::kThr
   const bool normed = a.y && !a.y_plain;
   const bool g_vec = a.gate_mode == PROJ_GATE_CHANNEL || a.gate_mode == PROJ_GATE_ELEMENT;
   const bool g_token = a.gate_mode == PROJ_GATE_TOKEN;
-  const bool col_gate = a.gate_mode == PROJ_GATE_CHANNEL && a.dgate;
+  const bool g_channel = a.gate_mode == PROJ_GATE_CHANNEL;
   Rows<S, 5> rows;
   rows.base[0] = static_cast<const T*>(a.residual);
   rows.ld[0] = a.ldr;
@@ -439,20 +448,26 @@ __global__ void __launch_bounds__(S::kThreads, S::kThreads < 512 ? 512 / S::kThr
   rows.ld[3] = a.lddo;
   rows.base[4] = static_cast<const T*>(a.dnormed);
   rows.ld[4] = a.lddn;
-  rows.smem = smem;
+  rows.smem = smem + threadIdx.x / TPR * (stages * 5) * slot;
   rows.m = a.m;
   rows.D = D;
   rows.slot = slot;
   rows.stages = stages;
 
   constexpr int H = E / 2;  // the arithmetic runs on pairs of elements
+  // Eight elements a thread stay in registers between the passes; of sixteen the
+  // second pass makes them anew.
+  constexpr bool kKeep = NV * E <= 8;
+  constexpr int kKept = kKeep ? NV : 1;
   const F2 zero = f2(0.f), one = f2(1.f), minus = f2(-1.f);
   const F2 alpha = f2(a.alpha), beta = f2(a.beta);
-  F2 acc_post[NV][H], acc_pre[NV][H], acc_gate[NV][H];
+  // dw_post and dw_pre; for a gate per channel the first holds sum_rows beta du yn,
+  // of which dw_post is g times and the gate's gradient n / yn act' times
+  F2 acc_post[NV][H], acc_pre[NV][H];
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
-    for (int i = 0; i < H; ++i) acc_post[j][i] = acc_pre[j][i] = acc_gate[j][i] = zero;
+    for (int i = 0; i < H; ++i) acc_post[j][i] = acc_pre[j][i] = zero;
 
   float rp_next = 1.f, ru_next = 1.f;  // the next row's factors, read a row ahead
   auto factors = [&](int64_t row) {
@@ -460,9 +475,9 @@ __global__ void __launch_bounds__(S::kThreads, S::kThreads < 512 ? 512 / S::kThr
     if (normed) rp_next = a.rstd_post[row];
     if (a.dnormed) ru_next = a.rstd_pre[row];
   };
-  factors(part_row);
+  factors(first);
 
-  over_rows<S>(rows, a.m, part_row, static_cast<int64_t>(gridDim.x) * S::kRows, tid,
+  over_rows<S>(rows, a.m, first, static_cast<int64_t>(gridDim.x) * S::kRows, tid,
                [&](int64_t row, int stage) {
     const Row<S, 5> at(rows, row, stage, tid);
     const F2 rp = f2(rp_next);
@@ -473,8 +488,12 @@ __global__ void __launch_bounds__(S::kThreads, S::kThreads < 512 ? 512 / S::kThr
         g_token ? act<T>(to_f32(static_cast<const T*>(a.gate)[row]), a.gate_act) : 1.f;
     // group j's yn, n, un, dh, t = dh w_pre and e = du' + ru t, and w_post, with the
     // activated gate in g
-    F2 yn[H], n[H], un[H], dh[H], t[H], e[H], wpo[H];
+    F2 yn_[kKept][H], n_[kKept][H], un_[kKept][H], dh_[kKept][H], t_[kKept][H], e_[kKept][H],
+        wpo_[kKept][H];
     auto group = [&](int j, const F2 (&g)[H]) {
+      const int at_j = kKeep ? j : 0;
+      F2(&yn)[H] = yn_[at_j], (&n)[H] = n_[at_j], (&un)[H] = un_[at_j], (&dh)[H] = dh_[at_j];
+      F2(&t)[H] = t_[at_j], (&e)[H] = e_[at_j], (&wpo)[H] = wpo_[at_j];
       float v[E];
       at.load(0, j, v);
       pairs<E>(v, un);
@@ -547,6 +566,8 @@ __global__ void __launch_bounds__(S::kThreads, S::kThreads < 512 ? 512 / S::kThr
         for (int i = 0; i < H; ++i) g[j][i] = f2(g_row);
       }
       group(j, g[j]);
+      const int at_j = kKeep ? j : 0;
+      F2(&n)[H] = n_[at_j], (&un)[H] = un_[at_j], (&t)[H] = t_[at_j], (&e)[H] = e_[at_j];
 #pragma unroll
       for (int i = 0; i < H; ++i) {
         s2x[0] = fma2(t[i], un[i], s2x[0]);
@@ -563,6 +584,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kThreads < 512 ? 512 / S::kThr
       s[i] = x + y;
     }
     row_sums<TPR, 3>(s, room, turn);
+    asm volatile("" ::: "memory");  // the second pass reads the weights again: no registers hold them
     const float s1 = a.dnormed ? ru_row * s[0] * inv_d : 0.f;
     const float ab = a.beta * (s[1] - s1 * s[2]);  // sum of beta [g] n du
     const F2 s2 = f2(normed ? -(g_token ? g_row * ab : ab) * inv_d : 0.f);
@@ -572,7 +594,10 @@ __global__ void __launch_bounds__(S::kThreads, S::kThreads < 512 ? 512 / S::kThr
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       if (!reaches<S>(j, tid, D)) break;
-      group(j, g[j]);
+      if constexpr (!kKeep) group(j, g[j]);
+      const int at_j = kKeep ? j : 0;
+      F2(&yn)[H] = yn_[at_j], (&n)[H] = n_[at_j], (&un)[H] = un_[at_j], (&dh)[H] = dh_[at_j];
+      F2(&e)[H] = e_[at_j], (&wpo)[H] = wpo_[at_j];
       F2 o[H];
       float out[E];
 #pragma unroll
@@ -593,14 +618,14 @@ __global__ void __launch_bounds__(S::kThreads, S::kThreads < 512 ? 512 / S::kThr
       for (int i = 0; i < H; ++i) {
         e[i] = mul2(e[i], beta);
         const F2 c = mul2(g[j][i], e[i]);
-        acc_post[j][i] = fma2(c, yn[i], acc_post[j][i]);
+        acc_post[j][i] = fma2(g_channel ? e[i] : c, yn[i], acc_post[j][i]);
         o[i] = normed ? mul2(rp, fma2(c, wpo[i], mul2(yn[i], s2))) : c;
       }
       if (a.dy) {
         unpair<E>(o, out);
         store_global<S>(static_cast<T*>(a.dy) + row * a.lddy, j, tid, D, out);
       }
-      if (g_vec && a.dgate) {
+      if (a.gate_mode == PROJ_GATE_ELEMENT && a.dgate) {
 #pragma unroll
         for (int i = 0; i < H; ++i) o[i] = mul2(n[i], e[i]);
         if (a.gate_act == PROJ_GATE_SIGMOID) {
@@ -608,39 +633,67 @@ __global__ void __launch_bounds__(S::kThreads, S::kThreads < 512 ? 512 / S::kThr
           for (int i = 0; i < H; ++i)
             o[i] = mul2(o[i], mul2(g[j][i], fma2(g[j][i], minus, one)));
         }
-        if (col_gate) {
-#pragma unroll
-          for (int i = 0; i < H; ++i) acc_gate[j][i] = add2(acc_gate[j][i], o[i]);
-        } else {
-          unpair<E>(o, out);
-          store_global<S>(static_cast<T*>(a.dgate) + row * a.lddg, j, tid, D, out);
-        }
+        unpair<E>(o, out);
+        store_global<S>(static_cast<T*>(a.dgate) + row * a.lddg, j, tid, D, out);
       }
     }
   });
+  const bool col_gate = g_channel && a.dgate;
   if (!a.dw_post && !a.dw_pre && !col_gate) return;
-  float* part = static_cast<float*>(a.workspace) + static_cast<size_t>(part_row) * 3 * D;
+  float* const part = static_cast<float*>(a.workspace) + static_cast<size_t>(blockIdx.x) * 3 * D;
+  // rows of one CTA meet in shared memory, where no copies are under way now
+  float* const to = S::kRows > 1 ? reinterpret_cast<float*>(smem) + threadIdx.x / TPR * 3 * D : part;
+  if (S::kRows > 1) __syncthreads();
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
+    if (!reaches<S>(j, tid, D)) break;
     float post[E], pre[E], gate[E];
     unpair<E>(acc_post[j], post);
     unpair<E>(acc_pre[j], pre);
-    unpair<E>(acc_gate[j], gate);
+#pragma unroll
+    for (int i = 0; i < E; ++i) gate[i] = 0.f;
+    if (g_channel) {
+      float w[E];
+      load_global<S>(static_cast<const T*>(a.gate), j, tid, D, gate);
+      act_all<T>(gate, a.gate_act);
+      if (a.w_post) {
+        load_global<S>(static_cast<const T*>(a.w_post), j, tid, D, w);
+      } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i) w[i] = 1.f;
+      }
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const float q = post[i];
+        post[i] = gate[i] * q;
+        gate[i] = w[i] * act_slope(gate[i], a.gate_act) * q;
+      }
+    }
 #pragma unroll
     for (int i = 0; i < E; ++i) {
       const int c = S::kVec ? (j * TPR + tid) * E + i : (j * E + i) * TPR + tid;
       if (c < D) {
-        if (a.dw_post) part[c] = post[i];
-        if (a.dw_pre) part[D + c] = pre[i];
-        if (col_gate) part[2 * D + c] = gate[i];
+        to[c] = post[i];
+        to[D + c] = pre[i];
+        to[2 * D + c] = gate[i];
       }
+    }
+  }
+  if constexpr (S::kRows > 1) {
+    __syncthreads();
+    const float* const all = reinterpret_cast<const float*>(smem);
+    for (int c = threadIdx.x; c < 3 * D; c += S::kThreads) {
+      float t = 0.f;
+#pragma unroll
+      for (int k = 0; k < S::kRows; ++k) t += all[k * 3 * D + c];
+      part[c] = t;
     }
   }
 }
 
 // Sums the partial rows of each column in order: warps of a CTA take every
 // kSumWarps-th row of 32 columns, then meet in shared memory.
-constexpr int kSumWarps = 8;
+constexpr int kSumWarps = 32;
 __global__ void __launch_bounds__(32 * kSumWarps)
     norm_grad_sum_kernel(const float* __restrict__ part, int rows, int D, float* d0, float* d1,
                          float* d2) {
@@ -684,10 +737,8 @@ cudaLaunchConfig_t config(unsigned grid_x, unsigned grid_y, unsigned threads, si
 
 // CTAs of the gradient, and with it rows of the column sums' workspace, at
 // most: longer rows have more threads and fewer CTAs fit an SM.
-int grad_ctas(int64_t D) { return D > 4096 ? 152 : D > 2048 ? 304 : 608; }
-int grad_parts(int64_t m, int64_t D) {
-  return static_cast<int>(std::min<int64_t>(m, grad_ctas(D)));
-}
+constexpr int kGradSms = 152;
+int grad_ctas(int64_t D) { return kGradSms * (D > 4096 ? 1 : D > 1024 ? 2 : 4); }
 
 constexpr int kSmemMost = 220 * 1024;
 
@@ -696,7 +747,7 @@ constexpr int kSmemMost = 220 * 1024;
 template <typename S>
 void ring_shape(int64_t D, int tensors, int budget, int most, int* slot, int* stages) {
   *slot = static_cast<int>((D * sizeof(typename S::Type) + 15) / 16 * 16 + 16);
-  *stages = S::kRing ? std::max(1, std::min(most, budget / (tensors * *slot))) : 0;
+  *stages = S::kRing ? std::max(1, std::min(most, budget / (S::kRows * tensors * *slot))) : 0;
 }
 
 template <typename S>
@@ -705,7 +756,7 @@ cudaError_t forward(const proj_norm_args& a, cudaStream_t s) {
   int slot, stages;
   ring_shape<S>(a.D, 3, kSmemMost / 2, 3, &slot, &stages);
   if (S::kRing && stages < 2) ring_shape<S>(a.D, 3, kSmemMost, 3, &slot, &stages);
-  const size_t smem = static_cast<size_t>(3) * slot * stages;
+  const size_t smem = static_cast<size_t>(S::kRows) * 3 * slot * stages;
   if (smem > 48 * 1024) {
     static std::atomic<uint64_t> done{0};
     const cudaError_t e =
@@ -724,12 +775,15 @@ cudaError_t forward(const proj_norm_args& a, cudaStream_t s) {
 
 template <typename S>
 cudaError_t backward(const proj_norm_grad_args& a, cudaStream_t s) {
-  const int grid = (grad_parts(a.m, a.D) + S::kRows - 1) / S::kRows;
+  // as many CTAs an SM as have 128 registers a thread (never more than grad_ctas)
+  constexpr int per_sm = S::kThreads < 512 ? 512 / S::kThreads : 1;
+  const int grid = static_cast<int>(
+      std::min<int64_t>((a.m + S::kRows - 1) / S::kRows, kGradSms * per_sm));
   int slot, stages;
-  // as many CTAs an SM as the grid has for it
-  const int per_sm = std::max(1, grad_ctas(a.D) / 152);
   ring_shape<S>(a.D, 5, kSmemMost / per_sm, 3, &slot, &stages);
-  const size_t smem = static_cast<size_t>(5) * slot * stages;
+  const size_t ring = static_cast<size_t>(S::kRows) * 5 * slot * stages;
+  const size_t joined = S::kRows > 1 ? static_cast<size_t>(S::kRows) * 3 * a.D * 4 : 0;
+  const size_t smem = std::max(ring, joined);
   if (smem > 48 * 1024) {
     static std::atomic<uint64_t> done{0};
     const cudaError_t e =
@@ -745,38 +799,54 @@ cudaError_t backward(const proj_norm_grad_args& a, cudaStream_t s) {
   cfg = config(static_cast<unsigned>((a.D + 31) / 32), 3, 32 * kSumWarps, 0, s, attr);
   return cudaLaunchKernelEx(&cfg, norm_grad_sum_kernel,
                             static_cast<const float*>(static_cast<float*>(a.workspace)),
-                            grid * S::kRows, static_cast<int>(a.D), a.dw_post, a.dw_pre, dgate);
+                            grid, static_cast<int>(a.D), a.dw_post, a.dw_pre, dgate);
 }
 
-// Threads per row by its length: 16 elements of 16 bits a thread (8 or 16 of
-// fp32), a warp for the shortest rows.  Beyond 512 threads a row (D > 8192 in
-// 16 bits) there is no ring, and both passes read global memory.
-#define PROJ_NORM_PICK(FN, T, a, s)                                      \
-  if (vec) {                                                             \
-    const int64_t n = (a).D / kFullVec<T>;                               \
-    if (n <= 64) return FN<Shape<T, true, 32, 2>>(a, s);                 \
-    if (n <= 256) return FN<Shape<T, true, 128, 2>>(a, s);               \
-    if (n <= 512) return FN<Shape<T, true, 256, 2>>(a, s);               \
-    if (n <= 1024) return FN<Shape<T, true, 512, 2>>(a, s);              \
-    if constexpr (kFullVec<T> == 4)                                      \
-      if (n > 2048) return FN<Shape<T, true, 1024, 4>>(a, s);            \
-    return FN<Shape<T, true, 1024, 2>>(a, s);                            \
-  } else {                                                               \
-    if ((a).D <= 512) return FN<Shape<T, false, 32, 4>>(a, s);           \
-    if ((a).D <= 2048) return FN<Shape<T, false, 128, 4>>(a, s);         \
-    if ((a).D <= 4096) return FN<Shape<T, false, 256, 4>>(a, s);         \
-    if ((a).D <= 8192) return FN<Shape<T, false, 512, 4>>(a, s);         \
-    return FN<Shape<T, false, 1024, 4>>(a, s);                           \
-  }
-
+// Threads per row by its length.  Forward: 16 elements of 16 bits a thread (8
+// or 16 of fp32), a warp for the shortest rows.  Gradient: eight elements while
+// 512 threads have the row so, else 16, with a warp for the shortest rows.
+// Beyond 512 threads a row (D > 8192 in 16 bits) there is no ring, and both
+// passes read global memory.
 template <typename T>
 cudaError_t forward_any(const proj_norm_args& a, bool vec, cudaStream_t s) {
-  PROJ_NORM_PICK(forward, T, a, s)
+  if (vec) {
+    const int64_t n = a.D / kFullVec<T>;
+    if (n <= 64) return forward<Shape<T, true, 32, 2>>(a, s);
+    if (n <= 256) return forward<Shape<T, true, 128, 2>>(a, s);
+    if (n <= 512) return forward<Shape<T, true, 256, 2>>(a, s);
+    if (n <= 1024) return forward<Shape<T, true, 512, 2>>(a, s);
+    if constexpr (kFullVec<T> == 4)
+      if (n > 2048) return forward<Shape<T, true, 1024, 4>>(a, s);
+    return forward<Shape<T, true, 1024, 2>>(a, s);
+  }
+  if (a.D <= 512) return forward<Shape<T, false, 32, 4>>(a, s);
+  if (a.D <= 2048) return forward<Shape<T, false, 128, 4>>(a, s);
+  if (a.D <= 4096) return forward<Shape<T, false, 256, 4>>(a, s);
+  if (a.D <= 8192) return forward<Shape<T, false, 512, 4>>(a, s);
+  return forward<Shape<T, false, 1024, 4>>(a, s);
 }
 
 template <typename T>
 cudaError_t backward_any(const proj_norm_grad_args& a, bool vec, cudaStream_t s) {
-  PROJ_NORM_PICK(backward, T, a, s)
+  constexpr int kEight = 8 / kFullVec<T>;  // groups of eight elements
+  if (vec) {
+    const int64_t n = a.D / kFullVec<T>;
+    if (n <= 64) return backward<Shape<T, true, 32, 2>>(a, s);
+    if (a.D <= 1024) return backward<Shape<T, true, 128, kEight>>(a, s);
+    if (a.D <= 2048) return backward<Shape<T, true, 256, kEight>>(a, s);
+    if constexpr (kFullVec<T> == 8)
+      if (a.D <= 4096) return backward<Shape<T, true, 256, 2>>(a, s);
+    if (n <= 1024) return backward<Shape<T, true, 512, 2>>(a, s);
+    if constexpr (kFullVec<T> == 4)
+      if (n > 2048) return backward<Shape<T, true, 1024, 4>>(a, s);
+    return backward<Shape<T, true, 1024, 2>>(a, s);
+  }
+  if (a.D <= 512) return backward<Shape<T, false, 32, 4>>(a, s);
+  if (a.D <= 1024) return backward<Shape<T, false, 128, 2>>(a, s);
+  if (a.D <= 2048) return backward<Shape<T, false, 256, 2>>(a, s);
+  if (a.D <= 4096) return backward<Shape<T, false, 256, 4>>(a, s);
+  if (a.D <= 8192) return backward<Shape<T, false, 512, 4>>(a, s);
+  return backward<Shape<T, false, 1024, 4>>(a, s);
 }
 
 int element_size(int dtype) { return dtype == PROJ_FP32 ? 4 : 2; }
@@ -865,8 +935,7 @@ extern "C" int64_t proj_norm_workspace(int64_t m, int64_t D) {
     refuse(PROJ_EINVAL, "proj_norm_workspace", "m < 0 or D outside 1 .. 16384");
     return -1;
   }
-  // rows are rounded up to the four that a block of warps holds
-  return static_cast<int64_t>((grad_parts(m, D) + 3) / 4 * 4) * 3 * D * 4;
+  return std::min<int64_t>(m, grad_ctas(D)) * 3 * D * 4;
 }
 
 extern "C" int proj_norm_backward(const proj_norm_grad_args* args, proj_stream stream) {

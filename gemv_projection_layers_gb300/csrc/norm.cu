@@ -91,7 +91,7 @@ __device__ __forceinline__ void cp_async_wait_all_but(int pending) {
 
 // How TPR threads share a row.  kVec: group j of a thread is the 16 bytes at
 // element (j TPR + tid) E; else E elements TPR apart, from j E TPR + tid.
-template <typename T, bool kVec_, int TPR_, int NV_>
+template <typename T, bool kVec_, int TPR_, int NV_, bool kRing_ = (TPR_ >= 128 && TPR_ <= 512)>
 struct Shape {
   using Type = T;
   static constexpr bool kVec = kVec_;
@@ -99,7 +99,7 @@ struct Shape {
   static constexpr int E = kVec ? kFullVec<T> : 4;
   static constexpr int kRows = TPR < 128 ? 128 / TPR : 1;  // rows of a CTA at a time
   static constexpr int kThreads = TPR < 128 ? 128 : TPR;
-  static constexpr bool kRing = TPR <= 512;  // rows come through shared memory
+  static constexpr bool kRing = kRing_;  // rows come through shared memory
 };
 
 // Whether the row reaches group j of a thread (kVec: with all of it, or not at
@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kThreads < 512 ? 512 / S::kThr
   constexpr int H = E / 2;  // the arithmetic runs on pairs of elements
   // Eight elements a thread stay in registers between the passes; of sixteen the
   // second pass makes them anew.
-  constexpr bool kKeep = NV * E <= 8;
+  constexpr bool kKeep = NV * E <= 8 && TPR <= 512;
   constexpr int kKept = kKeep ? NV : 1;
   const F2 zero = f2(0.f), one = f2(1.f), minus = f2(-1.f);
   const F2 alpha = f2(a.alpha), beta = f2(a.beta);
@@ -584,7 +584,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kThreads < 512 ? 512 / S::kThr
       s[i] = x + y;
     }
     row_sums<TPR, 3>(s, room, turn);
-    asm volatile("" ::: "memory");  // the second pass reads the weights again: no registers hold them
+    if constexpr (TPR == 32) __syncwarp();  // keeps the passes apart: fewer registers
     const float s1 = a.dnormed ? ru_row * s[0] * inv_d : 0.f;
     const float ab = a.beta * (s[1] - s1 * s[2]);  // sum of beta [g] n du
     const F2 s2 = f2(normed ? -(g_token ? g_row * ab : ab) * inv_d : 0.f);
@@ -815,9 +815,12 @@ cudaError_t forward_any(const proj_norm_args& a, bool vec, cudaStream_t s) {
     if (n <= 256) return forward<Shape<T, true, 128, 2>>(a, s);
     if (n <= 512) return forward<Shape<T, true, 256, 2>>(a, s);
     if (n <= 1024) return forward<Shape<T, true, 512, 2>>(a, s);
-    if constexpr (kFullVec<T> == 4)
-      if (n > 2048) return forward<Shape<T, true, 1024, 4>>(a, s);
-    return forward<Shape<T, true, 1024, 2>>(a, s);
+    if constexpr (kFullVec<T> == 4) {
+      if (n <= 2048) return forward<Shape<T, true, 512, 4>>(a, s);
+      return forward<Shape<T, true, 1024, 4>>(a, s);
+    } else {
+      return forward<Shape<T, true, 1024, 2>>(a, s);
+    }
   }
   if (a.D <= 512) return forward<Shape<T, false, 32, 4>>(a, s);
   if (a.D <= 2048) return forward<Shape<T, false, 128, 4>>(a, s);
@@ -831,17 +834,20 @@ cudaError_t backward_any(const proj_norm_grad_args& a, bool vec, cudaStream_t s)
   constexpr int kEight = 8 / kFullVec<T>;  // groups of eight elements
   if (vec) {
     const int64_t n = a.D / kFullVec<T>;
-    if (n <= 64) return backward<Shape<T, true, 32, 2>>(a, s);
+    if (n <= 64) return backward<Shape<T, true, 32, 2, true>>(a, s);
     if (a.D <= 1024) return backward<Shape<T, true, 128, kEight>>(a, s);
     if (a.D <= 2048) return backward<Shape<T, true, 256, kEight>>(a, s);
     if constexpr (kFullVec<T> == 8)
       if (a.D <= 4096) return backward<Shape<T, true, 256, 2>>(a, s);
     if (n <= 1024) return backward<Shape<T, true, 512, 2>>(a, s);
-    if constexpr (kFullVec<T> == 4)
-      if (n > 2048) return backward<Shape<T, true, 1024, 4>>(a, s);
-    return backward<Shape<T, true, 1024, 2>>(a, s);
+    if constexpr (kFullVec<T> == 4) {
+      if (n <= 2048) return backward<Shape<T, true, 512, 4>>(a, s);
+      return backward<Shape<T, true, 1024, 4>>(a, s);
+    } else {
+      return backward<Shape<T, true, 1024, 2>>(a, s);
+    }
   }
-  if (a.D <= 512) return backward<Shape<T, false, 32, 4>>(a, s);
+  if (a.D <= 512) return backward<Shape<T, false, 32, 4, true>>(a, s);
   if (a.D <= 1024) return backward<Shape<T, false, 128, 2>>(a, s);
   if (a.D <= 2048) return backward<Shape<T, false, 256, 2>>(a, s);
   if (a.D <= 4096) return backward<Shape<T, false, 256, 4>>(a, s);

@@ -23,9 +23,11 @@
 // column sums stay in registers over all of a CTA's rows and meet in a second
 // kernel, in a fixed order.  The forward kernel comes to 0.8 of the measured
 // copy rate (8192 x 8192 bf16, a gate per element: 125 us, 5.4 TB/s); the
-// gradient, with the three column sums' registers, has one row at a time on an
-// SM, and its two passes (some 100 instructions an element) and their barrier
-// bound it: 315 us for the kernel, 3.4 TB/s.
+// gradient, with its column sums in registers, has 16 warps an SM -- of long
+// rows, one row at a time -- and its two passes (some 100 instructions an
+// element) and their barrier bound it: 315 us there, 3.4 TB/s; 64 us for 8192 x
+// 1024 (2.1 TB/s), where a row is worked on by four warps with eight elements a
+// thread, 75 with sixteen; 34 us for 8192 x 512 by a warp a row.
 //
 // Rows that do not start on 16 bytes (an odd D, say) keep their misalignment
 // in shared memory, where the 16-byte words that hold them go, and the threads
@@ -100,6 +102,8 @@ struct Shape {
   static constexpr int kRows = TPR < 128 ? 128 / TPR : 1;  // rows of a CTA at a time
   static constexpr int kThreads = TPR < 128 ? 128 : TPR;
   static constexpr bool kRing = kRing_;  // rows come through shared memory
+  // threads of an SM in the forward kernel, by its registers
+  static constexpr int kResident = kVec && NV == 1 ? 1536 : 1024;
 };
 
 // Whether the row reaches group j of a thread (kVec: with all of it, or not at
@@ -312,7 +316,7 @@ __device__ __forceinline__ void over_rows(const R& rows, int64_t m, int64_t firs
 }
 
 template <typename S>
-__global__ void __launch_bounds__(S::kThreads)
+__global__ void __launch_bounds__(S::kThreads, S::kResident / S::kThreads)
     norm_kernel(const __grid_constant__ proj_norm_args a, const int slot, const int stages) {
   using T = typename S::Type;
   constexpr int NV = S::NV, E = S::E, TPR = S::TPR;
@@ -642,7 +646,8 @@ __global__ void __launch_bounds__(S::kThreads, S::kThreads < 512 ? 512 / S::kThr
   if (!a.dw_post && !a.dw_pre && !col_gate) return;
   float* const part = static_cast<float*>(a.workspace) + static_cast<size_t>(blockIdx.x) * 3 * D;
   // rows of one CTA meet in shared memory, where no copies are under way now
-  float* const to = S::kRows > 1 ? reinterpret_cast<float*>(smem) + threadIdx.x / TPR * 3 * D : part;
+  float* const to =
+      S::kRows > 1 ? reinterpret_cast<float*>(smem) + threadIdx.x / TPR * 3 * D : part;
   if (S::kRows > 1) __syncthreads();
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
@@ -752,10 +757,13 @@ void ring_shape(int64_t D, int tensors, int budget, int most, int* slot, int* st
 
 template <typename S>
 cudaError_t forward(const proj_norm_args& a, cudaStream_t s) {
-  // Two CTAs an SM where two stages of the rows fit half of it.
+  // As many CTAs an SM as its registers hold, fewer where two stages of the
+  // rows do not fit their part of its shared memory.
   int slot, stages;
-  ring_shape<S>(a.D, 3, kSmemMost / 2, 3, &slot, &stages);
-  if (S::kRing && stages < 2) ring_shape<S>(a.D, 3, kSmemMost, 3, &slot, &stages);
+  int ctas = S::kResident / S::kThreads;
+  ring_shape<S>(a.D, 3, kSmemMost / ctas, 3, &slot, &stages);
+  while (S::kRing && stages < 2 && ctas > 1)
+    ring_shape<S>(a.D, 3, kSmemMost / --ctas, 3, &slot, &stages);
   const size_t smem = static_cast<size_t>(S::kRows) * 3 * slot * stages;
   if (smem > 48 * 1024) {
     static std::atomic<uint64_t> done{0};
@@ -765,7 +773,8 @@ cudaError_t forward(const proj_norm_args& a, cudaStream_t s) {
   }
   int64_t grid = (a.m + S::kRows - 1) / S::kRows;
   if (S::kRing) {
-    const int per_sm = std::max(1, std::min(static_cast<int>(kSmemMost / smem), 1024 / S::kThreads));
+    const int per_sm =
+        std::max(1, std::min(static_cast<int>(kSmemMost / smem), S::kResident / S::kThreads));
     grid = std::min<int64_t>(grid, static_cast<int64_t>(per_sm) * std::max(1, proj_num_sms()));
   }
   cudaLaunchAttribute attr[1];
@@ -802,16 +811,20 @@ cudaError_t backward(const proj_norm_grad_args& a, cudaStream_t s) {
                             grid, static_cast<int>(a.D), a.dw_post, a.dw_pre, dgate);
 }
 
-// Threads per row by its length.  Forward: 16 elements of 16 bits a thread (8
-// or 16 of fp32), a warp for the shortest rows.  Gradient: eight elements while
-// 512 threads have the row so, else 16, with a warp for the shortest rows.
-// Beyond 512 threads a row (D > 8192 in 16 bits) there is no ring, and both
-// passes read global memory.
+// Threads per row by its length: 16 elements of 16 bits a thread (8 or 16 of
+// fp32), a warp for the shortest rows, which has no ring forward (a ring: 7.6 us
+// for 8192 x 128 bf16 against 6.9).  Eight elements are better for up to 1024
+// columns forward (8192 x 520: 17.8 us against 20.6; 1024 the same) and up to
+// 2048 in the gradient, whose second pass then finds them in registers (8192 x
+// 2048: 90 us against 117; at 4096, with one row an SM at a time, 179 against
+// 160).  Beyond 8192 columns there is no ring, and both passes read global
+// memory.
 template <typename T>
 cudaError_t forward_any(const proj_norm_args& a, bool vec, cudaStream_t s) {
   if (vec) {
     const int64_t n = a.D / kFullVec<T>;
     if (n <= 64) return forward<Shape<T, true, 32, 2>>(a, s);
+    if (a.D <= 1024) return forward<Shape<T, true, 128, 8 / kFullVec<T>>>(a, s);
     if (n <= 256) return forward<Shape<T, true, 128, 2>>(a, s);
     if (n <= 512) return forward<Shape<T, true, 256, 2>>(a, s);
     if (n <= 1024) return forward<Shape<T, true, 512, 2>>(a, s);

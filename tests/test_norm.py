@@ -228,6 +228,27 @@ def test_backward(m, D, extra, dtype):
         check_backward(Case(m, D, dtype, gate, (m + gate) % 2, D + gate, extra, no_w=gate == 3 and m % 2 == 0))
 
 
+# More rows than are on the GPU at a time, so that the rows ahead go around their room: a warp a row, four
+# warps, eight and sixteen; rows on and off 16 bytes.
+MANY = [(6000, 40, 0), (5000, 301, 0), (5200, 512, 0), (2000, 776, 8), (1300, 1025, 0), (1000, 2050, 6), (500, 6000, 0)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("m,D,extra", MANY)
+def test_forward_many_rows(m, D, extra, dtype):
+    test_forward(m, D, extra, dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("m,D,extra", MANY)
+def test_backward_many_rows(m, D, extra, dtype):
+    """Sums over tokens: a few rows a thread, at most 4 + 19 + 32 partial sums, and the 64 of a row's values."""
+    for gate in (1, 2, 3):
+        check_backward(Case(m, D, dtype, gate, gate % 2, D + gate, extra))
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("form", ["no block", "plain", "plain gated", "plain token", "no dout", "no dnormed"])
 @pytest.mark.parametrize("m,D", [(3, 256), (2, 333), (5, 8192)])

@@ -462,21 +462,26 @@ struct Plan {
 // and 99, at 8.5 rows 121 and 100.  Experts with fewer units of K than
 // kStreamUnits keep a streaming CTA too short for what it takes to start: 104
 // experts of 8192 x 512 take 204 us streamed and 76 on the tensor cores, whose
-// CTAs stay; of 2048 x 4096 both take 83 us.
+// CTAs stay; of 2048 x 4096 both take 83 us.  Unless there are few such CTAs,
+// kStreamCtas an SM at most: 8 experts of 1024 x 2048, a row each (288 CTAs),
+// 8.4 us streamed and 12.4 on the tensor cores, of 2048 x 768 (576) 8.3 and
+// 9.6, of 5173 x 1081 (1458) 17.6 and 13.5.
 constexpr int64_t kStreamRows = 16, kStreamRowsExperts = 6;
-constexpr int kStreamUnits = 64;
+constexpr int kStreamUnits = 64, kStreamCtas = 4;
 
 Plan make_plan(const proj_w4_ctx* h, int64_t m, bool experts) {
   const W4Params& p = h->p;
   Plan pl = {};
   const int64_t rows = experts ? (m + p.E - 1) / p.E : m;
-  pl.tc = p.E > 1 ? rows > kStreamRowsExperts || p.KU < kStreamUnits : rows > kStreamRows;
+  StreamShape& s = pl.stream;
+  s.NT = rows <= 8 ? 1 : 2;
+  const int64_t per = 8 * s.NT;
+  // of the experts that have rows, each has at most one part-filled tile
+  s.tiles = experts ? std::min<int64_t>(p.E, m) + m / per : (m + per - 1) / per;
+  pl.tc = p.E > 1 ? rows > kStreamRowsExperts ||
+                        (p.KU < kStreamUnits && (p.RB + 1) / 2 * s.tiles > kStreamCtas * h->sms)
+                  : rows > kStreamRows;
   if (!pl.tc) {
-    StreamShape& s = pl.stream;
-    s.NT = rows <= 8 ? 1 : 2;
-    const int64_t per = 8 * s.NT;
-    // of the experts that have rows, each has at most one part-filled tile
-    s.tiles = experts ? std::min<int64_t>(p.E, m) + m / per : (m + per - 1) / per;
     // Two blocks of rows share the loads of x where that leaves a CTA per SM
     // or so; K is split over a cluster while that puts at most two CTAs on an SM.
     s.RB = experts || p.RB * 3 >= h->sms * 4 ? 2 : 1;

@@ -300,6 +300,27 @@ def test_experts_of_long_rows(counts, dtype, group, zeros, N, K):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype,group,zeros,N,K", [("bf16", 32, True, 520, 513), ("fp16", 128, False, 700, 96)])
+@pytest.mark.parametrize("counts", [[1, 0, 2] * 100, [0] * 100 + [1] * 200 + [0, 0, 29]])
+def test_many_experts_of_few_rows(counts, dtype, group, zeros, N, K):
+    """So many of them that short rows are not streamed either: tiles with one or two rows on the tensor cores."""
+    E, m = len(counts), sum(counts)
+    with Weights(E, N, K, group, zeros, dtype, E) as w:
+        assert not is_exact(w.h, m)
+        x, ld = make_x(m, K, dtype, E)
+        off = offsets_of(counts)
+        out = torch.full((m + 1, N), -7.0, device="cuda", dtype=x.dtype)
+        B.proj_w4_run_experts(w.h, x, ld, m, off, out, N)
+        torch.cuda.synchronize()
+        assert (out[m:] == -7.0).all()
+        o = off.tolist()
+        for e in range(E):
+            if o[e] < o[e + 1]:
+                rows = slice(o[e], o[e + 1])
+                assert_close(out[rows], x[rows, :K].double(), w.w64(e), dtype, is_exact(w.h, m), K)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("counts", [[40000] + [1, 0] * 511 + [3], [70000, 0, 1, 75000]])
 def test_experts_with_more_token_tiles_than_the_table_holds(counts):
     E, m, N, K = len(counts), sum(counts), 17, 96

@@ -494,9 +494,10 @@ Plan make_plan(const proj_w4_ctx* h, int64_t m, bool experts) {
     const int64_t tiles =
         experts ? std::min<int64_t>(p.E, m) + m / pl.tn : (m + pl.tn - 1) / pl.tn;
     const int64_t items = tiles * p.RT;
-    // K is split while the clusters run at once and a CTA keeps two steps
+    // K is split while the clusters run at once and a CTA keeps two steps (146
+    // rows over 8 experts of 536 x 6208: 18.5 us, 28.0 unsplit)
     pl.C = 1;
-    for (int c = 2; c <= 8 && !experts; ++c)
+    for (int c = 2; c <= 8; ++c)
       if (items <= h->clusters[c] && p.KU >= 4 * c) pl.C = c;
     pl.grid = pl.C > 1 ? items * pl.C : std::min<int64_t>(items, h->sms);
   }

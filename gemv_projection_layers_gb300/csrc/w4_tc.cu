@@ -34,7 +34,7 @@
 // and x: 64 KB of x a step from L2, eight MMAs of 128 x 256 x 16.  (8192 x
 // 4096, 256 tokens: 18.9 us, 0.91 PFLOP/s.)
 //
-// One matrix and few tiles: a cluster of C CTAs splits K, and the partial
+// Where there are few tiles, a cluster of C CTAs splits K, and the partial
 // sums meet in rank order through distributed shared memory.
 #include <cuda_runtime.h>
 

@@ -321,6 +321,27 @@ def test_many_experts_of_few_rows(counts, dtype, group, zeros, N, K):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype,group,zeros,N,K", [("bf16", 128, False, 40, 4200), ("fp16", 32, True, 270, 2050), ("bf16", 64, True, 129, 600)])
+@pytest.mark.parametrize("counts", [[7], [0, 30, 0, 65, 1, 128, 0], [0, 0, 100], [40, 0, 0], [200, 1, 130, 0], [0, 900, 3]])
+def test_experts_with_few_tiles_of_long_rows(counts, dtype, group, zeros, N, K):
+    """K is split over clusters, some of which have no tile."""
+    E, m = len(counts), sum(counts)
+    with Weights(E, N, K, group, zeros, dtype, E + 1) as w:
+        x, ld = make_x(m, K, dtype, E)
+        off = offsets_of(counts)
+        out, again = (torch.full((m + 1, N), -7.0, device="cuda", dtype=x.dtype) for _ in range(2))
+        B.proj_w4_run_experts(w.h, x, ld, m, off, out, N)
+        B.proj_w4_run_experts(w.h, x, ld, m, off, again, N)
+        torch.cuda.synchronize()
+        assert torch.equal(out, again) and (out[m:] == -7.0).all()
+        o = off.tolist()
+        for e in range(E):
+            if o[e] < o[e + 1]:
+                rows = slice(o[e], o[e + 1])
+                assert_close(out[rows], x[rows, :K].double(), w.w64(e), dtype, is_exact(w.h, m), K)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("counts", [[40000] + [1, 0] * 511 + [3], [70000, 0, 1, 75000]])
 def test_experts_with_more_token_tiles_than_the_table_holds(counts):
     E, m, N, K = len(counts), sum(counts), 17, 96

@@ -34,6 +34,7 @@ PROJ_UNPACK_RUNS = 128  # proj_unpack_weights: the row-run GEMV's copy (all N ro
 PROJ_UNPACK_RUNS_SLICE = 256  # proj_unpack_weights: the unpooler's row-run copy of its slice
 PROJ_READ_PDL = 4  # proj_read_floor mode flag: launched as a programmatic dependent launch
 
+PROJ_W4_EXACT = 1  # proj_w4_prepare_ex: no rounding of s (q - z) at any number of rows
 PROJ_ROUTE_CHOSEN, PROJ_ROUTE_ALL = 0, 1  # proj_moe_route: softmax over the chosen / all logits
 PROJ_GATE_NONE, PROJ_GATE_CHANNEL, PROJ_GATE_ELEMENT, PROJ_GATE_TOKEN = range(4)
 PROJ_GATE_LINEAR, PROJ_GATE_SIGMOID = 0, 1
@@ -150,6 +151,9 @@ def load() -> ctypes.CDLL:
     lib.proj_gemv_static_status.restype = i32
     lib.proj_w4_prepare.argtypes = [vp, vp, vp, i64, i64, i64, i64, i32, ctypes.POINTER(i32)]
     lib.proj_w4_prepare.restype = vp
+    lib.proj_w4_prepare_ex.argtypes = [vp, vp, vp, i64, i64, i64, i64, i32, u32,
+                                       ctypes.POINTER(i32)]
+    lib.proj_w4_prepare_ex.restype = vp
     lib.proj_w4_run.argtypes = [vp, vp, i64, i64, vp, i64, vp]
     lib.proj_w4_run.restype = i32
     lib.proj_w4_run_experts.argtypes = [vp, vp, i64, i64, vp, vp, i64, vp]
@@ -362,9 +366,14 @@ def proj_gemv_static_status(stream=None) -> int:
 
 def proj_w4_prepare(codes, scales, zeros, experts: int, N: int, K: int, group: int,
                     dtype: int) -> int:
+    return proj_w4_prepare_ex(codes, scales, zeros, experts, N, K, group, dtype, 0)
+
+
+def proj_w4_prepare_ex(codes, scales, zeros, experts: int, N: int, K: int, group: int,
+                       dtype: int, flags: int) -> int:
     st = ctypes.c_int(0)
-    h = load().proj_w4_prepare(_addr(codes), _addr(scales), _addr(zeros), int(experts), int(N),
-                               int(K), int(group), int(dtype), ctypes.byref(st))
+    h = load().proj_w4_prepare_ex(_addr(codes), _addr(scales), _addr(zeros), int(experts), int(N),
+                                  int(K), int(group), int(dtype), int(flags), ctypes.byref(st))
     if not h:
         raise ProjError(st.value, f"proj_w4_prepare ({last_cuda_error()})")
     return h

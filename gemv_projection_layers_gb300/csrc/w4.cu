@@ -86,10 +86,13 @@ __global__ void pack_codes_kernel(const uint8_t* __restrict__ codes, uint4* __re
 }
 
 // One thread per packed scale.  Groups beyond K and rows beyond N get 0.
+// *wide becomes 1 if a finite scale s has s (q - z) above `most`, the largest
+// number of its type, for a q in 0..15.
+template <typename T>
 __global__ void pack_scales_kernel(const uint16_t* __restrict__ scales,
                                    const uint8_t* __restrict__ zeros, uint16_t* __restrict__ ds,
                                    uint8_t* __restrict__ dz, int64_t E, int64_t N, int64_t NG,
-                                   int64_t NGp, int64_t RT, bool g32) {
+                                   int64_t NGp, int64_t RT, bool g32, float most, uint32_t* wide) {
   const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
   if (i >= E * RT * NGp * 128) return;
   const int64_t j = i % (NGp * 128);  // within the tile
@@ -101,8 +104,15 @@ __global__ void pack_scales_kernel(const uint16_t* __restrict__ scales,
   const int64_t n = rt * 128 + b * 16 + g + 8 * (j & 1);
   const bool in = n < N && grp < NG;
   const int64_t src = (e * N + n) * NG + grp;
-  ds[i] = in ? scales[src] : 0;
-  if (dz) dz[i] = in ? static_cast<uint8_t>(zeros[src] & 15) : 0;
+  const uint16_t s = in ? scales[src] : 0;
+  ds[i] = s;
+  int z = 8;
+  if (dz) {
+    z = in ? zeros[src] & 15 : 0;
+    dz[i] = static_cast<uint8_t>(z);
+  }
+  const float size = fabsf(to_f32(*reinterpret_cast<const T*>(&s)));
+  if (size <= most && size * static_cast<float>(max(z, 15 - z)) > most) atomicOr(wide, 1u);
 }
 
 // ------------------------------------------------------ streaming kernel --
@@ -248,23 +258,25 @@ __global__ void __launch_bounds__(32 * kStreamWarps, kD == 2 && NT == 1 ? 3 : 2)
   };
 
   griddep_launch_dependents();
+  const int index = static_cast<int>(blockIdx.z * gridDim.y + blockIdx.y);
   Tile tile;
   if (p.offsets) {
     griddep_wait();
-    tile = find_tile<32 * W>(p.offsets, p.E, p.m, 8 * NT, blockIdx.y);
+    tile = find_tile<32 * W>(p.offsets, p.E, p.m, 8 * NT, index);
     if (tile.rows == 0) return;  // every CTA of the cluster
     open(tile.expert);
 #pragma unroll
     for (int d = 0; d < kD; ++d) fetch_w(d, d, u0 + d);
   } else {
     tile.expert = 0;
-    tile.row0 = static_cast<int64_t>(blockIdx.y) * 8 * NT;
+    tile.row0 = static_cast<int64_t>(index) * 8 * NT;
     tile.rows = static_cast<int>(min(static_cast<int64_t>(8 * NT), p.m - tile.row0));
     // the weights are constant: their first loads do not wait for the kernel before
     open(0);
 #pragma unroll
     for (int d = 0; d < kD; ++d) fetch_w(d, d, u0 + d);
     griddep_wait();
+    if (tile.rows <= 0) return;  // behind the last tile: every CTA of the cluster
   }
   const T* x[NT];
   bool live[NT];
@@ -392,8 +404,10 @@ __global__ void __launch_bounds__(32 * kStreamWarps, kD == 2 && NT == 1 ? 3 : 2)
 template <typename T, bool kG32, bool kZeros, int NT, int RB, int kD>
 cudaError_t stream_launch(const W4Params& p, const StreamShape& sh, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((p.RB + RB - 1) / RB * sh.C),
-                     static_cast<unsigned>(sh.tiles));
+  // y has at most 65,535: 2^20 rows are more tiles
+  const int64_t y = std::min<int64_t>(sh.tiles, 32768);
+  cfg.gridDim = dim3(static_cast<unsigned>((p.RB + RB - 1) / RB * sh.C), static_cast<unsigned>(y),
+                     static_cast<unsigned>((sh.tiles + y - 1) / y));
   cfg.blockDim = dim3(32 * kStreamWarps);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -441,6 +455,7 @@ struct proj_w4_ctx {
   W4Params p;       // sizes and the packed weights; x, out, offsets are each call's
   int dtype;
   uint8_t* base;    // one allocation: codes, scales, zeros, status word
+  bool exact;       // products of the 4-bit numbers at any number of rows
   int sms;
   int clusters[9];  // [C]: clusters of C CTAs of the tensor-core kernel that run at once
 };
@@ -466,6 +481,8 @@ struct Plan {
 // kStreamCtas an SM at most: 8 experts of 1024 x 2048, a row each (288 CTAs),
 // 8.4 us streamed and 12.4 on the tensor cores, of 2048 x 768 (576) 8.3 and
 // 9.6, of 5173 x 1081 (1458) 17.6 and 13.5.
+// A handle that is to be exact is always streamed; every tile of 16 tokens
+// then decodes the weights again.
 constexpr int64_t kStreamRows = 16, kStreamRowsExperts = 6;
 constexpr int kStreamUnits = 64, kStreamCtas = 4;
 
@@ -478,9 +495,10 @@ Plan make_plan(const proj_w4_ctx* h, int64_t m, bool experts) {
   const int64_t per = 8 * s.NT;
   // of the experts that have rows, each has at most one part-filled tile
   s.tiles = experts ? std::min<int64_t>(p.E, m) + m / per : (m + per - 1) / per;
-  pl.tc = p.E > 1 ? rows > kStreamRowsExperts ||
-                        (p.KU < kStreamUnits && (p.RB + 1) / 2 * s.tiles > kStreamCtas * h->sms)
-                  : rows > kStreamRows;
+  pl.tc = !h->exact &&
+          (p.E > 1 ? rows > kStreamRowsExperts ||
+                         (p.KU < kStreamUnits && (p.RB + 1) / 2 * s.tiles > kStreamCtas * h->sms)
+                   : rows > kStreamRows);
   if (!pl.tc) {
     // Two blocks of rows share the loads of x where that leaves a CTA per SM
     // or so; K is split over a cluster while that puts at most two CTAs on an SM
@@ -546,6 +564,13 @@ int run(const char* call, proj_w4_handle h, const void* x, int64_t ldx, int64_t 
 extern "C" proj_w4_handle proj_w4_prepare(const void* codes, const void* scales, const void* zeros,
                                           int64_t experts, int64_t N, int64_t K, int64_t group,
                                           int dtype, int* status) {
+  return proj_w4_prepare_ex(codes, scales, zeros, experts, N, K, group, dtype, 0u, status);
+}
+
+extern "C" proj_w4_handle proj_w4_prepare_ex(const void* codes, const void* scales,
+                                             const void* zeros, int64_t experts, int64_t N,
+                                             int64_t K, int64_t group, int dtype, uint32_t flags,
+                                             int* status) {
   const char* const call = "proj_w4_prepare";
   auto refused = [&](int st, const char* why) -> proj_w4_handle {
     refuse(st, call, why);
@@ -558,6 +583,7 @@ extern "C" proj_w4_handle proj_w4_prepare(const void* codes, const void* scales,
     return refused(PROJ_EINVAL, "group is neither 32 nor a multiple of 64");
   if (dtype != PROJ_BF16 && dtype != PROJ_FP16)
     return refused(PROJ_EINVAL, "dtype is neither PROJ_BF16 nor PROJ_FP16");
+  if (flags & ~static_cast<uint32_t>(PROJ_W4_EXACT)) return refused(PROJ_EINVAL, "unknown flags");
   constexpr int64_t kMost = int64_t{1} << 20;
   if (experts > 1024 || N > kMost || K > kMost || group > kMost)
     return refused(PROJ_EUNSUPPORTED, "experts > 1024, or N, K or group > 2^20");
@@ -598,13 +624,20 @@ extern "C" proj_w4_handle proj_w4_prepare(const void* codes, const void* scales,
   p.zeros = zeros ? h->base + code_bytes + scale_bytes : nullptr;
   p.status = reinterpret_cast<uint32_t*>(h->base + code_bytes + scale_bytes + zero_bytes);
   const int64_t lanes = row_tiles * p.KU * 256, cells = row_tiles * p.NGp * 128;
+  // the status word, and behind it the word that says whether a scale is wide
+  e = cudaMemsetAsync(p.status, 0, 8, nullptr);
   pack_codes_kernel<<<static_cast<unsigned>((lanes + 255) / 256), 256>>>(
       static_cast<const uint8_t*>(codes), const_cast<uint4*>(p.codes), experts, N, K, p.RT, p.KU);
-  pack_scales_kernel<<<static_cast<unsigned>((cells + 255) / 256), 256>>>(
+  auto* const pack_scales =
+      dtype == PROJ_FP16 ? pack_scales_kernel<__half> : pack_scales_kernel<__nv_bfloat16>;
+  pack_scales<<<static_cast<unsigned>((cells + 255) / 256), 256>>>(
       static_cast<const uint16_t*>(scales), static_cast<const uint8_t*>(zeros),
-      const_cast<uint16_t*>(p.scales), const_cast<uint8_t*>(p.zeros), experts, N, NG, p.NGp, p.RT, group == 32);
-  e = cudaGetLastError();
-  if (e == cudaSuccess) e = cudaMemsetAsync(p.status, 0, 4, nullptr);
+      const_cast<uint16_t*>(p.scales), const_cast<uint8_t*>(p.zeros), experts, N, NG, p.NGp, p.RT,
+      group == 32, dtype == PROJ_FP16 ? 65504.f : 0x1.FEp127f, p.status + 1);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  uint32_t wide = 0;
+  if (e == cudaSuccess)
+    e = cudaMemcpyAsync(&wide, p.status + 1, 4, cudaMemcpyDeviceToHost, nullptr);
   if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
   if (e != cudaSuccess) {
     record_cuda(e, call);
@@ -613,6 +646,9 @@ extern "C" proj_w4_handle proj_w4_prepare(const void* codes, const void* scales,
     if (status) *status = PROJ_ECUDA;
     return nullptr;
   }
+  // Where s (q - z) leaves the range of the type, the tensor cores would be
+  // given infinities: such a handle streams at any number of rows.
+  h->exact = (flags & PROJ_W4_EXACT) || wide;
   if (status) *status = PROJ_OK;
   return h;
 }

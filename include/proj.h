@@ -438,12 +438,20 @@ int proj_gemv_static_status(proj_stream stream, uint32_t *code);
  * proj_w4_run_experts the same for rows sorted by expert.  Products are
  * summed in fp32 and rounded once, to the type of x.  Up to a few tokens per
  * matrix, s multiplies the fp32 sum of its group, so the 4-bit numbers enter
- * exactly.  For more (and for experts with K below 4096) s (q - z) is first
- * rounded to the type of x, as in a checkpoint that was dequantised to it; it
- * then has to lie in that type's range.  proj_w4_describe says which of the
- * two a call does.
+ * exactly.  For more (and for many experts with K below 4096, whatever their
+ * rows) s (q - z) is first rounded to the type of x, as in a checkpoint that
+ * was dequantised to it, which adds errors of the size of the output's own
+ * rounding.  proj_w4_describe says which of the two a call does.
+ * PROJ_W4_EXACT keeps a handle to the first at any number of rows, and so does
+ * a scale with which s (q - z) would leave the range of the type.
  */
 typedef struct proj_w4_ctx *proj_w4_handle;
+
+enum proj_w4_flags {
+    /* No rounding of s (q - z) in any call.  Beyond some 16 rows a matrix the
+     * weights are decoded again for every 16 rows, and calls take longer. */
+    PROJ_W4_EXACT = 1u << 0
+};
 
 /*
  * Repack E matrices (device to device; the sources are consumed before the
@@ -462,6 +470,11 @@ typedef struct proj_w4_ctx *proj_w4_handle;
 proj_w4_handle proj_w4_prepare(const void *codes, const void *scales, const void *zeros,
                                int64_t experts, int64_t N, int64_t K, int64_t group, int dtype,
                                int *status);
+
+/* As proj_w4_prepare, with flags of enum proj_w4_flags. */
+proj_w4_handle proj_w4_prepare_ex(const void *codes, const void *scales, const void *zeros,
+                                  int64_t experts, int64_t N, int64_t K, int64_t group, int dtype,
+                                  uint32_t flags, int *status);
 
 /*
  * out[i, n] = sum over k of x[i, k] w[0, n, k], i < m (E must be 1).

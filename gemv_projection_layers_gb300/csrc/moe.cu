@@ -51,13 +51,13 @@ __device__ __forceinline__ float exp_below(float v, float top) {
 // One warp chooses for one token; EPL = experts a lane holds (expert
 // i 32 + lane).  Lane j < k returns choice j (-1: none left) and its weight.
 template <int EPL>
-__device__ __forceinline__ void choose(const float* __restrict__ logits, int E, int k, int mode,
-                                       int lane, int& expert, float& weight) {
+__device__ __forceinline__ void choose(const float* logits, int E, int k, int mode, int lane,
+                                       int& expert, float& weight) {
   uint32_t key[EPL];
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
     const int e = i * 32 + lane;
-    key[i] = e < E ? order_key(__ldg(logits + e)) : 0u;
+    key[i] = e < E ? order_key(logits[e]) : 0u;
   }
   float all = 0.f;
   uint32_t top = 0u;
@@ -325,6 +325,23 @@ constexpr int kRowThreads = 256;
 
 __device__ __forceinline__ bool is_slot(int s, int64_t rows) { return s >= 0 && s < rows; }
 
+// The slots and weights of eight entries of a token from j0 on (-1: no row).
+// Kernels before this one on the stream may have made them, so they are read
+// by ordinary loads, as everything but a handle's weights is.
+struct Eight {
+  int s[8];
+  float w[8];
+  __device__ __forceinline__ void slots(const RowsParams& p, int64_t t, int j0) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s[j] = j0 + j < p.k ? p.slot[t * p.k + j0 + j] : -1;
+  }
+  __device__ __forceinline__ void weights(const RowsParams& p, int64_t t, int j0) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      w[j] = p.weight && j0 + j < p.k ? p.weight[t * p.k + j0 + j] : 1.f;
+  }
+};
+
 // Rows are read and written V elements at a time, as wide as every row's
 // alignment allows (16, 8 or 4 bytes, or single elements for an odd width);
 // a thread has U of them under way, so that narrow accesses keep about as
@@ -345,7 +362,6 @@ __global__ void __launch_bounds__(kRowThreads) gather_kernel(const RowsParams p)
   const int64_t t = blockIdx.x;
   const int64_t nvec = p.D / V, rows = p.m * p.k;
   const T* x = static_cast<const T*>(p.a) + t * p.lda;
-  const int32_t* slot = p.slot + t * p.k;
   T* xs = static_cast<T*>(p.out);
   for (int64_t v0 = static_cast<int64_t>(blockIdx.y) * kRowThreads * U + threadIdx.x; v0 < nvec;
        v0 += static_cast<int64_t>(gridDim.y) * kRowThreads * U) {
@@ -353,14 +369,18 @@ __global__ void __launch_bounds__(kRowThreads) gather_kernel(const RowsParams p)
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (v0 + u * kRowThreads < nvec) val[u] = load_vec<T, V>(x + (v0 + u * kRowThreads) * V);
-    for (int j = 0; j < p.k; ++j) {
-      const int s = __ldg(slot + j);
-      if (!is_slot(s, rows)) continue;
-      T* to = xs + s * p.ldo + v0 * V;
+    for (int j0 = 0; j0 < p.k; j0 += 8) {
+      Eight to;
+      to.slots(p, t, j0);
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (v0 + u * kRowThreads < nvec)
-          *reinterpret_cast<Vec<T, V>*>(to + u * kRowThreads * V) = val[u];
+      for (int j = 0; j < 8; ++j) {
+        if (!is_slot(to.s[j], rows)) continue;
+        T* at = xs + to.s[j] * p.ldo + v0 * V;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (v0 + u * kRowThreads < nvec)
+            *reinterpret_cast<Vec<T, V>*>(at + u * kRowThreads * V) = val[u];
+      }
     }
   }
 }
@@ -368,21 +388,6 @@ __global__ void __launch_bounds__(kRowThreads) gather_kernel(const RowsParams p)
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-
-// The slots and weights of eight entries of a token from j0 on (-1: no row).
-struct Eight {
-  int s[8];
-  float w[8];
-  __device__ __forceinline__ void slots(const RowsParams& p, int64_t t, int j0) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) s[j] = j0 + j < p.k ? __ldg(p.slot + t * p.k + j0 + j) : -1;
-  }
-  __device__ __forceinline__ void weights(const RowsParams& p, int64_t t, int j0) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      w[j] = p.weight && j0 + j < p.k ? __ldg(p.weight + t * p.k + j0 + j) : 1.f;
-  }
-};
 
 // The combine is bound by the loads of k rows per token from anywhere.  A CTA
 // takes pieces (token, 4 KB of columns, eight entries) in turn and has the rows
@@ -563,9 +568,9 @@ __global__ void __launch_bounds__(kRowThreads) combine_grad_kernel(const RowsPar
     float w[KJ], dot[KJ];
 #pragma unroll
     for (int j = 0; j < KJ; ++j) {
-      s[j] = j0 + j < p.k ? __ldg(slot + j0 + j) : -1;
+      s[j] = j0 + j < p.k ? slot[j0 + j] : -1;
       if (!is_slot(s[j], rows)) s[j] = -1;
-      w[j] = s[j] >= 0 && p.out ? (p.weight ? __ldg(p.weight + t * p.k + j0 + j) : 1.f) : 0.f;
+      w[j] = s[j] >= 0 && p.out ? (p.weight ? p.weight[t * p.k + j0 + j] : 1.f) : 0.f;
       dot[j] = 0.f;
     }
     for (int64_t v0 = threadIdx.x; v0 < nvec; v0 += kRowThreads * U) {
@@ -659,7 +664,7 @@ __global__ void __launch_bounds__(32 * kGradWarps) route_grad_kernel(const Route
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
       const int x = i * 32 + lane;
-      key[i] = x < p.E ? order_key(__ldg(p.logits + t * p.ldl + x)) : 0u;
+      key[i] = x < p.E ? order_key(p.logits[t * p.ldl + x]) : 0u;
       top = max(top, key[i]);
     }
     top = __reduce_max_sync(0xFFFFFFFFu, top);

@@ -700,8 +700,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kThreads < 512 ? 512 / S::kThr
 // kSumWarps-th row of 32 columns, then meet in shared memory.
 constexpr int kSumWarps = 32;
 __global__ void __launch_bounds__(32 * kSumWarps)
-    norm_grad_sum_kernel(const float* __restrict__ part, int rows, int D, float* d0, float* d1,
-                         float* d2) {
+    norm_grad_sum_kernel(const float* part, int rows, int D, float* d0, float* d1, float* d2) {
   __shared__ float room[kSumWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int which = blockIdx.y;

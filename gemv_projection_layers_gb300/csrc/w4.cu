@@ -155,8 +155,8 @@ struct Tile {
 // row outside x is ever named.  Returns rows = 0 beyond the last tile.  All
 // threads of the block call it.
 template <int kThreads>
-__device__ __forceinline__ Tile find_tile(const int32_t* __restrict__ offsets, int E, int64_t m,
-                                          int T, int index) {
+__device__ __forceinline__ Tile find_tile(const int32_t* offsets, int E, int64_t m, int T,
+                                          int index) {
   __shared__ int s_sum[32];
   __shared__ int s_found[3];
   constexpr int W = kThreads / 32;
@@ -168,8 +168,8 @@ __device__ __forceinline__ Tile find_tile(const int32_t* __restrict__ offsets, i
     const int e = e0 + threadIdx.x;
     int lo = 0, hi = 0;
     if (e < E) {
-      lo = min(max(__ldg(offsets + e), 0), lim);
-      hi = min(max(__ldg(offsets + e + 1), lo), lim);
+      lo = min(max(offsets[e], 0), lim);
+      hi = min(max(offsets[e + 1], lo), lim);
     }
     const int tiles = (hi - lo + T - 1) / T;
     int inc = tiles;

@@ -309,8 +309,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int e = threadIdx.x * kPer + i;
       tiles[i] = 0;
       if (e < p.E) {
-        const int lo = min(max(__ldg(p.offsets + e), 0), items.m);
-        const int hi = min(max(__ldg(p.offsets + e + 1), lo), items.m);
+        const int lo = min(max(p.offsets[e], 0), items.m);
+        const int hi = min(max(p.offsets[e + 1], lo), items.m);
         s_off[e] = lo;
         s_end[e] = hi;
         tiles[i] = (hi - lo + TN - 1) / TN;

@@ -71,9 +71,19 @@ __device__ __forceinline__ void act_all(float (&g)[E], int kind) {
 #pragma unroll
   for (int i = 0; i < E; ++i) g[i] = sigmoid<T>(g[i]);
 }
-// d act / d gate from the activated value.
-__device__ __forceinline__ float act_slope(float g, int kind) {
-  return kind == PROJ_GATE_SIGMOID ? g * (1.f - g) : 1.f;
+// d act / d gate, from the gate x and its value g: 1, or the sigmoid's
+// sigmoid(x) sigmoid(-x).  1 - g cancels where the gate is open (in fp32 a
+// relative error of 1e-4 at x = 8, and nothing is left from x = 17), so there
+// sigmoid(-x) = exp(-x) g.
+template <typename T>
+__device__ __forceinline__ float act_slope(float x, float g, int kind) {
+  if (kind != PROJ_GATE_SIGMOID) return 1.f;
+  float e;
+  if constexpr (sizeof(T) == 2)
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
+  else
+    e = expf(-x);
+  return g * (x > 0.f ? e * g : 1.f - g);
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
@@ -463,7 +473,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kThreads < 512 ? 512 / S::kThr
   // second pass makes them anew.
   constexpr bool kKeep = NV * E <= 8 && TPR <= 512;
   constexpr int kKept = kKeep ? NV : 1;
-  const F2 zero = f2(0.f), one = f2(1.f), minus = f2(-1.f);
+  const F2 zero = f2(0.f), one = f2(1.f);
   const F2 alpha = f2(a.alpha), beta = f2(a.beta);
   // dw_post and dw_pre; for a gate per channel the first holds sum_rows beta du yn,
   // of which dw_post is g times and the gate's gradient n / yn act' times
@@ -488,8 +498,8 @@ __global__ void __launch_bounds__(S::kThreads, S::kThreads < 512 ? 512 / S::kThr
     const float ru_row = ru_next;
     const F2 ru = f2(ru_row);
     factors(row + static_cast<int64_t>(gridDim.x) * S::kRows);
-    const float g_row =
-        g_token ? act<T>(to_f32(static_cast<const T*>(a.gate)[row]), a.gate_act) : 1.f;
+    const float raw_row = g_token ? to_f32(static_cast<const T*>(a.gate)[row]) : 1.f;
+    const float g_row = g_token ? act<T>(raw_row, a.gate_act) : 1.f;
     // group j's yn, n, un, dh, t = dh w_pre and e = du' + ru t, and w_post, with the
     // activated gate in g
     F2 yn_[kKept][H], n_[kKept][H], un_[kKept][H], dh_[kKept][H], t_[kKept][H], e_[kKept][H],
@@ -594,7 +604,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kThreads < 512 ? 512 / S::kThr
     const F2 s2 = f2(normed ? -(g_token ? g_row * ab : ab) * inv_d : 0.f);
     const F2 minus_s1 = f2(-s1);
     if (g_token && a.dgate && tid == 0)
-      static_cast<T*>(a.dgate)[row] = from_f32<T>(ab * act_slope(g_row, a.gate_act));
+      static_cast<T*>(a.dgate)[row] = from_f32<T>(ab * act_slope<T>(raw_row, g_row, a.gate_act));
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       if (!reaches<S>(j, tid, D)) break;
@@ -632,12 +642,14 @@ __global__ void __launch_bounds__(S::kThreads, S::kThreads < 512 ? 512 / S::kThr
       if (a.gate_mode == PROJ_GATE_ELEMENT && a.dgate) {
 #pragma unroll
         for (int i = 0; i < H; ++i) o[i] = mul2(n[i], e[i]);
-        if (a.gate_act == PROJ_GATE_SIGMOID) {
-#pragma unroll
-          for (int i = 0; i < H; ++i)
-            o[i] = mul2(o[i], mul2(g[j][i], fma2(g[j][i], minus, one)));
-        }
         unpair<E>(o, out);
+        if (a.gate_act == PROJ_GATE_SIGMOID) {
+          float v[E], gv[E];
+          at.load(2, j, v);
+          unpair<E>(g[j], gv);
+#pragma unroll
+          for (int i = 0; i < E; ++i) out[i] *= act_slope<T>(v[i], gv[i], PROJ_GATE_SIGMOID);
+        }
         store_global<S>(static_cast<T*>(a.dgate) + row * a.lddg, j, tid, D, out);
       }
     }
@@ -660,7 +672,6 @@ __global__ void __launch_bounds__(S::kThreads, S::kThreads < 512 ? 512 / S::kThr
     if (g_channel) {
       float w[E];
       load_global<S>(static_cast<const T*>(a.gate), j, tid, D, gate);
-      act_all<T>(gate, a.gate_act);
       if (a.w_post) {
         load_global<S>(static_cast<const T*>(a.w_post), j, tid, D, w);
       } else {
@@ -669,9 +680,10 @@ __global__ void __launch_bounds__(S::kThreads, S::kThreads < 512 ? 512 / S::kThr
       }
 #pragma unroll
       for (int i = 0; i < E; ++i) {
-        const float q = post[i];
-        post[i] = gate[i] * q;
-        gate[i] = w[i] * act_slope(gate[i], a.gate_act) * q;
+        // fp32 outputs, once a column: the exact exponential whatever T is
+        const float q = post[i], g = act<float>(gate[i], a.gate_act);
+        post[i] = g * q;
+        gate[i] = w[i] * act_slope<float>(gate[i], g, a.gate_act) * q;
       }
     }
 #pragma unroll

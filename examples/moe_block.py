@@ -60,7 +60,13 @@ class MoeBlock:
         self.room = torch.zeros(max(16, B.proj_moe_workspace(tokens, EXPERTS, k)), device="cuda", dtype=torch.uint8)
 
     def __call__(self, residual: torch.Tensor, stream=None):
-        """(new residual, input of the next block), views of the block's buffers."""
+        """(new residual, input of the next block), views of the block's buffers.  Everything runs on `stream`
+        (a torch stream; left out: torch's current one), the gated unit between the products included."""
+        stream = stream or torch.cuda.current_stream()
+        with torch.cuda.stream(stream):
+            return self._steps(residual, stream)
+
+    def _steps(self, residual: torch.Tensor, stream):
         m, k, D, F = residual.shape[0], self.k, HIDDEN, self.inner
         common = dict(m=m, D=D, dtype=B.PROJ_BF16, eps=1e-6, residual=residual, ldr=D)
         B.proj_norm(B.norm_args(**common, w_pre=self.w_in, normed=self.h, ldn=D), stream)

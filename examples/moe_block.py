@@ -38,7 +38,7 @@ class MoeBlock:
     def __init__(self, tokens: int, inner: int = 256, k: int = 8, group: int = 128, seed: int = 0):
         gen = torch.Generator("cuda").manual_seed(seed)
         rand = lambda *s: torch.randn(*s, device="cuda", generator=gen)  # noqa: E731
-        self.k, self.inner, self.group = k, inner, group
+        self.tokens, self.k, self.inner, self.group = tokens, k, inner, group
         self.w_router = rand(EXPERTS, HIDDEN) / HIDDEN ** 0.5
         up = rand(EXPERTS, 2 * inner, HIDDEN) / HIDDEN ** 0.5
         down = rand(EXPERTS, HIDDEN, inner) / inner ** 0.5
@@ -62,6 +62,8 @@ class MoeBlock:
     def __call__(self, residual: torch.Tensor, stream=None):
         """(new residual, input of the next block), views of the block's buffers.  Everything runs on `stream`
         (a torch stream; left out: torch's current one), the gated unit between the products included."""
+        if residual.shape[0] > self.tokens or residual.shape[1:] != (HIDDEN,) or not residual.is_contiguous():
+            raise ValueError(f"residual: at most {self.tokens} contiguous rows of {HIDDEN}, not {tuple(residual.shape)}")
         stream = stream or torch.cuda.current_stream()
         with torch.cuda.stream(stream):
             return self._steps(residual, stream)

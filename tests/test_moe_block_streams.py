@@ -1,4 +1,4 @@
-"""examples/moe_block.py: every step of the block on one stream."""
+"""examples/moe_block.py: every step of the block on one stream, and no more than its buffers hold."""
 import contextlib
 import importlib.util
 
@@ -71,6 +71,20 @@ def test_every_step_on_one_stream(given, monkeypatch):
     assert len(seen) == 9
     assert {stream for _, stream in seen} == {given or "current"}, seen
     assert current.stream == "current"
+
+
+@pytest.mark.parametrize("rows,width", [(4, 0), (3, -8), (3, 8)])
+def test_a_residual_that_does_not_fit_is_refused(rows, width, monkeypatch):
+    """Before any step: the calls would run past the block's buffers or the residual's."""
+    ex, seen = example(), []
+    monkeypatch.setattr(ex, "B", Library(seen))
+    Current(monkeypatch, "current")
+    block = block_without_device(ex, 3)
+    with pytest.raises(ValueError):
+        block(torch.zeros(rows, ex.HIDDEN + width))
+    with pytest.raises(ValueError):
+        block(torch.zeros(3, 2 * ex.HIDDEN)[:, ::2])
+    assert not seen
 
 
 @pytest.mark.gpu

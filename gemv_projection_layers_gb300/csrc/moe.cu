@@ -11,7 +11,9 @@
 // shared atomic additions are of whole numbers, whose order does not matter).
 // One block: one launch does everything.  More: a first launch chooses and
 // counts, a second places.  (4096 tokens, 8 of 256 experts: 11 and 13 us; the
-// choice is bound by its instructions, some 970 a token and warp.)
+// choice is bound by its instructions, some 970 a token and warp.)  Of few
+// blocks each sums the counts of all; of more than kScanBlocks a launch
+// between the two does so once, or the time would grow with the tokens' square.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -115,6 +117,7 @@ struct SortParams {
   int E, k, mode;
   int tokens;  // per block
   int blocks;
+  bool scanned;  // the table holds sums over the blocks before, and behind them the totals
 };
 
 // Counts of each expert in the chunks of this block, from its entries'
@@ -227,6 +230,38 @@ __global__ void __launch_bounds__(kSortThreads) choose_count_kernel(const SortPa
   for (int i = kept + tid; i < n; i += kSortThreads) p.order[i] = -1;
 }
 
+// Turns the blocks' counts of 32 experts into the sums over the blocks before,
+// and writes the totals behind them: a lane an expert, a warp a run of blocks,
+// twice over the table.
+__global__ void __launch_bounds__(kSortThreads) scan_blocks_kernel(int32_t* table, int blocks,
+                                                                   int E) {
+  __shared__ int s_sum[kSortWarps][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int e = static_cast<int>(blockIdx.x) * 32 + lane;
+  const int b0 = static_cast<int>(static_cast<int64_t>(warp) * blocks / kSortWarps);
+  const int b1 = static_cast<int>(static_cast<int64_t>(warp + 1) * blocks / kSortWarps);
+  griddep_launch_dependents();
+  griddep_wait();
+  int sum = 0;
+  if (e < E) {
+#pragma unroll 8
+    for (int b = b0; b < b1; ++b) sum += table[static_cast<int64_t>(b) * E + e];
+  }
+  s_sum[warp][lane] = sum;
+  __syncthreads();
+  if (e >= E) return;
+  int run = 0;
+  for (int w = 0; w < warp; ++w) run += s_sum[w][lane];
+#pragma unroll 8
+  for (int b = b0; b < b1; ++b) {
+    int32_t* const at = table + static_cast<int64_t>(b) * E + e;
+    const int v = *at;
+    *at = run;
+    run += v;
+  }
+  if (warp == kSortWarps - 1) table[static_cast<int64_t>(blocks) * E + e] = run;
+}
+
 // Places the entries of one block, from every block's counts.
 __global__ void __launch_bounds__(kSortThreads) place_kernel(const SortParams p) {
   extern __shared__ __align__(16) uint16_t s_table[];
@@ -255,9 +290,14 @@ __global__ void __launch_bounds__(kSortThreads) place_kernel(const SortParams p)
     if (real && last) s_table[c * p.E + e] = static_cast<uint16_t>(count);
   }
   // Every block's counts, by as many threads per expert as there are (sums of
-  // whole numbers: their order does not matter).
+  // whole numbers: their order does not matter), where nobody has summed them.
   const int parts = kSortThreads / p.E;
-  if (tid < parts * p.E) {
+  if (p.scanned) {
+    if (tid < p.E) {
+      s_base[tid] = p.table[static_cast<int64_t>(blockIdx.x) * p.E + tid];
+      s_total[tid] = p.table[static_cast<int64_t>(p.blocks) * p.E + tid];
+    }
+  } else if (tid < parts * p.E) {
     const int e = tid % p.E;
     int before = 0, total = 0;
 #pragma unroll 8
@@ -736,6 +776,13 @@ int64_t sort_blocks(int64_t m, int E, int k) {
   const int tokens = sort_tokens(m, E, k);
   return (m + tokens - 1) / tokens;
 }
+// Blocks beyond which their counts are summed by a launch of its own.  (Sort of
+// 8 of 256 experts, every block for itself and by one launch: 196 blocks 52.0
+// and 52.8 us, 261 blocks 54.0 and 51.4, 1366 blocks 363 and 212; 8 of 1024,
+// 2^20 tokens in 5462 blocks: 12,036 and 397.)
+constexpr int64_t kScanBlocks = 256;
+// Rows of the table in the workspace.
+int64_t table_rows(int64_t blocks) { return blocks > kScanBlocks ? blocks + 1 : blocks; }
 size_t sort_smem(int tokens, int E, int k) {
   const int chunks = (tokens * k + 31) / 32;
   return (static_cast<size_t>(chunks) * E * 2 + 15) & ~static_cast<size_t>(15);
@@ -770,6 +817,11 @@ cudaError_t sort_launch(const SortParams& p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
   }
   cudaLaunchAttribute attr[1];
+  if (p.scanned) {
+    const cudaLaunchConfig_t cfg = config((p.E + 31) / 32, 1, kSortThreads, 0, s, attr);
+    e = cudaLaunchKernelEx(&cfg, scan_blocks_kernel, p.table, p.blocks, p.E);
+    if (e != cudaSuccess) return e;
+  }
   const cudaLaunchConfig_t cfg = config(p.blocks, 1, kSortThreads, smem, s, attr);
   return cudaLaunchKernelEx(&cfg, place_kernel, p);
 }
@@ -804,12 +856,13 @@ int sort_call(const char* call, SortParams p, void* workspace, int64_t workspace
   p.tokens = sort_tokens(p.m, p.E, p.k);
   p.blocks = static_cast<int>(sort_blocks(p.m, p.E, p.k));
   if (p.offsets && p.blocks > 1) {
-    const int64_t want = static_cast<int64_t>(p.blocks) * p.E * 4;
+    const int64_t want = table_rows(p.blocks) * p.E * 4;
     if (!workspace || workspace_bytes < want)
       return refuse(PROJ_EINVAL, call, "workspace is NULL or too small");
     if (!aligned_to(workspace, 16))
       return refuse(PROJ_EALIGN, call, "workspace is not 16-byte aligned");
     p.table = static_cast<int32_t*>(workspace);
+    p.scanned = p.blocks > kScanBlocks;
   }
   const cudaError_t e = sort_launch(p, s);
   return e == cudaSuccess ? PROJ_OK : record_cuda(e, call);
@@ -910,7 +963,7 @@ extern "C" int64_t proj_moe_workspace(int64_t m, int64_t experts, int64_t k) {
     return -1;
   }
   const int64_t blocks = sort_blocks(m, static_cast<int>(experts), static_cast<int>(k));
-  return blocks > 1 ? blocks * experts * 4 : 0;
+  return blocks > 1 ? table_rows(blocks) * experts * 4 : 0;
 }
 
 extern "C" int proj_moe_route(const float* logits, int64_t ldl, int64_t m, int64_t experts,

@@ -346,7 +346,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     items.off = s_off;
     items.end = s_end;
     items.tile = s_pre[p.E] <= kTileTable ? s_tile : nullptr;
-    all_items = s_pre[p.E] * items.RT;
+    // offsets that decrease all the same can claim rows twice: no more tiles are
+    // worked on than the launch was planned for (with C > 1 one item a cluster)
+    all_items = min(s_pre[p.E], min(p.E, items.m) + items.m / TN) * items.RT;
   } else {
     __syncthreads();  // the barriers are initialised
     items.pre = nullptr;

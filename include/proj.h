@@ -488,8 +488,9 @@ int proj_w4_run(proj_w4_handle h, const void *x, int64_t ldx, int64_t m, void *o
 /*
  * Rows offsets[e] .. offsets[e + 1] - 1 of x meet matrix e.  offsets: E + 1
  * int32 on the device, not decreasing, 0 .. m (values outside are moved into
- * that range).  Rows that belong to no expert are not read, and their rows of
- * out keep what they held.
+ * that range; if they decrease all the same, a row that several experts claim
+ * meets some of them or none).  Rows that belong to no expert are not read, and
+ * their rows of out keep what they held.
  */
 int proj_w4_run_experts(proj_w4_handle h, const void *x, int64_t ldx, int64_t m,
                         const int32_t *offsets, void *out, int64_t ldo, proj_stream stream);

@@ -34,6 +34,7 @@
 
 #include <algorithm>
 #include <cstdio>
+#include <cstring>
 #include <new>
 
 #include "../../include/proj.h"
@@ -667,14 +668,24 @@ extern "C" int proj_w4_run_experts(proj_w4_handle h, const void* x, int64_t ldx,
 extern "C" int proj_w4_describe(proj_w4_handle h, int64_t m, char* buf, size_t cap) {
   if (!h || !buf || cap == 0 || m < 0)
     return refuse(PROJ_EINVAL, "proj_w4_describe", "NULL handle or buffer, cap = 0 or m < 0");
-  const Plan pl = make_plan(h, m, h->p.E > 1);
-  if (pl.tc)
-    std::snprintf(buf, cap, "w4 tcgen05, %d-token tiles, grid %lld, cluster %d, weights rounded to %s",
-                  pl.tn, static_cast<long long>(pl.grid), pl.C,
-                  h->dtype == PROJ_FP16 ? "fp16" : "bf16");
+  char text[2][128];
+  for (int experts = 0; experts < 2; ++experts) {
+    const Plan pl = make_plan(h, m, experts);
+    if (pl.tc)
+      std::snprintf(text[experts], sizeof text[experts],
+                    "w4 tcgen05, %d-token tiles, grid %lld, cluster %d, weights rounded to %s",
+                    pl.tn, static_cast<long long>(pl.grid), pl.C,
+                    h->dtype == PROJ_FP16 ? "fp16" : "bf16");
+    else
+      std::snprintf(text[experts], sizeof text[experts],
+                    "w4 stream, %d-token tiles, %d rows, cluster %d, exact 4-bit products",
+                    8 * pl.stream.NT, 16 * pl.stream.RB, pl.stream.C);
+  }
+  // a stack of one takes both calls
+  if (h->p.E == 1 && std::strcmp(text[0], text[1]))
+    std::snprintf(buf, cap, "%s; with offsets: %s", text[0], text[1]);
   else
-    std::snprintf(buf, cap, "w4 stream, %d-token tiles, %d rows, cluster %d, exact 4-bit products",
-                  8 * pl.stream.NT, 16 * pl.stream.RB, pl.stream.C);
+    std::snprintf(buf, cap, "%s", text[h->p.E > 1]);
   return PROJ_OK;
 }
 

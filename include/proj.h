@@ -496,7 +496,9 @@ int proj_w4_run_experts(proj_w4_handle h, const void *x, int64_t ldx, int64_t m,
                         const int32_t *offsets, void *out, int64_t ldo, proj_stream stream);
 
 /* The kernel and launch shape a call with m rows uses (at most `cap` bytes,
- * NUL-terminated). */
+ * NUL-terminated; 256 are enough).  For a handle of one matrix that is
+ * proj_w4_run's, and where proj_w4_run_experts differs, "; with offsets: " and
+ * its own behind it. */
 int proj_w4_describe(proj_w4_handle h, int64_t m, char *buf, size_t cap);
 
 /* Read and clear the handle's device status word (synchronises `stream`), as

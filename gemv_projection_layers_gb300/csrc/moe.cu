@@ -385,10 +385,12 @@ struct Eight {
 // Rows are read and written V elements at a time, as wide as every row's
 // alignment allows (16, 8 or 4 bytes, or single elements for an odd width);
 // a thread has U of them under way, so that narrow accesses keep about as
-// many bytes in flight as wide ones.  All of this is bound by HBM.  (Gather of
-// 4096 x 8 rows of 8192 bf16: 86 us, 7.0 TB/s; of 2000 x 6 rows of 5001: 33 us,
-// 4.2 TB/s.  Gradient of the combine, 1000 tokens x 6 of 4100 fp16: 29 us, 3.6
-// TB/s.)
+// many bytes in flight as wide ones.  Rows on 16 bytes are bound by HBM (gather
+// of 4096 x 8 rows of 8192 bf16: 92 us, 6.6 TB/s), others by the number of
+// accesses (of 2000 x 6 rows of 5001: 32 us, 4.4 TB/s).  (Gradient of the
+// combine, the same tensors: 174 us, 6.6 TB/s, and 67 us, 3.9 TB/s; 1000 tokens
+// x 6 of 4100 fp16: 23 us, 4.6 TB/s, where the third trip of a row of 1025
+// words has one thread at work.)
 template <typename T, int V>
 constexpr int kAhead = 16 / (V * static_cast<int>(sizeof(T))) < 8
                            ? 16 / (V * static_cast<int>(sizeof(T)))

@@ -22,12 +22,13 @@
 // others, and both passes over a row read shared memory.  The gradient's
 // column sums stay in registers over all of a CTA's rows and meet in a second
 // kernel, in a fixed order.  The forward kernel comes to 0.8 of the measured
-// copy rate (8192 x 8192 bf16, a gate per element: 125 us, 5.4 TB/s); the
+// copy rate (8192 x 8192 bf16, a gate per element: 125 us, 5.4 TB/s).  The
 // gradient, with its column sums in registers, has 16 warps an SM -- of long
-// rows, one row at a time -- and its two passes (some 100 instructions an
-// element) and their barrier bound it: 315 us there, 3.4 TB/s; 64 us for 8192 x
-// 1024 (2.1 TB/s), where a row is worked on by four warps with eight elements a
-// thread, 75 with sixteen; 34 us for 8192 x 512 by a warp a row.
+// rows, one row at a time: 55 % of the cycles issue one of its some 100
+// instructions an element, in the others its warps wait for their operands or
+// at the barrier between the passes, and there is no other row to turn to.  (8192 rows bf16, a sigmoid gate per element: 8192 columns 320 us,
+// 3.4 TB/s; 1024, where four warps work on a row, 71 us, 1.9 TB/s; 512, a warp a
+// row, 30 us.)
 //
 // Rows that do not start on 16 bytes (an odd D, say) keep their misalignment
 // in shared memory, where the 16-byte words that hold them go, and the threads
@@ -48,8 +49,8 @@ namespace {
 constexpr int kMaxD = 16384;
 
 // The sigmoid's exponential and reciprocal: the 16-bit types' outputs are
-// rounded to 2^-8 or 2^-11, so the hardware's approximations (2^-21 or so) do;
-// fp32 takes expf and a true quotient.
+// rounded to 2^-8 or 2^-11, so the hardware's approximations (2^-21 or so, of
+// the value and of the slope) do; fp32 takes expf and a true quotient.
 template <typename T>
 __device__ __forceinline__ float sigmoid(float g) {
   if constexpr (sizeof(T) == 2) {

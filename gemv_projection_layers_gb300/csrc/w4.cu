@@ -4,13 +4,15 @@
 //   out[i, n] = sum_g s[n, g] sum_{k in g} (q[n, k] - z[n, g]) x[i, k]
 //
 // The weights are read once, as 4 bits; the kernel's floor is their bytes.
-// What bounds the streaming kernel is the decode all the same: some 200
-// instructions a warp for 32 rows x 64 columns (44 to make the operands of one
-// block of 16 rows, the MMAs, the scales, the loads), at about one issue in two
-// cycles with the 16 warps that 128 registers leave an SM.  (4096 x 8192, 8
-// tokens, groups of 64 with zeros: 9.5 us, 1.9 TB/s; 8192 x 1024, 1 token: 3.6
-// us back to back, where a launch alone is 2.6; 64 rows over 256 experts of
-// 1024 x 8192: 76 us, 3.3 TB/s.)
+// The streaming kernel stays above it for two reasons of about equal weight: the
+// decode, some 200 instructions a warp for 32 rows x 64 columns (44 to make the
+// operands of one block of 16 rows, the MMAs, the scales, the loads), and the
+// latency of loads that go straight to registers, which the 16 warps that 128
+// registers leave an SM do not hide: they issue on one cycle in two.  (4096 x
+// 8192, groups of 128, 8 tokens: 10.0 us with the weights in HBM, 8.7 in L2,
+// where its bf16 form takes 13.1; 8192 x 1024, 1 token: 3.4 and 3.0 us, where a
+// launch alone is 2.6; 64 rows over 256 experts of 1024 x 8192: 75 us, 3.3
+// TB/s.)
 // Each product is one step of the warp-level MMA m16n8k16 with 16 weight rows
 // on its M side and 8 tokens on its N side.  The integers q - z (at most five
 // bits) are exact in bf16 and fp16, so a group's sum is the exact products'

@@ -35,9 +35,9 @@ struct W4Params {
   }
 };
 
-// The tensor-core kernel (w4_tc.cu): token tiles of tn = 64, 128 or, for one
-// matrix, 256; clusters of C CTAs along K (C > 1: grid = C times the number of
-// items, one matrix).
+// The tensor-core kernel (w4_tc.cu): token tiles of tn = 64, 128 or, without
+// offsets, 256; clusters of C CTAs along K (C > 1: grid = C times the most items
+// that a call of that size can have).
 cudaError_t w4_tc_launch(bool fp16, int tn, const W4Params& p, int64_t grid, int C,
                          cudaStream_t s);
 

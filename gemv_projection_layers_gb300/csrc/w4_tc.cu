@@ -26,13 +26,14 @@
 // columns.
 // What bounds it: at few tokens the decode warps.  A pair of weights costs 0.75
 // shifts, a mask-or, a subtraction and a multiplication, a step of 128 x 128
-// some 350 issue slots of each scheduler, and the roles' waits come on top: a
-// step takes about 1000 cycles, in which HBM would deliver more than twice its
-// 8.5 KB.  (256 experts of 8192 x 512 in groups of 32 with zeros, 8000 rows
-// spread 1 / rank: 272 us, 2.86 TB/s of the 775 MB that it reads and writes;
+// some 350 issue slots of each scheduler, and waits come on top (a decode group
+// asks for a step's x and waits for it within that step): a step takes about
+// 1000 cycles, in which HBM would deliver more than twice its 8.5 KB.  (256
+// experts of 8192 x 512 in groups of 32 with zeros, 8000 rows spread 1 / rank:
+// 274 us, 2.83 TB/s of the 775 MB that it reads and writes;
 // DRAM traffic is 742 MB, so nothing is read twice.)  At 256 tokens the MMAs
 // and x: 64 KB of x a step from L2, eight MMAs of 128 x 256 x 16.  (8192 x
-// 4096, 256 tokens: 18.9 us, 0.91 PFLOP/s.)
+// 4096, 256 tokens: 18.8 us, 0.91 PFLOP/s, from L2 and from HBM alike.)
 //
 // Where there are few tiles, a cluster of C CTAs splits K, and the partial
 // sums meet in rank order through distributed shared memory.
@@ -85,7 +86,7 @@ struct Cfg {
   static constexpr int kBars = 2 * S + 2 * SA + 2 * SW + 6;
   static constexpr int kRing = S * kStage;        // the partial sums' staging afterwards
   static constexpr int kBarsAt = kRing + SW * kWStage;
-  // rings, barriers, tensor-memory address, and for experts (TN = 128) the
+  // rings, barriers, tensor-memory address, and for experts (TN up to 128) the
   // tile and row tables
   static constexpr int kTables = kBarsAt + kBars * 8 + 16;
   static constexpr int kSmem =

@@ -38,6 +38,7 @@ PROJ_W4_EXACT = 1  # proj_w4_prepare_ex: no rounding of s (q - z) at any number 
 PROJ_ROUTE_CHOSEN, PROJ_ROUTE_ALL = 0, 1  # proj_moe_route: softmax over the chosen / all logits
 PROJ_GATE_NONE, PROJ_GATE_CHANNEL, PROJ_GATE_ELEMENT, PROJ_GATE_TOKEN = range(4)
 PROJ_GATE_LINEAR, PROJ_GATE_SIGMOID = 0, 1
+PROJ_KV_ROWS, PROJ_KV_E4M3, PROJ_KV_INT8 = range(3)  # entries of a key and value cache
 
 LAYER_INDEX = {"qkv_gate": 0, "o": 1, "pooler": 2, "unpooler": 3, "router": 4}
 
@@ -93,6 +94,26 @@ class proj_norm_grad_args(ctypes.Structure):
                              ("dgate", ctypes.c_void_p), ("lddg", ctypes.c_int64),
                              ("dw_post", ctypes.c_void_p), ("dw_pre", ctypes.c_void_p),
                              ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)]
+
+
+class proj_kv_cache(ctypes.Structure):
+    _fields_ = [("format", ctypes.c_int), ("dtype", ctypes.c_int), ("pages", ctypes.c_int64),
+                ("page", ctypes.c_int64), ("heads", ctypes.c_int64), ("D", ctypes.c_int64),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("table", ctypes.c_void_p), ("ldt", ctypes.c_int64), ("width", ctypes.c_int64),
+                ("sequences", ctypes.c_int64)]
+
+
+class proj_attn_args(ctypes.Structure):
+    _fields_ = [("cache", ctypes.c_void_p), ("m", ctypes.c_int64), ("heads", ctypes.c_int64),
+                ("q", ctypes.c_void_p), ("ldq", ctypes.c_int64), ("offsets", ctypes.c_void_p),
+                ("start", ctypes.c_void_p), ("mask", ctypes.c_void_p), ("ldm", ctypes.c_int64),
+                ("words", ctypes.c_int64), ("scale", ctypes.c_float), ("gate_act", ctypes.c_int),
+                ("gate", ctypes.c_void_p), ("ldg", ctypes.c_int64), ("out", ctypes.c_void_p),
+                ("ldo", ctypes.c_int64), ("lse", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)]
 
 
 _lib = None
@@ -185,6 +206,21 @@ def load() -> ctypes.CDLL:
     lib.proj_norm_workspace.restype = i64
     lib.proj_norm_backward.argtypes = [ctypes.POINTER(proj_norm_grad_args), vp]
     lib.proj_norm_backward.restype = i32
+    cache = ctypes.POINTER(proj_kv_cache)
+    lib.proj_kv_write.argtypes = [cache, vp, vp, i64, vp, i64, vp, i64, vp]
+    lib.proj_kv_write.restype = i32
+    lib.proj_kv_read.argtypes = [cache, vp, vp, i64, vp, i64, vp, i64, vp]
+    lib.proj_kv_read.restype = i32
+    lib.proj_kv_move.argtypes = [cache, vp, vp, i64, i64, vp, vp]
+    lib.proj_kv_move.restype = i32
+    lib.proj_attn_workspace.argtypes = [cache, i64, i64]
+    lib.proj_attn_workspace.restype = i64
+    lib.proj_attn.argtypes = [ctypes.POINTER(proj_attn_args), vp]
+    lib.proj_attn.restype = i32
+    lib.proj_attn_describe.argtypes = [cache, i64, i64, ctypes.c_char_p, ctypes.c_size_t]
+    lib.proj_attn_describe.restype = i32
+    lib.proj_attn_device_status.argtypes = [vp, ctypes.POINTER(u32)]
+    lib.proj_attn_device_status.restype = i32
     _lib = lib
     return lib
 
@@ -204,6 +240,8 @@ def _addr(p) -> int | None:
     data_ptr = getattr(p, "data_ptr", None)
     if data_ptr is not None:
         return data_ptr()
+    if isinstance(p, ctypes.Structure):
+        return ctypes.addressof(p)
     if isinstance(p, int):
         return p
     if hasattr(p, "ctypes"):
@@ -498,3 +536,60 @@ def proj_norm_workspace(m: int, D: int) -> int:
 
 def proj_norm_backward(args: proj_norm_grad_args, stream=None) -> None:
     _checked(load().proj_norm_backward(ctypes.byref(args), _stream(stream)), "proj_norm_backward")
+
+
+# ------------------------------------------------ the cache of keys and values --
+
+def kv_cache(**named) -> proj_kv_cache:
+    """A proj_kv_cache from its fields by name (tensors, addresses or numbers; what is left out is 0
+    or NULL)."""
+    return _fill(proj_kv_cache(), named)
+
+
+def attn_args(cache: proj_kv_cache, **named) -> proj_attn_args:
+    """A proj_attn_args from a cache and its other fields by name (scale is 0 unless given)."""
+    return _fill(proj_attn_args(), {**named, "cache": cache})
+
+
+def proj_kv_write(cache: proj_kv_cache, offsets, start, m: int, k, ldk: int, v, ldv: int,
+                  stream=None) -> None:
+    _checked(load().proj_kv_write(ctypes.byref(cache), _addr(offsets), _addr(start), m, _addr(k),
+                                  ldk, _addr(v), ldv, _stream(stream)), "proj_kv_write")
+
+
+def proj_kv_read(cache: proj_kv_cache, offsets, start, m: int, k, ldk: int, v, ldv: int,
+                 stream=None) -> None:
+    _checked(load().proj_kv_read(ctypes.byref(cache), _addr(offsets), _addr(start), m, _addr(k),
+                                 ldk, _addr(v), ldv, _stream(stream)), "proj_kv_read")
+
+
+def proj_kv_move(cache: proj_kv_cache, start, path, ldp: int, depth: int, next_start=None,
+                 stream=None) -> None:
+    _checked(load().proj_kv_move(ctypes.byref(cache), _addr(start), _addr(path), ldp, depth,
+                                 _addr(next_start), _stream(stream)), "proj_kv_move")
+
+
+def proj_attn_workspace(cache: proj_kv_cache, m: int, heads: int) -> int:
+    n = int(load().proj_attn_workspace(ctypes.byref(cache), int(m), int(heads)))
+    if n < 0:
+        raise ProjError(proj_last_status(), f"proj_attn_workspace ({last_cuda_error()})")
+    return n
+
+
+def proj_attn(args: proj_attn_args, stream=None) -> None:
+    _checked(load().proj_attn(ctypes.byref(args), _stream(stream)), "proj_attn")
+
+
+def proj_attn_describe(cache: proj_kv_cache, m: int, heads: int) -> str:
+    buf = ctypes.create_string_buffer(256)
+    _checked(load().proj_attn_describe(ctypes.byref(cache), int(m), int(heads), buf, 256),
+             "proj_attn_describe")
+    return buf.value.decode()
+
+
+def proj_attn_device_status(stream=None) -> int:
+    code = ctypes.c_uint32(0)
+    st = load().proj_attn_device_status(_stream(stream), ctypes.byref(code))
+    if st not in (PROJ_OK, PROJ_EDEVICE):
+        raise ProjError(st, f"proj_attn_device_status ({last_cuda_error()})")
+    return int(code.value)

@@ -1,0 +1,828 @@
+// attn.cu -- attention of drafted tokens over the cache: the calls, the kernel
+// for few rows, and the join of partial results.
+//
+// The kernel for few rows (a group's heads times a sequence's drafts up to 32)
+// is a stream over the cache.  Per key and head it reads 2 D entries and does
+// 4 D operations a row, so with 8 rows and 8-bit entries the cache's bytes at
+// HBM's rate leave the tensor cores of the warp-level MMA a fifth of their
+// time; what counts is that the bytes flow.  Each of a CTA's eight warps has
+// a ring of its own in shared memory, filled by 16-byte asynchronous copies,
+// and takes every eighth 16 keys of the CTA's share: nothing but the end of an
+// item is a barrier for the CTA.
+//
+// Keys are the M side of both products, rows the N side (eight at a time, so
+// nothing is padded to 16):
+//   S^T [16 keys x 8 rows] = K [16 x D] Q^T,   O^T [D x 8 rows] += V^T [D x 16] P^T.
+// K and V come out of the ring as A fragments (ldmatrix, V transposed) and are
+// decoded in registers, once, for all rows: 8-bit codes are exact in fp16.  A
+// 16-bit unit of ldmatrix is then two codes, so the order of dimensions within
+// 16 is the one it gives, for Q alike, and output rows 2 i, 2 i + 1 are
+// neighbours.  P^T goes from accumulators to B fragments by transposing 8 x 8
+// blocks in registers.
+//
+// Softmax, one pass: each warp holds for its rows a reference m and sums
+// relative to 2^m.  A score beyond m + 6 moves m (a vote; no shuffles
+// otherwise), so with p = 2^(t - m + 8) at most 2^14 and, where it counts, at
+// least 2^-16 below that: in fp16's range, which ends at 2^16 and 2^-24.
+// Scales of V multiply p, relative to the largest one seen.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+#include <cstdio>
+#include <type_traits>
+
+#include "attn.h"
+#include "kernels.h"
+#include "kv_num.cuh"
+
+namespace proj {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+__device__ uint32_t g_attn_status;  // what bounded waits that gave up leave
+
+constexpr int kStep = 16;  // keys of a warp's step, the unit of work
+
+template <int kFormat, int D, int NT>
+struct Stream {
+  static constexpr int kRow = kFormat == PROJ_KV_ROWS ? 2 * D : D;  // bytes of an entry
+  static constexpr int kHalf = kStep * kRow;                       // K or V of a step
+  static constexpr int kStage = 2 * kHalf + 128;                   // and their scales
+  static constexpr int kStages = kRow == 256 ? 3 : kRow == 128 ? 6 : 8;
+  static constexpr int kRing = kStages * kStage;  // of a warp
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kPitch = D + 4;            // floats of a row in the merge
+  static constexpr int kMerge = kWarps * kRows * kPitch * 4;
+  static constexpr int kMl = kWarps * kRows * 8;
+  static constexpr int kSmem = (kWarps * kRing > kMerge ? kWarps * kRing : kMerge) + kMl;
+  static_assert(kSmem + 1024 <= 232448, "shared memory");
+};
+
+// Where 16-byte piece c of a row stands: eight rows' pieces of one column fall
+// into different banks.
+template <int kRow>
+__device__ __forceinline__ uint32_t place(int row, int c) {
+  const int turn = kRow == 64 ? (row >> 1) & 3 : row & 7;
+  return row * kRow + ((c ^ turn) << 4);
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t a) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+  return r;
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1, __half) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1, __nv_bfloat16) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float ld_shared_f(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+  return v;
+}
+
+// Whether one of a pair of 16-bit numbers is an infinity or a NaN.
+__device__ __forceinline__ bool odd_pair(uint32_t w, __half) {
+  return (w & 0x7C00u) == 0x7C00u || (w & 0x7C000000u) == 0x7C000000u;
+}
+__device__ __forceinline__ bool odd_pair(uint32_t w, __nv_bfloat16) {
+  return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+}
+
+template <typename T, int kFormat, int D, int NT>
+__global__ void __launch_bounds__(kThreads, 1) attn_stream_kernel(const AttnParams p) {
+  using F = Stream<kFormat, D, NT>;
+  constexpr bool kCoded = kFormat != PROJ_KV_ROWS;
+  using C = std::conditional_t<kCoded, __half, T>;  // what is multiplied
+  constexpr int kRow = F::kRow, S = F::kStages, KK = D / 16, kPieces = kRow / 16;
+  constexpr int kTurn = 32 / kPieces;  // rows that a warp copies at a time
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ uint32_t s_valid[kWarps][S];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, c4 = lane & 3;
+  const uint32_t ring = smem_u32(smem) + warp * F::kRing;
+  float* const merge = reinterpret_cast<float*>(smem);
+  float* const s_ml = reinterpret_cast<float*>(smem + F::kSmem - F::kMl);
+
+  griddep_launch_dependents();
+  griddep_wait();
+  Share share;
+  if (!find_share<kThreads>(p, blockIdx.x, share)) return;
+
+  const int G = static_cast<int>(p.group.d);
+  int b = share.b;
+  int64_t before = share.before;
+  Sequence seq = sequence_at(p, b);
+  for (int64_t at = share.first; at < share.end;) {
+    while (at >= before + units_of(p, seq)) {
+      before += units_of(p, seq);
+      if (++b >= p.c.sequences) return;
+      seq = sequence_at(p, b);
+    }
+    const int64_t local = at - before;
+    const int64_t item = local / seq.units;
+    const int u0 = static_cast<int>(local - item * seq.units);
+    const int u1 = static_cast<int>(min(static_cast<int64_t>(seq.units), u0 + (share.end - at)));
+    const int head = static_cast<int>(item / seq.tiles);
+    const int row0 = static_cast<int>(item - static_cast<int64_t>(head) * seq.tiles) * F::kRows;
+    const int all_rows = seq.rows * G;
+
+    // ------------------------------------------------------------ queries --
+    uint32_t qf[KK][NT][2];
+    float fq[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = row0 + nt * 8 + g;
+      const int t = quotient(r, p.group);
+      const uint8_t* from = p.q + (seq.lo + t) * p.ldq + static_cast<int64_t>(head * G + r - t * G) * D * 2;
+      const bool real = r < all_rows;
+      if constexpr (!kCoded) {
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk) {
+          qf[kk][nt][0] = real ? *reinterpret_cast<const uint32_t*>(from + kk * 32 + c4 * 4) : 0u;
+          qf[kk][nt][1] = real ? *reinterpret_cast<const uint32_t*>(from + kk * 32 + 16 + c4 * 4) : 0u;
+        }
+        fq[nt][0] = fq[nt][1] = p.scale_log2;
+      } else {
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk) {
+          const uint2 w = real ? *reinterpret_cast<const uint2*>(from + kk * 32 + c4 * 8) : make_uint2(0u, 0u);
+          qf[kk][nt][0] = w.x;
+          qf[kk][nt][1] = w.y;
+        }
+        float f = 1.f;
+        if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+          // bf16 to fp16: the row's largest magnitude is brought to 2^14 .. 2^15
+          uint32_t top = 0;
+#pragma unroll
+          for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              top = max(max(top, qf[kk][nt][i] & 0x7FFFu), qf[kk][nt][i] >> 16 & 0x7FFFu);
+          top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+          top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+          int e = 0;
+          if (top > 0 && top < 0x7F80u) {
+            const float v = __uint_as_float(top << 16);
+            e = 14 - ilogbf(v);
+          }
+          // two factors: 2^e alone can leave fp32's range
+          const float fa = scalbnf(1.f, e / 2), fb = scalbnf(1.f, e - e / 2);
+#pragma unroll
+          for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float x, y;
+              widen2(qf[kk][nt][i], x, y, __nv_bfloat16());
+              qf[kk][nt][i] = pack2(x * fa * fb, y * fa * fb, __half());
+            }
+          f = scalbnf(1.f, -e);
+        }
+        fq[nt][0] = __shfl_sync(0xFFFFFFFFu, f, c4 * 8) * p.scale_log2;
+        fq[nt][1] = __shfl_sync(0xFFFFFFFFu, f, c4 * 8 + 4) * p.scale_log2;
+      }
+    }
+
+    float o[KK][NT][4], ref[NT][2], sum[NT][2];
+    float v_ref = 0.f, v_inv = 0.f;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      ref[nt][0] = ref[nt][1] = kNoScore;
+      sum[nt][0] = sum[nt][1] = 0.f;
+#pragma unroll
+      for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[kk][nt][i] = 0.f;
+    }
+
+    // --------------------------------------------------------------- ring --
+    const int steps = u1 - u0 > warp ? (u1 - u0 - warp + kWarps - 1) / kWarps : 0;
+    const auto first_key = [&](int i) { return (u0 + warp + i * kWarps) * kStep; };
+    // the page of key `lane` (< 16) of step i, or -1
+    const auto page_id = [&](int i) {
+      const int pos = first_key(i) + lane;
+      if (i >= steps || lane >= kStep || pos >= seq.len) return -1;
+      return p.c.table[b * p.c.ldt + quotient(pos, p.c.page)];
+    };
+    const auto issue = [&](int i, int id) {
+      if (i < steps) {
+        const int slot = i % S;
+        const int pos = first_key(i) + lane;
+        const int spot = pos - quotient(pos, p.c.page) * static_cast<int>(p.c.page.d);
+        const bool ok = id >= 0 && id < p.c.pages;
+        const Entry e = ok ? entry_at(p.c, id, spot, head) : Entry{0, 0};
+        const uint32_t valid = __ballot_sync(0xFFFFFFFFu, ok) & 0xFFFFu;
+        const uint32_t stage = ring + slot * F::kStage;
+        if (lane == 0) s_valid[warp][slot] = valid;
+#pragma unroll
+        for (int j = 0; j < kStep / kTurn; ++j) {
+          const int key = j * kTurn + lane / kPieces, piece = lane % kPieces;
+          const int64_t from = __shfl_sync(0xFFFFFFFFu, e.at, key) + piece * 16;
+          const int bytes = valid >> key & 1 ? 16 : 0;
+          const uint32_t to = stage + place<kRow>(key, piece);
+          copy16(to, p.c.k + from, bytes);
+          copy16(to + F::kHalf, p.c.v + from, bytes);
+        }
+        if constexpr (kCoded) {
+          if (lane < kStep) {
+            copy4(stage + 2 * F::kHalf + lane * 4, p.c.k_scale + e.scale, ok ? 4 : 0);
+            copy4(stage + 2 * F::kHalf + 64 + lane * 4, p.c.v_scale + e.scale, ok ? 4 : 0);
+          }
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    int ids[S];
+#pragma unroll
+    for (int i = 0; i < S; ++i) ids[i] = page_id(i);
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) issue(i, ids[i]);
+    int next_id = ids[S - 1];
+
+    for (int i = 0; i < steps; ++i) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
+      __syncwarp();
+      {
+        const int id = next_id;
+        next_id = page_id(i + S);
+        issue(i + S - 1, id);
+      }
+      const int slot = i % S;
+      const uint32_t stage = ring + slot * F::kStage;
+      const int key0 = first_key(i);
+      const uint32_t valid = *reinterpret_cast<volatile uint32_t*>(&s_valid[warp][slot]);
+
+      // ---------------------------------------------------- S^T = K Q^T --
+      float s[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[nt][j] = 0.f;
+      // matrices: keys 0-7 and 8-15 of one piece, then of the next
+      const int mrow = (lane & 7) + (lane & 8), mpiece = lane >> 4;
+#pragma unroll
+      for (int kk = 0; kk < (kCoded ? KK / 2 : KK); ++kk) {
+        uint32_t w[4];
+        ldsm4(w, stage + place<kRow>(mrow, 2 * kk + mpiece));
+        if constexpr (kCoded) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t a[4] = {decode_pair<kFormat>(w[2 * h], 0), decode_pair<kFormat>(w[2 * h + 1], 0),
+                                   decode_pair<kFormat>(w[2 * h], 1), decode_pair<kFormat>(w[2 * h + 1], 1)};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma16816(s[nt], a, qf[2 * kk + h][nt][0], qf[2 * kk + h][nt][1], C());
+          }
+        } else {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma16816(s[nt], w, qf[kk][nt][0], qf[kk][nt][1], C());
+        }
+      }
+
+      // -------------------------------------------------------- softmax --
+      float vs[2] = {1.f, 1.f};
+      if constexpr (kCoded) {
+        const float ks[2] = {ld_shared_f(stage + 2 * F::kHalf + g * 4),
+                             ld_shared_f(stage + 2 * F::kHalf + g * 4 + 32)};
+        vs[0] = ld_shared_f(stage + 2 * F::kHalf + 64 + g * 4);
+        vs[1] = ld_shared_f(stage + 2 * F::kHalf + 96 + g * 4);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[nt][j] = s[nt][j] * fq[nt][j & 1] * ks[j >> 1];
+      } else {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[nt][j] *= fq[nt][j & 1];
+      }
+      // Steps with keys without a page or beyond the last, or with drafts: what
+      // a row does not see is taken out.  Bit 4 nt + j: seen.
+      const bool partial = valid != 0xFFFFu || key0 + kStep > seq.start;
+      uint32_t seen = 0xFFFFFFFFu;
+      if (partial) {
+        seen = 0;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int spot = g + (j >> 1) * 8, draft = key0 + spot - seq.start;
+            const int r = row0 + nt * 8 + c4 * 2 + (j & 1);
+            bool sees = (valid >> spot & 1) && r < all_rows;
+            if (sees && draft >= 0) {
+              const int t = quotient(r, p.group);
+              if (p.mask)
+                sees = (draft >> 5) < p.words && (p.mask[(seq.lo + t) * p.ldm + (draft >> 5)] >> (draft & 31) & 1);
+              else
+                sees = draft <= t;
+            }
+            if (sees)
+              seen |= 1u << (4 * nt + j);
+            else
+              s[nt][j] = -INFINITY;
+          }
+      }
+      bool beyond = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i2 = 0; i2 < 2; ++i2) beyond |= fmaxf(s[nt][i2], s[nt][2 + i2]) > ref[nt][i2] + 6.f;
+      if (__any_sync(0xFFFFFFFFu, beyond)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i2 = 0; i2 < 2; ++i2) {
+            float top = fmaxf(s[nt][i2], s[nt][2 + i2]);
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
+            top = fmaxf(top, ref[nt][i2]);
+            const float down = exp2_fast(ref[nt][i2] - top);
+            ref[nt][i2] = top;
+            sum[nt][i2] *= down;
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk) {
+              o[kk][nt][i2] *= down;
+              o[kk][nt][2 + i2] *= down;
+            }
+          }
+      }
+      if constexpr (kCoded) {
+        // scales that are no finite number do not enter the reference: they make
+        // p NaN for the rows that see the key, and only for those
+        if (!(vs[0] < INFINITY)) vs[0] = __uint_as_float(0x7FC00000u);
+        if (!(vs[1] < INFINITY)) vs[1] = __uint_as_float(0x7FC00000u);
+        float top = fmaxf(fabsf(vs[0]), fabsf(vs[1]));  // the finite one, if only one is
+        if (__any_sync(0xFFFFFFFFu, top > 2.f * v_ref)) {
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
+          top = fmaxf(fmaxf(top, v_ref), 1.17549435e-38f);  // its reciprocal is finite
+          const float down = v_ref / top;
+          v_ref = top;
+          v_inv = 1.f / top;
+#pragma unroll
+          for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) o[kk][nt][j] *= down;
+        }
+        vs[0] *= v_inv;
+        vs[1] *= v_inv;
+      }
+      uint32_t pb[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float e[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) e[j] = exp2_fast(s[nt][j] - (ref[nt][j & 1] - 8.f));
+        sum[nt][0] += e[0] + e[2];
+        sum[nt][1] += e[1] + e[3];
+        if constexpr (kCoded) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            e[j] = !partial || (seen >> (4 * nt + j) & 1) ? e[j] * vs[j >> 1] : 0.f;
+        }
+        pb[nt][0] = transpose8(pack2(e[0], e[1], C()));
+        pb[nt][1] = transpose8(pack2(e[2], e[3], C()));
+      }
+
+      // -------------------------------------------------- O^T += V^T P^T --
+      uint32_t odd = 0;
+      const int trow = (lane & 7) + (kCoded ? lane & 8 : lane >> 4 << 3);
+      const int tpiece = kCoded ? lane >> 4 : lane >> 3 & 1;
+      const auto v_frag = [&](int kk, uint32_t (&a)[4], uint32_t (&a2)[4]) {
+        // 8 bit: dimensions 32 kk .. + 31 as two fragments; 16 bit: 16 kk .. + 15
+        uint32_t w[4];
+        ldsm4t(w, stage + F::kHalf + place<kRow>(trow, 2 * kk + tpiece));
+        if constexpr (kCoded) {
+          decode_cross<kFormat>(w[0], a[0], a[1]);
+          decode_cross<kFormat>(w[1], a[2], a[3]);
+          decode_cross<kFormat>(w[2], a2[0], a2[1]);
+          decode_cross<kFormat>(w[3], a2[2], a2[3]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) a[j] = w[j];
+        }
+      };
+      constexpr int kSteps = kCoded ? KK / 2 : KK;
+      if (kFormat != PROJ_KV_INT8 && partial) {
+#pragma unroll 1
+        for (int kk = 0; kk < kSteps; ++kk) {
+          uint32_t a[4], a2[4] = {0u, 0u, 0u, 0u};
+          v_frag(kk, a, a2);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) odd |= odd_pair(a[j], C()) || odd_pair(a2[j], C());
+        }
+        odd = __any_sync(0xFFFFFFFFu, odd);
+      }
+      if (!odd) {
+#pragma unroll
+        for (int kk = 0; kk < kSteps; ++kk) {
+          uint32_t a[4], a2[4];
+          v_frag(kk, a, a2);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            if constexpr (kCoded) {
+              mma16816(o[2 * kk][nt], a, pb[nt][0], pb[nt][1], C());
+              mma16816(o[2 * kk + 1][nt], a2, pb[nt][0], pb[nt][1], C());
+            } else {
+              mma16816(o[kk][nt], a, pb[nt][0], pb[nt][1], C());
+            }
+          }
+        }
+      } else {
+        // A value of V in this step is no finite number, and 0 times it is NaN:
+        // key by key, added where the row sees the key.
+#pragma unroll
+        for (int kk = 0; kk < kSteps; ++kk) {
+          uint32_t a[2][4];
+          v_frag(kk, a[0], a[1]);
+#pragma unroll 1
+          for (int key = 0; key < kStep; ++key) {
+            const uint32_t sees = __shfl_sync(0xFFFFFFFFu, seen, (key & 7) * 4 + c4) >> (key & 8 ? 2 : 0);
+            const bool mine = (key & 7) >> 1 == c4;
+            const uint32_t half = mine ? (key & 1 ? 0xFFFF0000u : 0xFFFFu) : 0u;
+            const uint32_t lo = key & 8 ? 0u : half, hi = key & 8 ? half : 0u;
+#pragma unroll
+            for (int h = 0; h < (kCoded ? 2 : 1); ++h) {
+              const uint32_t one[4] = {a[h][0] & lo, a[h][1] & lo, a[h][2] & hi, a[h][3] & hi};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                float d[4] = {0.f, 0.f, 0.f, 0.f};
+                mma16816(d, one, pb[nt][0] & lo, pb[nt][1] & hi, C());
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  if (sees >> (4 * nt + (j & 1)) & 1) o[kCoded ? 2 * kk + h : kk][nt][j] += d[j];
+              }
+            }
+          }
+        }
+      }
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+
+    // --------------------------------------------- the warps' sums joined --
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) sum[nt][i] += __shfl_xor_sync(0xFFFFFFFFu, sum[nt][i], x);
+    __syncthreads();  // every warp is done with its ring
+    const float up = kCoded ? v_ref : 1.f;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = nt * 8 + c4 * 2 + i;
+        if (g == 0) {
+          s_ml[(warp * F::kRows + r) * 2] = ref[nt][i] - 8.f;
+          s_ml[(warp * F::kRows + r) * 2 + 1] = sum[nt][i];
+        }
+        float* to = merge + (warp * F::kRows + r) * F::kPitch;
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk) {
+          if constexpr (kCoded) {
+            *reinterpret_cast<float2*>(to + kk * 16 + 2 * g) =
+                make_float2(o[kk][nt][i] * up, o[kk][nt][2 + i] * up);
+          } else {
+            to[kk * 16 + g] = o[kk][nt][i];
+            to[kk * 16 + 8 + g] = o[kk][nt][2 + i];
+          }
+        }
+      }
+    }
+    __syncthreads();
+    const bool whole = u0 == 0 && u1 == seq.units;
+    const int slot = 2 * static_cast<int>(blockIdx.x) + (u0 == 0 ? 1 : 0);
+    for (int x = threadIdx.x; x < F::kRows * (D / 4); x += kThreads) {
+      const int r = x / (D / 4), quad = x % (D / 4);
+      if (row0 + r >= all_rows) continue;
+      float top = s_ml[r * 2];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_ml[(w * F::kRows + r) * 2]);
+      float l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = exp2_fast(s_ml[(w * F::kRows + r) * 2] - top);
+        l += f * s_ml[(w * F::kRows + r) * 2 + 1];
+        const float4 v = *reinterpret_cast<const float4*>(merge + (w * F::kRows + r) * F::kPitch + quad * 4);
+        acc[0] += f * v.x;
+        acc[1] += f * v.y;
+        acc[2] += f * v.z;
+        acc[3] += f * v.w;
+      }
+      if (whole) {
+        const int t = quotient(row0 + r, p.group);
+        const int j = head * G + row0 + r - t * G;
+        write_out<T>(p, seq.lo + t, j * D + quad * 4, acc, l);
+        if (p.lse && quad == 0) p.lse[static_cast<int64_t>(seq.lo + t) * p.heads + j] = lse_of(top, l);
+      } else {
+        float* to = p.part_o + (static_cast<int64_t>(slot) * F::kRows + r) * D + quad * 4;
+        *reinterpret_cast<float4*>(to) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        if (quad == 0)
+          *reinterpret_cast<float2*>(p.part_ml + (static_cast<int64_t>(slot) * F::kRows + r) * 2) =
+              make_float2(top, l);
+      }
+    }
+    __syncthreads();  // the ring is free again
+    at += u1 - u0;
+  }
+}
+
+// The join.  CTA (c, y) looks at the item in which the share of CTA c begins;
+// if that is the first such CTA of the item, it joins the item's partial
+// results, rows y, y + gridDim.y, ... .  Warps take the partial results in
+// turn, each relative to a running maximum, and meet in shared memory.
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) attn_join_kernel(const AttnParams p) {
+  constexpr int kLanes = D / 4, kSets = kThreads / kLanes;
+  __shared__ float s_o[kSets][D], s_ml[kSets][2];
+  griddep_launch_dependents();
+  griddep_wait();
+  Share share;
+  if (!find_share<kThreads>(p, blockIdx.x, share)) return;
+  const Sequence seq = sequence_at(p, share.b);
+  const int64_t local = share.first - share.before;
+  const int64_t item = local / seq.units;
+  const int64_t begin = share.before + item * seq.units;
+  if (begin == share.first) return;
+  const int c0 = share_owner(share.units, share.active, begin);
+  if (static_cast<int>(blockIdx.x) != c0 + 1) return;
+  const int c1 = share_owner(share.units, share.active, begin + seq.units - 1);
+  const int G = static_cast<int>(p.group.d);
+  const int head = static_cast<int>(item / seq.tiles);
+  const int row0 = static_cast<int>(item - static_cast<int64_t>(head) * seq.tiles) * p.tile_rows;
+  const int rows = min(p.tile_rows, seq.rows * G - row0);
+  const int set = threadIdx.x / kLanes, quad = threadIdx.x % kLanes;
+  for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+    float top = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int c = c0 + set; c <= c1; c += kSets) {
+      const int64_t slot = 2ll * c + (c == c0 ? 1 : 0);
+      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (slot * p.tile_rows + r) * 2);
+      const float4 v = *reinterpret_cast<const float4*>(p.part_o + (slot * p.tile_rows + r) * D + quad * 4);
+      const float now = fmaxf(top, ml.x);
+      const float a = exp2_fast(top - now), f = exp2_fast(ml.x - now);
+      top = now;
+      l = l * a + ml.y * f;
+      acc[0] = acc[0] * a + v.x * f;
+      acc[1] = acc[1] * a + v.y * f;
+      acc[2] = acc[2] * a + v.z * f;
+      acc[3] = acc[3] * a + v.w * f;
+    }
+    *reinterpret_cast<float4*>(&s_o[set][quad * 4]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    if (quad == 0) {
+      s_ml[set][0] = top;
+      s_ml[set][1] = l;
+    }
+    __syncthreads();
+    if (set == 0) {
+      top = s_ml[0][0];
+#pragma unroll
+      for (int i = 1; i < kSets; ++i) top = fmaxf(top, s_ml[i][0]);
+      l = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i] = 0.f;
+#pragma unroll
+      for (int i = 0; i < kSets; ++i) {
+        const float f = exp2_fast(s_ml[i][0] - top);
+        l += f * s_ml[i][1];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[j] += f * s_o[i][quad * 4 + j];
+      }
+      const int t = quotient(row0 + r, p.group);
+      const int j = head * G + row0 + r - t * G;
+      write_out<T>(p, seq.lo + t, j * D + quad * 4, acc, l);
+      if (p.lse && quad == 0) p.lse[static_cast<int64_t>(seq.lo + t) * p.heads + j] = lse_of(top, l);
+    }
+    __syncthreads();
+  }
+}
+
+// ------------------------------------------------------------------- host --
+
+template <typename P>
+cudaError_t launch(void (*kernel)(P), dim3 grid, size_t smem, const P& p, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <typename T, int kFormat, int D, int NT>
+cudaError_t stream_launch(const AttnParams& p, cudaStream_t s) {
+  using F = Stream<kFormat, D, NT>;
+  const auto kernel = attn_stream_kernel<T, kFormat, D, NT>;
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), F::kSmem, done);
+  return e == cudaSuccess ? launch(kernel, dim3(p.ctas), F::kSmem, p, s) : e;
+}
+
+template <typename T, int kFormat, int D>
+cudaError_t stream_rows(const AttnParams& p, cudaStream_t s) {
+  return p.tile_rows == 8    ? stream_launch<T, kFormat, D, 1>(p, s)
+         : p.tile_rows == 16 ? stream_launch<T, kFormat, D, 2>(p, s)
+                             : stream_launch<T, kFormat, D, 4>(p, s);
+}
+
+template <typename T, int D>
+cudaError_t stream_format(int format, const AttnParams& p, cudaStream_t s) {
+  return format == PROJ_KV_ROWS   ? stream_rows<T, PROJ_KV_ROWS, D>(p, s)
+         : format == PROJ_KV_E4M3 ? stream_rows<T, PROJ_KV_E4M3, D>(p, s)
+                                  : stream_rows<T, PROJ_KV_INT8, D>(p, s);
+}
+
+struct Plan {
+  int tile_rows, unit, ctas, min_units;
+  int64_t bytes;
+};
+
+// Rows of an item by the rows that a sequence has on average.
+const char* make_plan(const proj_kv_cache* cache, int64_t m, int64_t heads, Plan* plan,
+                      int* status) {
+  if (const char* why = refuse_cache(cache, status)) return why;
+  *status = PROJ_EINVAL;
+  if (m < 0) return "m < 0";
+  if (heads < 1 || heads % cache->heads) return "heads is no multiple of the cache's";
+  *status = PROJ_EUNSUPPORTED;
+  if (heads > 1024) return "more than 1024 heads";
+  if (m > (int64_t{1} << 20)) return "m > 2^20";
+  *status = PROJ_OK;
+  const int64_t rows = cache->sequences
+                           ? (m + cache->sequences - 1) / cache->sequences * (heads / cache->heads)
+                           : 1;
+  plan->unit = kStep;
+  plan->tile_rows = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+  plan->min_units = 2 * kWarps;
+  int sms = 0, dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
+    sms = 152;
+  plan->ctas = sms;
+  plan->bytes = int64_t{2} * plan->ctas * plan->tile_rows * (cache->D + 2) * 4;
+  return nullptr;
+}
+
+}  // namespace
+}  // namespace proj
+
+using namespace proj;
+
+extern "C" int64_t proj_attn_workspace(const proj_kv_cache* cache, int64_t m, int64_t heads) {
+  Plan plan;
+  int status = PROJ_OK;
+  if (const char* why = make_plan(cache, m, heads, &plan, &status)) {
+    kv_refuse(status, "proj_attn_workspace", why);
+    return -1;
+  }
+  return plan.bytes;
+}
+
+extern "C" int proj_attn(const proj_attn_args* args, proj_stream stream) {
+  const char* const call = "proj_attn";
+  if (!args) return kv_refuse(PROJ_EINVAL, call, "args is NULL");
+  const proj_attn_args& a = *args;
+  Plan plan;
+  int status = PROJ_OK;
+  if (const char* why = make_plan(a.cache, a.m, a.heads, &plan, &status)) return kv_refuse(status, call, why);
+  const proj_kv_cache& c = *a.cache;
+  const int64_t width = a.heads * c.D;
+  if (a.gate_act != PROJ_GATE_LINEAR && a.gate_act != PROJ_GATE_SIGMOID)
+    return kv_refuse(PROJ_EINVAL, call, "unknown gate_act");
+  if (!std::isfinite(a.scale)) return kv_refuse(PROJ_EINVAL, call, "scale is no finite number");
+  if (a.m > 0 && c.sequences > 0 && (!a.q || !a.out || !a.offsets || !a.start))
+    return kv_refuse(PROJ_EINVAL, call, "q, out, offsets or start is NULL");
+  if (a.ldq < width || a.ldo < width || (a.gate && a.ldg < width))
+    return kv_refuse(PROJ_EINVAL, call, "a row stride is below heads D");
+  if (a.mask && (a.words < 1 || a.ldm < a.words))
+    return kv_refuse(PROJ_EINVAL, call, "words < 1, or ldm below words");
+  if ((a.out == a.q && a.ldo != a.ldq) || (a.gate && a.out == a.gate && a.ldo != a.ldg))
+    return kv_refuse(PROJ_EINVAL, call, "out is q or the gate, but with another stride");
+  if (a.mask && a.words > 1024) return kv_refuse(PROJ_EUNSUPPORTED, call, "words > 1024");
+  const int64_t most = int64_t{1} << 31;
+  if (a.ldq >= most || a.ldo >= most || a.ldg >= most || a.ldm >= most)
+    return kv_refuse(PROJ_EUNSUPPORTED, call, "a row stride of 2^31 or more");
+  if (!kv_aligned(a.q, 16) || !kv_aligned(a.out, 16) || !kv_aligned(a.gate, 16) || a.ldq % 8 ||
+      a.ldo % 8 || (a.gate && a.ldg % 8))
+    return kv_refuse(PROJ_EALIGN, call, "rows of q, out or the gate do not start on 16 bytes");
+  if (!kv_aligned(a.offsets, 4) || !kv_aligned(a.start, 4) || !kv_aligned(a.mask, 4) ||
+      !kv_aligned(a.lse, 4))
+    return kv_refuse(PROJ_EALIGN, call, "offsets, start, mask or lse is not aligned to 4 bytes");
+  if (a.m == 0 || c.sequences == 0) return PROJ_OK;
+  if (!a.workspace || a.workspace_bytes < plan.bytes)
+    return kv_refuse(PROJ_EINVAL, call, "workspace is NULL or smaller than proj_attn_workspace");
+  if (!kv_aligned(a.workspace, 16)) return kv_refuse(PROJ_EALIGN, call, "workspace is not aligned to 16 bytes");
+  AttnParams p = {};
+  p.c = device_cache(c);
+  p.q = static_cast<const uint8_t*>(a.q);
+  p.ldq = a.ldq * 2;
+  p.offsets = a.offsets;
+  p.start = a.start;
+  p.mask = a.mask;
+  p.ldm = a.ldm;
+  p.words = static_cast<int>(a.words);
+  p.scale_log2 = static_cast<float>(a.scale * 1.4426950408889634);
+  p.gate = static_cast<const uint8_t*>(a.gate);
+  p.ldg = a.ldg * 2;
+  p.sigmoid = a.gate_act == PROJ_GATE_SIGMOID;
+  p.out = static_cast<uint8_t*>(a.out);
+  p.ldo = a.ldo * 2;
+  p.lse = a.lse;
+  p.m = static_cast<int>(a.m);
+  p.heads = static_cast<int>(a.heads);
+  p.D = static_cast<int>(c.D);
+  p.group = make_divisor(static_cast<uint32_t>(a.heads / c.heads));
+  p.tile_rows = plan.tile_rows;
+  p.unit = plan.unit;
+  p.ctas = plan.ctas;
+  p.min_units = plan.min_units;
+  p.status = nullptr;
+  p.part_o = static_cast<float*>(a.workspace);
+  p.part_ml = p.part_o + int64_t{2} * plan.ctas * plan.tile_rows * c.D;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (c.dtype == PROJ_BF16)
+    e = c.D == 64 ? stream_format<__nv_bfloat16, 64>(c.format, p, s)
+                  : stream_format<__nv_bfloat16, 128>(c.format, p, s);
+  else
+    e = c.D == 64 ? stream_format<__half, 64>(c.format, p, s) : stream_format<__half, 128>(c.format, p, s);
+  if (e != cudaSuccess) return record_cuda(e, call);
+  // rows of an item over grid y: all of them where few items can be split
+  const int64_t items = std::max<int64_t>(1, a.m * (a.heads / c.heads) / plan.tile_rows) * c.heads;
+  const dim3 grid(plan.ctas, static_cast<unsigned>(std::max<int64_t>(
+                                 1, std::min<int64_t>(plan.tile_rows, 4 * plan.ctas / items))));
+  if (c.dtype == PROJ_BF16)
+    e = c.D == 64 ? launch(attn_join_kernel<__nv_bfloat16, 64>, grid, 0, p, s)
+                  : launch(attn_join_kernel<__nv_bfloat16, 128>, grid, 0, p, s);
+  else
+    e = c.D == 64 ? launch(attn_join_kernel<__half, 64>, grid, 0, p, s)
+                  : launch(attn_join_kernel<__half, 128>, grid, 0, p, s);
+  return e == cudaSuccess ? PROJ_OK : record_cuda(e, call);
+}
+
+extern "C" int proj_attn_describe(const proj_kv_cache* cache, int64_t m, int64_t heads, char* buf,
+                                  size_t cap) {
+  const char* const call = "proj_attn_describe";
+  Plan plan;
+  int status = PROJ_OK;
+  if (const char* why = make_plan(cache, m, heads, &plan, &status)) return kv_refuse(status, call, why);
+  if (!buf || cap == 0) return kv_refuse(PROJ_EINVAL, call, "buf is NULL or cap 0");
+  std::snprintf(buf, cap, "attn stream, items of %d rows, units of %d keys, up to %d CTAs, join", plan.tile_rows,
+                plan.unit, plan.ctas);
+  return PROJ_OK;
+}
+
+extern "C" int proj_attn_device_status(proj_stream stream, uint32_t* code) {
+  const char* const call = "proj_attn_device_status";
+  void* at = nullptr;
+  uint32_t word = 0;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaGetSymbolAddress(&at, g_attn_status);
+  if (e == cudaSuccess) e = cudaMemcpyAsync(&word, at, 4, cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaMemsetAsync(at, 0, 4, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e != cudaSuccess) return record_cuda(e, call);
+  if (code) *code = word;
+  return word ? kv_refuse(PROJ_EDEVICE, call, "a kernel recorded a fault") : PROJ_OK;
+}

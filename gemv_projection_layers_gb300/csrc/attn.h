@@ -1,0 +1,180 @@
+// attn.h -- attention of drafted tokens over the cache: what its kernels share
+// (attn.cu: calls, streaming kernel, join; attn_tc.cu: tcgen05 kernel).
+//
+// Work is cut on the device, by the lengths that the call has: an item is a
+// sequence, a head of keys and values, and `tile_rows` of its rows (a row is a
+// drafted token and a query head of the group; row r is token r / group, head
+// r % group); it has ceil(keys / unit) units.  The items' units stand in one
+// line, and CTA c of the `active` takes units [c W / active, (c + 1) W /
+// active) of the W.  So every SM has the same share whatever the lengths, a CTA
+// leaves at most two items unfinished (one it did not begin, one it does not
+// end), and the partial results need room for two items a CTA and nothing that
+// grows with the batch.  A second kernel joins them in the order of their CTAs.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "kv.h"
+#include "ptx.cuh"
+#include "vec.cuh"
+
+namespace proj {
+
+struct AttnParams {
+  KvCache c;
+  const uint8_t* q;
+  int64_t ldq;  // bytes, as ldg and ldo
+  const int32_t* offsets;
+  const int32_t* start;
+  const uint32_t* mask;
+  int64_t ldm;
+  int words;
+  float scale_log2;  // scale * log2(e)
+  const uint8_t* gate;
+  int64_t ldg;
+  int sigmoid;
+  uint8_t* out;
+  int64_t ldo;
+  float* lse;
+  int m, heads, D;
+  Divisor group;
+  int tile_rows, unit, ctas, min_units;
+  float* part_o;   // [2 ctas][tile_rows][D]: sums relative to 2^m
+  float* part_ml;  // [2 ctas][tile_rows][2]: m, sum
+  uint32_t* status;
+};
+
+// A sequence's part in the call.
+struct Sequence {
+  int lo, rows;     // first row of the call, drafted tokens
+  int start, len;   // positions before the drafts, positions in all
+  int tiles, units;
+};
+
+__device__ __forceinline__ Sequence sequence_at(const AttnParams& p, int b) {
+  Sequence s;
+  int hi;
+  rows_of(p.offsets, b, p.m, s.lo, hi);
+  s.rows = hi - s.lo;
+  s.start = min(max(p.start[b], 0), p.c.capacity);
+  s.len = min(s.start + s.rows, p.c.capacity);
+  const int64_t rows = static_cast<int64_t>(s.rows) * static_cast<int>(p.group.d);
+  s.tiles = static_cast<int>((rows + p.tile_rows - 1) / p.tile_rows);
+  // an item without keys has one unit all the same: its rows are written
+  s.units = max(1, (s.len + p.unit - 1) / p.unit);
+  return s;
+}
+
+// Units of a sequence; no more than 2^35 are worked on, so that sums and
+// products below stay within 64 bits whatever stands in offsets and start.
+__device__ __forceinline__ int64_t units_of(const AttnParams& p, const Sequence& s) {
+  const int64_t all = static_cast<int64_t>(s.tiles) * s.units;
+  return min(all < (int64_t{1} << 45) ? all * p.c.heads : all, int64_t{1} << 35);
+}
+
+// This CTA's share.
+struct Share {
+  int64_t units, first, end;  // W, and this CTA's range
+  int active;
+  int b;           // the sequence that holds `first`
+  int64_t before;  // units of the sequences before b
+};
+
+__device__ __forceinline__ int64_t share_begin(int64_t W, int active, int cta) {
+  return W / active * cta + W % active * cta / active;
+}
+// The CTA that holds unit x.
+__device__ __forceinline__ int share_owner(int64_t W, int active, int64_t x) {
+  return static_cast<int>(((x + 1) * active - 1) / W);
+}
+
+// All threads of the CTA; kThreads of them.  `cta`: whose share.  False: none.
+template <int kThreads>
+__device__ __forceinline__ bool find_share(const AttnParams& p, int cta, Share& s) {
+  __shared__ int64_t warp_sum[kThreads / 32];
+  __shared__ int found_b;
+  __shared__ int64_t found_before;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (p.c.sequences + kThreads - 1) / kThreads;
+  const int b0 = min(tid * per, p.c.sequences), b1 = min(b0 + per, p.c.sequences);
+  int64_t sum = 0;
+  for (int b = b0; b < b1; ++b) sum += units_of(p, sequence_at(p, b));
+  int64_t inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 31) warp_sum[warp] = inc;
+  if (tid == 0) found_b = -1;
+  __syncthreads();
+  int64_t before = inc - sum, W = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += warp_sum[w];
+    W += warp_sum[w];
+  }
+  s.units = W;
+  s.active = static_cast<int>(min(static_cast<int64_t>(p.ctas), max(W / p.min_units, int64_t{1})));
+  if (W == 0 || cta >= s.active) return false;
+  s.first = share_begin(W, s.active, cta);
+  s.end = share_begin(W, s.active, cta + 1);
+  if (s.first >= before && s.first < before + sum) {
+    int b = b0;
+    for (; b < b1 - 1; ++b) {
+      const int64_t u = units_of(p, sequence_at(p, b));
+      if (s.first < before + u) break;
+      before += u;
+    }
+    found_b = b;
+    found_before = before;
+  }
+  __syncthreads();
+  s.b = found_b;
+  s.before = found_before;
+  return s.b >= 0;
+}
+
+// exp2 by the special-function unit: relative error 2^-22; -inf gives 0.
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// The reference of a row that has seen nothing yet.
+constexpr float kNoScore = -3e38f;
+
+template <typename T>
+__device__ __forceinline__ float gate_value(float x, int sigmoid) {
+  return sigmoid ? __fdividef(1.f, 1.f + __expf(-x)) : x;
+}
+
+// Four neighbouring entries of a finished row: o = sum / l, gated, rounded.
+template <typename T>
+__device__ __forceinline__ void write_out(const AttnParams& p, int64_t row, int column,
+                                          const float (&sum)[4], float l) {
+  const float inv = 1.f / l;
+  float f[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = l == 0.f ? 0.f : sum[i] * inv;  // nothing seen: 0
+  if (p.gate) {
+    float g[4];
+    widen(load_vec<T, 4>(reinterpret_cast<const T*>(p.gate + row * p.ldg) + column), g);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] *= gate_value<T>(g[i], p.sigmoid);
+  }
+  store_vec<T, 4>(reinterpret_cast<T*>(p.out + row * p.ldo) + column, f);
+}
+
+__device__ __forceinline__ float lse_of(float m, float l) {
+  return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+// tcgen05 kernel (attn_tc.cu).
+constexpr int kAttnTcRows = 128;  // rows of an item there
+constexpr int kAttnTcUnit = 64;
+cudaError_t attn_tc_launch(const AttnParams& p, int dtype, int format, cudaStream_t s);
+
+}  // namespace proj

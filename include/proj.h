@@ -672,6 +672,139 @@ int64_t proj_norm_workspace(int64_t m, int64_t D);
 /* Gradients of proj_norm; sums over tokens are taken in a fixed order. */
 int proj_norm_backward(const proj_norm_grad_args *args, proj_stream stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * The cache of keys and values between the qkv_gate and o projections: rows
+ * quantised as they are written, read back, moved when drafts are accepted,
+ * and attention of drafted tokens over it.  What stands above for the
+ * operators around the projections holds here too.
+ *
+ * A cache is pages of `page` tokens.  For each token and head of keys and
+ * values it keeps D entries of keys and D of values, 16 bits wide or 8 bits
+ * with one fp32 scale:
+ *
+ *     value = code * scale,   scale = max(amax / top, 2^-126),
+ *     code  = round(x * (1 / scale)),  top = 448 (e4m3) or 127 (int8),
+ *
+ * with amax the row's largest magnitude, each step rounded to fp32 and the
+ * code to nearest even.  A row with a NaN or an infinity gets codes 0 and the
+ * scale NaN: it reads back as NaN.
+ *
+ * The pages of sequence b are table[b, 0 .. width - 1]: position p stands in
+ * page table[b, p / page] at place p % page.  A page id outside 0 .. pages - 1
+ * is no page: nothing is written there, it reads back as zeros and no query
+ * sees it.  Sequences may share pages that no call writes.
+ *
+ * Rows of a call belong to sequences by `offsets` [sequences + 1] on the
+ * device, 0 <= offsets[b] <= offsets[b + 1] <= m (values outside are moved
+ * into that range): row offsets[b] + i stands for position start[b] + i.  Rows
+ * before offsets[0] and from offsets[sequences] on are no sequence's and left
+ * alone.  A negative start counts as 0 in proj_attn; the other calls leave the
+ * rows of negative positions as rows without a page.
+ * ---------------------------------------------------------------------------
+ */
+enum proj_kv_format {
+    PROJ_KV_ROWS = 0, /* entries of the cache's dtype, no scales */
+    PROJ_KV_E4M3 = 1, /* 8-bit floating point, 4 bits of exponent, no infinities */
+    PROJ_KV_INT8 = 2  /* -127 .. 127 */
+};
+
+typedef struct proj_kv_cache {
+    int format;            /* enum proj_kv_format */
+    int dtype;             /* PROJ_BF16 or PROJ_FP16: rows written and read back, queries, outputs */
+    int64_t pages, page;   /* pages in all; tokens of one, 1 .. 65536 */
+    int64_t heads, D;      /* heads of keys and values, 1 .. 1024; D = 64 or 128 */
+    void *k, *v;           /* entries, 16-byte aligned */
+    float *k_scale;        /* [pages, heads, page]; NULL for PROJ_KV_ROWS */
+    float *v_scale;
+    int64_t page_stride;   /* entry (page, head, place) starts at page page_stride + head head_stride */
+    int64_t head_stride;   /* + place token_stride entries; multiples of 16 bytes, at least D */
+    int64_t token_stride;
+    const int32_t *table;  /* device [sequences, width], row stride ldt >= width */
+    int64_t ldt, width;    /* width page < 2^30 */
+    int64_t sequences;     /* 0 .. 65536 */
+} proj_kv_cache;
+
+/*
+ * Write rows k and v (m rows of heads D values, dtype; 16-byte aligned, strides
+ * multiples of 8) to their positions.  Two rows of one position: one of them
+ * is kept.
+ */
+int proj_kv_write(const proj_kv_cache *cache, const int32_t *offsets, const int32_t *start,
+                  int64_t m, const void *k, int64_t ldk, const void *v, int64_t ldv,
+                  proj_stream stream);
+
+/* Read the same rows back, rounded once to dtype.  k or v may be NULL. */
+int proj_kv_read(const proj_kv_cache *cache, const int32_t *offsets, const int32_t *start,
+                 int64_t m, void *k, int64_t ldk, void *v, int64_t ldv, proj_stream stream);
+
+/*
+ * Accepted drafts to their places: entry i of path[b] (row stride ldp >=
+ * depth) moves from position start[b] + path[b, i] to start[b] + i, codes and
+ * scales as they are.  A path ascends from 0 or more (a draft comes after its
+ * parent); the first entry that does not, or is negative, ends it.  Where one
+ * of the two positions has no page, that entry is not moved.
+ *   next_start : optional [sequences], start[b] + the number of entries; not
+ *                `start` itself.
+ */
+int proj_kv_move(const proj_kv_cache *cache, const int32_t *start, const int32_t *path,
+                 int64_t ldp, int64_t depth, int32_t *next_start, proj_stream stream);
+
+/*
+ * Attention of drafted tokens over the cache, which holds their own keys and
+ * values already (proj_kv_write with the same offsets and start).  Query head
+ * j meets head j / (heads / cache heads) of keys and values.  Row i of a
+ * sequence sees all start[b] positions before the drafts, and of draft d
+ *
+ *     mask given : bit d % 32 of mask[row, d / 32] (d < 32 words), else
+ *     mask NULL  : d <= i.
+ *
+ *     out = (softmax(scale q k^T over what the row sees) v) act(gate)
+ *
+ * A row that sees nothing gets zeros, and lse = -infinity.  What a row does not
+ * see does not reach it, NaN and infinities included.  Scores, their maximum
+ * and sums are fp32; the products of 8-bit caches and of fp16 are computed in
+ * fp16 with codes and queries exact in it (a row of bf16 queries is brought
+ * to its range by a power of two; what is 2^-29 below the row's largest loses
+ * digits) and probabilities rounded to it; those of bf16 caches in bf16.
+ * The gate is applied in fp32 and the result rounded once.
+ */
+typedef struct proj_attn_args {
+    const proj_kv_cache *cache;
+    int64_t m, heads;        /* rows of q; query heads, a multiple of the cache's, at most 1024 */
+    const void *q;           /* [m, heads D], dtype; 16-byte aligned, strides multiples of 8 */
+    int64_t ldq;
+    const int32_t *offsets;  /* device [sequences + 1] */
+    const int32_t *start;    /* device [sequences] */
+    const uint32_t *mask;    /* device [m, words], row stride ldm, or NULL */
+    int64_t ldm, words;      /* words: 1 .. 1024 */
+    float scale;             /* finite */
+    int gate_act;            /* enum proj_gate_act */
+    const void *gate;        /* [m, heads D], dtype, as q; NULL: none */
+    int64_t ldg;
+    void *out;               /* [m, heads D], dtype, as q; may be q itself or the gate (same stride) */
+    int64_t ldo;
+    float *lse;              /* [m, heads] natural logarithm of each row's sum, or NULL */
+    void *workspace;         /* proj_attn_workspace bytes, 16-byte aligned */
+    int64_t workspace_bytes;
+} proj_attn_args;
+
+/* Bytes of workspace of proj_attn on this device; -1 for arguments it refuses.
+ * A workspace holds nothing between calls, and calls that may overlap need one
+ * each. */
+int64_t proj_attn_workspace(const proj_kv_cache *cache, int64_t m, int64_t heads);
+
+int proj_attn(const proj_attn_args *args, proj_stream stream);
+
+/* The kernel and launch shape of proj_attn for m rows (at most `cap` bytes,
+ * NUL-terminated; 256 are enough). */
+int proj_attn_describe(const proj_kv_cache *cache, int64_t m, int64_t heads, char *buf, size_t cap);
+
+/* Read and clear the status word of the current device's proj_attn calls
+ * (synchronises `stream`; not while it is being captured), as
+ * proj_device_status: PROJ_EDEVICE where a kernel's bounded wait gave up. */
+int proj_attn_device_status(proj_stream stream, uint32_t *code);
+
 #ifdef __cplusplus
 }
 #endif

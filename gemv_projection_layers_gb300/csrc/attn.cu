@@ -674,6 +674,7 @@ cudaError_t stream_format(int format, const AttnParams& p, cudaStream_t s) {
 }
 
 struct Plan {
+  bool tc;
   int tile_rows, unit, ctas, min_units;
   int64_t bytes;
 };
@@ -692,9 +693,10 @@ const char* make_plan(const proj_kv_cache* cache, int64_t m, int64_t heads, Plan
   const int64_t rows = cache->sequences
                            ? (m + cache->sequences - 1) / cache->sequences * (heads / cache->heads)
                            : 1;
-  plan->unit = kStep;
-  plan->tile_rows = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
-  plan->min_units = 2 * kWarps;
+  plan->tc = rows > 32;
+  plan->unit = plan->tc ? kAttnTcUnit : kStep;
+  plan->tile_rows = plan->tc ? kAttnTcRows : rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+  plan->min_units = plan->tc ? 4 : 2 * kWarps;
   int sms = 0, dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
@@ -777,12 +779,16 @@ extern "C" int proj_attn(const proj_attn_args* args, proj_stream stream) {
   p.unit = plan.unit;
   p.ctas = plan.ctas;
   p.min_units = plan.min_units;
-  p.status = nullptr;
+  void* status_word = nullptr;
+  cudaError_t e = cudaGetSymbolAddress(&status_word, g_attn_status);
+  if (e != cudaSuccess) return record_cuda(e, call);
+  p.status = static_cast<uint32_t*>(status_word);
   p.part_o = static_cast<float*>(a.workspace);
   p.part_ml = p.part_o + int64_t{2} * plan.ctas * plan.tile_rows * c.D;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e;
-  if (c.dtype == PROJ_BF16)
+  if (plan.tc)
+    e = attn_tc_launch(p, c.dtype, c.format, s);
+  else if (c.dtype == PROJ_BF16)
     e = c.D == 64 ? stream_format<__nv_bfloat16, 64>(c.format, p, s)
                   : stream_format<__nv_bfloat16, 128>(c.format, p, s);
   else
@@ -808,8 +814,8 @@ extern "C" int proj_attn_describe(const proj_kv_cache* cache, int64_t m, int64_t
   int status = PROJ_OK;
   if (const char* why = make_plan(cache, m, heads, &plan, &status)) return kv_refuse(status, call, why);
   if (!buf || cap == 0) return kv_refuse(PROJ_EINVAL, call, "buf is NULL or cap 0");
-  std::snprintf(buf, cap, "attn stream, items of %d rows, units of %d keys, up to %d CTAs, join", plan.tile_rows,
-                plan.unit, plan.ctas);
+  std::snprintf(buf, cap, "attn %s, items of %d rows, units of %d keys, up to %d CTAs, join",
+                plan.tc ? "tcgen05" : "stream", plan.tile_rows, plan.unit, plan.ctas);
   return PROJ_OK;
 }
 

@@ -140,7 +140,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_stream_kernel(const AttnPara
   griddep_launch_dependents();
   griddep_wait();
   Share share;
-  if (!find_share<kThreads>(p, blockIdx.x, share)) return;
+  const bool mine = find_share<kThreads>(p, blockIdx.x, share);
+  if (threadIdx.x == 0) p.splits[blockIdx.x] = mine ? split_of(p, share, blockIdx.x) : Split{};
+  if (!mine) return;
 
   const int G = static_cast<int>(p.group.d);
   int b = share.b;
@@ -563,36 +565,29 @@ __global__ void __launch_bounds__(kThreads, 1) attn_stream_kernel(const AttnPara
   }
 }
 
-// The join.  CTA (c, y) looks at the item in which the share of CTA c begins;
-// if that is the first such CTA of the item, it joins the item's partial
-// results, rows y, y + gridDim.y, ... .  Warps take the partial results in
-// turn, each relative to a running maximum, and meet in shared memory.
+// The join.  CTA (c, y) has what CTA c left to be joined, rows y, y + gridDim.y,
+// ... in sets of threads that span a row.  Few partial results: each set takes
+// a row; many: a CTA's sets share a row's partial results, each relative to a
+// running maximum, and meet in shared memory.
+constexpr int kFewParts = 16;
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) attn_join_kernel(const AttnParams p) {
   constexpr int kLanes = D / 4, kSets = kThreads / kLanes;
   __shared__ float s_o[kSets][D], s_ml[kSets][2];
   griddep_launch_dependents();
   griddep_wait();
-  Share share;
-  if (!find_share<kThreads>(p, blockIdx.x, share)) return;
-  const Sequence seq = sequence_at(p, share.b);
-  const int64_t local = share.first - share.before;
-  const int64_t item = local / seq.units;
-  const int64_t begin = share.before + item * seq.units;
-  if (begin == share.first) return;
-  const int c0 = share_owner(share.units, share.active, begin);
-  if (static_cast<int>(blockIdx.x) != c0 + 1) return;
-  const int c1 = share_owner(share.units, share.active, begin + seq.units - 1);
+  const Split it = p.splits[blockIdx.x];
+  if (it.rows == 0) return;
   const int G = static_cast<int>(p.group.d);
-  const int head = static_cast<int>(item / seq.tiles);
-  const int row0 = static_cast<int>(item - static_cast<int64_t>(head) * seq.tiles) * p.tile_rows;
-  const int rows = min(p.tile_rows, seq.rows * G - row0);
   const int set = threadIdx.x / kLanes, quad = threadIdx.x % kLanes;
-  for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+  const bool few = it.last - it.first < kFewParts;
+  const int y0 = few ? blockIdx.y * kSets + set : blockIdx.y, dy = few ? gridDim.y * kSets : gridDim.y;
+  for (int r = y0; r < it.rows; r += dy) {
     float top = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-    for (int c = c0 + set; c <= c1; c += kSets) {
-      const int64_t slot = 2ll * c + (c == c0 ? 1 : 0);
+    for (int c = it.first + (few ? 0 : set); c <= it.last; c += few ? 1 : kSets) {
+      const int64_t slot = 2ll * c + (c == it.first ? 1 : 0);
       const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (slot * p.tile_rows + r) * 2);
       const float4 v = *reinterpret_cast<const float4*>(p.part_o + (slot * p.tile_rows + r) * D + quad * 4);
       const float now = fmaxf(top, ml.x);
@@ -604,32 +599,36 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(const AttnParams p)
       acc[2] = acc[2] * a + v.z * f;
       acc[3] = acc[3] * a + v.w * f;
     }
-    *reinterpret_cast<float4*>(&s_o[set][quad * 4]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-    if (quad == 0) {
-      s_ml[set][0] = top;
-      s_ml[set][1] = l;
-    }
-    __syncthreads();
-    if (set == 0) {
-      top = s_ml[0][0];
-#pragma unroll
-      for (int i = 1; i < kSets; ++i) top = fmaxf(top, s_ml[i][0]);
-      l = 0.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] = 0.f;
-#pragma unroll
-      for (int i = 0; i < kSets; ++i) {
-        const float f = exp2_fast(s_ml[i][0] - top);
-        l += f * s_ml[i][1];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[j] += f * s_o[i][quad * 4 + j];
+    if (!few) {
+      *reinterpret_cast<float4*>(&s_o[set][quad * 4]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      if (quad == 0) {
+        s_ml[set][0] = top;
+        s_ml[set][1] = l;
       }
-      const int t = quotient(row0 + r, p.group);
-      const int j = head * G + row0 + r - t * G;
-      write_out<T>(p, seq.lo + t, j * D + quad * 4, acc, l);
-      if (p.lse && quad == 0) p.lse[static_cast<int64_t>(seq.lo + t) * p.heads + j] = lse_of(top, l);
+      __syncthreads();
+      if (set == 0) {
+        top = s_ml[0][0];
+#pragma unroll
+        for (int i = 1; i < kSets; ++i) top = fmaxf(top, s_ml[i][0]);
+        l = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] = 0.f;
+#pragma unroll
+        for (int i = 0; i < kSets; ++i) {
+          const float f = exp2_fast(s_ml[i][0] - top);
+          l += f * s_ml[i][1];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[j] += f * s_o[i][quad * 4 + j];
+        }
+      }
+      __syncthreads();
     }
-    __syncthreads();
+    if (few || set == 0) {
+      const int t = quotient(it.row0 + r, p.group);
+      const int j = it.head * G + it.row0 + r - t * G;
+      write_out<T>(p, it.lo + t, j * D + quad * 4, acc, l);
+      if (p.lse && quad == 0) p.lse[static_cast<int64_t>(it.lo + t) * p.heads + j] = lse_of(top, l);
+    }
   }
 }
 
@@ -702,7 +701,8 @@ const char* make_plan(const proj_kv_cache* cache, int64_t m, int64_t heads, Plan
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
     sms = 152;
   plan->ctas = sms;
-  plan->bytes = int64_t{2} * plan->ctas * plan->tile_rows * (cache->D + 2) * 4;
+  plan->bytes = int64_t{2} * plan->ctas * plan->tile_rows * (cache->D + 2) * 4 +
+                plan->ctas * static_cast<int64_t>(sizeof(Split));
   return nullptr;
 }
 
@@ -783,7 +783,8 @@ extern "C" int proj_attn(const proj_attn_args* args, proj_stream stream) {
   cudaError_t e = cudaGetSymbolAddress(&status_word, g_attn_status);
   if (e != cudaSuccess) return record_cuda(e, call);
   p.status = static_cast<uint32_t*>(status_word);
-  p.part_o = static_cast<float*>(a.workspace);
+  p.splits = static_cast<Split*>(a.workspace);
+  p.part_o = reinterpret_cast<float*>(p.splits + plan.ctas);
   p.part_ml = p.part_o + int64_t{2} * plan.ctas * plan.tile_rows * c.D;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (plan.tc)
@@ -794,10 +795,11 @@ extern "C" int proj_attn(const proj_attn_args* args, proj_stream stream) {
   else
     e = c.D == 64 ? stream_format<__half, 64>(c.format, p, s) : stream_format<__half, 128>(c.format, p, s);
   if (e != cudaSuccess) return record_cuda(e, call);
-  // rows of an item over grid y: all of them where few items can be split
+  // Few items are split into many parts, a CTA a row; else a set of threads a row.
   const int64_t items = std::max<int64_t>(1, a.m * (a.heads / c.heads) / plan.tile_rows) * c.heads;
-  const dim3 grid(plan.ctas, static_cast<unsigned>(std::max<int64_t>(
-                                 1, std::min<int64_t>(plan.tile_rows, 4 * plan.ctas / items))));
+  const int sets = kThreads / (static_cast<int>(c.D) / 4);
+  const int rows = items * kFewParts < plan.ctas ? plan.tile_rows : std::max(1, plan.tile_rows / sets);
+  const dim3 grid(plan.ctas, static_cast<unsigned>(rows));
   if (c.dtype == PROJ_BF16)
     e = c.D == 64 ? launch(attn_join_kernel<__nv_bfloat16, 64>, grid, 0, p, s)
                   : launch(attn_join_kernel<__nv_bfloat16, 128>, grid, 0, p, s);

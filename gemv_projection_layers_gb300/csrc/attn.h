@@ -40,6 +40,7 @@ struct AttnParams {
   int m, heads, D;
   Divisor group;
   int tile_rows, unit, ctas, min_units;
+  struct Split* splits;  // [ctas]
   float* part_o;   // [2 ctas][tile_rows][D]: sums relative to 2^m
   float* part_ml;  // [2 ctas][tile_rows][2]: m, sum
   uint32_t* status;
@@ -72,6 +73,12 @@ __device__ __forceinline__ int64_t units_of(const AttnParams& p, const Sequence&
   const int64_t all = static_cast<int64_t>(s.tiles) * s.units;
   return min(all < (int64_t{1} << 45) ? all * p.c.heads : all, int64_t{1} << 35);
 }
+
+// What a CTA leaves to be joined: the item in which its share begins, if that
+// began before and this is its second CTA (rows 0: nothing).
+struct alignas(32) Split {
+  int rows, lo, row0, head, first, last;  // first, last: the item's CTAs
+};
 
 // This CTA's share.
 struct Share {
@@ -136,6 +143,22 @@ __device__ __forceinline__ bool find_share(const AttnParams& p, int cta, Share& 
   return s.b >= 0;
 }
 
+__device__ __forceinline__ Split split_of(const AttnParams& p, const Share& s, int cta) {
+  Split r = {};
+  const Sequence seq = sequence_at(p, s.b);
+  const int64_t item = (s.first - s.before) / seq.units;
+  const int64_t begin = s.before + item * seq.units;
+  if (begin == s.first) return r;
+  r.first = share_owner(s.units, s.active, begin);
+  if (cta != r.first + 1) return r;
+  r.last = share_owner(s.units, s.active, begin + seq.units - 1);
+  r.lo = seq.lo;
+  r.head = static_cast<int>(item / seq.tiles);
+  r.row0 = static_cast<int>(item - static_cast<int64_t>(r.head) * seq.tiles) * p.tile_rows;
+  r.rows = min(p.tile_rows, seq.rows * static_cast<int>(p.group.d) - r.row0);
+  return r;
+}
+
 // exp2 by the special-function unit: relative error 2^-22; -inf gives 0.
 __device__ __forceinline__ float exp2_fast(float x) {
   float r;
@@ -146,26 +169,38 @@ __device__ __forceinline__ float exp2_fast(float x) {
 // The reference of a row that has seen nothing yet.
 constexpr float kNoScore = -3e38f;
 
-template <typename T>
-__device__ __forceinline__ float gate_value(float x, int sigmoid) {
-  return sigmoid ? __fdividef(1.f, 1.f + __expf(-x)) : x;
-}
-
-// Four neighbouring entries of a finished row: o = sum / l, gated, rounded.
-template <typename T>
+// N neighbouring entries of a finished row: sum / l, gated, rounded.  The gate
+// is read before anything is written: it may be `out` itself.
+template <typename T, int N>
 __device__ __forceinline__ void write_out(const AttnParams& p, int64_t row, int column,
-                                          const float (&sum)[4], float l) {
-  const float inv = 1.f / l;
-  float f[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) f[i] = l == 0.f ? 0.f : sum[i] * inv;  // nothing seen: 0
+                                          const float (&sum)[N], float l) {
+  constexpr int V = N < 8 ? N : 8;
+  const float inv = l == 0.f ? 0.f : __frcp_rn(l);  // nothing seen: 0
+  float f[N];
   if (p.gate) {
-    float g[4];
-    widen(load_vec<T, 4>(reinterpret_cast<const T*>(p.gate + row * p.ldg) + column), g);
+    Vec<T, V> g[N / V];
+    const T* from = reinterpret_cast<const T*>(p.gate + row * p.ldg) + column;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] *= gate_value<T>(g[i], p.sigmoid);
+    for (int i = 0; i < N / V; ++i) g[i] = load_vec<T, V>(from + i * V);
+#pragma unroll
+    for (int i = 0; i < N / V; ++i) {
+      float x[V];
+      widen(g[i], x);
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        f[i * V + j] = inv * (p.sigmoid ? __fdividef(1.f, 1.f + __expf(-x[j])) : x[j]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = inv;
   }
-  store_vec<T, 4>(reinterpret_cast<T*>(p.out + row * p.ldo) + column, f);
+#pragma unroll
+  for (int i = 0; i < N / V; ++i) {
+    float o[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) o[j] = l == 0.f ? 0.f : sum[i * V + j] * f[i * V + j];
+    store_vec<T, V>(reinterpret_cast<T*>(p.out + row * p.ldo) + column + i * V, o);
+  }
 }
 
 __device__ __forceinline__ float lse_of(float m, float l) {

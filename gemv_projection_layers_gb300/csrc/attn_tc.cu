@@ -9,20 +9,24 @@
 // rows of 128 bytes in the 128-byte swizzle: K-major for the first product,
 // N-major for the second, so V needs no transposition.
 //
-// Roles (20 warps): 0-3 and 4-7 are two softmax groups, a thread a row, which
+// Roles (16 warps): 0-3 and 4-7 are two softmax groups, a thread a row, which
 // take the tiles in turn and have an S, a P and an O each -- so one group's
 // exponentials run beside the other's products, and neither waits for the
-// other's sums; they meet at the item's end.  8-15 bring the cache: 8-bit
-// codes come to registers by 16-byte loads, four tiles ahead, and go to shared
-// memory as fp16, which holds them exactly (through shared memory twice they
-// would cost it half as much again as the MMAs' own reads); 16-bit entries by
-// asynchronous copies.  Warp 16 issues the MMAs; 17-19 only complete its
-// warpgroup, which gives registers to the others.
+// other's sums; they meet at the item's end.  8-11 bring the cache by 16-byte
+// asynchronous copies: 16-bit entries to their stage, 8-bit codes to a ring of
+// their own, from where the thread that copied them takes them to their stage
+// as fp16, which holds them exactly.  12 issues the MMAs.  13 walks the CTA's
+// share: it looks up pages, and hands each tile's addresses to the loading warps
+// and each segment to the others, so that no other warp divides or waits for a
+// table.  14 brings the scales; 15 only completes its warpgroup, which gives
+// registers to the softmax.
+// The loops are short on purpose: five roles share a scheduler's instruction
+// cache, and with loops unrolled over several tiles two thirds of the cycles
+// went to waiting for instructions.
 //
 // Softmax as in the streaming kernel: a reference per row that moves only when
-// a score is more than 6 above it (in powers of two), whereupon O is scaled in
-// tensor memory; probabilities are 2^8 at the reference, in fp16 (bf16 caches:
-// bf16).  Scales of K multiply the fp32 score; those of V the probability,
+// a score is well above it, whereupon O is scaled in tensor memory;
+// probabilities are fp16 (bf16 caches: bf16).  Scales of K multiply the fp32 score; those of V the probability,
 // relative to a power-of-two reference that the loading warps keep.
 #include <cuda_runtime.h>
 
@@ -36,32 +40,59 @@
 namespace proj {
 namespace {
 
-constexpr int kSoftWarps = 8, kLoadWarp = 8, kLoadWarps = 8, kMmaWarp = 16;
-constexpr int kThreads = 32 * 20;
+constexpr int kSoftWarps = 8, kLoadWarp = 8, kLoadWarps = 4, kMmaWarp = 12, kWalkWarp = 13, kScaleWarp = 14;
+constexpr int kThreads = 32 * 16;
 // Registers a thread: at launch, and of the three kinds of warpgroups (two of
-// softmax, two of loading, one of the MMA warp).
-constexpr int kRegs = 96, kSoftRegs = 128, kLoadRegs = 88, kMmaRegs = 48;
-static_assert(2 * kSoftRegs + 2 * kLoadRegs + kMmaRegs <= 5 * kRegs && 5 * kRegs * 128 <= 65536, "registers");
+// softmax, one of loading, one of the MMA warp).
+constexpr int kRegs = 128, kSoftRegs = 176, kLoadRegs = 96, kMmaRegs = 64;
+static_assert(2 * kSoftRegs + kLoadRegs + kMmaRegs <= 4 * kRegs && 4 * kRegs * 128 <= 65536, "registers");
 constexpr int kLoadThreads = 32 * kLoadWarps;
 constexpr int kKeys = kAttnTcUnit;
 constexpr int kTmemCols = 512;
-constexpr int kAhead = 4;  // tiles on their way to registers
+constexpr int kRaw = 5;       // tiles of 8-bit codes in shared memory or on their way there
+constexpr int kRawScales = 4;
+// A row's reference moves when a score is more than 2^kSlack above it, and is
+// 2^kLift as a probability: at most 2^14 and, where fp16 ends, 2^-28 of it.
+constexpr float kSlack = 10.f, kLift = 4.f;
+constexpr int kSlots = 8;     // tiles whose addresses are known
+constexpr int kSegments = 4;  // segments that are known
 
-template <int D>
+// What the walking warp says of a tile.
+struct alignas(16) Tile {
+  int64_t at[kKeys], scale[kKeys];  // offsets of entries (-1: no page) and scales
+  uint32_t valid[2];
+  int kind;  // 0: no more tiles, 1: a tile, + 2: of drafts, + 4: a segment's first
+  int pad;
+};
+
+// A part of an item.
+struct alignas(16) Segment {
+  int tiles;  // 0: no more segments
+  int b, lo, start, len, head, row0, rows, u0, whole;
+  int pad[2];
+};
+
+template <int kFormat, int D>
 struct Tc {
   static constexpr int kHalves = D / 64;            // of 64 dimensions
   static constexpr int kHalf = kKeys * 128;         // bytes
   static constexpr int kOperand = kHalves * kHalf;  // K or V of a tile
   static constexpr int kStage = 2 * kOperand;
-  static constexpr int kStages = D == 128 ? 6 : 8;
-  // beside a stage: scales of K and V, the reference of V's, keys that exist, keys
-  // of drafts with a value that is no finite number
-  static constexpr int kSide = 640, kVScale = 256, kRef = 512, kValid = 520, kOdd = 576;
-  static constexpr int kSideAt = kStages * kStage;
+  static constexpr bool kCoded = kFormat != PROJ_KV_ROWS;
+  static constexpr int kStages = kCoded ? (D == 128 ? 4 : 6) : (D == 128 ? 6 : 8);
+  static constexpr int kRawTile = 2 * kKeys * D;  // codes of K and V
+  // beside a stage: scales of K and V, the reference of V's, keys that exist; of
+  // drafts: keys whose scale of V, and keys of which a value is no finite number
+  static constexpr int kSide = 640, kVScale = 256, kRef = 512, kValid = 520, kOddScale = 528, kOdd = 576;
+  static constexpr int kRawAt = kStages * kStage;
+  static constexpr int kSideAt = kRawAt + (kCoded ? kRaw * kRawTile : 0);
   static constexpr int kFq = kSideAt + kStages * kSide;  // float[128]
   static constexpr int kMl = kFq + 512;                  // float[2][128][3]
-  static constexpr int kBarsAt = kMl + 3072;
-  static constexpr int kBars = 2 * kStages + 9;
+  static constexpr int kRawScaleAt = kMl + 3072;         // float[kRawScales][2][kKeys]
+  static constexpr int kTiles = kRawScaleAt + kRawScales * 8 * kKeys;
+  static constexpr int kSegs = kTiles + kSlots * static_cast<int>(sizeof(Tile));
+  static constexpr int kBarsAt = kSegs + kSegments * static_cast<int>(sizeof(Segment));
+  static constexpr int kBars = 2 * kStages + 9 + 2 * kSlots + 2 * kSegments;
   static constexpr int kSmem = 1024 + kBarsAt + kBars * 8 + 16;
   // tensor memory, in columns
   static constexpr int kQ = 0, kS = D / 2, kP = kS + 2 * kKeys, kO = kP + kKeys;
@@ -158,6 +189,15 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes)
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
 }
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void copies_sealed() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 __device__ __forceinline__ void st_shared_u4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
                                              uint32_t d) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
@@ -233,16 +273,15 @@ struct Walk {
   }
 };
 
-// What row `token` of a sequence sees of the 64 keys from key0 on.
 __device__ __forceinline__ uint64_t low_bits(int n) {
   return n <= 0 ? 0 : n >= 64 ? ~uint64_t{0} : (uint64_t{1} << n) - 1;
 }
-__device__ __forceinline__ uint64_t seen_of(const AttnParams& p, const Sequence& s, int token,
-                                            int key0) {
-  const int draft = key0 - s.start;  // of the first key
+// What row `token` of a sequence (whose first row is lo) sees of 64 keys, the
+// first of which is draft `draft` (below 0: before the drafts).
+__device__ __forceinline__ uint64_t seen_of(const AttnParams& p, int lo, int token, int draft) {
   uint64_t own;
   if (p.mask) {
-    const uint32_t* row = p.mask + (s.lo + token) * p.ldm;
+    const uint32_t* row = p.mask + static_cast<int64_t>(lo + token) * p.ldm;
     const int w = draft >> 5, shift = draft & 31;
     uint32_t v[3];
 #pragma unroll
@@ -257,7 +296,7 @@ __device__ __forceinline__ uint64_t seen_of(const AttnParams& p, const Sequence&
 
 template <typename T, int kFormat, int D>
 __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p) {
-  using F = Tc<D>;
+  using F = Tc<kFormat, D>;
   constexpr bool kCoded = kFormat != PROJ_KV_ROWS;
   using C = std::conditional_t<kCoded, __half, T>;
   constexpr bool kBf16 = std::is_same_v<C, __nv_bfloat16>;
@@ -270,12 +309,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
   const uint32_t full = base + F::kBarsAt, empty = full + 8 * NS;
   const uint32_t s_full = empty + 8 * NS, s_free = s_full + 16, p_full = s_free + 16;
   const uint32_t o_done = p_full + 16, q_full = o_done + 16;
+  const uint32_t t_full = q_full + 8, t_empty = t_full + 8 * kSlots;
+  const uint32_t g_full = t_empty + 8 * kSlots, g_empty = g_full + 8 * kSegments;
+  Tile* const s_tiles = reinterpret_cast<Tile*>(smem + F::kTiles);
+  Segment* const s_segs = reinterpret_cast<Segment*>(smem + F::kSegs);
   const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);
   const int lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
-      mbar_init(full + 8 * s, kLoadWarps);
+      mbar_init(full + 8 * s, kLoadWarps + 1);
       mbar_init(empty + 8 * s, 1);
     }
     for (int g = 0; g < 2; ++g) {
@@ -285,6 +328,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
       mbar_init(o_done + 8 * g, 1);
     }
     mbar_init(q_full, kSoftWarps);
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(t_full + 8 * s, 1);
+      mbar_init(t_empty + 8 * s, kLoadWarps + 1);
+    }
+    for (int s = 0; s < kSegments; ++s) {
+      mbar_init(g_full + 8 * s, 1);
+      mbar_init(g_empty + 8 * s, kSoftWarps + 1);
+    }
     fence_mbar_init();
   }
   // Tensor memory is taken when the kernel before has completed (it might hold
@@ -302,110 +353,240 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
 
   Share share;
   const bool mine = find_share<kThreads>(p, blockIdx.x, share);
-  Walk walk;
-  if (mine) walk.begin(p, share);
+  if (threadIdx.x == 0) p.splits[blockIdx.x] = mine ? split_of(p, share, blockIdx.x) : Split{};
 
   if (!mine) {
     // nothing to do but to give the tensor memory back
   } else if (warp >= kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
+    if (warp == kMmaWarp) {
     // ----------------------------------------------------------------- MMA
     const bool one = elect_one();
     bool ok = true;
     int stage = 0;        // of the next tile of keys
     uint32_t phase = 0;
     uint32_t turn[2] = {0u, 0u};  // tiles that each group has had
-    uint32_t items = 0;
     constexpr uint32_t kIdQk = instruction(kBf16, 0, 128, kKeys), kIdPv = instruction(kBf16, 1, 128, D);
-    const auto qk = [&](int g) {
-      ok = ok && wait_bar(full + 8 * stage, phase, p.status, kStatusTimeoutMma);
-      tc_fence_after();
-      if (one && ok) {
-        const uint32_t k = base + stage * F::kStage;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          mma_ts(tmem + F::kS + g * kKeys, tmem + F::kQ + kk * 8,
-                 smem_desc_sw128(k + (kk >> 2) * F::kHalf + (kk & 3) * 32), kIdQk, kk > 0);
-        tc_commit(s_full + 8 * g);
-      }
-      __syncwarp();
-      if (++stage == NS) {
-        stage = 0;
-        phase ^= 1u;
-      }
-    };
     int pv_stage = 0;
-    while (warp == kMmaWarp && walk.next(p)) {
-      const int tiles = walk.u1 - walk.u0;
-      ok = ok && wait_bar(q_full, items & 1u, p.status, kStatusTimeoutMma);
-      ++items;
-      tc_fence_after();
-      qk(0);
-      if (tiles > 1) qk(1);
-      for (int i = 0; i < tiles; ++i) {
+    for (int n = 0;; ++n) {
+      const int seg = n % kSegments;
+      ok = ok && wait_bar(g_full + 8 * seg, n / kSegments & 1u, p.status, kStatusTimeoutMma);
+      const int tiles = ok ? s_segs[seg].tiles : 0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(g_empty + 8 * seg);
+      if (tiles == 0) break;
+      ok = ok && wait_bar(q_full, n & 1u, p.status, kStatusTimeoutMma);
+      // the first product of tile i, then the second of tile i - 2
+#pragma unroll 1
+      for (int i = 0; i < tiles + 2; ++i) {
         const int g = i & 1;
-        if (i + 2 < tiles) {
-          ok = ok && wait_bar(s_free + 8 * g, turn[g] & 1u, p.status, kStatusTimeoutMma);
-          qk(g);
-        }
-        ok = ok && wait_bar(p_full + 8 * g, turn[g] & 1u, p.status, kStatusTimeoutMma);
-        ++turn[g];
-        tc_fence_after();
-        if (one && ok) {
-          const uint32_t v = base + pv_stage * F::kStage + F::kOperand;
+        if (i < tiles) {
+          if (i >= 2) ok = ok && wait_bar(s_free + 8 * g, turn[g] & 1u, p.status, kStatusTimeoutMma);
+          ok = ok && wait_bar(full + 8 * stage, phase, p.status, kStatusTimeoutMma);
+          tc_fence_after();
+          if (one && ok) {
+            const uint32_t k = base + stage * F::kStage;
 #pragma unroll
-          for (int kk = 0; kk < kKeys / 16; ++kk)
-            mma_ts(tmem + F::kO + g * D, tmem + F::kP + g * (kKeys / 2) + kk * 8,
-                   smem_desc_n_major(v + kk * 2048, F::kHalf), kIdPv, i >= 2 || kk > 0);
-          tc_commit(o_done + 8 * g);
-          tc_commit(empty + 8 * pv_stage);
+            for (int kk = 0; kk < D / 16; ++kk)
+              mma_ts(tmem + F::kS + g * kKeys, tmem + F::kQ + kk * 8,
+                     smem_desc_sw128(k + (kk >> 2) * F::kHalf + (kk & 3) * 32), kIdQk, kk > 0);
+            tc_commit(s_full + 8 * g);
+          }
+          __syncwarp();
+          if (++stage == NS) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (i >= 2) {
+          ok = ok && wait_bar(p_full + 8 * g, turn[g] & 1u, p.status, kStatusTimeoutMma);
+          ++turn[g];
+          tc_fence_after();
+          if (one && ok) {
+            const uint32_t v = base + pv_stage * F::kStage + F::kOperand;
+#pragma unroll
+            for (int kk = 0; kk < kKeys / 16; ++kk)
+              mma_ts(tmem + F::kO + g * D, tmem + F::kP + g * (kKeys / 2) + kk * 8,
+                     smem_desc_n_major(v + kk * 2048, F::kHalf), kIdPv, i >= 4 || kk > 0);
+            tc_commit(o_done + 8 * g);
+            tc_commit(empty + 8 * pv_stage);
+          }
+          __syncwarp();
+          if (++pv_stage == NS) pv_stage = 0;
+        }
+      }
+    }
+    } else if (warp == kWalkWarp) {
+      // ---------------------------------------------------- the CTA's share
+      Walk walk;
+      walk.begin(p, share);
+      bool ok = true;
+      int slot = 0;
+      uint32_t phase = 0;
+      for (int n = 0;; ++n) {
+        const bool more = ok && walk.next(p);
+        const int seg = n % kSegments;
+        ok = ok && wait_bar(g_empty + 8 * seg, (n / kSegments & 1u) ^ 1u, p.status, kStatusTimeoutProducer);
+        if (lane == 0) {
+          Segment& s = s_segs[seg];
+          s.tiles = more ? walk.u1 - walk.u0 : 0;
+          s.b = walk.share.b;
+          s.lo = walk.seq.lo;
+          s.start = walk.seq.start;
+          s.len = walk.seq.len;
+          s.head = walk.head;
+          s.row0 = walk.row0;
+          s.rows = walk.rows;
+          s.u0 = walk.u0;
+          s.whole = walk.u0 == 0 && walk.u1 == walk.seq.units;
+          mbar_arrive(g_full + 8 * seg);
         }
         __syncwarp();
-        if (++pv_stage == NS) pv_stage = 0;
+        const auto id_of = [&](int key) {
+          return key < walk.seq.len ? p.c.table[walk.share.b * p.c.ldt + quotient(key, p.c.page)] : -1;
+        };
+        int id[2] = {-1, -1};
+        if (more) {
+          id[0] = id_of(walk.u0 * kKeys + lane);
+          id[1] = id_of(walk.u0 * kKeys + 32 + lane);
+        }
+        for (int u = more ? walk.u0 : 0; u < (more ? walk.u1 : 1); ++u) {
+          const int key0 = u * kKeys;
+          int next[2] = {-1, -1};
+          if (more && u + 1 < walk.u1) {
+            next[0] = id_of(key0 + kKeys + lane);
+            next[1] = id_of(key0 + kKeys + 32 + lane);
+          }
+          ok = ok && wait_bar(t_empty + 8 * slot, phase ^ 1u, p.status, kStatusTimeoutProducer);
+          Tile& tile = s_tiles[slot];
+          if (more) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int key = key0 + j * 32 + lane;
+              const bool good = id[j] >= 0 && id[j] < p.c.pages;
+              const int spot = key - quotient(key, p.c.page) * static_cast<int>(p.c.page.d);
+              const Entry e = entry_at(p.c, id[j], spot, walk.head);
+              tile.at[j * 32 + lane] = good ? e.at : -1;
+              if (kCoded) tile.scale[j * 32 + lane] = e.scale;
+              const uint32_t valid = __ballot_sync(0xFFFFFFFFu, good);
+              if (lane == 0) tile.valid[j] = valid;
+            }
+          }
+          if (lane == 0) tile.kind = more ? 1 + (key0 + kKeys > walk.seq.start ? 2 : 0) + (u == walk.u0 ? 4 : 0) : 0;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(t_full + 8 * slot);
+          if (++slot == kSlots) {
+            slot = 0;
+            phase ^= 1u;
+          }
+          id[0] = next[0];
+          id[1] = next[1];
+        }
+        if (!more) break;
       }
+    } else if (warp == kScaleWarp) {
+      // ------------------------------------------------------------- scales
+      // A lane has keys lane and lane + 32, from the copy to what the softmax reads.
+      bool ok = true;
+      int slot = 0, from_slot = 0, stage = 0;
+      uint32_t t_phase = 0, phase = 0;
+      float ref = 0.f;
+      bool open = true;
+      const uint32_t raw = base + F::kRawScaleAt + lane * 4;
+      const auto fetch = [&] {
+        if (open) {
+          ok = ok && wait_bar(t_full + 8 * slot, t_phase, p.status, kStatusTimeoutDecode);
+          const Tile& tile = s_tiles[slot];
+          open = ok && tile.kind != 0;
+          if (kCoded && open) {
+            const uint32_t to = raw + slot % kRawScales * (8 * kKeys);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int bytes = tile.valid[j] >> lane & 1 ? 4 : 0;
+              const int64_t at = bytes ? tile.scale[j * 32 + lane] : 0;
+              copy4(to + j * 128, p.c.k_scale + at, bytes);
+              copy4(to + 4 * kKeys + j * 128, p.c.v_scale + at, bytes);
+            }
+          }
+          if (++slot == kSlots) {
+            slot = 0;
+            t_phase ^= 1u;
+          }
+        }
+        copies_sealed();
+      };
+      static_assert(kSlots % kRawScales == 0, "a slot's scales have one place");
+#pragma unroll 1
+      for (int s = 0; s < kRawScales - 1; ++s) fetch();
+#pragma unroll 1
+      for (;;) {
+        fetch();
+        if (!ok) break;
+        copies_wait<kRawScales - 1>();
+        const Tile& tile = s_tiles[from_slot];
+        const int kind = tile.kind;
+        if (kind == 0) break;
+        ok = ok && wait_bar(empty + 8 * stage, phase ^ 1u, p.status, kStatusTimeoutProducer);
+        const uint32_t side = base + F::kSideAt + stage * F::kSide;
+        if (lane < 2) st_shared_u(side + F::kValid + 4 * lane, tile.valid[lane]);
+        if constexpr (kCoded) {
+          const uint32_t at = raw + from_slot % kRawScales * (8 * kKeys);
+          if (kind & 4) ref = 0.f;
+          float w[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            // before the drafts every row sees the key, and NaN is what all of them get
+            const float v = ld_shared_f(at + 4 * kKeys + j * 128);
+            const bool fine = fabsf(v) < INFINITY;
+            w[j] = fine ? v : kind & 2 ? 0.f : __uint_as_float(0x7FC00000u);
+            const uint32_t odd = __ballot_sync(0xFFFFFFFFu, !fine);
+            if (lane == 0) st_shared_u(side + F::kOddScale + 4 * j, odd);
+          }
+          float top = fmaxf(fabsf(w[0]), fabsf(w[1]));  // the finite one, if only one is
+#pragma unroll
+          for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+          // a power of two not above the largest scale: its reciprocal is exact, and
+          // what is stored is at most 2
+          if (top > 2.f * ref) ref = __uint_as_float(max(__float_as_uint(top) & 0x7F800000u, 0x00800000u));
+          const float inv = ref > 0.f ? __frcp_rn(ref) : 0.f;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            st_shared_f(side + j * 128 + lane * 4, ld_shared_f(at + j * 128));
+            st_shared_f(side + F::kVScale + j * 128 + lane * 4, w[j] * inv);
+          }
+          if (lane == 0) st_shared_f(side + F::kRef, ref);
+        }
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(full + 8 * stage);
+          mbar_arrive(t_empty + 8 * from_slot);
+        }
+        if (++from_slot == kSlots) from_slot = 0;
+        if (++stage == NS) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      copies_wait<0>();
     }
   } else if (warp >= kLoadWarp) {
     // --------------------------------------------------------------- cache
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
-    const int tid = threadIdx.x - 32 * kLoadWarp, lwarp = warp - kLoadWarp;
+    const int tid = threadIdx.x - 32 * kLoadWarp;
     constexpr int kRow = kCoded ? D : 2 * D, kPieces = kRow / 16, kTurn = kLoadThreads / kPieces;
     constexpr int kPasses = kKeys / kTurn;
     const int piece = tid % kPieces, key_of = tid / kPieces;
-    bool ok = true;
-    int stage = 0;
-    uint32_t phase = 0;
-    // The tile that is fetched next, and the pages of its keys.
-    bool more = walk.next(p);
-    int unit = more ? walk.u0 : 0;
-    bool first = true;
-    int ids[kPasses], side_ids[2];
-    const auto id_of = [&](int key) {
-      return key < walk.seq.len ? p.c.table[walk.share.b * p.c.ldt + quotient(key, p.c.page)] : -1;
-    };
-    const auto pages = [&] {
-      if (!more) return;
-#pragma unroll
-      for (int j = 0; j < kPasses; ++j) ids[j] = id_of(unit * kKeys + j * kTurn + key_of);
-      if (lwarp < 2) {
-        side_ids[0] = id_of(unit * kKeys + lane);
-        side_ids[1] = id_of(unit * kKeys + 32 + lane);
-      }
-    };
-    const auto entry_of = [&](int id, int key, Entry& e) {
-      const bool good = id >= 0 && id < p.c.pages;
-      const int spot = key - quotient(key, p.c.page) * static_cast<int>(p.c.page.d);
-      e = good ? entry_at(p.c, id, spot, walk.head) : Entry{0, 0};
-      return good;
-    };
-    const auto advance = [&] {
-      first = false;
-      if (++unit == walk.u1) {
-        more = walk.next(p);
-        unit = more ? walk.u0 : 0;
-        first = true;
-      }
-      pages();
-    };
+    const uint8_t* const from_k = p.c.k + piece * 16;
+    const uint8_t* const from_v = p.c.v + piece * 16;
+    // Tiles are issued kLag before they are handed over.  16-bit entries: a tile is
+    // handed over when the copies of the kLag-th tile after it are issued, and those
+    // wait for the stage of the tile NS - kLag before; the MMA warp asks for tile n
+    // before it releases n - 2.
+    constexpr int kLag = kCoded ? kRaw - 1 : NS - 3;
+    uint32_t kinds = 0;  // of the tiles issued: three bits each, the oldest lowest
+    bool ok = true, open = true;
+    int stage = 0, slot = 0;
+    uint32_t phase = 0, t_phase = 0;
     const auto place = [&](int key, int half, int chunk) {
       return half * F::kHalf + key * 128 + ((chunk ^ (key & 7)) << 4);
     };
@@ -418,187 +599,102 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
         phase ^= 1u;
       }
     };
-    pages();
-    if constexpr (kCoded) {
-      uint4 rk[kAhead][kPasses], rv[kAhead][kPasses];
-      float scale[kAhead][2];
-      uint32_t valid[kAhead][2];
-      int kind[kAhead];  // 0: no tile, 1: a tile, + 2: of drafts, + 4: an item's first
-      float ref = 0.f;
-      const auto fetch = [&](int s) {
-        kind[s] = 0;
-        if (!more) return;
-        const int key0 = unit * kKeys;
-        kind[s] = 1 + (key0 + kKeys > walk.seq.start ? 2 : 0) + (first ? 4 : 0);
-#pragma unroll
-        for (int j = 0; j < kPasses; ++j) {
-          Entry e;
-          const bool good = entry_of(ids[j], key0 + j * kTurn + key_of, e);
-          rk[s][j] = rv[s][j] = make_uint4(0u, 0u, 0u, 0u);
-          if (good) {
-            rk[s][j] = *reinterpret_cast<const uint4*>(p.c.k + e.at + piece * 16);
-            rv[s][j] = *reinterpret_cast<const uint4*>(p.c.v + e.at + piece * 16);
-          }
-        }
-        if (lwarp < 2) {
-          const float* from = lwarp ? p.c.v_scale : p.c.k_scale;
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            Entry e;
-            const bool good = entry_of(side_ids[j], key0 + j * 32 + lane, e);
-            scale[s][j] = good ? from[e.scale] : 0.f;
-            valid[s][j] = __ballot_sync(0xFFFFFFFFu, good);
-          }
-        }
-        advance();
-      };
-      const auto spread = [&](uint32_t to, const uint4& w, int key, bool check, uint32_t& odd) {
-        const uint32_t word[4] = {w.x, w.y, w.z, w.w};
-        uint32_t h[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          h[2 * i] = decode_pair<kFormat>(word[i], 0);
-          h[2 * i + 1] = decode_pair<kFormat>(word[i], 1);
-        }
-        if (kFormat == PROJ_KV_E4M3 && check) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) h[i] = finite_pair<false>(h[i], odd);
-        }
-        // the second half's lanes store their two chunks in the other order: the
-        // eight lanes of a key then meet eight different banks
-        const int half = piece >> 2, c = 2 * (piece & 3), x = half & 1;
-        st_shared_u4(to + place(key, half, c + x), x ? h[4] : h[0], x ? h[5] : h[1], x ? h[6] : h[2],
-                     x ? h[7] : h[3]);
-        st_shared_u4(to + place(key, half, c + 1 - x), x ? h[0] : h[4], x ? h[1] : h[5],
-                     x ? h[2] : h[6], x ? h[3] : h[7]);
-      };
-      const auto store = [&](int s) {
-        ok = ok && wait_bar(empty + 8 * stage, phase ^ 1u, p.status, kStatusTimeoutProducer);
-        const uint32_t to = base + stage * F::kStage, side = base + F::kSideAt + stage * F::kSide;
-        const bool check = kind[s] & 2;
+    // Tiles of drafts: what is no finite number is taken out of this thread's own
+    // chunks of V, and the keys that had some are noted.
+    const auto finite_only = [&](int key) {
+      const uint32_t v = base + stage * F::kStage + F::kOperand;
+      uint32_t odd = 0;
+#pragma unroll 1
+      for (int i = 0; i < (kCoded ? 2 : 1); ++i) {
+        const uint32_t at = v + (kCoded ? place(key, piece >> 2, 2 * (piece & 3) + i) : place(key, piece >> 3, piece & 7));
+        const uint4 w = ld_shared_u4(at);
+        uint32_t o = 0;
+        const uint32_t a = finite_pair<kBf16>(w.x, o), b = finite_pair<kBf16>(w.y, o);
+        const uint32_t c = finite_pair<kBf16>(w.z, o), d = finite_pair<kBf16>(w.w, o);
+        if (o) st_shared_u4(at, a, b, c, d);
+        odd |= o;
+      }
+      const uint32_t who = __ballot_sync(0xFFFFFFFFu, odd) >> (lane - piece) & ((1u << kPieces) - 1u);
+      if (piece == 0) st_shared_byte(base + F::kSideAt + stage * F::kSide + F::kOdd + key, who ? 1u : 0u);
+    };
+    int in = 0;  // raw slot, or stage, of the tile that is issued
+    uint32_t in_phase = 0;
+    const auto issue = [&] {
+      int kind = 0;
+      if (open) {
+        ok = ok && wait_bar(t_full + 8 * slot, t_phase, p.status, kStatusTimeoutDecode);
+        kind = ok ? s_tiles[slot].kind : 0;
+        open = kind != 0;
+      }
+      if (kind) {
+        if constexpr (!kCoded)
+          ok = ok && wait_bar(empty + 8 * in, in_phase ^ 1u, p.status, kStatusTimeoutProducer);
+        const uint32_t to = kCoded ? base + F::kRawAt + in * F::kRawTile + tid * 16 : base + in * F::kStage;
 #pragma unroll
         for (int j = 0; j < kPasses; ++j) {
           const int key = j * kTurn + key_of;
-          uint32_t odd = 0;
-          spread(to, rk[s][j], key, false, odd);
-          spread(to + F::kOperand, rv[s][j], key, check, odd);
-          if (kFormat == PROJ_KV_E4M3 && check) {
-            const uint32_t who = __ballot_sync(0xFFFFFFFFu, odd) >> (lane - piece) & ((1u << kPieces) - 1u);
-            if (piece == 0) st_shared_byte(side + F::kOdd + key, who ? 1u : 0u);
-          }
+          const int64_t at = s_tiles[slot].at[key];
+          const int64_t from = at >= 0 ? at : 0;
+          const int bytes = at >= 0 ? 16 : 0;
+          const uint32_t dst = to + (kCoded ? j * kLoadThreads * 16 : place(key, piece >> 3, piece & 7));
+          copy16(dst, from_k + from, bytes);
+          copy16(dst + (kCoded ? F::kRawTile / 2 : F::kOperand), from_v + from, bytes);
         }
-        if (lwarp == 0) {
-          st_shared_f(side + lane * 4, scale[s][0]);
-          st_shared_f(side + 128 + lane * 4, scale[s][1]);
-          if (lane == 0) {
-            st_shared_u(side + F::kValid, valid[s][0]);
-            st_shared_u(side + F::kValid + 4, valid[s][1]);
-          }
-        } else if (lwarp == 1) {
-          if (kind[s] & 4) ref = 0.f;
-          float v[2] = {scale[s][0], scale[s][1]};
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            if (!(fabsf(v[j]) < INFINITY)) v[j] = __uint_as_float(0x7FC00000u);
-          float top = fmaxf(fabsf(v[0]), fabsf(v[1]));
-#pragma unroll
-          for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-          // a power of two not above the largest scale: its reciprocal is exact, and
-          // what is stored is at most 2
-          if (top > 2.f * ref) ref = __uint_as_float(max(__float_as_uint(top) & 0x7F800000u, 0x00800000u));
-          const float inv = ref > 0.f ? 1.f / ref : 0.f;
-          st_shared_f(side + F::kVScale + lane * 4, v[0] * inv);
-          st_shared_f(side + F::kVScale + 128 + lane * 4, v[1] * inv);
-          if (lane == 0) st_shared_f(side + F::kRef, ref);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(t_empty + 8 * slot);
+        if (++slot == kSlots) {
+          slot = 0;
+          t_phase ^= 1u;
         }
-        landed();
-      };
-#pragma unroll
-      for (int s = 0; s < kAhead; ++s) fetch(s);
-      for (bool going = true; going;) {
-#pragma unroll
-        for (int s = 0; s < kAhead; ++s) {
-          if (kind[s] == 0) {
-            going = false;
-            break;
-          }
-          store(s);
-          fetch(s);
+        if (++in == (kCoded ? kRaw : NS)) {
+          in = 0;
+          in_phase ^= 1u;
         }
       }
-    } else {
-      // copies two tiles behind their issue
-      constexpr int kLag = 3;
-      int kind[kLag + 1];
-      int in_stage = 0, slot = 0;
-      uint32_t in_phase = 0;
-      const auto issue = [&](int s) {
-        kind[s] = 0;
-        if (more) {
-          ok = ok && wait_bar(empty + 8 * in_stage, in_phase ^ 1u, p.status, kStatusTimeoutProducer);
-          const int key0 = unit * kKeys;
-          kind[s] = 1 + (key0 + kKeys > walk.seq.start ? 2 : 0);
-          const uint32_t to = base + in_stage * F::kStage, side = base + F::kSideAt + in_stage * F::kSide;
-#pragma unroll
-          for (int j = 0; j < kPasses; ++j) {
-            Entry e;
-            const int key = j * kTurn + key_of;
-            const int bytes = entry_of(ids[j], key0 + key, e) ? 16 : 0;
-            const uint32_t at = to + place(key, piece >> 3, piece & 7);
-            copy16(at, p.c.k + e.at + piece * 16, bytes);
-            copy16(at + F::kOperand, p.c.v + e.at + piece * 16, bytes);
-          }
-          if (lwarp == 0) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              Entry e;
-              const uint32_t v = __ballot_sync(0xFFFFFFFFu, entry_of(side_ids[j], key0 + j * 32 + lane, e));
-              if (lane == 0) st_shared_u(side + F::kValid + 4 * j, v);
-            }
-          }
-          if (++in_stage == NS) {
-            in_stage = 0;
-            in_phase ^= 1u;
-          }
-          advance();
+      copies_sealed();
+      kinds = kinds >> 3 | static_cast<uint32_t>(kind) << (3 * kLag);
+    };
+#pragma unroll 1
+    for (int i = 0; i < kLag; ++i) issue();
+    int raw = 0;
+#pragma unroll 1
+    for (;;) {
+      issue();
+      const uint32_t kind = kinds & 7u;
+      if (kind == 0) break;
+      copies_wait<kLag>();
+      if constexpr (kCoded) {
+        // this thread's own pieces: codes to fp16
+        ok = ok && wait_bar(empty + 8 * stage, phase ^ 1u, p.status, kStatusTimeoutProducer);
+        uint32_t from = base + F::kRawAt + raw * F::kRawTile + tid * 16;
+        const uint32_t to = base + stage * F::kStage;
+        // the second half's lanes store their two chunks in the other order: the
+        // eight lanes of a key then meet eight different banks
+        const int half = piece >> 2, c = 2 * (piece & 3), x = half & 1;
+#pragma unroll 2
+        for (int j = 0; j < 2 * kPasses; ++j) {
+          const uint4 w = ld_shared_u4(from);
+          from += kLoadThreads * 16;
+          const uint32_t dst = to + (j >= kPasses ? F::kOperand : 0);
+          const int key = (j >= kPasses ? j - kPasses : j) * kTurn + key_of;
+          const uint32_t a[4] = {decode_pair<kFormat>(w.x, 0), decode_pair<kFormat>(w.x, 1),
+                                 decode_pair<kFormat>(w.y, 0), decode_pair<kFormat>(w.y, 1)};
+          const uint32_t b[4] = {decode_pair<kFormat>(w.z, 0), decode_pair<kFormat>(w.z, 1),
+                                 decode_pair<kFormat>(w.w, 0), decode_pair<kFormat>(w.w, 1)};
+          st_shared_u4(dst + place(key, half, c + x), x ? b[0] : a[0], x ? b[1] : a[1], x ? b[2] : a[2],
+                       x ? b[3] : a[3]);
+          st_shared_u4(dst + place(key, half, c + 1 - x), x ? a[0] : b[0], x ? a[1] : b[1],
+                       x ? a[2] : b[2], x ? a[3] : b[3]);
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-      };
-      (void)slot;
-#pragma unroll
-      for (int s = 0; s < kLag; ++s) issue(s);
-      for (bool going = true; going;) {
-#pragma unroll
-        for (int s = 0; s <= kLag; ++s) {
-          if (kind[s] == 0) {
-            going = false;
-            break;
-          }
-          issue((s + kLag) % (kLag + 1));
-          asm volatile("cp.async.wait_group %0;" ::"n"(kLag) : "memory");
-          if (kind[s] & 2) {
-            // this thread's own pieces of V: what is no finite number is taken out
-            const uint32_t v = base + stage * F::kStage + F::kOperand;
-            const uint32_t side = base + F::kSideAt + stage * F::kSide;
-#pragma unroll
-            for (int j = 0; j < kPasses; ++j) {
-              const int key = j * kTurn + key_of;
-              const uint32_t at = v + place(key, piece >> 3, piece & 7);
-              const uint4 w = ld_shared_u4(at);
-              uint32_t odd = 0;
-              const uint32_t a = finite_pair<kBf16>(w.x, odd), b = finite_pair<kBf16>(w.y, odd);
-              const uint32_t c = finite_pair<kBf16>(w.z, odd), d = finite_pair<kBf16>(w.w, odd);
-              if (odd) st_shared_u4(at, a, b, c, d);
-              const uint32_t who = __ballot_sync(0xFFFFFFFFu, odd) >> (lane - piece % 32) &
-                                   ((1u << kPieces) - 1u);
-              if (piece == 0) st_shared_byte(side + F::kOdd + key, who ? 1u : 0u);
-            }
-          }
-          landed();
-        }
+        if (++raw == kRaw) raw = 0;
       }
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      if (kFormat != PROJ_KV_INT8 && (kind & 2u)) {
+#pragma unroll 1
+        for (int j = 0; j < kPasses; ++j) finite_only(j * kTurn + key_of);
+      }
+      landed();
     }
+    copies_wait<0>();
   } else {
     // ------------------------------------------------------------- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
@@ -611,17 +707,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
     uint32_t turn = 0;   // tiles that this group has had
     int tile_stage = 0;  // of the item's first tile
     uint32_t tile_phase = 0;
-    while (walk.next(p)) {
-      const Sequence& seq = walk.seq;
-      const int tiles = walk.u1 - walk.u0;
-      const bool real = row < walk.rows;
-      const bool busy = (warp & 3) * 32 < walk.rows;  // one of the warp's rows is real
-      const int r = walk.row0 + (real ? row : 0);
-      const int token = quotient(r, p.group), head = walk.head * G + r - token * G;
+    for (int n = 0;; ++n) {
+      const int slot_of = n % kSegments;
+      ok = ok && wait_bar(g_full + 8 * slot_of, n / kSegments & 1u, p.status, kStatusTimeoutEpilogue);
+      const Segment seg = s_segs[slot_of];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(g_empty + 8 * slot_of);
+      if (seg.tiles == 0) break;
+      const int tiles = seg.tiles;
+      const bool real = row < seg.rows;
+      const bool busy = (warp & 3) * 32 < seg.rows;  // one of the warp's rows is real
+      const int r = seg.row0 + (real ? row : 0);
+      const int token = quotient(r, p.group), head = seg.head * G + r - token * G;
       // -------------------------------------------------------- queries --
       if (group == 0) {
         if (busy) {
-          const uint8_t* from = p.q + (seq.lo + token) * p.ldq + static_cast<int64_t>(head) * D * 2;
+          const uint8_t* from = p.q + static_cast<int64_t>(seg.lo + token) * p.ldq + static_cast<int64_t>(head) * D * 2;
           uint32_t q[D / 2];
 #pragma unroll
           for (int i = 0; i < D / 8; ++i) {
@@ -631,23 +732,32 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
             q[4 * i + 2] = w.z;
             q[4 * i + 3] = w.w;
           }
+          // The factor of a row's scores is positive (its sign goes to the queries, and
+          // so does a zero), so the largest product is the largest score.
           float f = 1.f;
           if constexpr (kCoded && std::is_same_v<T, __nv_bfloat16>) {
+            // bf16 to fp16: the row's largest magnitude is brought to 2^14 .. 2^15
             uint32_t top = 0;
 #pragma unroll
             for (int i = 0; i < D / 2; ++i) top = max(max(top, q[i] & 0x7FFFu), q[i] >> 16 & 0x7FFFu);
             int e = 0;
-            if (top > 0 && top < 0x7F80u) e = 14 - ilogbf(__uint_as_float(top << 16));
-            const float fa = scalbnf(1.f, e / 2), fb = scalbnf(1.f, e - e / 2);
+            if (top > 0 && top < 0x7F80u) e = min(126, 14 - ilogbf(__uint_as_float(top << 16)));
+            const F2 up = f2(scalbnf(1.f, e));
 #pragma unroll
             for (int i = 0; i < D / 2; ++i) {
               float x, y;
               widen2(q[i], x, y, __nv_bfloat16());
-              q[i] = pack2(x * fa * fb, y * fa * fb, __half());
+              parts(mul2(f2(x, y), up), x, y);
+              q[i] = pack2(x, y, __half());
             }
             f = scalbnf(1.f, -e);
           }
-          st_shared_f(base + F::kFq + row * 4, f * p.scale_log2);
+          if (p.scale_log2 <= 0.f) {
+            const uint32_t keep = p.scale_log2 == 0.f ? 0u : 0xFFFFFFFFu, turned = p.scale_log2 < 0.f ? 0x80008000u : 0u;
+#pragma unroll
+            for (int i = 0; i < D / 2; ++i) q[i] = (q[i] & keep) ^ turned;
+          }
+          st_shared_f(base + F::kFq + row * 4, fmaxf(f * fabsf(p.scale_log2), 1.17549435e-38f));
 #pragma unroll
           for (int i = 0; i < D / 32; ++i) tmem_st16(tmem + lanes + F::kQ + i * 16, q + i * 16);
           tmem_st_wait();
@@ -670,41 +780,47 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
       for (int i = group; i < tiles; i += 2) {
         const uint32_t side = base + F::kSideAt + stage * F::kSide;
         ok = ok && wait_bar(s_full + 8 * group, turn & 1u, p.status, kStatusTimeoutEpilogue);
-        ok = ok && wait_bar(full + 8 * stage, phase, p.status, kStatusTimeoutEpilogue);
         tc_fence_after();
         if (busy) {
           float f[kKeys];
           tmem_ld32(my_s, f);
           tmem_ld32(my_s + 32, f + 32);
+          // what stands beside the stage
+          ok = ok && wait_bar(full + 8 * stage, phase, p.status, kStatusTimeoutEpilogue);
           tmem_ld_wait();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(s_free + 8 * group);
-          const int key0 = (walk.u0 + i) * kKeys;
+          const int key0 = (seg.u0 + i) * kKeys;
           const uint2 valid = ld_shared_u2(side + F::kValid);
-          const bool partial = (valid.x & valid.y) != 0xFFFFFFFFu || key0 + kKeys > seq.start;
+          const bool partial = (valid.x & valid.y) != 0xFFFFFFFFu || key0 + kKeys > seg.start;
           if constexpr (kCoded) {
-            const F2 q2 = f2(fq);
 #pragma unroll
-            for (int j = 0; j < kKeys; j += 4) {
-              const float4 ks = ld_shared_f4(side + j * 4);
-              parts(mul2(f2(f[j], f[j + 1]), mul2(f2(ks.x, ks.y), q2)), f[j], f[j + 1]);
-              parts(mul2(f2(f[j + 2], f[j + 3]), mul2(f2(ks.z, ks.w), q2)), f[j + 2], f[j + 3]);
+            for (int c = 0; c < kKeys; c += 16) {
+              float4 ks[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) ks[j] = ld_shared_f4(side + (c + 4 * j) * 4);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                float* x = f + c + 4 * j;
+                parts(mul2(f2(x[0], x[1]), f2(ks[j].x, ks[j].y)), x[0], x[1]);
+                parts(mul2(f2(x[2], x[3]), f2(ks[j].z, ks[j].w)), x[2], x[3]);
+              }
             }
-          } else {
-            const F2 q2 = f2(fq);
-#pragma unroll
-            for (int j = 0; j < kKeys; j += 2) parts(mul2(f2(f[j], f[j + 1]), q2), f[j], f[j + 1]);
           }
           uint32_t seen[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
           if (partial) {
-            const uint64_t all = seen_of(p, seq, token, key0);
+            const uint64_t all = seen_of(p, seg.lo, token, key0 - seg.start);
             seen[0] = static_cast<uint32_t>(all) & valid.x;
             seen[1] = static_cast<uint32_t>(all >> 32) & valid.y;
 #pragma unroll
             for (int j = 0; j < kKeys; ++j)
               if (!(seen[j >> 5] >> (j & 31) & 1)) f[j] = -INFINITY;
-            if (kFormat != PROJ_KV_INT8 && key0 + kKeys > seq.start) {
+            if (kCoded && key0 + kKeys > seg.start) {
+              const uint2 w = ld_shared_u2(side + F::kOddScale);
+              odd |= (w.x & seen[0]) || (w.y & seen[1]);
+            }
+            if (kFormat != PROJ_KV_INT8 && key0 + kKeys > seg.start) {
 #pragma unroll 1
               for (int j = 0; j < kKeys; j += 4) {
                 uint32_t w;
@@ -716,11 +832,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
               }
             }
           }
-          float top = f[0];
+          float tops[4] = {f[0], f[1], f[2], f[3]};
 #pragma unroll
-          for (int j = 1; j < kKeys; ++j) top = fmaxf(top, f[j]);
+          for (int j = 4; j < kKeys; ++j) tops[j & 3] = fmaxf(tops[j & 3], f[j]);
+          const float top = fq * fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
           float down = 1.f;
-          if (top > ref + 6.f) {
+          if (top > ref + kSlack) {
             down = exp2_fast(ref - top);
             ref = top;
             sum *= down;
@@ -732,51 +849,57 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
               v_ref = now;
             }
           }
-          // the group's products before: P is free, and O complete
-          if (turn > 0) ok = ok && wait_bar(o_done + 8 * group, (turn - 1) & 1u, p.status, kStatusTimeoutEpilogue);
-          tc_fence_after();
-          if (i >= 2 && __any_sync(0xFFFFFFFFu, down != 1.f)) {
-#pragma unroll 1
-            for (int c = 0; c < D; c += 16) {
-              float o[16];
-              tmem_ld16(my_o + c, o);
-              tmem_ld_wait();
-              uint32_t w[16];
-#pragma unroll
-              for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(o[j] * down);
-              tmem_st16(my_o + c, w);
-            }
-          }
-          const F2 low = f2(8.f - ref);
-          F2 total = f2(0.f);
+          const F2 low = f2(kLift - ref), q2 = f2(fq);
+          F2 total[2] = {f2(0.f), f2(0.f)};
 #pragma unroll
           for (int c = 0; c < kKeys; c += 32) {
             uint32_t w[16];
 #pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-              float e[4];
-              parts(add2(f2(f[c + j], f[c + j + 1]), low), e[0], e[1]);
-              parts(add2(f2(f[c + j + 2], f[c + j + 3]), low), e[2], e[3]);
-#pragma unroll
-              for (int x = 0; x < 4; ++x) e[x] = exp2_fast(e[x]);
-              total = add2(total, add2(f2(e[0], e[1]), f2(e[2], e[3])));
+            for (int j = 0; j < 32; j += 16) {
+              float4 vs[4];
               if constexpr (kCoded) {
-                const float4 vs = ld_shared_f4(side + F::kVScale + (c + j) * 4);
-                parts(mul2(f2(e[0], e[1]), f2(vs.x, vs.y)), e[0], e[1]);
-                parts(mul2(f2(e[2], e[3]), f2(vs.z, vs.w)), e[2], e[3]);
-                if (partial) {
 #pragma unroll
-                  for (int x = 0; x < 4; ++x)
-                    if (!(seen[c >> 5] >> (j + x) & 1)) e[x] = 0.f;
+                for (int x = 0; x < 4; ++x) vs[x] = ld_shared_f4(side + F::kVScale + (c + j + 4 * x) * 4);
+              }
+              float e[16];
+#pragma unroll
+              for (int x = 0; x < 16; x += 2) parts(fma2(f2(f[c + j + x], f[c + j + x + 1]), q2, low), e[x], e[x + 1]);
+#pragma unroll
+              for (int x = 0; x < 16; ++x) e[x] = exp2_fast(e[x]);
+#pragma unroll
+              for (int x = 0; x < 16; x += 4) {
+                const F2 e0 = f2(e[x], e[x + 1]), e1 = f2(e[x + 2], e[x + 3]);
+                total[0] = add2(total[0], e0);
+                total[1] = add2(total[1], e1);
+                if constexpr (kCoded) {
+                  parts(mul2(e0, f2(vs[x / 4].x, vs[x / 4].y)), e[x], e[x + 1]);
+                  parts(mul2(e1, f2(vs[x / 4].z, vs[x / 4].w)), e[x + 2], e[x + 3]);
+                }
+                w[(j + x) / 2] = pack2(e[x], e[x + 1], C());
+                w[(j + x) / 2 + 1] = pack2(e[x + 2], e[x + 3], C());
+              }
+            }
+            if (c == 0) {
+              // the group's products before: P is free, and O complete
+              if (turn > 0) ok = ok && wait_bar(o_done + 8 * group, (turn - 1) & 1u, p.status, kStatusTimeoutEpilogue);
+              tc_fence_after();
+              if (i >= 2 && __any_sync(0xFFFFFFFFu, down != 1.f)) {
+#pragma unroll 1
+                for (int c = 0; c < D; c += 16) {
+                  float o[16];
+                  tmem_ld16(my_o + c, o);
+                  tmem_ld_wait();
+                  uint32_t w[16];
+#pragma unroll
+                  for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(o[j] * down);
+                  tmem_st16(my_o + c, w);
                 }
               }
-              w[j / 2] = pack2(e[0], e[1], C());
-              w[j / 2 + 1] = pack2(e[2], e[3], C());
             }
             tmem_st16(my_p + c / 2, w);
           }
           float a, b;
-          parts(total, a, b);
+          parts(add2(total[0], total[1]), a, b);
           sum += a + b;
           tmem_st_wait();
         } else {
@@ -801,7 +924,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
 
       // ----------------------------------------------- the groups' sums joined --
       const uint32_t ml = base + F::kMl;
-      st_shared_f(ml + (group * 128 + row) * 12, ref - 8.f);
+      st_shared_f(ml + (group * 128 + row) * 12, ref - kLift);
       st_shared_f(ml + (group * 128 + row) * 12 + 4, sum);
       st_shared_f(ml + (group * 128 + row) * 12 + 8, kCoded ? v_ref : 1.f);
       if (tiles > group) ok = ok && wait_bar(o_done + 8 * group, (turn - 1) & 1u, p.status, kStatusTimeoutEpilogue);
@@ -820,8 +943,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
         const float f0 = exp2_fast(m[0] - top), f1 = exp2_fast(m[1] - top);
         const float all = l[0] * f0 + l[1] * f1;
         const float a0 = f0 * up[0], a1 = f1 * up[1];
-        const bool whole = walk.u0 == 0 && walk.u1 == seq.units;
-        const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (walk.u0 == 0 ? 1 : 0);
+        const bool whole = seg.whole;
+        const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (seg.u0 == 0 ? 1 : 0);
         float* part = p.part_o + (slot * kAttnTcRows + row) * D;
         constexpr int kCols = D / 2;  // each group writes half of the columns
 #pragma unroll 1
@@ -832,21 +955,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
           tmem_ld_wait();
 #pragma unroll
           for (int j = 0; j < 16; ++j) o[j] = tiles > 1 ? o[j] * a0 + o1[j] * a1 : o[j] * a0;
-          if (kFormat != PROJ_KV_INT8 && any_odd && real) {
+          if (any_odd && real) {
             // the drafts of this part once more: what is no finite number goes to
             // the rows that see it
-            const int d0 = max(0, walk.u0 * kKeys - seq.start);
-            const int d1 = min(seq.len - seq.start, walk.u1 * kKeys - seq.start);
+            const int d0 = max(0, seg.u0 * kKeys - seg.start);
+            const int d1 = min(seg.len - seg.start, (seg.u0 + seg.tiles) * kKeys - seg.start);
             for (int d = d0; d < d1; ++d) {
-              const bool sees = p.mask ? (d >> 5) < p.words && (p.mask[(seq.lo + token) * p.ldm + (d >> 5)] >> (d & 31) & 1)
+              const bool sees = p.mask ? (d >> 5) < p.words && (p.mask[static_cast<int64_t>(seg.lo + token) * p.ldm + (d >> 5)] >> (d & 31) & 1)
                                        : d <= token;
               int id, spot;
-              if (!sees || !page_of(p.c, walk.share.b, seq.start + d, id, spot)) continue;
-              const uint8_t* v = p.c.v + entry_at(p.c, id, spot, walk.head).at;
+              if (!sees || !page_of(p.c, seg.b, seg.start + d, id, spot)) continue;
+              const Entry e = entry_at(p.c, id, spot, seg.head);
+              const uint8_t* v = p.c.v + e.at;
+              const bool fine = !kCoded || fabsf(p.c.v_scale[e.scale]) < INFINITY;
               for (int j = 0; j < 16; ++j) {
                 float x;
                 if constexpr (kCoded)
-                  x = (v[c + j] & 0x7F) == 0x7F ? __uint_as_float(0x7FC00000u) : 0.f;
+                  x = !fine || (kFormat == PROJ_KV_E4M3 && (v[c + j] & 0x7F) == 0x7F) ? __uint_as_float(0x7FC00000u) : 0.f;
                 else
                   x = to_f32(reinterpret_cast<const T*>(v)[c + j]);
                 if (!(fabsf(x) < INFINITY)) {
@@ -857,19 +982,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
               }
             }
           }
+          if (real && whole) {
+            write_out<T>(p, static_cast<int64_t>(seg.lo + token), head * D + c, o, all);
+          } else if (real) {
 #pragma unroll
-          for (int j = 0; j < 16; j += 4) {
-            const float v[4] = {o[j], o[j + 1], o[j + 2], o[j + 3]};
-            if (real && whole)
-              write_out<T>(p, seq.lo + token, head * D + c + j, v, all);
-            else if (real)
-              *reinterpret_cast<float4*>(part + c + j) = make_float4(v[0], v[1], v[2], v[3]);
+            for (int j = 0; j < 16; j += 4)
+              *reinterpret_cast<float4*>(part + c + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
           }
           __syncwarp();
         }
         if (real && group == 0) {
           if (whole) {
-            if (p.lse) p.lse[static_cast<int64_t>(seq.lo + token) * p.heads + head] = lse_of(top, all);
+            if (p.lse) p.lse[static_cast<int64_t>(seg.lo + token) * p.heads + head] = lse_of(top, all);
           } else {
             *reinterpret_cast<float2*>(p.part_ml + (slot * kAttnTcRows + row) * 2) = make_float2(top, all);
           }
@@ -893,13 +1017,13 @@ template <typename T, int kFormat, int D>
 cudaError_t tc_run(const AttnParams& p, cudaStream_t s) {
   const auto kernel = attn_tc_kernel<T, kFormat, D>;
   static std::atomic<uint64_t> done{0};
-  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), Tc<D>::kSmem, done);
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), Tc<kFormat, D>::kSmem, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   cfg.gridDim = dim3(p.ctas);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Tc<D>::kSmem;
+  cfg.dynamicSmemBytes = Tc<kFormat, D>::kSmem;
   cfg.stream = s;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;

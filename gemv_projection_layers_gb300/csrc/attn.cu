@@ -155,10 +155,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_stream_kernel(const AttnPara
       seq = sequence_at(p, b);
     }
     const int64_t local = at - before;
-    const int64_t item = local / seq.units;
+    const int64_t item = divide(local, seq.units);
     const int u0 = static_cast<int>(local - item * seq.units);
     const int u1 = static_cast<int>(min(static_cast<int64_t>(seq.units), u0 + (share.end - at)));
-    const int head = static_cast<int>(item / seq.tiles);
+    const int head = static_cast<int>(divide(item, seq.tiles));
     const int row0 = static_cast<int>(item - static_cast<int64_t>(head) * seq.tiles) * F::kRows;
     const int all_rows = seq.rows * G;
 
@@ -565,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_stream_kernel(const AttnPara
   }
 }
 
-// The join.  CTA (c, y) has what CTA c left to be joined, rows y, y + gridDim.y,
+// The join.  CTA (x, y) has the x-th item that was split, rows y, y + gridDim.y,
 // ... in sets of threads that span a row.  Few partial results: each set takes
 // a row; many: a CTA's sets share a row's partial results, each relative to a
 // running maximum, and meet in shared memory.
@@ -575,10 +575,28 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) attn_join_kernel(const AttnParams p) {
   constexpr int kLanes = D / 4, kSets = kThreads / kLanes;
   __shared__ float s_o[kSets][D], s_ml[kSets][2];
+  __shared__ int s_found;
   griddep_launch_dependents();
   griddep_wait();
-  const Split it = p.splits[blockIdx.x];
-  if (it.rows == 0) return;
+  // the item: the x-th CTA that left one
+  if (threadIdx.x < 32) {
+    int found = -1, seen = 0;
+    for (int c = 0; c < p.ctas && found < 0; c += 32) {
+      const int at = c + static_cast<int>(threadIdx.x);
+      const uint32_t some = __ballot_sync(0xFFFFFFFFu, at < p.ctas && p.splits[at].rows > 0);
+      const int rank = static_cast<int>(blockIdx.x) - seen;
+      if (rank < __popc(some)) {
+        uint32_t left = some;
+        for (int i = 0; i < rank; ++i) left &= left - 1;
+        found = c + __ffs(left) - 1;
+      }
+      seen += __popc(some);
+    }
+    if (threadIdx.x == 0) s_found = found;
+  }
+  __syncthreads();
+  if (s_found < 0) return;
+  const Split it = p.splits[s_found];
   const int G = static_cast<int>(p.group.d);
   const int set = threadIdx.x / kLanes, quad = threadIdx.x % kLanes;
   const bool few = it.last - it.first < kFewParts;
@@ -674,6 +692,7 @@ cudaError_t stream_format(int format, const AttnParams& p, cudaStream_t s) {
 
 struct Plan {
   bool tc;
+  int64_t rows;  // of a sequence and a head of keys and values, on average
   int tile_rows, unit, ctas, min_units;
   int64_t bytes;
 };
@@ -692,6 +711,7 @@ const char* make_plan(const proj_kv_cache* cache, int64_t m, int64_t heads, Plan
   const int64_t rows = cache->sequences
                            ? (m + cache->sequences - 1) / cache->sequences * (heads / cache->heads)
                            : 1;
+  plan->rows = rows;
   plan->tc = rows > 32;
   plan->unit = plan->tc ? kAttnTcUnit : kStep;
   plan->tile_rows = plan->tc ? kAttnTcRows : rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
@@ -779,6 +799,8 @@ extern "C" int proj_attn(const proj_attn_args* args, proj_stream stream) {
   p.unit = plan.unit;
   p.ctas = plan.ctas;
   p.min_units = plan.min_units;
+  while ((1 << p.tile_shift) < p.tile_rows) ++p.tile_shift;
+  while ((1 << p.unit_shift) < p.unit) ++p.unit_shift;
   void* status_word = nullptr;
   cudaError_t e = cudaGetSymbolAddress(&status_word, g_attn_status);
   if (e != cudaSuccess) return record_cuda(e, call);
@@ -795,11 +817,13 @@ extern "C" int proj_attn(const proj_attn_args* args, proj_stream stream) {
   else
     e = c.D == 64 ? stream_format<__half, 64>(c.format, p, s) : stream_format<__half, 128>(c.format, p, s);
   if (e != cudaSuccess) return record_cuda(e, call);
-  // Few items are split into many parts, a CTA a row; else a set of threads a row.
-  const int64_t items = std::max<int64_t>(1, a.m * (a.heads / c.heads) / plan.tile_rows) * c.heads;
+  // No more items than this, and as many CTAs to one as its rows keep at work.
+  const int64_t rows = std::min<int64_t>(plan.tile_rows, plan.rows);
+  const int64_t items = (a.m * (a.heads / c.heads) / plan.tile_rows + c.sequences) * c.heads;
   const int sets = kThreads / (static_cast<int>(c.D) / 4);
-  const int rows = items * kFewParts < plan.ctas ? plan.tile_rows : std::max(1, plan.tile_rows / sets);
-  const dim3 grid(plan.ctas, static_cast<unsigned>(rows));
+  const int64_t x = std::min<int64_t>(items, plan.ctas);
+  const int64_t y = x * kFewParts < plan.ctas ? rows : (rows + sets - 1) / sets;
+  const dim3 grid(static_cast<unsigned>(x), static_cast<unsigned>(std::max<int64_t>(1, y)));
   if (c.dtype == PROJ_BF16)
     e = c.D == 64 ? launch(attn_join_kernel<__nv_bfloat16, 64>, grid, 0, p, s)
                   : launch(attn_join_kernel<__nv_bfloat16, 128>, grid, 0, p, s);

@@ -40,6 +40,7 @@ struct AttnParams {
   int m, heads, D;
   Divisor group;
   int tile_rows, unit, ctas, min_units;
+  int tile_shift, unit_shift;  // their logarithms
   struct Split* splits;  // [ctas]
   float* part_o;   // [2 ctas][tile_rows][D]: sums relative to 2^m
   float* part_ml;  // [2 ctas][tile_rows][2]: m, sum
@@ -61,9 +62,9 @@ __device__ __forceinline__ Sequence sequence_at(const AttnParams& p, int b) {
   s.start = min(max(p.start[b], 0), p.c.capacity);
   s.len = min(s.start + s.rows, p.c.capacity);
   const int64_t rows = static_cast<int64_t>(s.rows) * static_cast<int>(p.group.d);
-  s.tiles = static_cast<int>((rows + p.tile_rows - 1) / p.tile_rows);
+  s.tiles = static_cast<int>((rows + p.tile_rows - 1) >> p.tile_shift);
   // an item without keys has one unit all the same: its rows are written
-  s.units = max(1, (s.len + p.unit - 1) / p.unit);
+  s.units = max(1, (s.len + p.unit - 1) >> p.unit_shift);
   return s;
 }
 
@@ -88,12 +89,18 @@ struct Share {
   int64_t before;  // units of the sequences before b
 };
 
+// a / b of numbers that are not negative: mostly both have 32 bits.
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
 __device__ __forceinline__ int64_t share_begin(int64_t W, int active, int cta) {
-  return W / active * cta + W % active * cta / active;
+  const int64_t each = divide(W, active);
+  return each * cta + divide((W - each * active) * cta, active);
 }
 // The CTA that holds unit x.
 __device__ __forceinline__ int share_owner(int64_t W, int active, int64_t x) {
-  return static_cast<int>(((x + 1) * active - 1) / W);
+  return static_cast<int>(divide((x + 1) * active - 1, W));
 }
 
 // All threads of the CTA; kThreads of them.  `cta`: whose share.  False: none.
@@ -123,7 +130,7 @@ __device__ __forceinline__ bool find_share(const AttnParams& p, int cta, Share& 
     W += warp_sum[w];
   }
   s.units = W;
-  s.active = static_cast<int>(min(static_cast<int64_t>(p.ctas), max(W / p.min_units, int64_t{1})));
+  s.active = static_cast<int>(min(static_cast<int64_t>(p.ctas), max(divide(W, p.min_units), int64_t{1})));
   if (W == 0 || cta >= s.active) return false;
   s.first = share_begin(W, s.active, cta);
   s.end = share_begin(W, s.active, cta + 1);
@@ -146,14 +153,14 @@ __device__ __forceinline__ bool find_share(const AttnParams& p, int cta, Share& 
 __device__ __forceinline__ Split split_of(const AttnParams& p, const Share& s, int cta) {
   Split r = {};
   const Sequence seq = sequence_at(p, s.b);
-  const int64_t item = (s.first - s.before) / seq.units;
+  const int64_t item = divide(s.first - s.before, seq.units);
   const int64_t begin = s.before + item * seq.units;
   if (begin == s.first) return r;
   r.first = share_owner(s.units, s.active, begin);
   if (cta != r.first + 1) return r;
   r.last = share_owner(s.units, s.active, begin + seq.units - 1);
   r.lo = seq.lo;
-  r.head = static_cast<int>(item / seq.tiles);
+  r.head = static_cast<int>(divide(item, seq.tiles));
   r.row0 = static_cast<int>(item - static_cast<int64_t>(r.head) * seq.tiles) * p.tile_rows;
   r.rows = min(p.tile_rows, seq.rows * static_cast<int>(p.group.d) - r.row0);
   return r;
@@ -170,37 +177,32 @@ __device__ __forceinline__ float exp2_fast(float x) {
 constexpr float kNoScore = -3e38f;
 
 // N neighbouring entries of a finished row: sum / l, gated, rounded.  The gate
-// is read before anything is written: it may be `out` itself.
-template <typename T, int N>
+// has been read already: it may be `out` itself.
+template <typename T, int N, int V>
 __device__ __forceinline__ void write_out(const AttnParams& p, int64_t row, int column,
-                                          const float (&sum)[N], float l) {
-  constexpr int V = N < 8 ? N : 8;
+                                          const float (&sum)[N], float l,
+                                          const Vec<T, V> (&gate)[N / V]) {
   const float inv = l == 0.f ? 0.f : __frcp_rn(l);  // nothing seen: 0
-  float f[N];
-  if (p.gate) {
-    Vec<T, V> g[N / V];
-    const T* from = reinterpret_cast<const T*>(p.gate + row * p.ldg) + column;
-#pragma unroll
-    for (int i = 0; i < N / V; ++i) g[i] = load_vec<T, V>(from + i * V);
-#pragma unroll
-    for (int i = 0; i < N / V; ++i) {
-      float x[V];
-      widen(g[i], x);
-#pragma unroll
-      for (int j = 0; j < V; ++j)
-        f[i * V + j] = inv * (p.sigmoid ? __fdividef(1.f, 1.f + __expf(-x[j])) : x[j]);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) f[i] = inv;
-  }
 #pragma unroll
   for (int i = 0; i < N / V; ++i) {
     float o[V];
 #pragma unroll
-    for (int j = 0; j < V; ++j) o[j] = l == 0.f ? 0.f : sum[i * V + j] * f[i * V + j];
+    for (int j = 0; j < V; ++j) o[j] = l == 0.f ? 0.f : sum[i * V + j] * inv;
+    if (p.gate) {
+      float x[V];
+      widen(gate[i], x);
+#pragma unroll
+      for (int j = 0; j < V; ++j) o[j] *= p.sigmoid ? __fdividef(1.f, 1.f + __expf(-x[j])) : x[j];
+    }
     store_vec<T, V>(reinterpret_cast<T*>(p.out + row * p.ldo) + column + i * V, o);
   }
+}
+template <typename T, int N>
+__device__ __forceinline__ void write_out(const AttnParams& p, int64_t row, int column,
+                                          const float (&sum)[N], float l) {
+  Vec<T, N> gate[1] = {};
+  if (p.gate) gate[0] = load_vec<T, N>(reinterpret_cast<const T*>(p.gate + row * p.ldg) + column);
+  write_out<T>(p, row, column, sum, l, gate);
 }
 
 __device__ __forceinline__ float lse_of(float m, float l) {

@@ -9,17 +9,16 @@
 // rows of 128 bytes in the 128-byte swizzle: K-major for the first product,
 // N-major for the second, so V needs no transposition.
 //
-// Roles (16 warps): 0-3 and 4-7 are two softmax groups, a thread a row, which
+// Roles (19 warps): 0-3 and 4-7 are two softmax groups, a thread a row, which
 // take the tiles in turn and have an S, a P and an O each -- so one group's
 // exponentials run beside the other's products, and neither waits for the
-// other's sums; they meet at the item's end.  8-11 bring the cache by 16-byte
+// other's sums; they meet at the item's end.  8-15 bring the cache by 16-byte
 // asynchronous copies: 16-bit entries to their stage, 8-bit codes to a ring of
 // their own, from where the thread that copied them takes them to their stage
-// as fp16, which holds them exactly.  12 issues the MMAs.  13 walks the CTA's
+// as fp16, which holds them exactly.  16 issues the MMAs.  17 walks the CTA's
 // share: it looks up pages, and hands each tile's addresses to the loading warps
 // and each segment to the others, so that no other warp divides or waits for a
-// table.  14 brings the scales; 15 only completes its warpgroup, which gives
-// registers to the softmax.
+// table.  18 brings the scales.
 // The loops are short on purpose: five roles share a scheduler's instruction
 // cache, and with loops unrolled over several tiles two thirds of the cycles
 // went to waiting for instructions.
@@ -40,17 +39,20 @@
 namespace proj {
 namespace {
 
-constexpr int kSoftWarps = 8, kLoadWarp = 8, kLoadWarps = 4, kMmaWarp = 12, kWalkWarp = 13, kScaleWarp = 14;
-constexpr int kThreads = 32 * 16;
+constexpr int kSoftWarps = 8, kLoadWarp = 8, kLoadWarps = 8, kMmaWarp = 16, kWalkWarp = 17, kScaleWarp = 18,
+              kPvWarp = 19;
+constexpr int kThreads = 32 * 20;
 // Registers a thread: at launch, and of the three kinds of warpgroups (two of
-// softmax, one of loading, one of the MMA warp).
-constexpr int kRegs = 128, kSoftRegs = 176, kLoadRegs = 96, kMmaRegs = 64;
-static_assert(2 * kSoftRegs + kLoadRegs + kMmaRegs <= 4 * kRegs && 4 * kRegs * 128 <= 65536, "registers");
+// softmax, two of loading, one of the others).  Nothing may spill in a loop:
+// beside this much shared memory L1 does not hold what 640 threads spill.
+constexpr int kRegs = 96, kSoftRegs = 160, kLoadRegs = 48, kOtherRegs = 64;
+static_assert(2 * kSoftRegs + 2 * kLoadRegs + kOtherRegs <= 5 * kRegs && 5 * kRegs * 128 <= 65536, "registers");
 constexpr int kLoadThreads = 32 * kLoadWarps;
 constexpr int kKeys = kAttnTcUnit;
 constexpr int kTmemCols = 512;
-constexpr int kRaw = 5;       // tiles of 8-bit codes in shared memory or on their way there
+constexpr int kRaw = 4;       // tiles of 8-bit codes in shared memory or on their way there
 constexpr int kRawScales = 4;
+constexpr int kIds = 4;  // tiles whose page ids are known or on their way
 // A row's reference moves when a score is more than 2^kSlack above it, and is
 // 2^kLift as a probability: at most 2^14 and, where fp16 ends, 2^-28 of it.
 constexpr float kSlack = 10.f, kLift = 4.f;
@@ -86,10 +88,11 @@ struct Tc {
   static constexpr int kSide = 640, kVScale = 256, kRef = 512, kValid = 520, kOddScale = 528, kOdd = 576;
   static constexpr int kRawAt = kStages * kStage;
   static constexpr int kSideAt = kRawAt + (kCoded ? kRaw * kRawTile : 0);
-  static constexpr int kFq = kSideAt + kStages * kSide;  // float[128]
-  static constexpr int kMl = kFq + 512;                  // float[2][128][3]
+  static constexpr int kMl = kSideAt + kStages * kSide;  // float[2][128][3]
   static constexpr int kRawScaleAt = kMl + 3072;         // float[kRawScales][2][kKeys]
-  static constexpr int kTiles = kRawScaleAt + kRawScales * 8 * kKeys;
+  static constexpr int kSwapAt = kRawScaleAt + (kCoded ? kRawScales * 8 * kKeys : 0);  // float[2][2][16][64]
+  static constexpr int kIdsAt = kSwapAt + 16384;  // int[kIds][kKeys]
+  static constexpr int kTiles = kIdsAt + kIds * kKeys * 4;
   static constexpr int kSegs = kTiles + kSlots * static_cast<int>(sizeof(Tile));
   static constexpr int kBarsAt = kSegs + kSegments * static_cast<int>(sizeof(Segment));
   static constexpr int kBars = 2 * kStages + 9 + 2 * kSlots + 2 * kSegments;
@@ -219,6 +222,11 @@ __device__ __forceinline__ float ld_shared_f(uint32_t addr) {
 __device__ __forceinline__ void st_shared_u(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
+__device__ __forceinline__ uint32_t ld_shared_u(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
 __device__ __forceinline__ void st_shared_byte(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
@@ -262,10 +270,10 @@ struct Walk {
       seq = sequence_at(p, share.b);
     }
     const int64_t local = at - share.before;
-    const int64_t item = local / seq.units;
+    const int64_t item = divide(local, seq.units);
     u0 = static_cast<int>(local - item * seq.units);
     u1 = static_cast<int>(min(static_cast<int64_t>(seq.units), u0 + (share.end - at)));
-    head = static_cast<int>(item / seq.tiles);
+    head = static_cast<int>(divide(item, seq.tiles));
     row0 = static_cast<int>(item - static_cast<int64_t>(head) * seq.tiles) * kAttnTcRows;
     rows = min(kAttnTcRows, seq.rows * static_cast<int>(p.group.d) - row0);
     at += u1 - u0;
@@ -294,8 +302,61 @@ __device__ __forceinline__ uint64_t seen_of(const AttnParams& p, int lo, int tok
   return own | low_bits(-draft);
 }
 
+// The same of keys that exist (`valid`), and whether one that it sees is noted as
+// having a value or a scale that is no finite number.  Not inlined: few tiles are
+// asked, and the loop around it is short.
+template <int kFormat>
+__device__ __noinline__ uint64_t seen_here(const AttnParams& p, int lo, int token, int draft, uint2 valid,
+                                           uint32_t odd_scale, uint32_t odd_keys, bool& odd) {
+  const uint64_t seen = seen_of(p, lo, token, draft) & (valid.x | static_cast<uint64_t>(valid.y) << 32);
+  if (draft + kKeys > 0) {
+    if (kFormat != PROJ_KV_ROWS) {
+      const uint2 w = ld_shared_u2(odd_scale);
+      odd |= (seen & (w.x | static_cast<uint64_t>(w.y) << 32)) != 0;
+    }
+    if (kFormat != PROJ_KV_INT8) {
+#pragma unroll 1
+      for (int j = 0; j < kKeys; j += 4) {
+        const uint32_t w = ld_shared_u(odd_keys + j);
+        if (w == 0) continue;
+        const uint32_t here = static_cast<uint32_t>(seen >> j);
+        odd |= (w & 0xFFu && here & 1u) || (w & 0xFF00u && here & 2u) ||
+               (w & 0xFF0000u && here & 4u) || (w & 0xFF000000u && here & 8u);
+      }
+    }
+  }
+  return seen;
+}
+
+// The values of V at columns c .. c + 15 that are no finite numbers, of the
+// segment's drafts that the row sees, added to o.
+template <typename T, int kFormat>
+__device__ __noinline__ void add_odd(const AttnParams& p, const Segment& seg, int token, int c, float* o) {
+  const int d0 = max(0, seg.u0 * kKeys - seg.start);
+  const int d1 = min(seg.len - seg.start, (seg.u0 + seg.tiles) * kKeys - seg.start);
+#pragma unroll 1
+  for (int d = d0; d < d1; ++d) {
+    const bool sees = p.mask ? (d >> 5) < p.words && (p.mask[static_cast<int64_t>(seg.lo + token) * p.ldm + (d >> 5)] >> (d & 31) & 1)
+                             : d <= token;
+    int id, spot;
+    if (!sees || !page_of(p.c, seg.b, seg.start + d, id, spot)) continue;
+    const Entry e = entry_at(p.c, id, spot, seg.head);
+    const uint8_t* v = p.c.v + e.at;
+    const bool fine = kFormat == PROJ_KV_ROWS || fabsf(p.c.v_scale[e.scale]) < INFINITY;
+#pragma unroll 1
+    for (int j = 0; j < 16; ++j) {
+      float x;
+      if constexpr (kFormat != PROJ_KV_ROWS)
+        x = !fine || (kFormat == PROJ_KV_E4M3 && (v[c + j] & 0x7F) == 0x7F) ? __uint_as_float(0x7FC00000u) : 0.f;
+      else
+        x = to_f32(reinterpret_cast<const T*>(v)[c + j]);
+      if (!(fabsf(x) < INFINITY)) o[j] += x;
+    }
+  }
+}
+
 template <typename T, int kFormat, int D>
-__global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_constant__ AttnParams p) {
   using F = Tc<kFormat, D>;
   constexpr bool kCoded = kFormat != PROJ_KV_ROWS;
   using C = std::conditional_t<kCoded, __half, T>;
@@ -334,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
     }
     for (int s = 0; s < kSegments; ++s) {
       mbar_init(g_full + 8 * s, 1);
-      mbar_init(g_empty + 8 * s, kSoftWarps + 1);
+      mbar_init(g_empty + 8 * s, kSoftWarps + 2);
     }
     fence_mbar_init();
   }
@@ -353,69 +414,67 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
 
   Share share;
   const bool mine = find_share<kThreads>(p, blockIdx.x, share);
-  if (threadIdx.x == 0) p.splits[blockIdx.x] = mine ? split_of(p, share, blockIdx.x) : Split{};
 
   if (!mine) {
     // nothing to do but to give the tensor memory back
+    if (threadIdx.x == 0) p.splits[blockIdx.x] = Split{};
   } else if (warp >= kMmaWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
-    if (warp == kMmaWarp) {
-    // ----------------------------------------------------------------- MMA
-    const bool one = elect_one();
-    bool ok = true;
-    int stage = 0;        // of the next tile of keys
-    uint32_t phase = 0;
-    uint32_t turn[2] = {0u, 0u};  // tiles that each group has had
-    constexpr uint32_t kIdQk = instruction(kBf16, 0, 128, kKeys), kIdPv = instruction(kBf16, 1, 128, D);
-    int pv_stage = 0;
-    for (int n = 0;; ++n) {
-      const int seg = n % kSegments;
-      ok = ok && wait_bar(g_full + 8 * seg, n / kSegments & 1u, p.status, kStatusTimeoutMma);
-      const int tiles = ok ? s_segs[seg].tiles : 0;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(g_empty + 8 * seg);
-      if (tiles == 0) break;
-      ok = ok && wait_bar(q_full, n & 1u, p.status, kStatusTimeoutMma);
-      // the first product of tile i, then the second of tile i - 2
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == kMmaWarp || warp == kPvWarp) {
+      // --------------------------------------------------------------- MMA
+      // One warp each for the two products, so that neither waits for what the other
+      // waits for.
+      const bool one = elect_one(), first = warp == kMmaWarp;
+      constexpr uint32_t kIdQk = instruction(kBf16, 0, 128, kKeys), kIdPv = instruction(kBf16, 1, 128, D);
+      bool ok = true;
+      int stage = 0;
+      uint32_t phase = 0;
+      uint32_t turn[2] = {0u, 0u};  // tiles that each group has had
+      for (int n = 0;; ++n) {
+        const int seg = n % kSegments;
+        ok = ok && wait_bar(g_full + 8 * seg, n / kSegments & 1u, p.status, kStatusTimeoutMma);
+        const int tiles = ok ? s_segs[seg].tiles : 0;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(g_empty + 8 * seg);
+        if (tiles == 0) break;
+        if (first) ok = ok && wait_bar(q_full, n & 1u, p.status, kStatusTimeoutMma);
 #pragma unroll 1
-      for (int i = 0; i < tiles + 2; ++i) {
-        const int g = i & 1;
-        if (i < tiles) {
-          if (i >= 2) ok = ok && wait_bar(s_free + 8 * g, turn[g] & 1u, p.status, kStatusTimeoutMma);
-          ok = ok && wait_bar(full + 8 * stage, phase, p.status, kStatusTimeoutMma);
-          tc_fence_after();
-          if (one && ok) {
-            const uint32_t k = base + stage * F::kStage;
+        for (int i = 0; i < tiles; ++i) {
+          const int g = i & 1;
+          if (first) {
+            // S of the group's tile before has been read
+            if (i >= 2) ok = ok && wait_bar(s_free + 8 * g, (turn[g] - 1) & 1u, p.status, kStatusTimeoutMma);
+            ok = ok && wait_bar(full + 8 * stage, phase, p.status, kStatusTimeoutMma);
+            tc_fence_after();
+            if (one && ok) {
+              const uint32_t k = base + stage * F::kStage;
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              mma_ts(tmem + F::kS + g * kKeys, tmem + F::kQ + kk * 8,
-                     smem_desc_sw128(k + (kk >> 2) * F::kHalf + (kk & 3) * 32), kIdQk, kk > 0);
-            tc_commit(s_full + 8 * g);
+              for (int kk = 0; kk < D / 16; ++kk)
+                mma_ts(tmem + F::kS + g * kKeys, tmem + F::kQ + kk * 8,
+                       smem_desc_sw128(k + (kk >> 2) * F::kHalf + (kk & 3) * 32), kIdQk, kk > 0);
+              tc_commit(s_full + 8 * g);
+            }
+          } else {
+            ok = ok && wait_bar(p_full + 8 * g, turn[g] & 1u, p.status, kStatusTimeoutMma);
+            tc_fence_after();
+            if (one && ok) {
+              const uint32_t v = base + stage * F::kStage + F::kOperand;
+#pragma unroll
+              for (int kk = 0; kk < kKeys / 16; ++kk)
+                mma_ts(tmem + F::kO + g * D, tmem + F::kP + g * (kKeys / 2) + kk * 8,
+                       smem_desc_n_major(v + kk * 2048, F::kHalf), kIdPv, i >= 2 || kk > 0);
+              tc_commit(o_done + 8 * g);
+              tc_commit(empty + 8 * stage);
+            }
           }
+          ++turn[g];
           __syncwarp();
           if (++stage == NS) {
             stage = 0;
             phase ^= 1u;
           }
         }
-        if (i >= 2) {
-          ok = ok && wait_bar(p_full + 8 * g, turn[g] & 1u, p.status, kStatusTimeoutMma);
-          ++turn[g];
-          tc_fence_after();
-          if (one && ok) {
-            const uint32_t v = base + pv_stage * F::kStage + F::kOperand;
-#pragma unroll
-            for (int kk = 0; kk < kKeys / 16; ++kk)
-              mma_ts(tmem + F::kO + g * D, tmem + F::kP + g * (kKeys / 2) + kk * 8,
-                     smem_desc_n_major(v + kk * 2048, F::kHalf), kIdPv, i >= 4 || kk > 0);
-            tc_commit(o_done + 8 * g);
-            tc_commit(empty + 8 * pv_stage);
-          }
-          __syncwarp();
-          if (++pv_stage == NS) pv_stage = 0;
-        }
       }
-    }
     } else if (warp == kWalkWarp) {
       // ---------------------------------------------------- the CTA's share
       Walk walk;
@@ -442,47 +501,64 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
           mbar_arrive(g_full + 8 * seg);
         }
         __syncwarp();
-        const auto id_of = [&](int key) {
-          return key < walk.seq.len ? p.c.table[walk.share.b * p.c.ldt + quotient(key, p.c.page)] : -1;
-        };
-        int id[2] = {-1, -1};
-        if (more) {
-          id[0] = id_of(walk.u0 * kKeys + lane);
-          id[1] = id_of(walk.u0 * kKeys + 32 + lane);
-        }
-        for (int u = more ? walk.u0 : 0; u < (more ? walk.u1 : 1); ++u) {
-          const int key0 = u * kKeys;
-          int next[2] = {-1, -1};
-          if (more && u + 1 < walk.u1) {
-            next[0] = id_of(key0 + kKeys + lane);
-            next[1] = id_of(key0 + kKeys + 32 + lane);
-          }
+        if (!more) {
+          // the end, for those that go by tiles
           ok = ok && wait_bar(t_empty + 8 * slot, phase ^ 1u, p.status, kStatusTimeoutProducer);
-          Tile& tile = s_tiles[slot];
-          if (more) {
+          if (lane == 0) {
+            s_tiles[slot].kind = 0;
+            mbar_arrive(t_full + 8 * slot);
+            p.splits[blockIdx.x] = split_of(p, share, blockIdx.x);
+          }
+          break;
+        }
+        // Page ids come through shared memory, kIds - 1 tiles ahead; lanes have keys
+        // lane and lane + 32.
+        const int32_t* const table = p.c.table + walk.share.b * p.c.ldt;
+        const int64_t head_at = walk.head * p.c.head_stride;
+        const int64_t head_scale = static_cast<int64_t>(walk.head) * p.c.page.d;
+        const uint32_t ids = base + F::kIdsAt + lane * 4;
+        const auto ask = [&](int u) {
+          if (u < walk.u1) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const int key = key0 + j * 32 + lane;
-              const bool good = id[j] >= 0 && id[j] < p.c.pages;
-              const int spot = key - quotient(key, p.c.page) * static_cast<int>(p.c.page.d);
-              const Entry e = entry_at(p.c, id[j], spot, walk.head);
-              tile.at[j * 32 + lane] = good ? e.at : -1;
-              if (kCoded) tile.scale[j * 32 + lane] = e.scale;
-              const uint32_t valid = __ballot_sync(0xFFFFFFFFu, good);
-              if (lane == 0) tile.valid[j] = valid;
+              const int key = u * kKeys + j * 32 + lane;
+              const bool here = key < walk.seq.len;
+              copy4(ids + u % kIds * (4 * kKeys) + j * 128, here ? table + quotient(key, p.c.page) : table, here ? 4 : 0);
             }
           }
-          if (lane == 0) tile.kind = more ? 1 + (key0 + kKeys > walk.seq.start ? 2 : 0) + (u == walk.u0 ? 4 : 0) : 0;
+          copies_sealed();
+        };
+#pragma unroll 1
+        for (int i = 0; i < kIds - 1; ++i) ask(walk.u0 + i);
+#pragma unroll 1
+        for (int u = walk.u0; u < walk.u1; ++u) {
+          const int key0 = u * kKeys;
+          ask(u + kIds - 1);
+          ok = ok && wait_bar(t_empty + 8 * slot, phase ^ 1u, p.status, kStatusTimeoutProducer);
+          copies_wait<kIds - 1>();
+          Tile& tile = s_tiles[slot];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int key = key0 + j * 32 + lane;
+            const int id = static_cast<int>(ld_shared_u(ids + u % kIds * (4 * kKeys) + j * 128));
+            const bool good = key < walk.seq.len && id >= 0 && id < p.c.pages;
+            const int spot = key - quotient(key, p.c.page) * static_cast<int>(p.c.page.d);
+            tile.at[j * 32 + lane] = good ? head_at + static_cast<int64_t>(id) * static_cast<int>(p.c.page_stride) +
+                                                static_cast<int64_t>(spot) * static_cast<int>(p.c.token_stride)
+                                          : -1;
+            if (kCoded) tile.scale[j * 32 + lane] = head_scale + static_cast<int64_t>(id) * p.c.page_scales + spot;
+            const uint32_t valid = __ballot_sync(0xFFFFFFFFu, good);
+            if (lane == 0) tile.valid[j] = valid;
+          }
+          if (lane == 0) tile.kind = 1 + (key0 + kKeys > walk.seq.start ? 2 : 0) + (u == walk.u0 ? 4 : 0);
           __syncwarp();
           if (lane == 0) mbar_arrive(t_full + 8 * slot);
           if (++slot == kSlots) {
             slot = 0;
             phase ^= 1u;
           }
-          id[0] = next[0];
-          id[1] = next[1];
         }
-        if (!more) break;
+        copies_wait<0>();
       }
     } else if (warp == kScaleWarp) {
       // ------------------------------------------------------------- scales
@@ -617,6 +693,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
       const uint32_t who = __ballot_sync(0xFFFFFFFFu, odd) >> (lane - piece) & ((1u << kPieces) - 1u);
       if (piece == 0) st_shared_byte(base + F::kSideAt + stage * F::kSide + F::kOdd + key, who ? 1u : 0u);
     };
+    static_assert(kTurn % 8 == 0, "a thread's rows have one place in the swizzle");
+    // 8-bit codes: the second half's lanes store their two chunks in the other
+    // order, so the eight lanes of a key meet eight different banks
+    const int swap = kCoded ? piece >> 2 & 1 : 0;
+    const uint32_t put_a = place(key_of, piece >> 2, 2 * (piece & 3) + swap);
+    const uint32_t put_b = place(key_of, piece >> 2, 2 * (piece & 3) + 1 - swap);
+    const uint32_t put_row = place(key_of, piece >> 3, piece & 7);
     int in = 0;  // raw slot, or stage, of the tile that is issued
     uint32_t in_phase = 0;
     const auto issue = [&] {
@@ -629,14 +712,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
       if (kind) {
         if constexpr (!kCoded)
           ok = ok && wait_bar(empty + 8 * in, in_phase ^ 1u, p.status, kStatusTimeoutProducer);
-        const uint32_t to = kCoded ? base + F::kRawAt + in * F::kRawTile + tid * 16 : base + in * F::kStage;
+        const uint32_t to = kCoded ? base + F::kRawAt + in * F::kRawTile + tid * 16 : base + in * F::kStage + put_row;
 #pragma unroll
         for (int j = 0; j < kPasses; ++j) {
           const int key = j * kTurn + key_of;
           const int64_t at = s_tiles[slot].at[key];
           const int64_t from = at >= 0 ? at : 0;
           const int bytes = at >= 0 ? 16 : 0;
-          const uint32_t dst = to + (kCoded ? j * kLoadThreads * 16 : place(key, piece >> 3, piece & 7));
+          const uint32_t dst = to + j * (kCoded ? kLoadThreads * 16 : kTurn * 128);
           copy16(dst, from_k + from, bytes);
           copy16(dst + (kCoded ? F::kRawTile / 2 : F::kOperand), from_v + from, bytes);
         }
@@ -666,25 +749,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
       if constexpr (kCoded) {
         // this thread's own pieces: codes to fp16
         ok = ok && wait_bar(empty + 8 * stage, phase ^ 1u, p.status, kStatusTimeoutProducer);
-        uint32_t from = base + F::kRawAt + raw * F::kRawTile + tid * 16;
+        const uint32_t from = base + F::kRawAt + raw * F::kRawTile + tid * 16;
         const uint32_t to = base + stage * F::kStage;
-        // the second half's lanes store their two chunks in the other order: the
-        // eight lanes of a key then meet eight different banks
-        const int half = piece >> 2, c = 2 * (piece & 3), x = half & 1;
-#pragma unroll 2
+#pragma unroll
         for (int j = 0; j < 2 * kPasses; ++j) {
-          const uint4 w = ld_shared_u4(from);
-          from += kLoadThreads * 16;
-          const uint32_t dst = to + (j >= kPasses ? F::kOperand : 0);
-          const int key = (j >= kPasses ? j - kPasses : j) * kTurn + key_of;
-          const uint32_t a[4] = {decode_pair<kFormat>(w.x, 0), decode_pair<kFormat>(w.x, 1),
-                                 decode_pair<kFormat>(w.y, 0), decode_pair<kFormat>(w.y, 1)};
-          const uint32_t b[4] = {decode_pair<kFormat>(w.z, 0), decode_pair<kFormat>(w.z, 1),
-                                 decode_pair<kFormat>(w.w, 0), decode_pair<kFormat>(w.w, 1)};
-          st_shared_u4(dst + place(key, half, c + x), x ? b[0] : a[0], x ? b[1] : a[1], x ? b[2] : a[2],
-                       x ? b[3] : a[3]);
-          st_shared_u4(dst + place(key, half, c + 1 - x), x ? a[0] : b[0], x ? a[1] : b[1],
-                       x ? a[2] : b[2], x ? a[3] : b[3]);
+          const int pass = j % kPasses;
+          const uint32_t src = from + j / kPasses * (F::kRawTile / 2) + pass * kLoadThreads * 16;
+          const uint32_t dst = to + j / kPasses * F::kOperand + pass * kTurn * 128;
+          const uint2 a = ld_shared_u2(src + swap * 8), b = ld_shared_u2(src + 8 - swap * 8);
+          st_shared_u4(dst + put_a, decode_pair<kFormat>(a.x, 0), decode_pair<kFormat>(a.x, 1),
+                       decode_pair<kFormat>(a.y, 0), decode_pair<kFormat>(a.y, 1));
+          st_shared_u4(dst + put_b, decode_pair<kFormat>(b.x, 0), decode_pair<kFormat>(b.x, 1),
+                       decode_pair<kFormat>(b.y, 0), decode_pair<kFormat>(b.y, 1));
         }
         if (++raw == kRaw) raw = 0;
       }
@@ -698,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
   } else {
     // ------------------------------------------------------------- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
-    const int group = warp >> 2, row = threadIdx.x & 127;
+    const int group = warp >> 2, quad = warp & 3, lane_row = threadIdx.x & 127;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t my_s = tmem + lanes + F::kS + group * kKeys, my_p = tmem + lanes + F::kP + group * (kKeys / 2);
     const uint32_t my_o = tmem + lanes + F::kO + group * D;
@@ -715,58 +791,79 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
       if (lane == 0) mbar_arrive(g_empty + 8 * slot_of);
       if (seg.tiles == 0) break;
       const int tiles = seg.tiles;
+      // Up to 64 rows: both halves of the lanes hold them, the MMAs make their scores
+      // twice at no cost, and each half takes 32 of a tile's 64 keys (of the other
+      // 32 its probabilities are zero): half the softmax for a warp.
+      const bool halves = seg.rows <= 64;
+      const int row = halves ? lane_row & 63 : lane_row;
       const bool real = row < seg.rows;
-      const bool busy = (warp & 3) * 32 < seg.rows;  // one of the warp's rows is real
+      const bool busy = (halves ? quad & 1 : quad) * 32 < seg.rows;  // one of the warp's rows is real
+      const int c0 = halves ? quad >> 1 : 0, c1 = halves ? c0 + 1 : 2;  // columns / 32
       const int r = seg.row0 + (real ? row : 0);
       const int token = quotient(r, p.group), head = seg.head * G + r - token * G;
       // -------------------------------------------------------- queries --
-      if (group == 0) {
-        if (busy) {
-          const uint8_t* from = p.q + static_cast<int64_t>(seg.lo + token) * p.ldq + static_cast<int64_t>(head) * D * 2;
-          uint32_t q[D / 2];
+      float fq = 1.f;
+      // Each group brings half of the columns.  The factor of a row's scores is
+      // positive (its sign goes to the queries, and so does a zero), so the largest
+      // product is the largest score.
+      constexpr bool kNarrow = kCoded && std::is_same_v<T, __nv_bfloat16>;
+      uint32_t q[D / 4];
+      if (busy) {
+        const uint8_t* from = p.q + static_cast<int64_t>(seg.lo + token) * p.ldq + static_cast<int64_t>(head) * D * 2 + group * D;
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            const uint4 w = real ? *reinterpret_cast<const uint4*>(from + i * 16) : make_uint4(0u, 0u, 0u, 0u);
-            q[4 * i] = w.x;
-            q[4 * i + 1] = w.y;
-            q[4 * i + 2] = w.z;
-            q[4 * i + 3] = w.w;
-          }
-          // The factor of a row's scores is positive (its sign goes to the queries, and
-          // so does a zero), so the largest product is the largest score.
-          float f = 1.f;
-          if constexpr (kCoded && std::is_same_v<T, __nv_bfloat16>) {
-            // bf16 to fp16: the row's largest magnitude is brought to 2^14 .. 2^15
-            uint32_t top = 0;
-#pragma unroll
-            for (int i = 0; i < D / 2; ++i) top = max(max(top, q[i] & 0x7FFFu), q[i] >> 16 & 0x7FFFu);
-            int e = 0;
-            if (top > 0 && top < 0x7F80u) e = min(126, 14 - ilogbf(__uint_as_float(top << 16)));
-            const F2 up = f2(scalbnf(1.f, e));
-#pragma unroll
-            for (int i = 0; i < D / 2; ++i) {
-              float x, y;
-              widen2(q[i], x, y, __nv_bfloat16());
-              parts(mul2(f2(x, y), up), x, y);
-              q[i] = pack2(x, y, __half());
-            }
-            f = scalbnf(1.f, -e);
-          }
-          if (p.scale_log2 <= 0.f) {
-            const uint32_t keep = p.scale_log2 == 0.f ? 0u : 0xFFFFFFFFu, turned = p.scale_log2 < 0.f ? 0x80008000u : 0u;
-#pragma unroll
-            for (int i = 0; i < D / 2; ++i) q[i] = (q[i] & keep) ^ turned;
-          }
-          st_shared_f(base + F::kFq + row * 4, fmaxf(f * fabsf(p.scale_log2), 1.17549435e-38f));
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i) tmem_st16(tmem + lanes + F::kQ + i * 16, q + i * 16);
-          tmem_st_wait();
+        for (int i = 0; i < D / 16; ++i) {
+          const uint4 w = *reinterpret_cast<const uint4*>(from + i * 16);
+          q[4 * i] = w.x;
+          q[4 * i + 1] = w.y;
+          q[4 * i + 2] = w.z;
+          q[4 * i + 3] = w.w;
         }
-        tc_fence_before();
       }
+      float f = 1.f;
+      F2 up = f2(1.f);
+      if constexpr (kNarrow) {
+        // bf16 to fp16: the row's largest magnitude is brought to 2^14 .. 2^15
+        uint32_t most = 0;
+        const uint32_t room = base + F::kMl + lane_row * 4;
+        if (busy) {
+#pragma unroll
+          for (int i = 0; i < D / 4; ++i) most = max(max(most, q[i] & 0x7FFFu), q[i] >> 16 & 0x7FFFu);
+          st_shared_u(room + group * 512, most);
+        }
+        named_bar_sync(1, 32 * kSoftWarps);
+        if (busy) most = max(most, ld_shared_u(room + (1 - group) * 512));
+        int e = 0;
+        if (most > 0 && most < 0x7F80u) e = min(126, 14 - ilogbf(__uint_as_float(most << 16)));
+        up = f2(scalbnf(1.f, e));
+        f = scalbnf(1.f, -e);
+      }
+      if (busy) {
+        const uint32_t keep = p.scale_log2 == 0.f || !real ? 0u : 0xFFFFFFFFu;
+        const uint32_t turned = p.scale_log2 < 0.f ? 0x80008000u : 0u;
+#pragma unroll
+        for (int i = 0; i < D / 4; ++i) {
+          if constexpr (kNarrow) {
+            float x, y;
+            widen2(q[i], x, y, __nv_bfloat16());
+            parts(mul2(f2(x, y), up), x, y);
+            q[i] = pack2(x, y, __half());
+          }
+          q[i] = (q[i] & keep) ^ turned;
+        }
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i)
+          tmem_st16(tmem + lanes + F::kQ + group * (D / 4) + i * 16, q + i * 16);
+        tmem_st_wait();
+        fq = fmaxf(f * fabsf(p.scale_log2), 1.17549435e-38f);
+      }
+      if (halves && busy) {
+        const uint32_t zero[16] = {};
+        tmem_st16(my_p + 16 * (1 - c0), zero);
+        tmem_st_wait();
+      }
+      tc_fence_before();
       named_bar_sync(1, 32 * kSoftWarps);
       if (lane == 0) mbar_arrive(q_full);
-      const float fq = ld_shared_f(base + F::kFq + row * 4);
 
       // ---------------------------------------------------------- tiles --
       float ref = kNoScore, sum = 0.f, v_ref = 0.f;
@@ -782,88 +879,89 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
         ok = ok && wait_bar(s_full + 8 * group, turn & 1u, p.status, kStatusTimeoutEpilogue);
         tc_fence_after();
         if (busy) {
-          float f[kKeys];
-          tmem_ld32(my_s, f);
-          tmem_ld32(my_s + 32, f + 32);
           // what stands beside the stage
-          ok = ok && wait_bar(full + 8 * stage, phase, p.status, kStatusTimeoutEpilogue);
-          tmem_ld_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(s_free + 8 * group);
           const int key0 = (seg.u0 + i) * kKeys;
+          uint64_t seen = ~uint64_t{0};
+          ok = ok && wait_bar(full + 8 * stage, phase, p.status, kStatusTimeoutEpilogue);
           const uint2 valid = ld_shared_u2(side + F::kValid);
           const bool partial = (valid.x & valid.y) != 0xFFFFFFFFu || key0 + kKeys > seg.start;
-          if constexpr (kCoded) {
-#pragma unroll
-            for (int c = 0; c < kKeys; c += 16) {
-              float4 ks[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j) ks[j] = ld_shared_f4(side + (c + 4 * j) * 4);
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                float* x = f + c + 4 * j;
-                parts(mul2(f2(x[0], x[1]), f2(ks[j].x, ks[j].y)), x[0], x[1]);
-                parts(mul2(f2(x[2], x[3]), f2(ks[j].z, ks[j].w)), x[2], x[3]);
-              }
-            }
-          }
-          uint32_t seen[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
-          if (partial) {
-            const uint64_t all = seen_of(p, seg.lo, token, key0 - seg.start);
-            seen[0] = static_cast<uint32_t>(all) & valid.x;
-            seen[1] = static_cast<uint32_t>(all >> 32) & valid.y;
-#pragma unroll
-            for (int j = 0; j < kKeys; ++j)
-              if (!(seen[j >> 5] >> (j & 31) & 1)) f[j] = -INFINITY;
-            if (kCoded && key0 + kKeys > seg.start) {
-              const uint2 w = ld_shared_u2(side + F::kOddScale);
-              odd |= (w.x & seen[0]) || (w.y & seen[1]);
-            }
-            if (kFormat != PROJ_KV_INT8 && key0 + kKeys > seg.start) {
-#pragma unroll 1
-              for (int j = 0; j < kKeys; j += 4) {
-                uint32_t w;
-                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(side + F::kOdd + j));
-                if (w == 0) continue;
-                const uint32_t here = seen[j >> 5] >> (j & 31);
-                odd |= (w & 0xFFu && here & 1u) || (w & 0xFF00u && here & 2u) ||
-                       (w & 0xFF0000u && here & 4u) || (w & 0xFF000000u && here & 8u);
-              }
-            }
-          }
-          float tops[4] = {f[0], f[1], f[2], f[3]};
-#pragma unroll
-          for (int j = 4; j < kKeys; ++j) tops[j & 3] = fmaxf(tops[j & 3], f[j]);
-          const float top = fq * fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-          float down = 1.f;
-          if (top > ref + kSlack) {
-            down = exp2_fast(ref - top);
-            ref = top;
-            sum *= down;
-          }
+          if (__builtin_expect(partial, 0))
+            seen = seen_here<kFormat>(p, seg.lo, token, key0 - seg.start, valid, side + F::kOddScale, side + F::kOdd, odd);
+          float down = 1.f, tile_sum = 0.f;
           if constexpr (kCoded) {
             const float now = ld_shared_f(side + F::kRef);
             if (now != v_ref) {
-              down *= v_ref / now;  // both powers of two, or v_ref 0 and nothing summed yet
+              down = v_ref / now;  // both powers of two, or v_ref 0 and nothing summed yet
               v_ref = now;
             }
           }
-          const F2 low = f2(kLift - ref), q2 = f2(fq);
-          F2 total[2] = {f2(0.f), f2(0.f)};
+          const F2 q2 = f2(fq);
+#pragma unroll 1
+          for (int c = c0; c < c1; ++c) {
+            float f[32];
+            tmem_ld32(my_s + c * 32, f);
+            tmem_ld_wait();
+            if (halves) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(s_free + 8 * group);
+            }
+            if constexpr (kCoded) {
 #pragma unroll
-          for (int c = 0; c < kKeys; c += 32) {
+              for (int j = 0; j < 32; j += 16) {
+                float4 ks[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) ks[x] = ld_shared_f4(side + c * 128 + (j + 4 * x) * 4);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                  float* y = f + j + 4 * x;
+                  parts(mul2(f2(y[0], y[1]), f2(ks[x].x, ks[x].y)), y[0], y[1]);
+                  parts(mul2(f2(y[2], y[3]), f2(ks[x].z, ks[x].w)), y[2], y[3]);
+                }
+              }
+            }
+            if (__builtin_expect(partial, 0)) {
+              const uint32_t here = static_cast<uint32_t>(c ? seen >> 32 : seen);
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (!(here >> j & 1)) f[j] = -INFINITY;
+            }
+            float tops[4] = {f[0], f[1], f[2], f[3]};
+#pragma unroll
+            for (int j = 4; j < 32; ++j) tops[j & 3] = fmaxf(tops[j & 3], f[j]);
+            const float top = fq * fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+            if (__builtin_expect(__any_sync(0xFFFFFFFFu, top > ref + kSlack), 0)) {
+              if (top > ref + kSlack) {
+                const float step = exp2_fast(ref - top);
+                ref = top;
+                sum *= step;
+                down *= step;
+              }
+              if (c > c0) {
+                // the tile's first half again, relative to the new reference
+                c = c0 - 1;
+                tile_sum = 0.f;
+                continue;
+              }
+            }
+            if (!halves && c == c1 - 1) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(s_free + 8 * group);
+            }
+            const F2 low = f2(kLift - ref);
+            F2 total[2] = {f2(0.f), f2(0.f)};
             uint32_t w[16];
 #pragma unroll
             for (int j = 0; j < 32; j += 16) {
               float4 vs[4];
               if constexpr (kCoded) {
 #pragma unroll
-                for (int x = 0; x < 4; ++x) vs[x] = ld_shared_f4(side + F::kVScale + (c + j + 4 * x) * 4);
+                for (int x = 0; x < 4; ++x) vs[x] = ld_shared_f4(side + F::kVScale + c * 128 + (j + 4 * x) * 4);
               }
               float e[16];
 #pragma unroll
-              for (int x = 0; x < 16; x += 2) parts(fma2(f2(f[c + j + x], f[c + j + x + 1]), q2, low), e[x], e[x + 1]);
+              for (int x = 0; x < 16; x += 2) parts(fma2(f2(f[j + x], f[j + x + 1]), q2, low), e[x], e[x + 1]);
 #pragma unroll
               for (int x = 0; x < 16; ++x) e[x] = exp2_fast(e[x]);
 #pragma unroll
@@ -879,28 +977,28 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
                 w[(j + x) / 2 + 1] = pack2(e[x + 2], e[x + 3], C());
               }
             }
-            if (c == 0) {
-              // the group's products before: P is free, and O complete
-              if (turn > 0) ok = ok && wait_bar(o_done + 8 * group, (turn - 1) & 1u, p.status, kStatusTimeoutEpilogue);
-              tc_fence_after();
-              if (i >= 2 && __any_sync(0xFFFFFFFFu, down != 1.f)) {
-#pragma unroll 1
-                for (int c = 0; c < D; c += 16) {
-                  float o[16];
-                  tmem_ld16(my_o + c, o);
-                  tmem_ld_wait();
-                  uint32_t w[16];
-#pragma unroll
-                  for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(o[j] * down);
-                  tmem_st16(my_o + c, w);
-                }
-              }
-            }
-            tmem_st16(my_p + c / 2, w);
+            float a, b;
+            parts(add2(total[0], total[1]), a, b);
+            tile_sum += a + b;
+            // the group's products before: P is free, and O complete
+            if (c == c0 && turn > 0)
+              ok = ok && wait_bar(o_done + 8 * group, (turn - 1) & 1u, p.status, kStatusTimeoutEpilogue);
+            tc_fence_after();
+            tmem_st16(my_p + c * 16, w);
           }
-          float a, b;
-          parts(add2(total[0], total[1]), a, b);
-          sum += a + b;
+          sum += tile_sum;
+          if (__builtin_expect(i >= 2 && __any_sync(0xFFFFFFFFu, down != 1.f), 0)) {
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+              float o[16];
+              tmem_ld16(my_o + c, o);
+              tmem_ld_wait();
+              uint32_t w[16];
+#pragma unroll
+              for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(o[j] * down);
+              tmem_st16(my_o + c, w);
+            }
+          }
           tmem_st_wait();
         } else {
           if (lane == 0) mbar_arrive(s_free + 8 * group);
@@ -924,74 +1022,87 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
 
       // ----------------------------------------------- the groups' sums joined --
       const uint32_t ml = base + F::kMl;
-      st_shared_f(ml + (group * 128 + row) * 12, ref - kLift);
-      st_shared_f(ml + (group * 128 + row) * 12 + 4, sum);
-      st_shared_f(ml + (group * 128 + row) * 12 + 8, kCoded ? v_ref : 1.f);
+      st_shared_f(ml + (group * 128 + lane_row) * 12, ref - kLift);
+      st_shared_f(ml + (group * 128 + lane_row) * 12 + 4, sum);
+      st_shared_f(ml + (group * 128 + lane_row) * 12 + 8, kCoded ? v_ref : 1.f);
       if (tiles > group) ok = ok && wait_bar(o_done + 8 * group, (turn - 1) & 1u, p.status, kStatusTimeoutEpilogue);
       // a value of V that is no finite number, seen by this row
       const bool any_odd = named_bar_sync_or(2, 32 * kSoftWarps, odd);
       tc_fence_after();
-      if (busy) {
-        float m[2], l[2], up[2];
+      {
+        // the row's sums: of both groups, and of both halves of the lanes
+        float m[4], l[4], up[2];
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-          m[g] = ld_shared_f(ml + (g * 128 + row) * 12);
-          l[g] = ld_shared_f(ml + (g * 128 + row) * 12 + 4);
-          up[g] = ld_shared_f(ml + (g * 128 + row) * 12 + 8);
+          const uint32_t mine = ml + (g * 128 + lane_row) * 12, other = ml + (g * 128 + (lane_row ^ 64)) * 12;
+          m[g] = ld_shared_f(mine);
+          l[g] = ld_shared_f(mine + 4);
+          up[g] = ld_shared_f(mine + 8);
+          m[2 + g] = halves ? ld_shared_f(other) : -INFINITY;
+          l[2 + g] = halves ? ld_shared_f(other + 4) : 0.f;
         }
-        const float top = fmaxf(m[0], m[1]);
-        const float f0 = exp2_fast(m[0] - top), f1 = exp2_fast(m[1] - top);
-        const float all = l[0] * f0 + l[1] * f1;
-        const float a0 = f0 * up[0], a1 = f1 * up[1];
+        const float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+        float all = 0.f;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) all += l[g] * exp2_fast(m[g] - top);
+        const float a0 = exp2_fast(m[0] - top) * up[0], a1 = exp2_fast(m[1] - top) * up[1];
         const bool whole = seg.whole;
         const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (seg.u0 == 0 ? 1 : 0);
         float* part = p.part_o + (slot * kAttnTcRows + row) * D;
+        const bool writes = real && busy && !(halves && quad >= 2);
         constexpr int kCols = D / 2;  // each group writes half of the columns
+        const bool gated = writes && whole && p.gate;
+        const T* const gates = reinterpret_cast<const T*>(p.gate + static_cast<int64_t>(seg.lo + token) * p.ldg) + head * D;
+        Vec<T, 8> gate[2];
+        if (gated) {
+          gate[0] = load_vec<T, 8>(gates + group * kCols);
+          gate[1] = load_vec<T, 8>(gates + group * kCols + 8);
+        }
 #pragma unroll 1
         for (int c = group * kCols; c < (group + 1) * kCols; c += 16) {
+          const Vec<T, 8> now[2] = {gate[0], gate[1]};
+          if (gated && c + 16 < (group + 1) * kCols) {
+            gate[0] = load_vec<T, 8>(gates + c + 16);
+            gate[1] = load_vec<T, 8>(gates + c + 24);
+          }
           float o[16], o1[16];
-          tmem_ld16(tmem + lanes + F::kO + c, o);
-          if (tiles > 1) tmem_ld16(tmem + lanes + F::kO + D + c, o1);
-          tmem_ld_wait();
+          if (busy) {
+            tmem_ld16(tmem + lanes + F::kO + c, o);
+            if (tiles > 1) tmem_ld16(tmem + lanes + F::kO + D + c, o1);
+            tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < 16; ++j) o[j] = tiles > 1 ? o[j] * a0 + o1[j] * a1 : o[j] * a0;
-          if (any_odd && real) {
-            // the drafts of this part once more: what is no finite number goes to
-            // the rows that see it
-            const int d0 = max(0, seg.u0 * kKeys - seg.start);
-            const int d1 = min(seg.len - seg.start, (seg.u0 + seg.tiles) * kKeys - seg.start);
-            for (int d = d0; d < d1; ++d) {
-              const bool sees = p.mask ? (d >> 5) < p.words && (p.mask[static_cast<int64_t>(seg.lo + token) * p.ldm + (d >> 5)] >> (d & 31) & 1)
-                                       : d <= token;
-              int id, spot;
-              if (!sees || !page_of(p.c, seg.b, seg.start + d, id, spot)) continue;
-              const Entry e = entry_at(p.c, id, spot, seg.head);
-              const uint8_t* v = p.c.v + e.at;
-              const bool fine = !kCoded || fabsf(p.c.v_scale[e.scale]) < INFINITY;
-              for (int j = 0; j < 16; ++j) {
-                float x;
-                if constexpr (kCoded)
-                  x = !fine || (kFormat == PROJ_KV_E4M3 && (v[c + j] & 0x7F) == 0x7F) ? __uint_as_float(0x7FC00000u) : 0.f;
-                else
-                  x = to_f32(reinterpret_cast<const T*>(v)[c + j]);
-                if (!(fabsf(x) < INFINITY)) {
+            for (int j = 0; j < 16; ++j) o[j] = tiles > 1 ? o[j] * a0 + o1[j] * a1 : o[j] * a0;
+          }
+          if (halves) {
+            const uint32_t swap = base + F::kSwapAt + group * 8192 + (c >> 4 & 1) * 4096 + row * 4;
+            if (quad >= 2) {
 #pragma unroll
-                  for (int y = 0; y < 16; ++y)
-                    if (y == j) o[y] += x;
-                }
-              }
+              for (int j = 0; j < 16; ++j) st_shared_f(swap + j * 256, o[j]);
+            }
+            named_bar_sync(3 + group, 128);
+            if (quad < 2) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) o[j] += ld_shared_f(swap + j * 256);
             }
           }
-          if (real && whole) {
-            write_out<T>(p, static_cast<int64_t>(seg.lo + token), head * D + c, o, all);
-          } else if (real) {
+          if (__builtin_expect(any_odd && writes, 0)) {
+            float with[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) with[j] = o[j];
+            add_odd<T, kFormat>(p, seg, token, c, with);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) o[j] = with[j];
+          }
+          if (writes && whole) {
+            write_out<T>(p, static_cast<int64_t>(seg.lo + token), head * D + c, o, all, now);
+          } else if (writes) {
 #pragma unroll
             for (int j = 0; j < 16; j += 4)
               *reinterpret_cast<float4*>(part + c + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
           }
           __syncwarp();
         }
-        if (real && group == 0) {
+        if (writes && group == 0) {
           if (whole) {
             if (p.lse) p.lse[static_cast<int64_t>(seg.lo + token) * p.heads + head] = lse_of(top, all);
           } else {

@@ -366,9 +366,9 @@ const char* refuse_cache(const proj_kv_cache* cache, int* status) {
   if (c.sequences > 65536) return "more than 65536 sequences";
   if (c.width >= (int64_t{1} << 30) / c.page) return "width page >= 2^30";
   if (c.ldt >= (int64_t{1} << 31)) return "ldt >= 2^31";
-  const int64_t el = scaled ? 1 : 2, most = int64_t{1} << 40;
-  if (c.page_stride > most || c.head_stride > most || c.token_stride > most)
-    return "a stride of the cache above 2^40";
+  const int64_t el = scaled ? 1 : 2, most = int64_t{1} << 31;
+  if (c.page_stride >= most / el || c.token_stride >= most / el || c.head_stride >= (most << 16))
+    return "a page or token stride of 2^31 bytes or a head stride of 2^47 or more";
   *status = PROJ_EALIGN;
   if (!kv_aligned(c.k, 16) || !kv_aligned(c.v, 16) || c.page_stride * el % 16 ||
       c.head_stride * el % 16 || c.token_stride * el % 16)
@@ -396,6 +396,7 @@ KvCache device_cache(const proj_kv_cache& c) {
   d.heads = static_cast<int>(c.heads);
   d.width = static_cast<int>(c.width);
   d.sequences = static_cast<int>(c.sequences);
+  d.page_scales = static_cast<int>(c.heads * c.page);
   d.capacity = static_cast<int>(c.width * c.page);
   return d;
 }

@@ -31,11 +31,12 @@ struct KvCache {
   uint8_t* v;
   float* k_scale;
   float* v_scale;
-  int64_t page_stride, head_stride, token_stride;  // bytes
+  int64_t page_stride, head_stride, token_stride;  // bytes; pages and tokens: below 2^31
   const int32_t* table;
   int64_t ldt;
   Divisor page;
   int pages, heads, width, sequences;
+  int page_scales;  // scales of a page: heads * page
   int capacity;  // positions of a sequence: width * page, below 2^31
 };
 

@@ -719,7 +719,7 @@ typedef struct proj_kv_cache {
     float *v_scale;
     int64_t page_stride;   /* entry (page, head, place) starts at page page_stride + head head_stride */
     int64_t head_stride;   /* + place token_stride entries; multiples of 16 bytes, at least D */
-    int64_t token_stride;
+    int64_t token_stride;  /* page and token: below 2^31 bytes */
     const int32_t *table;  /* device [sequences, width], row stride ldt >= width */
     int64_t ldt, width;    /* width page < 2^30 */
     int64_t sequences;     /* 0 .. 65536 */

@@ -21,10 +21,8 @@
 // blocks in registers.
 //
 // Softmax, one pass: each warp holds for its rows a reference m and sums
-// relative to 2^m.  A score beyond m + 6 moves m (a vote; no shuffles
-// otherwise), so with p = 2^(t - m + 8) at most 2^14 and, where it counts, at
-// least 2^-16 below that: in fp16's range, which ends at 2^16 and 2^-24.
-// Scales of V multiply p, relative to the largest one seen.
+// relative to 2^m, and a score well above m moves it (a vote; no shuffles
+// otherwise).  Scales of V multiply p, relative to the largest one seen.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -44,14 +42,16 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 __device__ uint32_t g_attn_status;  // what bounded waits that gave up leave
 
-constexpr int kStep = 16;  // keys of a warp's step, the unit of work
+constexpr int kUnit = 32;  // keys of a unit of work
 
 template <int kFormat, int D, int NT>
 struct Stream {
   static constexpr int kRow = kFormat == PROJ_KV_ROWS ? 2 * D : D;  // bytes of an entry
+  static constexpr int kStep = kRow == 256 ? 16 : 32;              // keys of a warp's step
+  static constexpr int kTiles = kStep / 16;
   static constexpr int kHalf = kStep * kRow;                       // K or V of a step
-  static constexpr int kStage = 2 * kHalf + 128;                   // and their scales
-  static constexpr int kStages = kRow == 256 ? 3 : kRow == 128 ? 6 : 8;
+  static constexpr int kStage = 2 * kHalf + 8 * kStep;             // and their scales
+  static constexpr int kStages = kRow == 64 ? 5 : 3;
   static constexpr int kRing = kStages * kStage;  // of a warp
   static constexpr int kRows = 8 * NT;
   static constexpr int kPitch = D + 4;            // floats of a row in the merge
@@ -129,6 +129,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_stream_kernel(const AttnPara
   using C = std::conditional_t<kCoded, __half, T>;  // what is multiplied
   constexpr int kRow = F::kRow, S = F::kStages, KK = D / 16, kPieces = kRow / 16;
   constexpr int kTurn = 32 / kPieces;  // rows that a warp copies at a time
+  constexpr int kStep = F::kStep, MT = F::kTiles, kUnitSteps = kUnit / kStep;
+  constexpr uint32_t kAll = kStep == 32 ? 0xFFFFFFFFu : 0xFFFFu;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ uint32_t s_valid[kWarps][S];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -231,37 +233,44 @@ __global__ void __launch_bounds__(kThreads, 1) attn_stream_kernel(const AttnPara
     }
 
     // --------------------------------------------------------------- ring --
-    const int steps = u1 - u0 > warp ? (u1 - u0 - warp + kWarps - 1) / kWarps : 0;
-    const auto first_key = [&](int i) { return (u0 + warp + i * kWarps) * kStep; };
-    // the page of key `lane` (< 16) of step i, or -1
+    const int all_steps = (u1 - u0) * kUnitSteps;
+    const int steps = all_steps > warp ? (all_steps - warp + kWarps - 1) / kWarps : 0;
+    const auto first_key = [&](int i) { return u0 * kUnit + (warp + i * kWarps) * kStep; };
+    const int32_t* const table = p.c.table + b * p.c.ldt;
+    const int64_t head_at = head * p.c.head_stride, head_scale = static_cast<int64_t>(head) * p.c.page.d;
+    // the page of key `lane` (< kStep) of step i, or -1
     const auto page_id = [&](int i) {
       const int pos = first_key(i) + lane;
       if (i >= steps || lane >= kStep || pos >= seq.len) return -1;
-      return p.c.table[b * p.c.ldt + quotient(pos, p.c.page)];
+      return table[quotient(pos, p.c.page)];
     };
-    const auto issue = [&](int i, int id) {
+    const auto issue = [&](int i, int id, int slot) {
       if (i < steps) {
-        const int slot = i % S;
         const int pos = first_key(i) + lane;
         const int spot = pos - quotient(pos, p.c.page) * static_cast<int>(p.c.page.d);
         const bool ok = id >= 0 && id < p.c.pages;
-        const Entry e = ok ? entry_at(p.c, id, spot, head) : Entry{0, 0};
-        const uint32_t valid = __ballot_sync(0xFFFFFFFFu, ok) & 0xFFFFu;
+        const int64_t at = ok ? head_at + static_cast<int64_t>(id) * static_cast<int>(p.c.page_stride) +
+                                    static_cast<int64_t>(spot) * static_cast<int>(p.c.token_stride)
+                              : 0;
+        const uint32_t valid = __ballot_sync(0xFFFFFFFFu, ok) & kAll;
         const uint32_t stage = ring + slot * F::kStage;
         if (lane == 0) s_valid[warp][slot] = valid;
+        const uint8_t* const k_from = p.c.k + lane % kPieces * 16;
+        const uint8_t* const v_from = p.c.v + lane % kPieces * 16;
 #pragma unroll
         for (int j = 0; j < kStep / kTurn; ++j) {
-          const int key = j * kTurn + lane / kPieces, piece = lane % kPieces;
-          const int64_t from = __shfl_sync(0xFFFFFFFFu, e.at, key) + piece * 16;
+          const int key = j * kTurn + lane / kPieces;
+          const int64_t from = __shfl_sync(0xFFFFFFFFu, at, key);
           const int bytes = valid >> key & 1 ? 16 : 0;
-          const uint32_t to = stage + place<kRow>(key, piece);
-          copy16(to, p.c.k + from, bytes);
-          copy16(to + F::kHalf, p.c.v + from, bytes);
+          const uint32_t to = stage + place<kRow>(key, lane % kPieces);
+          copy16(to, k_from + from, bytes);
+          copy16(to + F::kHalf, v_from + from, bytes);
         }
         if constexpr (kCoded) {
           if (lane < kStep) {
-            copy4(stage + 2 * F::kHalf + lane * 4, p.c.k_scale + e.scale, ok ? 4 : 0);
-            copy4(stage + 2 * F::kHalf + 64 + lane * 4, p.c.v_scale + e.scale, ok ? 4 : 0);
+            const int64_t from = ok ? head_scale + static_cast<int64_t>(id) * p.c.page_scales + spot : 0;
+            copy4(stage + 2 * F::kHalf + lane * 4, p.c.k_scale + from, ok ? 4 : 0);
+            copy4(stage + 2 * F::kHalf + 4 * kStep + lane * 4, p.c.v_scale + from, ok ? 4 : 0);
           }
         }
       }
@@ -271,103 +280,119 @@ __global__ void __launch_bounds__(kThreads, 1) attn_stream_kernel(const AttnPara
 #pragma unroll
     for (int i = 0; i < S; ++i) ids[i] = page_id(i);
 #pragma unroll
-    for (int i = 0; i < S - 1; ++i) issue(i, ids[i]);
-    int next_id = ids[S - 1];
+    for (int i = 0; i < S - 1; ++i) issue(i, ids[i], i);
+    int next_id = ids[S - 1], slot = 0, in_slot = S - 1;
 
+#pragma unroll 1
     for (int i = 0; i < steps; ++i) {
       asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
       __syncwarp();
       {
         const int id = next_id;
         next_id = page_id(i + S);
-        issue(i + S - 1, id);
+        issue(i + S - 1, id, in_slot);
+        if (++in_slot == S) in_slot = 0;
       }
-      const int slot = i % S;
       const uint32_t stage = ring + slot * F::kStage;
       const int key0 = first_key(i);
       const uint32_t valid = *reinterpret_cast<volatile uint32_t*>(&s_valid[warp][slot]);
+      if (++slot == S) slot = 0;
 
       // ---------------------------------------------------- S^T = K Q^T --
-      float s[NT][4];
+      float s[MT][NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[nt][j] = 0.f;
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[mt][nt][j] = 0.f;
       // matrices: keys 0-7 and 8-15 of one piece, then of the next
       const int mrow = (lane & 7) + (lane & 8), mpiece = lane >> 4;
 #pragma unroll
       for (int kk = 0; kk < (kCoded ? KK / 2 : KK); ++kk) {
-        uint32_t w[4];
-        ldsm4(w, stage + place<kRow>(mrow, 2 * kk + mpiece));
-        if constexpr (kCoded) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t a[4] = {decode_pair<kFormat>(w[2 * h], 0), decode_pair<kFormat>(w[2 * h + 1], 0),
-                                   decode_pair<kFormat>(w[2 * h], 1), decode_pair<kFormat>(w[2 * h + 1], 1)};
+        for (int mt = 0; mt < MT; ++mt) {
+          uint32_t w[4];
+          ldsm4(w, stage + mt * 16 * kRow + place<kRow>(mrow, 2 * kk + mpiece));
+          if constexpr (kCoded) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma16816(s[nt], a, qf[2 * kk + h][nt][0], qf[2 * kk + h][nt][1], C());
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t a[4] = {decode_pair<kFormat>(w[2 * h], 0), decode_pair<kFormat>(w[2 * h + 1], 0),
+                                     decode_pair<kFormat>(w[2 * h], 1), decode_pair<kFormat>(w[2 * h + 1], 1)};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma16816(s[mt][nt], a, qf[2 * kk + h][nt][0], qf[2 * kk + h][nt][1], C());
+            }
+          } else {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma16816(s[mt][nt], w, qf[kk][nt][0], qf[kk][nt][1], C());
           }
-        } else {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma16816(s[nt], w, qf[kk][nt][0], qf[kk][nt][1], C());
         }
       }
 
       // -------------------------------------------------------- softmax --
-      float vs[2] = {1.f, 1.f};
-      if constexpr (kCoded) {
-        const float ks[2] = {ld_shared_f(stage + 2 * F::kHalf + g * 4),
-                             ld_shared_f(stage + 2 * F::kHalf + g * 4 + 32)};
-        vs[0] = ld_shared_f(stage + 2 * F::kHalf + 64 + g * 4);
-        vs[1] = ld_shared_f(stage + 2 * F::kHalf + 96 + g * 4);
+      const uint32_t scales = stage + 2 * F::kHalf + g * 4;
+      float vs[MT][2];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        float ks[2] = {1.f, 1.f};
+        vs[mt][0] = vs[mt][1] = 1.f;
+        if constexpr (kCoded) {
+          ks[0] = ld_shared_f(scales + mt * 64);
+          ks[1] = ld_shared_f(scales + mt * 64 + 32);
+          vs[mt][0] = ld_shared_f(scales + 4 * kStep + mt * 64);
+          vs[mt][1] = ld_shared_f(scales + 4 * kStep + mt * 64 + 32);
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) s[nt][j] = s[nt][j] * fq[nt][j & 1] * ks[j >> 1];
-      } else {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) s[nt][j] *= fq[nt][j & 1];
+          for (int j = 0; j < 4; ++j)
+            s[mt][nt][j] = kCoded ? s[mt][nt][j] * fq[nt][j & 1] * ks[j >> 1] : s[mt][nt][j] * fq[nt][j & 1];
       }
-      // Steps with keys without a page or beyond the last, or with drafts: what
-      // a row does not see is taken out.  Bit 4 nt + j: seen.
-      const bool partial = valid != 0xFFFFu || key0 + kStep > seq.start;
+      // Steps with keys without a page or beyond the last, or with drafts: what a
+      // row does not see is taken out.  Bit 4 (NT mt + nt) + j: seen.
+      const bool partial = valid != kAll || key0 + kStep > seq.start;
       uint32_t seen = 0xFFFFFFFFu;
-      if (partial) {
+      if (__builtin_expect(partial, 0)) {
         seen = 0;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int spot = g + (j >> 1) * 8, draft = key0 + spot - seq.start;
-            const int r = row0 + nt * 8 + c4 * 2 + (j & 1);
-            bool sees = (valid >> spot & 1) && r < all_rows;
-            if (sees && draft >= 0) {
-              const int t = quotient(r, p.group);
-              if (p.mask)
-                sees = (draft >> 5) < p.words && (p.mask[(seq.lo + t) * p.ldm + (draft >> 5)] >> (draft & 31) & 1);
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int spot = mt * 16 + g + (j >> 1) * 8, draft = key0 + spot - seq.start;
+              const int r = row0 + nt * 8 + c4 * 2 + (j & 1);
+              bool sees = (valid >> spot & 1) && r < all_rows;
+              if (sees && draft >= 0) {
+                const int t = quotient(r, p.group);
+                if (p.mask)
+                  sees = (draft >> 5) < p.words && (p.mask[(seq.lo + t) * p.ldm + (draft >> 5)] >> (draft & 31) & 1);
+                else
+                  sees = draft <= t;
+              }
+              if (sees)
+                seen |= 1u << (4 * (NT * mt + nt) + j);
               else
-                sees = draft <= t;
+                s[mt][nt][j] = -INFINITY;
             }
-            if (sees)
-              seen |= 1u << (4 * nt + j);
-            else
-              s[nt][j] = -INFINITY;
-          }
       }
       bool beyond = false;
+      float tops[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int i2 = 0; i2 < 2; ++i2) beyond |= fmaxf(s[nt][i2], s[nt][2 + i2]) > ref[nt][i2] + 6.f;
+        for (int i2 = 0; i2 < 2; ++i2) {
+          tops[nt][i2] = fmaxf(s[0][nt][i2], s[0][nt][2 + i2]);
+          if (MT == 2) tops[nt][i2] = fmaxf(tops[nt][i2], fmaxf(s[MT - 1][nt][i2], s[MT - 1][nt][2 + i2]));
+          beyond |= tops[nt][i2] > ref[nt][i2] + kSlack;
+        }
       if (__any_sync(0xFFFFFFFFu, beyond)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i2 = 0; i2 < 2; ++i2) {
-            float top = fmaxf(s[nt][i2], s[nt][2 + i2]);
+            float top = tops[nt][i2];
 #pragma unroll
             for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
             top = fmaxf(top, ref[nt][i2]);
@@ -384,9 +409,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_stream_kernel(const AttnPara
       if constexpr (kCoded) {
         // scales that are no finite number do not enter the reference: they make
         // p NaN for the rows that see the key, and only for those
-        if (!(vs[0] < INFINITY)) vs[0] = __uint_as_float(0x7FC00000u);
-        if (!(vs[1] < INFINITY)) vs[1] = __uint_as_float(0x7FC00000u);
-        float top = fmaxf(fabsf(vs[0]), fabsf(vs[1]));  // the finite one, if only one is
+        float top = 0.f;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (!(fabsf(vs[mt][h]) < INFINITY)) vs[mt][h] = __uint_as_float(0x7FC00000u);
+            top = fmaxf(top, fabsf(vs[mt][h]));  // the finite ones
+          }
         if (__any_sync(0xFFFFFFFFu, top > 2.f * v_ref)) {
 #pragma unroll
           for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
@@ -401,34 +431,42 @@ __global__ void __launch_bounds__(kThreads, 1) attn_stream_kernel(const AttnPara
 #pragma unroll
               for (int j = 0; j < 4; ++j) o[kk][nt][j] *= down;
         }
-        vs[0] *= v_inv;
-        vs[1] *= v_inv;
-      }
-      uint32_t pb[NT][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float e[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) e[j] = exp2_fast(s[nt][j] - (ref[nt][j & 1] - 8.f));
-        sum[nt][0] += e[0] + e[2];
-        sum[nt][1] += e[1] + e[3];
-        if constexpr (kCoded) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            e[j] = !partial || (seen >> (4 * nt + j) & 1) ? e[j] * vs[j >> 1] : 0.f;
+        for (int mt = 0; mt < MT; ++mt) {
+          vs[mt][0] *= v_inv;
+          vs[mt][1] *= v_inv;
         }
-        pb[nt][0] = transpose8(pack2(e[0], e[1], C()));
-        pb[nt][1] = transpose8(pack2(e[2], e[3], C()));
       }
+      uint32_t pb[MT][NT][2];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float e[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) e[j] = exp2_fast(s[mt][nt][j] - (ref[nt][j & 1] - kLift));
+          sum[nt][0] += e[0] + e[2];
+          sum[nt][1] += e[1] + e[3];
+          if constexpr (kCoded) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) e[j] *= vs[mt][j >> 1];
+            if (__builtin_expect(partial, 0)) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (!(seen >> (4 * (NT * mt + nt) + j) & 1)) e[j] = 0.f;
+            }
+          }
+          pb[mt][nt][0] = transpose8(pack2(e[0], e[1], C()));
+          pb[mt][nt][1] = transpose8(pack2(e[2], e[3], C()));
+        }
 
       // -------------------------------------------------- O^T += V^T P^T --
-      uint32_t odd = 0;
       const int trow = (lane & 7) + (kCoded ? lane & 8 : lane >> 4 << 3);
       const int tpiece = kCoded ? lane >> 4 : lane >> 3 & 1;
-      const auto v_frag = [&](int kk, uint32_t (&a)[4], uint32_t (&a2)[4]) {
+      const auto v_frag = [&](int mt, int kk, uint32_t (&a)[4], uint32_t (&a2)[4]) {
         // 8 bit: dimensions 32 kk .. + 31 as two fragments; 16 bit: 16 kk .. + 15
         uint32_t w[4];
-        ldsm4t(w, stage + F::kHalf + place<kRow>(trow, 2 * kk + tpiece));
+        ldsm4t(w, stage + F::kHalf + mt * 16 * kRow + place<kRow>(trow, 2 * kk + tpiece));
         if constexpr (kCoded) {
           decode_cross<kFormat>(w[0], a[0], a[1]);
           decode_cross<kFormat>(w[1], a[2], a[3]);
@@ -440,58 +478,65 @@ __global__ void __launch_bounds__(kThreads, 1) attn_stream_kernel(const AttnPara
         }
       };
       constexpr int kSteps = kCoded ? KK / 2 : KK;
-      if (kFormat != PROJ_KV_INT8 && partial) {
+      uint32_t odd = 0;
+      if (kFormat != PROJ_KV_INT8 && __builtin_expect(partial, 0)) {
 #pragma unroll 1
-        for (int kk = 0; kk < kSteps; ++kk) {
-          uint32_t a[4], a2[4] = {0u, 0u, 0u, 0u};
-          v_frag(kk, a, a2);
+        for (int kk = 0; kk < kSteps; ++kk)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) odd |= odd_pair(a[j], C()) || odd_pair(a2[j], C());
-        }
+          for (int mt = 0; mt < MT; ++mt) {
+            uint32_t a[4], a2[4] = {0u, 0u, 0u, 0u};
+            v_frag(mt, kk, a, a2);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) odd |= odd_pair(a[j], C()) || odd_pair(a2[j], C());
+          }
         odd = __any_sync(0xFFFFFFFFu, odd);
       }
-      if (!odd) {
+      if (__builtin_expect(!odd, 1)) {
 #pragma unroll
-        for (int kk = 0; kk < kSteps; ++kk) {
-          uint32_t a[4], a2[4];
-          v_frag(kk, a, a2);
+        for (int kk = 0; kk < kSteps; ++kk)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            if constexpr (kCoded) {
-              mma16816(o[2 * kk][nt], a, pb[nt][0], pb[nt][1], C());
-              mma16816(o[2 * kk + 1][nt], a2, pb[nt][0], pb[nt][1], C());
-            } else {
-              mma16816(o[kk][nt], a, pb[nt][0], pb[nt][1], C());
+          for (int mt = 0; mt < MT; ++mt) {
+            uint32_t a[4], a2[4];
+            v_frag(mt, kk, a, a2);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              if constexpr (kCoded) {
+                mma16816(o[2 * kk][nt], a, pb[mt][nt][0], pb[mt][nt][1], C());
+                mma16816(o[2 * kk + 1][nt], a2, pb[mt][nt][0], pb[mt][nt][1], C());
+              } else {
+                mma16816(o[kk][nt], a, pb[mt][nt][0], pb[mt][nt][1], C());
+              }
             }
           }
-        }
       } else {
         // A value of V in this step is no finite number, and 0 times it is NaN:
         // key by key, added where the row sees the key.
 #pragma unroll
-        for (int kk = 0; kk < kSteps; ++kk) {
-          uint32_t a[2][4];
-          v_frag(kk, a[0], a[1]);
+        for (int kk = 0; kk < kSteps; ++kk)
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            uint32_t a[2][4];
+            v_frag(mt, kk, a[0], a[1]);
 #pragma unroll 1
-          for (int key = 0; key < kStep; ++key) {
-            const uint32_t sees = __shfl_sync(0xFFFFFFFFu, seen, (key & 7) * 4 + c4) >> (key & 8 ? 2 : 0);
-            const bool mine = (key & 7) >> 1 == c4;
-            const uint32_t half = mine ? (key & 1 ? 0xFFFF0000u : 0xFFFFu) : 0u;
-            const uint32_t lo = key & 8 ? 0u : half, hi = key & 8 ? half : 0u;
+            for (int key = 0; key < 16; ++key) {
+              const uint32_t sees = __shfl_sync(0xFFFFFFFFu, seen, (key & 7) * 4 + c4) >> (4 * NT * mt + (key & 8 ? 2 : 0));
+              const bool mine = (key & 7) >> 1 == c4;
+              const uint32_t half = mine ? (key & 1 ? 0xFFFF0000u : 0xFFFFu) : 0u;
+              const uint32_t lo = key & 8 ? 0u : half, hi = key & 8 ? half : 0u;
 #pragma unroll
-            for (int h = 0; h < (kCoded ? 2 : 1); ++h) {
-              const uint32_t one[4] = {a[h][0] & lo, a[h][1] & lo, a[h][2] & hi, a[h][3] & hi};
+              for (int h = 0; h < (kCoded ? 2 : 1); ++h) {
+                const uint32_t one[4] = {a[h][0] & lo, a[h][1] & lo, a[h][2] & hi, a[h][3] & hi};
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                float d[4] = {0.f, 0.f, 0.f, 0.f};
-                mma16816(d, one, pb[nt][0] & lo, pb[nt][1] & hi, C());
+                for (int nt = 0; nt < NT; ++nt) {
+                  float d[4] = {0.f, 0.f, 0.f, 0.f};
+                  mma16816(d, one, pb[mt][nt][0] & lo, pb[mt][nt][1] & hi, C());
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                  if (sees >> (4 * nt + (j & 1)) & 1) o[kCoded ? 2 * kk + h : kk][nt][j] += d[j];
+                  for (int j = 0; j < 4; ++j)
+                    if (sees >> (4 * nt + (j & 1)) & 1) o[kCoded ? 2 * kk + h : kk][nt][j] += d[j];
+                }
               }
             }
           }
-        }
       }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -511,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_stream_kernel(const AttnPara
       for (int i = 0; i < 2; ++i) {
         const int r = nt * 8 + c4 * 2 + i;
         if (g == 0) {
-          s_ml[(warp * F::kRows + r) * 2] = ref[nt][i] - 8.f;
+          s_ml[(warp * F::kRows + r) * 2] = ref[nt][i] - kLift;
           s_ml[(warp * F::kRows + r) * 2 + 1] = sum[nt][i];
         }
         float* to = merge + (warp * F::kRows + r) * F::kPitch;
@@ -529,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_stream_kernel(const AttnPara
     }
     __syncthreads();
     const bool whole = u0 == 0 && u1 == seq.units;
-    const int slot = 2 * static_cast<int>(blockIdx.x) + (u0 == 0 ? 1 : 0);
+    const int part = 2 * static_cast<int>(blockIdx.x) + (u0 == 0 ? 1 : 0);
     for (int x = threadIdx.x; x < F::kRows * (D / 4); x += kThreads) {
       const int r = x / (D / 4), quad = x % (D / 4);
       if (row0 + r >= all_rows) continue;
@@ -553,10 +598,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_stream_kernel(const AttnPara
         write_out<T>(p, seq.lo + t, j * D + quad * 4, acc, l);
         if (p.lse && quad == 0) p.lse[static_cast<int64_t>(seq.lo + t) * p.heads + j] = lse_of(top, l);
       } else {
-        float* to = p.part_o + (static_cast<int64_t>(slot) * F::kRows + r) * D + quad * 4;
+        float* to = p.part_o + (static_cast<int64_t>(part) * F::kRows + r) * D + quad * 4;
         *reinterpret_cast<float4*>(to) = make_float4(acc[0], acc[1], acc[2], acc[3]);
         if (quad == 0)
-          *reinterpret_cast<float2*>(p.part_ml + (static_cast<int64_t>(slot) * F::kRows + r) * 2) =
+          *reinterpret_cast<float2*>(p.part_ml + (static_cast<int64_t>(part) * F::kRows + r) * 2) =
               make_float2(top, l);
       }
     }
@@ -678,9 +723,7 @@ cudaError_t stream_launch(const AttnParams& p, cudaStream_t s) {
 
 template <typename T, int kFormat, int D>
 cudaError_t stream_rows(const AttnParams& p, cudaStream_t s) {
-  return p.tile_rows == 8    ? stream_launch<T, kFormat, D, 1>(p, s)
-         : p.tile_rows == 16 ? stream_launch<T, kFormat, D, 2>(p, s)
-                             : stream_launch<T, kFormat, D, 4>(p, s);
+  return p.tile_rows == 8 ? stream_launch<T, kFormat, D, 1>(p, s) : stream_launch<T, kFormat, D, 2>(p, s);
 }
 
 template <typename T, int D>
@@ -712,10 +755,10 @@ const char* make_plan(const proj_kv_cache* cache, int64_t m, int64_t heads, Plan
                            ? (m + cache->sequences - 1) / cache->sequences * (heads / cache->heads)
                            : 1;
   plan->rows = rows;
-  plan->tc = rows > 32;
-  plan->unit = plan->tc ? kAttnTcUnit : kStep;
-  plan->tile_rows = plan->tc ? kAttnTcRows : rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
-  plan->min_units = plan->tc ? 4 : 2 * kWarps;
+  plan->tc = rows > 16;
+  plan->unit = plan->tc ? kAttnTcUnit : kUnit;
+  plan->tile_rows = plan->tc ? kAttnTcRows : rows <= 8 ? 8 : 16;
+  plan->min_units = plan->tc ? 4 : kWarps;
   int sms = 0, dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)

@@ -173,6 +173,11 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return r;
 }
 
+// A row's reference moves when a score is more than 2^kSlack above it, and is
+// 2^kLift as a probability: at most 2^14, twice that with V's scale, and 2^-28 of
+// the reference is where fp16 ends (65504 and 2^-24).
+constexpr float kSlack = 10.f, kLift = 4.f;
+
 // The reference of a row that has seen nothing yet.
 constexpr float kNoScore = -3e38f;
 

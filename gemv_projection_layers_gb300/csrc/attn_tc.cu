@@ -53,9 +53,6 @@ constexpr int kTmemCols = 512;
 constexpr int kRaw = 4;       // tiles of 8-bit codes in shared memory or on their way there
 constexpr int kRawScales = 4;
 constexpr int kIds = 4;  // tiles whose page ids are known or on their way
-// A row's reference moves when a score is more than 2^kSlack above it, and is
-// 2^kLift as a probability: at most 2^14 and, where fp16 ends, 2^-28 of it.
-constexpr float kSlack = 10.f, kLift = 4.f;
 constexpr int kSlots = 8;     // tiles whose addresses are known
 constexpr int kSegments = 4;  // segments that are known
 
@@ -176,7 +173,7 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, uint32_t
   if (mbar_try_wait(bar, parity)) return true;
   uint64_t t0 = 0;
   for (uint32_t n = 1;; ++n) {
-    if (mbar_try_wait_hint(bar, parity, 1000u)) return true;
+    if (mbar_try_wait(bar, parity)) return true;
     if ((n & 255u) == 0) {
       const uint64_t now = globaltimer_ns();
       if (!t0) t0 = now;
@@ -609,18 +606,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
           const uint32_t at = raw + from_slot % kRawScales * (8 * kKeys);
           if (kind & 4) ref = 0.f;
           float w[2];
+          uint32_t top_bits = 0;
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
+            w[j] = ld_shared_f(at + 4 * kKeys + j * 128);
+            const uint32_t size = __float_as_uint(w[j]) & 0x7FFFFFFFu;
+            const bool fine = size < 0x7F800000u;
+            if (fine) top_bits = max(top_bits, size);
             // before the drafts every row sees the key, and NaN is what all of them get
-            const float v = ld_shared_f(at + 4 * kKeys + j * 128);
-            const bool fine = fabsf(v) < INFINITY;
-            w[j] = fine ? v : kind & 2 ? 0.f : __uint_as_float(0x7FC00000u);
-            const uint32_t odd = __ballot_sync(0xFFFFFFFFu, !fine);
-            if (lane == 0) st_shared_u(side + F::kOddScale + 4 * j, odd);
+            if (!fine) w[j] = kind & 2 ? 0.f : __uint_as_float(0x7FC00000u);
+            if (kind & 2) {
+              const uint32_t odd = __ballot_sync(0xFFFFFFFFu, !fine);
+              if (lane == 0) st_shared_u(side + F::kOddScale + 4 * j, odd);
+            }
           }
-          float top = fmaxf(fabsf(w[0]), fabsf(w[1]));  // the finite one, if only one is
-#pragma unroll
-          for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+          const float top = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, top_bits));
           // a power of two not above the largest scale: its reciprocal is exact, and
           // what is stored is at most 2
           if (top > 2.f * ref) ref = __uint_as_float(max(__float_as_uint(top) & 0x7F800000u, 0x00800000u));
@@ -654,11 +654,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     const int piece = tid % kPieces, key_of = tid / kPieces;
     const uint8_t* const from_k = p.c.k + piece * 16;
     const uint8_t* const from_v = p.c.v + piece * 16;
-    // Tiles are issued kLag before they are handed over.  16-bit entries: a tile is
-    // handed over when the copies of the kLag-th tile after it are issued, and those
-    // wait for the stage of the tile NS - kLag before; the MMA warp asks for tile n
-    // before it releases n - 2.
-    constexpr int kLag = kCoded ? kRaw - 1 : NS - 3;
+    // Tiles on their way when one is handed over.  A tile is handed over before the
+    // next one is asked for: its stage may still be busy with a tile that waits for
+    // nothing but this one's turn.
+    constexpr int kLag = kCoded ? kRaw : NS - 1;
     uint32_t kinds = 0;  // of the tiles issued: three bits each, the oldest lowest
     bool ok = true, open = true;
     int stage = 0, slot = 0;
@@ -735,17 +734,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         }
       }
       copies_sealed();
-      kinds = kinds >> 3 | static_cast<uint32_t>(kind) << (3 * kLag);
+      kinds = kinds >> 3 | static_cast<uint32_t>(kind) << (3 * kLag - 3);
     };
 #pragma unroll 1
     for (int i = 0; i < kLag; ++i) issue();
     int raw = 0;
 #pragma unroll 1
     for (;;) {
-      issue();
       const uint32_t kind = kinds & 7u;
       if (kind == 0) break;
-      copies_wait<kLag>();
+      copies_wait<kLag - 1>();
       if constexpr (kCoded) {
         // this thread's own pieces: codes to fp16
         ok = ok && wait_bar(empty + 8 * stage, phase ^ 1u, p.status, kStatusTimeoutProducer);
@@ -769,6 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         for (int j = 0; j < kPasses; ++j) finite_only(j * kTurn + key_of);
       }
       landed();
+      issue();
     }
     copies_wait<0>();
   } else {

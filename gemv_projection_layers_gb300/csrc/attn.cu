@@ -142,14 +142,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_stream_kernel(const AttnPara
   griddep_launch_dependents();
   griddep_wait();
   Share share;
-  const bool mine = find_share<kThreads>(p, blockIdx.x, share);
-  if (threadIdx.x == 0) p.splits[blockIdx.x] = mine ? split_of(p, share, blockIdx.x) : Split{};
-  if (!mine) return;
+  if (!find_share<kThreads>(p, blockIdx.x, share)) {
+    if (threadIdx.x == 0) p.splits[blockIdx.x] = Split{};
+    return;
+  }
 
   const int G = static_cast<int>(p.group.d);
   int b = share.b;
   int64_t before = share.before;
   Sequence seq = sequence_at(p, b);
+  bool told = false;
   for (int64_t at = share.first; at < share.end;) {
     while (at >= before + units_of(p, seq)) {
       before += units_of(p, seq);
@@ -163,6 +165,58 @@ __global__ void __launch_bounds__(kThreads, 1) attn_stream_kernel(const AttnPara
     const int head = static_cast<int>(divide(item, seq.tiles));
     const int row0 = static_cast<int>(item - static_cast<int64_t>(head) * seq.tiles) * F::kRows;
     const int all_rows = seq.rows * G;
+
+    // --------------------------------------------------------------- ring --
+    const int all_steps = (u1 - u0) * kUnitSteps;
+    const int steps = all_steps > warp ? (all_steps - warp + kWarps - 1) / kWarps : 0;
+    const auto first_key = [&](int i) { return u0 * kUnit + (warp + i * kWarps) * kStep; };
+    const int32_t* const table = p.c.table + b * p.c.ldt;
+    const int64_t head_at = head * p.c.head_stride, head_scale = static_cast<int64_t>(head) * p.c.page.d;
+    // the page of key `lane` (< kStep) of step i, or -1
+    const auto page_id = [&](int i) {
+      const int pos = first_key(i) + lane;
+      if (i >= steps || lane >= kStep || pos >= seq.len) return -1;
+      return table[quotient(pos, p.c.page)];
+    };
+    const auto issue = [&](int i, int id, int slot) {
+      if (i < steps) {
+        const int pos = first_key(i) + lane;
+        const int spot = pos - quotient(pos, p.c.page) * static_cast<int>(p.c.page.d);
+        const bool ok = id >= 0 && id < p.c.pages;
+        const int64_t at = ok ? head_at + static_cast<int64_t>(id) * static_cast<int>(p.c.page_stride) +
+                                    static_cast<int64_t>(spot) * static_cast<int>(p.c.token_stride)
+                              : 0;
+        const uint32_t valid = __ballot_sync(0xFFFFFFFFu, ok) & kAll;
+        const uint32_t stage = ring + slot * F::kStage;
+        if (lane == 0) s_valid[warp][slot] = valid;
+        const uint8_t* const k_from = p.c.k + lane % kPieces * 16;
+        const uint8_t* const v_from = p.c.v + lane % kPieces * 16;
+#pragma unroll
+        for (int j = 0; j < kStep / kTurn; ++j) {
+          const int key = j * kTurn + lane / kPieces;
+          const int64_t from = __shfl_sync(0xFFFFFFFFu, at, key);
+          const int bytes = valid >> key & 1 ? 16 : 0;
+          const uint32_t to = stage + place<kRow>(key, lane % kPieces);
+          copy16(to, k_from + from, bytes);
+          copy16(to + F::kHalf, v_from + from, bytes);
+        }
+        if constexpr (kCoded) {
+          if (lane < kStep) {
+            const int64_t from = ok ? head_scale + static_cast<int64_t>(id) * p.c.page_scales + spot : 0;
+            copy4(stage + 2 * F::kHalf + lane * 4, p.c.k_scale + from, ok ? 4 : 0);
+            copy4(stage + 2 * F::kHalf + 4 * kStep + lane * 4, p.c.v_scale + from, ok ? 4 : 0);
+          }
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    int ids[S];
+#pragma unroll
+    for (int i = 0; i < S; ++i) ids[i] = page_id(i);
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) issue(i, ids[i], i);
+    int next_id = ids[S - 1], slot = 0, in_slot = S - 1;
+
 
     // ------------------------------------------------------------ queries --
     uint32_t qf[KK][NT][2];
@@ -231,57 +285,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_stream_kernel(const AttnPara
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[kk][nt][i] = 0.f;
     }
-
-    // --------------------------------------------------------------- ring --
-    const int all_steps = (u1 - u0) * kUnitSteps;
-    const int steps = all_steps > warp ? (all_steps - warp + kWarps - 1) / kWarps : 0;
-    const auto first_key = [&](int i) { return u0 * kUnit + (warp + i * kWarps) * kStep; };
-    const int32_t* const table = p.c.table + b * p.c.ldt;
-    const int64_t head_at = head * p.c.head_stride, head_scale = static_cast<int64_t>(head) * p.c.page.d;
-    // the page of key `lane` (< kStep) of step i, or -1
-    const auto page_id = [&](int i) {
-      const int pos = first_key(i) + lane;
-      if (i >= steps || lane >= kStep || pos >= seq.len) return -1;
-      return table[quotient(pos, p.c.page)];
-    };
-    const auto issue = [&](int i, int id, int slot) {
-      if (i < steps) {
-        const int pos = first_key(i) + lane;
-        const int spot = pos - quotient(pos, p.c.page) * static_cast<int>(p.c.page.d);
-        const bool ok = id >= 0 && id < p.c.pages;
-        const int64_t at = ok ? head_at + static_cast<int64_t>(id) * static_cast<int>(p.c.page_stride) +
-                                    static_cast<int64_t>(spot) * static_cast<int>(p.c.token_stride)
-                              : 0;
-        const uint32_t valid = __ballot_sync(0xFFFFFFFFu, ok) & kAll;
-        const uint32_t stage = ring + slot * F::kStage;
-        if (lane == 0) s_valid[warp][slot] = valid;
-        const uint8_t* const k_from = p.c.k + lane % kPieces * 16;
-        const uint8_t* const v_from = p.c.v + lane % kPieces * 16;
-#pragma unroll
-        for (int j = 0; j < kStep / kTurn; ++j) {
-          const int key = j * kTurn + lane / kPieces;
-          const int64_t from = __shfl_sync(0xFFFFFFFFu, at, key);
-          const int bytes = valid >> key & 1 ? 16 : 0;
-          const uint32_t to = stage + place<kRow>(key, lane % kPieces);
-          copy16(to, k_from + from, bytes);
-          copy16(to + F::kHalf, v_from + from, bytes);
-        }
-        if constexpr (kCoded) {
-          if (lane < kStep) {
-            const int64_t from = ok ? head_scale + static_cast<int64_t>(id) * p.c.page_scales + spot : 0;
-            copy4(stage + 2 * F::kHalf + lane * 4, p.c.k_scale + from, ok ? 4 : 0);
-            copy4(stage + 2 * F::kHalf + 4 * kStep + lane * 4, p.c.v_scale + from, ok ? 4 : 0);
-          }
-        }
-      }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-    int ids[S];
-#pragma unroll
-    for (int i = 0; i < S; ++i) ids[i] = page_id(i);
-#pragma unroll
-    for (int i = 0; i < S - 1; ++i) issue(i, ids[i], i);
-    int next_id = ids[S - 1], slot = 0, in_slot = S - 1;
 
 #pragma unroll 1
     for (int i = 0; i < steps; ++i) {
@@ -542,12 +545,29 @@ __global__ void __launch_bounds__(kThreads, 1) attn_stream_kernel(const AttnPara
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 
     // --------------------------------------------- the warps' sums joined --
+    // A thread has kOuts rows, four columns of each; their gate is read meanwhile.
+    const bool whole = u0 == 0 && u1 == seq.units;
+    constexpr int kOuts = F::kRows * (D / 4) / kThreads > 0 ? F::kRows * (D / 4) / kThreads : 1;
+    const int quad = threadIdx.x % (D / 4);
+    const auto out_row = [&](int n) { return static_cast<int>(threadIdx.x) / (D / 4) + n * (kThreads / (D / 4)); };
+    Vec<T, 4> gate[kOuts][1] = {};
+    if (whole && p.gate) {
+#pragma unroll
+      for (int n = 0; n < kOuts; ++n) {
+        const int r = row0 + out_row(n), t = quotient(r, p.group);
+        if (r < all_rows && out_row(n) < F::kRows)
+          gate[n][0] = load_vec<T, 4>(reinterpret_cast<const T*>(p.gate + static_cast<int64_t>(seq.lo + t) * p.ldg) +
+                                      (head * G + r - t * G) * D + quad * 4);
+      }
+    }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) sum[nt][i] += __shfl_xor_sync(0xFFFFFFFFu, sum[nt][i], x);
+    if (!told && threadIdx.x == kThreads - 1) p.splits[blockIdx.x] = split_of(p, share, blockIdx.x);
+    told = true;
     __syncthreads();  // every warp is done with its ring
     const float up = kCoded ? v_ref : 1.f;
 #pragma unroll
@@ -573,11 +593,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_stream_kernel(const AttnPara
       }
     }
     __syncthreads();
-    const bool whole = u0 == 0 && u1 == seq.units;
-    const int part = 2 * static_cast<int>(blockIdx.x) + (u0 == 0 ? 1 : 0);
-    for (int x = threadIdx.x; x < F::kRows * (D / 4); x += kThreads) {
-      const int r = x / (D / 4), quad = x % (D / 4);
-      if (row0 + r >= all_rows) continue;
+#pragma unroll
+    for (int n = 0; n < kOuts; ++n) {
+      const int r = out_row(n);
+      if (row0 + r >= all_rows || r >= F::kRows) continue;
       float top = s_ml[r * 2];
 #pragma unroll
       for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_ml[(w * F::kRows + r) * 2]);
@@ -595,9 +614,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_stream_kernel(const AttnPara
       if (whole) {
         const int t = quotient(row0 + r, p.group);
         const int j = head * G + row0 + r - t * G;
-        write_out<T>(p, seq.lo + t, j * D + quad * 4, acc, l);
+        write_out<T>(p, static_cast<int64_t>(seq.lo + t), j * D + quad * 4, acc, l, gate[n]);
         if (p.lse && quad == 0) p.lse[static_cast<int64_t>(seq.lo + t) * p.heads + j] = lse_of(top, l);
       } else {
+        const int part = 2 * static_cast<int>(blockIdx.x) + (u0 == 0 ? 1 : 0);
         float* to = p.part_o + (static_cast<int64_t>(part) * F::kRows + r) * D + quad * 4;
         *reinterpret_cast<float4*>(to) = make_float4(acc[0], acc[1], acc[2], acc[3]);
         if (quad == 0)
@@ -620,35 +640,42 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) attn_join_kernel(const AttnParams p) {
   constexpr int kLanes = D / 4, kSets = kThreads / kLanes;
   __shared__ float s_o[kSets][D], s_ml[kSets][2];
-  __shared__ int s_found;
+  __shared__ Split s_split;
+  __shared__ int s_count[kThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   griddep_launch_dependents();
   griddep_wait();
-  // the item: the x-th CTA that left one
-  if (threadIdx.x < 32) {
-    int found = -1, seen = 0;
-    for (int c = 0; c < p.ctas && found < 0; c += 32) {
-      const int at = c + static_cast<int>(threadIdx.x);
-      const uint32_t some = __ballot_sync(0xFFFFFFFFu, at < p.ctas && p.splits[at].rows > 0);
-      const int rank = static_cast<int>(blockIdx.x) - seen;
-      if (rank < __popc(some)) {
-        uint32_t left = some;
-        for (int i = 0; i < rank; ++i) left &= left - 1;
-        found = c + __ffs(left) - 1;
-      }
-      seen += __popc(some);
+  // the item: the x-th that a CTA left
+  if (threadIdx.x == 0) s_split.rows = 0;
+  int before = 0;
+  for (int c = 0; c < p.ctas; c += kThreads) {
+    const int at = c + static_cast<int>(threadIdx.x);
+    const Split mine = at < p.ctas ? p.splits[at] : Split{};
+    const uint32_t some = __ballot_sync(0xFFFFFFFFu, mine.rows > 0);
+    if (lane == 0) s_count[warp] = __popc(some);
+    __syncthreads();
+    int rank = before + __popc(some & ((1u << lane) - 1u));
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) rank += s_count[w];
+      before += s_count[w];
     }
-    if (threadIdx.x == 0) s_found = found;
+    if (mine.rows > 0 && rank == static_cast<int>(blockIdx.x)) s_split = mine;
+    __syncthreads();
   }
-  __syncthreads();
-  if (s_found < 0) return;
-  const Split it = p.splits[s_found];
+  const Split it = s_split;
+  if (it.rows == 0) return;
   const int G = static_cast<int>(p.group.d);
   const int set = threadIdx.x / kLanes, quad = threadIdx.x % kLanes;
   const bool few = it.last - it.first < kFewParts;
   const int y0 = few ? blockIdx.y * kSets + set : blockIdx.y, dy = few ? gridDim.y * kSets : gridDim.y;
   for (int r = y0; r < it.rows; r += dy) {
     float top = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
+    const int t = quotient(it.row0 + r, p.group);
+    const int j = it.head * G + it.row0 + r - t * G;
+    Vec<T, 4> gate[1] = {};
+    if (p.gate) gate[0] = load_vec<T, 4>(reinterpret_cast<const T*>(p.gate + static_cast<int64_t>(it.lo + t) * p.ldg) + j * D + quad * 4);
+#pragma unroll 8
     for (int c = it.first + (few ? 0 : set); c <= it.last; c += few ? 1 : kSets) {
       const int64_t slot = 2ll * c + (c == it.first ? 1 : 0);
       const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (slot * p.tile_rows + r) * 2);
@@ -687,9 +714,7 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(const AttnParams p)
       __syncthreads();
     }
     if (few || set == 0) {
-      const int t = quotient(it.row0 + r, p.group);
-      const int j = it.head * G + it.row0 + r - t * G;
-      write_out<T>(p, it.lo + t, j * D + quad * 4, acc, l);
+      write_out<T>(p, static_cast<int64_t>(it.lo + t), j * D + quad * 4, acc, l, gate);
       if (p.lse && quad == 0) p.lse[static_cast<int64_t>(it.lo + t) * p.heads + j] = lse_of(top, l);
     }
   }
@@ -841,7 +866,7 @@ extern "C" int proj_attn(const proj_attn_args* args, proj_stream stream) {
   p.tile_rows = plan.tile_rows;
   p.unit = plan.unit;
   p.ctas = plan.ctas;
-  p.min_units = plan.min_units;
+  while ((1 << p.min_shift) < plan.min_units) ++p.min_shift;
   while ((1 << p.tile_shift) < p.tile_rows) ++p.tile_shift;
   while ((1 << p.unit_shift) < p.unit) ++p.unit_shift;
   void* status_word = nullptr;

@@ -6,7 +6,8 @@
 // drafted token and a query head of the group; row r is token r / group, head
 // r % group); it has ceil(keys / unit) units.  The items' units stand in one
 // line, and CTA c of the `active` takes units [c W / active, (c + 1) W /
-// active) of the W.  So every SM has the same share whatever the lengths, a CTA
+// active) of the W; there are as many as have min_units units, and no fewer than
+// items.  So every SM has the same share whatever the lengths, a CTA
 // leaves at most two items unfinished (one it did not begin, one it does not
 // end), and the partial results need room for two items a CTA and nothing that
 // grows with the batch.  A second kernel joins them in the order of their CTAs.
@@ -39,8 +40,8 @@ struct AttnParams {
   float* lse;
   int m, heads, D;
   Divisor group;
-  int tile_rows, unit, ctas, min_units;
-  int tile_shift, unit_shift;  // their logarithms
+  int tile_rows, unit, ctas;
+  int tile_shift, unit_shift, min_shift;  // logarithms; min_shift: of a share's least units
   struct Split* splits;  // [ctas]
   float* part_o;   // [2 ctas][tile_rows][D]: sums relative to 2^m
   float* part_ml;  // [2 ctas][tile_rows][2]: m, sum
@@ -107,30 +108,42 @@ __device__ __forceinline__ int share_owner(int64_t W, int active, int64_t x) {
 template <int kThreads>
 __device__ __forceinline__ bool find_share(const AttnParams& p, int cta, Share& s) {
   __shared__ int64_t warp_sum[kThreads / 32];
+  __shared__ int warp_items[kThreads / 32];
   __shared__ int found_b;
   __shared__ int64_t found_before;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.c.sequences + kThreads - 1) / kThreads;
   const int b0 = min(tid * per, p.c.sequences), b1 = min(b0 + per, p.c.sequences);
   int64_t sum = 0;
-  for (int b = b0; b < b1; ++b) sum += units_of(p, sequence_at(p, b));
+  int items = 0;  // no more than there are CTAs are counted
+  for (int b = b0; b < b1; ++b) {
+    const Sequence seq = sequence_at(p, b);
+    sum += units_of(p, seq);
+    items = static_cast<int>(min(items + static_cast<int64_t>(seq.tiles) * p.c.heads, int64_t{1} << 16));
+  }
   int64_t inc = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int64_t v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
     if (lane >= o) inc += v;
   }
-  if (lane == 31) warp_sum[warp] = inc;
+  items = __reduce_add_sync(0xFFFFFFFFu, items);
+  if (lane == 31) {
+    warp_sum[warp] = inc;
+    warp_items[warp] = items;
+  }
   if (tid == 0) found_b = -1;
   __syncthreads();
   int64_t before = inc - sum, W = 0;
+  items = 0;
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) before += warp_sum[w];
     W += warp_sum[w];
+    items += warp_items[w];
   }
   s.units = W;
-  s.active = static_cast<int>(min(static_cast<int64_t>(p.ctas), max(divide(W, p.min_units), int64_t{1})));
+  s.active = static_cast<int>(min(static_cast<int64_t>(p.ctas), max(W >> p.min_shift, static_cast<int64_t>(items))));
   if (W == 0 || cta >= s.active) return false;
   s.first = share_begin(W, s.active, cta);
   s.end = share_begin(W, s.active, cta + 1);
@@ -202,14 +215,6 @@ __device__ __forceinline__ void write_out(const AttnParams& p, int64_t row, int 
     store_vec<T, V>(reinterpret_cast<T*>(p.out + row * p.ldo) + column + i * V, o);
   }
 }
-template <typename T, int N>
-__device__ __forceinline__ void write_out(const AttnParams& p, int64_t row, int column,
-                                          const float (&sum)[N], float l) {
-  Vec<T, N> gate[1] = {};
-  if (p.gate) gate[0] = load_vec<T, N>(reinterpret_cast<const T*>(p.gate + row * p.ldg) + column);
-  write_out<T>(p, row, column, sum, l, gate);
-}
-
 __device__ __forceinline__ float lse_of(float m, float l) {
   return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }

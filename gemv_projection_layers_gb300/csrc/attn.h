@@ -104,9 +104,64 @@ __device__ __forceinline__ int share_owner(int64_t W, int active, int64_t x) {
   return static_cast<int>(divide((x + 1) * active - 1, W));
 }
 
+// The share's ends, once the units and items of all sequences are known.
+__device__ __forceinline__ bool share_ends(const AttnParams& p, int cta, int64_t W, int items, Share& s) {
+  s.units = W;
+  s.active = static_cast<int>(min(static_cast<int64_t>(p.ctas), max(W >> p.min_shift, static_cast<int64_t>(items))));
+  if (W == 0 || cta >= s.active) return false;
+  s.first = share_begin(W, s.active, cta);
+  s.end = share_begin(W, s.active, cta + 1);
+  return true;
+}
+// Items are counted up to what CTAs there can be.
+__device__ __forceinline__ int add_items(const AttnParams& p, int items, const Sequence& seq) {
+  return static_cast<int>(min(items + static_cast<int64_t>(seq.tiles) * p.c.heads, int64_t{1} << 16));
+}
+
+// Few sequences: every warp finds the share by itself, without a barrier.
+constexpr int kWarpSequences = 64;
+__device__ __forceinline__ bool find_share_warp(const AttnParams& p, int cta, Share& s) {
+  const int lane = threadIdx.x & 31, n = p.c.sequences;
+  int64_t u[kWarpSequences / 32], sum = 0;
+  int items = 0;
+#pragma unroll
+  for (int i = 0; i < kWarpSequences / 32; ++i) {
+    const int b = lane * (kWarpSequences / 32) + i;
+    u[i] = 0;
+    if (b < n) {
+      const Sequence seq = sequence_at(p, b);
+      u[i] = units_of(p, seq);
+      items = add_items(p, items, seq);
+    }
+    sum += u[i];
+  }
+  int64_t inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  items = __reduce_add_sync(0xFFFFFFFFu, items);
+  if (!share_ends(p, cta, __shfl_sync(0xFFFFFFFFu, inc, 31), items, s)) return false;
+  int64_t before = inc - sum;
+  const uint32_t here = __ballot_sync(0xFFFFFFFFu, s.first >= before && s.first < inc);
+  int b = lane * (kWarpSequences / 32);
+#pragma unroll
+  for (int i = 0; i < kWarpSequences / 32 - 1; ++i)
+    if (s.first >= before + u[i]) {
+      before += u[i];
+      ++b;
+    }
+  const int from = __ffs(here) - 1;
+  s.b = __shfl_sync(0xFFFFFFFFu, b, from & 31);
+  s.before = __shfl_sync(0xFFFFFFFFu, before, from & 31);
+  return here != 0;
+}
+
 // All threads of the CTA; kThreads of them.  `cta`: whose share.  False: none.
 template <int kThreads>
 __device__ __forceinline__ bool find_share(const AttnParams& p, int cta, Share& s) {
+  if (p.c.sequences <= kWarpSequences) return find_share_warp(p, cta, s);
   __shared__ int64_t warp_sum[kThreads / 32];
   __shared__ int warp_items[kThreads / 32];
   __shared__ int found_b;
@@ -115,11 +170,11 @@ __device__ __forceinline__ bool find_share(const AttnParams& p, int cta, Share& 
   const int per = (p.c.sequences + kThreads - 1) / kThreads;
   const int b0 = min(tid * per, p.c.sequences), b1 = min(b0 + per, p.c.sequences);
   int64_t sum = 0;
-  int items = 0;  // no more than there are CTAs are counted
+  int items = 0;
   for (int b = b0; b < b1; ++b) {
     const Sequence seq = sequence_at(p, b);
     sum += units_of(p, seq);
-    items = static_cast<int>(min(items + static_cast<int64_t>(seq.tiles) * p.c.heads, int64_t{1} << 16));
+    items = add_items(p, items, seq);
   }
   int64_t inc = sum;
 #pragma unroll
@@ -142,11 +197,7 @@ __device__ __forceinline__ bool find_share(const AttnParams& p, int cta, Share& 
     W += warp_sum[w];
     items += warp_items[w];
   }
-  s.units = W;
-  s.active = static_cast<int>(min(static_cast<int64_t>(p.ctas), max(W >> p.min_shift, static_cast<int64_t>(items))));
-  if (W == 0 || cta >= s.active) return false;
-  s.first = share_begin(W, s.active, cta);
-  s.end = share_begin(W, s.active, cta + 1);
+  if (!share_ends(p, cta, W, items, s)) return false;
   if (s.first >= before && s.first < before + sum) {
     int b = b0;
     for (; b < b1 - 1; ++b) {

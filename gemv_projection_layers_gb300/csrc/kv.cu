@@ -2,8 +2,7 @@
 // drafts to their places.
 //
 // Writing quantises: a row's largest magnitude, the scale and its reciprocal
-// (one division each a row, both rounded to nearest), a multiplication and a
-// rounding an entry.  Reading multiplies code by scale and rounds.  Moving
+// (rounded to nearest each), a multiplication and a rounding an entry.  Reading multiplies code by scale and rounds.  Moving
 // copies bytes.  All three are bound by the bytes they move, and by one chain
 // of dependent loads (offsets, start, table, entry) where there are few rows.
 //
@@ -68,10 +67,11 @@ __device__ __forceinline__ bool position_of(const RowsParams& p, int row, int la
   return true;
 }
 
-// kFormat: enum proj_kv_format.  A lane has eight entries of a head's row.
+// kFormat: enum proj_kv_format.  A lane has 16 entries of a head's row: what a row
+// costs beside its entries (scale, addresses) weighs half as much as with eight.
 template <typename T, int kFormat, int D>
 __global__ void __launch_bounds__(kThreads) kv_write_kernel(const RowsParams p) {
-  constexpr int L = D / 8;  // lanes of a row
+  constexpr int L = D / 16;  // lanes of a row
   const int lane = threadIdx.x & 31;
   const int64_t warp = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   griddep_launch_dependents();
@@ -83,46 +83,54 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const RowsParams p) 
   if (!page_of(p.c, sequence, position, id, spot)) return;
   const int items = 2 * p.c.heads, passes = (items * L + 31) / 32;
   const int part = static_cast<int>(warp - row * p.split);
+  const Entry first = entry_at(p.c, id, spot, 0);
+  const uint8_t* const k_row = p.k + row * p.ldk;
+  const uint8_t* const v_row = p.v + row * p.ldv;
 #pragma unroll 4
   for (int pass = part; pass < passes; pass += p.split) {
     const int item = pass * (32 / L) + lane / L;
     const bool real = item < items;
     const bool is_v = item >= p.c.heads;
     const int head = real ? item - (is_v ? p.c.heads : 0) : 0;
-    const uint8_t* from = (is_v ? p.v + row * p.ldv : p.k + row * p.ldk) +
-                          (static_cast<int64_t>(head) * D + (lane % L) * 8) * 2;
-    const Vec<T, 8> x = load_vec<T, 8>(reinterpret_cast<const T*>(from));
-    const Entry e = entry_at(p.c, id, spot, head);
-    uint8_t* to = (is_v ? p.c.v : p.c.k) + e.at;
+    const uint8_t* from = (is_v ? v_row : k_row) + (head * D + (lane % L) * 16) * 2;
+    const uint4 x = *reinterpret_cast<const uint4*>(from), y = *reinterpret_cast<const uint4*>(from + 16);
+    uint8_t* to = (is_v ? p.c.v : p.c.k) + first.at + head * p.c.head_stride;
     if constexpr (kFormat == PROJ_KV_ROWS) {
-      if (real) *reinterpret_cast<Vec<T, 8>*>(to + (lane % L) * 16) = x;
-    } else {
-      float f[8];
-      widen(x, f);
-      // a NaN anywhere makes the largest magnitude NaN
-      float top = 0.f;
-      bool odd = false;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        top = fmaxf(top, fabsf(f[i]));
-        odd |= !(fabsf(f[i]) < INFINITY);
-      }
-      if (odd) top = INFINITY;
-#pragma unroll
-      for (int o = L / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-      const bool finite = top < INFINITY;
-      constexpr float kTop = kFormat == PROJ_KV_E4M3 ? 448.f : 127.f;
-      const float scale = fmaxf(__fdiv_rn(top, kTop), 1.17549435e-38f);
-      const float inv = finite ? __frcp_rn(scale) : 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = finite ? __fmul_rn(f[i], inv) : 0.f;
-      uint2 code;
-      code.x = encode4<kFormat>(f[0], f[1], f[2], f[3]);
-      code.y = encode4<kFormat>(f[4], f[5], f[6], f[7]);
       if (real) {
-        *reinterpret_cast<uint2*>(to + (lane % L) * 8) = code;
+        *reinterpret_cast<uint4*>(to + (lane % L) * 32) = x;
+        *reinterpret_cast<uint4*>(to + (lane % L) * 32 + 16) = y;
+      }
+    } else {
+      // Magnitudes order as their bits, with infinities and NaN above the rest.
+      const uint32_t m = 0x7FFF7FFFu;
+      uint32_t top = __vmaxu2(__vmaxu2(__vmaxu2(x.x & m, x.y & m), __vmaxu2(x.z & m, x.w & m)),
+                              __vmaxu2(__vmaxu2(y.x & m, y.y & m), __vmaxu2(y.z & m, y.w & m)));
+#pragma unroll
+      for (int o = L / 2; o; o >>= 1) top = __vmaxu2(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+      float amax, other;
+      top = max(top & 0xFFFFu, top >> 16);
+      widen2(top, amax, other, T());
+      const bool finite = amax < INFINITY;
+      constexpr float kTop = kFormat == PROJ_KV_E4M3 ? 448.f : 127.f;
+      const float scale = fmaxf(__fdiv_rn(amax, kTop), 1.17549435e-38f);
+      const F2 inv = f2(finite ? __frcp_rn(scale) : 0.f);
+      const uint32_t word[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+      uint32_t code[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float f[4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          widen2(finite ? word[2 * i + j] : 0u, f[2 * j], f[2 * j + 1], T());
+          parts(mul2(f2(f[2 * j], f[2 * j + 1]), inv), f[2 * j], f[2 * j + 1]);
+        }
+        code[i] = encode4<kFormat>(f[0], f[1], f[2], f[3]);
+      }
+      if (real) {
+        *reinterpret_cast<uint4*>(to + (lane % L) * 16) = make_uint4(code[0], code[1], code[2], code[3]);
         if (lane % L == 0)
-          (is_v ? p.c.v_scale : p.c.k_scale)[e.scale] = finite ? scale : __uint_as_float(0x7FC00000u);
+          (is_v ? p.c.v_scale : p.c.k_scale)[first.scale + static_cast<int64_t>(head) * p.c.page.d] =
+              finite ? scale : __uint_as_float(0x7FC00000u);
       }
     }
   }
@@ -188,78 +196,93 @@ struct MoveParams {
   const int32_t* start;
   const int32_t* path;
   int64_t ldp;
-  int depth, words, scales;  // 16-byte words of an entry; 1: a scale as well
+  int depth, words, word_shift, scales;  // 16-byte words of an entry and their logarithm; 1: a scale as well
   int32_t* next;
 };
 
-// A thread has one 16-byte word (or the scale) of a sequence's entries of one
-// head of keys or values, and takes the path's entries in order, eight at a
-// time: their loads are all issued before the first store.  A target is not
-// behind its source, and later sources are behind that, so no store meets an
-// entry that is still to be read.
-__global__ void __launch_bounds__(kThreads) kv_move_kernel(const MoveParams p) {
-  const int per = p.words + p.scales;
-  const int64_t units = 2ll * p.c.heads * per;
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+// A CTA has 32 of the 16-byte words of a sequence's entries (scales behind them),
+// one a lane, and goes through the path in runs of 32: lanes check that it
+// ascends and find the places of an entry each, and the warps take the entries in
+// turn.  All loads of a run come before its first store: a target can be another
+// entry's source, of the same run or an earlier one, but not of a later one, whose
+// sources lie behind.  (Runs of 64 hold twice as much in registers; 256 paths of 32 x
+// 16 heads' rows then went in seven rounds of CTAs instead of four, 19.5 us.)
+constexpr int kRun = 32;
+
+__global__ void __launch_bounds__(kThreads, 5) kv_move_kernel(const MoveParams p) {
+  constexpr int kEach = kRun / kWarps;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int b = blockIdx.y;
+  const int words = 2 * p.c.heads * p.words;
+  int unit = blockIdx.x * 32 + lane;
+  const bool is_scale = unit >= words;
+  const bool mine = unit < words + 2 * p.c.heads * p.scales;
+  if (is_scale) unit -= words;
+  const int item = is_scale ? unit : unit >> p.word_shift, word = unit - (item << p.word_shift);
+  const bool is_v = item >= p.c.heads;
+  const int head = mine ? item - (is_v ? p.c.heads : 0) : 0;
+  uint8_t* const entries = (is_v ? p.c.v : p.c.k) + head * p.c.head_stride + word * 16;
+  float* const scales = (is_v ? p.c.v_scale : p.c.k_scale) + static_cast<int64_t>(head) * p.c.page.d;
   griddep_launch_dependents();
   griddep_wait();
-  if (unit >= units) return;
-  const int word = static_cast<int>(unit % per);
-  const int item = static_cast<int>(unit / per);
-  const bool is_v = item >= p.c.heads;
-  const int head = item - (is_v ? p.c.heads : 0);
-  const bool is_scale = word == p.words;
-  uint8_t* const entries = is_v ? p.c.v : p.c.k;
-  float* const scales = is_v ? p.c.v_scale : p.c.k_scale;
   const int start = p.start[b];
   const int32_t* path = p.path + b * p.ldp;
   int before = -1, n = 0;
-  constexpr int kBatch = 8;
   for (bool more = true; more && n < p.depth;) {
-    int id[kBatch], spot[kBatch], to_id[kBatch], to_spot[kBatch];
-    uint4 w[kBatch];
-    float f[kBatch];
-    bool moved[kBatch];
-    int step[kBatch];
+    // Entry `lane` of the run: both of its pages are asked for together.
+    const int step = n + lane < p.depth ? path[n + lane] : -1;
+    const int64_t at[2] = {static_cast<int64_t>(start) + step, static_cast<int64_t>(start) + n + lane};
+    // entries that stay where they are are not touched
+    bool ok = at[0] != at[1] && step >= 0;
+    int id[2], spot[2];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) step[i] = n + i < p.depth ? path[n + i] : -1;
-    int count = 0;
+    for (int x = 0; x < 2; ++x) {
+      ok = ok && at[x] >= 0 && at[x] < p.c.capacity;
+      const int position = ok ? static_cast<int>(at[x]) : 0;
+      const int slot = quotient(position, p.c.page);
+      spot[x] = position - slot * static_cast<int>(p.c.page.d);
+      id[x] = p.c.table[b * p.c.ldt + slot];
+    }
+    const int above = __shfl_up_sync(0xFFFFFFFFu, step, 1);
+    const uint32_t rises = __ballot_sync(0xFFFFFFFFu, step > (lane ? above : before));
+    const int length = __ffs(~rises) - 1;  // of the leading part that rises; -1: all do
+    const int count = length < 0 ? 32 : length;
+    more = count == 32;
+    before = __shfl_sync(0xFFFFFFFFu, step, 31);
+    Entry place[2];  // source, target
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      more = more && step[i] > before;
-      moved[i] = false;
-      if (more) {
-        before = step[i];
-        const int64_t from = static_cast<int64_t>(start) + step[i], to = static_cast<int64_t>(start) + n + i;
-        // entries that stay where they are are not touched
-        moved[i] = from != to && to >= 0 && from < p.c.capacity &&
-                   page_of(p.c, b, static_cast<int>(from), id[i], spot[i]) &&
-                   page_of(p.c, b, static_cast<int>(to), to_id[i], to_spot[i]);
-        ++count;
+    for (int x = 0; x < 2; ++x) {
+      ok = ok && id[x] >= 0 && id[x] < p.c.pages;
+      place[x] = entry_at(p.c, id[x], spot[x], 0);
+    }
+    const uint32_t good = __ballot_sync(0xFFFFFFFFu, ok && lane < count);
+    uint4 w[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int e = i * kWarps + warp;
+      if (!(good >> e & 1)) continue;  // the whole warp
+      const int64_t source = __shfl_sync(0xFFFFFFFFu, place[0].at, e);
+      if (mine && !is_scale) w[i] = *reinterpret_cast<const uint4*>(entries + source);
+      if (p.scales) {
+        const int64_t scale = __shfl_sync(0xFFFFFFFFu, place[0].scale, e);
+        if (mine && is_scale) w[i].x = __float_as_uint(scales[scale]);
       }
     }
+    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      if (!moved[i]) continue;
-      const Entry e = entry_at(p.c, id[i], spot[i], head);
-      if (is_scale)
-        f[i] = scales[e.scale];
-      else
-        w[i] = *reinterpret_cast<const uint4*>(entries + e.at + word * 16);
-    }
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      if (!moved[i]) continue;
-      const Entry e = entry_at(p.c, to_id[i], to_spot[i], head);
-      if (is_scale)
-        scales[e.scale] = f[i];
-      else
-        *reinterpret_cast<uint4*>(entries + e.at + word * 16) = w[i];
+    for (int i = 0; i < kEach; ++i) {
+      const int e = i * kWarps + warp;
+      if (!(good >> e & 1)) continue;
+      const int64_t target = __shfl_sync(0xFFFFFFFFu, place[1].at, e);
+      if (mine && !is_scale) *reinterpret_cast<uint4*>(entries + target) = w[i];
+      if (p.scales) {
+        const int64_t scale = __shfl_sync(0xFFFFFFFFu, place[1].scale, e);
+        if (mine && is_scale) scales[scale] = __uint_as_float(w[i].x);
+      }
     }
     n += count;
   }
-  if (unit == 0 && p.next) p.next[b] = start + n;
+  if (blockIdx.x == 0 && threadIdx.x == 0 && p.next) p.next[b] = start + n;
 }
 
 cudaLaunchConfig_t config(int64_t grid_x, int64_t grid_y, cudaStream_t s,
@@ -319,7 +342,7 @@ int rows_call(const char* call, bool write, const proj_kv_cache* cache, const in
   p.v = static_cast<uint8_t*>(const_cast<void*>(v));
   p.ldk = ldk * 2;
   p.ldv = ldv * 2;
-  const int lanes = static_cast<int>(c.D) / (write || c.format == PROJ_KV_ROWS ? 8 : 16);
+  const int lanes = static_cast<int>(c.D) / (!write && c.format == PROJ_KV_ROWS ? 8 : 16);
   const int64_t passes = (2 * c.heads * lanes + 31) / 32;
   // 4096 warps: some 27 an SM, enough to have the bytes in flight that HBM wants
   p.split = static_cast<int>(std::max<int64_t>(1, std::min(passes, 4096 / m)));
@@ -441,6 +464,7 @@ extern "C" int proj_kv_move(const proj_kv_cache* cache, const int32_t* start, co
   p.depth = static_cast<int>(depth);
   p.scales = c.format != PROJ_KV_ROWS;
   p.words = static_cast<int>(c.D) * (p.scales ? 1 : 2) / 16;
+  p.word_shift = p.words == 4 ? 2 : p.words == 8 ? 3 : 4;
   p.next = next_start;
   const int64_t units = 2 * c.heads * (p.words + p.scales);
   // grid y: sequences, of which 65535 are allowed there; the last one of 65536 goes alone
@@ -452,7 +476,7 @@ extern "C" int proj_kv_move(const proj_kv_cache* cache, const int32_t* start, co
     q.next = next_start ? next_start + at : nullptr;
     cudaLaunchAttribute attr[1];
     const cudaLaunchConfig_t cfg =
-        config((units + kThreads - 1) / kThreads, std::min<int64_t>(65535, c.sequences - at),
+        config((units + 31) / 32, std::min<int64_t>(65535, c.sequences - at),
                reinterpret_cast<cudaStream_t>(stream), attr);
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kv_move_kernel, q);
     if (e != cudaSuccess) return record_cuda(e, call);

@@ -19,8 +19,11 @@ __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) 
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
     return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
   } else {
-    const int x = __float2int_rn(a), y = __float2int_rn(b), z = __float2int_rn(c), w = __float2int_rn(d);
-    return (x & 255) | (y & 255) << 8 | (z & 255) << 16 | static_cast<uint32_t>(w) << 24;
+    // 1.5 2^23 leaves whole numbers in the low bits, rounded to nearest even
+    constexpr float kWhole = 12582912.f;
+    const uint32_t x = __float_as_uint(a + kWhole), y = __float_as_uint(b + kWhole);
+    const uint32_t z = __float_as_uint(c + kWhole), w = __float_as_uint(d + kWhole);
+    return __byte_perm(__byte_perm(x, y, 0x0040), __byte_perm(z, w, 0x0040), 0x5410);
   }
 }
 

@@ -70,7 +70,7 @@ __device__ __forceinline__ bool position_of(const RowsParams& p, int row, int la
 // kFormat: enum proj_kv_format.  A lane has 16 entries of a head's row: what a row
 // costs beside its entries (scale, addresses) weighs half as much as with eight.
 template <typename T, int kFormat, int D>
-__global__ void __launch_bounds__(kThreads) kv_write_kernel(const RowsParams p) {
+__global__ void __launch_bounds__(kThreads, 8) kv_write_kernel(const RowsParams p) {
   constexpr int L = D / 16;  // lanes of a row
   const int lane = threadIdx.x & 31;
   const int64_t warp = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const RowsParams p) 
   const Entry first = entry_at(p.c, id, spot, 0);
   const uint8_t* const k_row = p.k + row * p.ldk;
   const uint8_t* const v_row = p.v + row * p.ldv;
-#pragma unroll 4
+#pragma unroll 1
   for (int pass = part; pass < passes; pass += p.split) {
     const int item = pass * (32 / L) + lane / L;
     const bool real = item < items;
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const RowsParams p) 
 
 // A lane has 16 bytes of entries.
 template <typename T, int kFormat, int D>
-__global__ void __launch_bounds__(kThreads) kv_read_kernel(const RowsParams p) {
+__global__ void __launch_bounds__(kThreads, 8) kv_read_kernel(const RowsParams p) {
   constexpr int E = kFormat == PROJ_KV_ROWS ? 8 : 16;
   constexpr int L = D / E;
   const int lane = threadIdx.x & 31;
@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const RowsParams p) {
   if (!here) id = spot = 0;
   const int items = 2 * p.c.heads, passes = (items * L + 31) / 32;
   const int part = static_cast<int>(warp - row * p.split);
-#pragma unroll 4
+#pragma unroll 1
   for (int pass = part; pass < passes; pass += p.split) {
     const int item = pass * (32 / L) + lane / L;
     const bool is_v = item >= p.c.heads;

@@ -47,7 +47,10 @@ constexpr int kThreads = 32 * 20;
 // beside this much shared memory L1 does not hold what 640 threads spill.
 constexpr int kRegs = 96, kSoftRegs = 160, kLoadRegs = 48, kOtherRegs = 64;
 static_assert(2 * kSoftRegs + 2 * kLoadRegs + kOtherRegs <= 5 * kRegs && 5 * kRegs * 128 <= 65536, "registers");
-constexpr int kLoadThreads = 32 * kLoadWarps;
+// The loading warps are teams that take the tiles in turn: what one warp does for a
+// tile is a chain of waits, some two tiles' time long, whatever its share.
+template <int kFormat>
+constexpr int kTeams = kFormat == PROJ_KV_ROWS ? 4 : 2;
 constexpr int kKeys = kAttnTcUnit;
 constexpr int kTmemCols = 512;
 constexpr int kRaw = 4;       // tiles of 8-bit codes in shared memory or on their way there
@@ -359,6 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   using C = std::conditional_t<kCoded, __half, T>;
   constexpr bool kBf16 = std::is_same_v<C, __nv_bfloat16>;
   constexpr int NS = F::kStages;
+  constexpr int kTeam = kLoadWarps / kTeams<kFormat>;  // warps
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -376,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
-      mbar_init(full + 8 * s, kLoadWarps + 1);
+      mbar_init(full + 8 * s, kTeam + 1);
       mbar_init(empty + 8 * s, 1);
     }
     for (int g = 0; g < 2; ++g) {
@@ -388,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     mbar_init(q_full, kSoftWarps);
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(t_full + 8 * s, 1);
-      mbar_init(t_empty + 8 * s, kLoadWarps + 1);
+      mbar_init(t_empty + 8 * s, kTeam + 1);
     }
     for (int s = 0; s < kSegments; ++s) {
       mbar_init(g_full + 8 * s, 1);
@@ -499,13 +503,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         }
         __syncwarp();
         if (!more) {
-          // the end, for those that go by tiles
-          ok = ok && wait_bar(t_empty + 8 * slot, phase ^ 1u, p.status, kStatusTimeoutProducer);
-          if (lane == 0) {
-            s_tiles[slot].kind = 0;
-            mbar_arrive(t_full + 8 * slot);
-            p.splits[blockIdx.x] = split_of(p, share, blockIdx.x);
+          // the end, for each team that goes by tiles
+#pragma unroll 1
+          for (int i = 0; i < kTeams<kFormat>; ++i) {
+            ok = ok && wait_bar(t_empty + 8 * slot, phase ^ 1u, p.status, kStatusTimeoutProducer);
+            if (lane == 0) {
+              s_tiles[slot].kind = 0;
+              mbar_arrive(t_full + 8 * slot);
+            }
+            if (++slot == kSlots) {
+              slot = 0;
+              phase ^= 1u;
+            }
           }
+          if (lane == 0) p.splits[blockIdx.x] = split_of(p, share, blockIdx.x);
           break;
         }
         // Page ids come through shared memory, kIds - 1 tiles ahead; lanes have keys
@@ -648,20 +659,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   } else if (warp >= kLoadWarp) {
     // --------------------------------------------------------------- cache
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
-    const int tid = threadIdx.x - 32 * kLoadWarp;
+    constexpr int kLoadThreads = 32 * kTeam, TM = kTeams<kFormat>;
+    const int team = (warp - kLoadWarp) / kTeam, tid = threadIdx.x - 32 * (kLoadWarp + team * kTeam);
     constexpr int kRow = kCoded ? D : 2 * D, kPieces = kRow / 16, kTurn = kLoadThreads / kPieces;
     constexpr int kPasses = kKeys / kTurn;
     const int piece = tid % kPieces, key_of = tid / kPieces;
     const uint8_t* const from_k = p.c.k + piece * 16;
     const uint8_t* const from_v = p.c.v + piece * 16;
-    // Tiles on their way when one is handed over.  A tile is handed over before the
-    // next one is asked for: its stage may still be busy with a tile that waits for
-    // nothing but this one's turn.
-    constexpr int kLag = kCoded ? kRaw : NS - 1;
+    // Tiles of a team on their way when it hands one over.  A tile is handed over
+    // before the next one is asked for: its stage may still be busy with a tile that
+    // waits for nothing but this one's turn.
+    static_assert(kSlots % TM == 0 && NS % 2 == 0 && (!kCoded || kRaw % TM == 0), "a team's places");
+    constexpr int kLag = kCoded ? kRaw / TM : (NS - 1) / TM > 0 ? (NS - 1) / TM : 1;
     uint32_t kinds = 0;  // of the tiles issued: three bits each, the oldest lowest
     bool ok = true, open = true;
-    int stage = 0, slot = 0;
-    uint32_t phase = 0, t_phase = 0;
+    int stage = team % NS, slot = team;
+    uint32_t phase = team / NS, t_phase = 0;
     const auto place = [&](int key, int half, int chunk) {
       return half * F::kHalf + key * 128 + ((chunk ^ (key & 7)) << 4);
     };
@@ -669,8 +682,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(full + 8 * stage);
-      if (++stage == NS) {
-        stage = 0;
+      if ((stage += TM) >= NS) {
+        stage -= NS;
         phase ^= 1u;
       }
     };
@@ -692,14 +705,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       const uint32_t who = __ballot_sync(0xFFFFFFFFu, odd) >> (lane - piece) & ((1u << kPieces) - 1u);
       if (piece == 0) st_shared_byte(base + F::kSideAt + stage * F::kSide + F::kOdd + key, who ? 1u : 0u);
     };
-    static_assert(kTurn % 8 == 0, "a thread's rows have one place in the swizzle");
+    static_assert(!kCoded || kTurn % 8 == 0, "a thread's rows have one place in the swizzle");
     // 8-bit codes: the second half's lanes store their two chunks in the other
     // order, so the eight lanes of a key meet eight different banks
     const int swap = kCoded ? piece >> 2 & 1 : 0;
     const uint32_t put_a = place(key_of, piece >> 2, 2 * (piece & 3) + swap);
     const uint32_t put_b = place(key_of, piece >> 2, 2 * (piece & 3) + 1 - swap);
-    const uint32_t put_row = place(key_of, piece >> 3, piece & 7);
-    int in = 0;  // raw slot, or stage, of the tile that is issued
+    int in = team;  // raw slot, or stage, of the tile that is issued
     uint32_t in_phase = 0;
     const auto issue = [&] {
       int kind = 0;
@@ -711,25 +723,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       if (kind) {
         if constexpr (!kCoded)
           ok = ok && wait_bar(empty + 8 * in, in_phase ^ 1u, p.status, kStatusTimeoutProducer);
-        const uint32_t to = kCoded ? base + F::kRawAt + in * F::kRawTile + tid * 16 : base + in * F::kStage + put_row;
+        const uint32_t to = kCoded ? base + F::kRawAt + in * F::kRawTile + tid * 16 : base + in * F::kStage;
 #pragma unroll
         for (int j = 0; j < kPasses; ++j) {
           const int key = j * kTurn + key_of;
           const int64_t at = s_tiles[slot].at[key];
           const int64_t from = at >= 0 ? at : 0;
           const int bytes = at >= 0 ? 16 : 0;
-          const uint32_t dst = to + j * (kCoded ? kLoadThreads * 16 : kTurn * 128);
+          const uint32_t dst = to + (kCoded ? j * kLoadThreads * 16 : place(key, piece >> 3, piece & 7));
           copy16(dst, from_k + from, bytes);
           copy16(dst + (kCoded ? F::kRawTile / 2 : F::kOperand), from_v + from, bytes);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(t_empty + 8 * slot);
-        if (++slot == kSlots) {
-          slot = 0;
+        if ((slot += TM) >= kSlots) {
+          slot -= kSlots;
           t_phase ^= 1u;
         }
-        if (++in == (kCoded ? kRaw : NS)) {
-          in = 0;
+        if ((in += TM) >= (kCoded ? kRaw : NS)) {
+          in -= kCoded ? kRaw : NS;
           in_phase ^= 1u;
         }
       }
@@ -738,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     };
 #pragma unroll 1
     for (int i = 0; i < kLag; ++i) issue();
-    int raw = 0;
+    int raw = team;
 #pragma unroll 1
     for (;;) {
       const uint32_t kind = kinds & 7u;
@@ -760,7 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
           st_shared_u4(dst + put_b, decode_pair<kFormat>(b.x, 0), decode_pair<kFormat>(b.x, 1),
                        decode_pair<kFormat>(b.y, 0), decode_pair<kFormat>(b.y, 1));
         }
-        if (++raw == kRaw) raw = 0;
+        if ((raw += TM) >= kRaw) raw -= kRaw;
       }
       if (kFormat != PROJ_KV_INT8 && (kind & 2u)) {
 #pragma unroll 1

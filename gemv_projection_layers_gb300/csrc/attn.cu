@@ -139,6 +139,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_stream_kernel(const AttnPara
   float* const merge = reinterpret_cast<float*>(smem);
   float* const s_ml = reinterpret_cast<float*>(smem + F::kSmem - F::kMl);
 
+  touch(p);
   griddep_launch_dependents();
   griddep_wait();
   Share share;
@@ -643,6 +644,7 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(const AttnParams p)
   __shared__ Split s_split;
   __shared__ int s_count[kThreads / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  touch(p);
   griddep_launch_dependents();
   griddep_wait();
   // the item: the x-th that a CTA left

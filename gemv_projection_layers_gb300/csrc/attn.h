@@ -90,10 +90,19 @@ struct Share {
   int64_t before;  // units of the sequences before b
 };
 
-// a / b of numbers that are not negative: mostly both have 32 bits.
+// a / b of numbers that are not negative: mostly both have 32 bits, and the long
+// division stands out of the way.
+static __device__ __noinline__ int64_t divide_long(int64_t a, int64_t b) { return a / b; }
 __device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
-  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-  return a / b;
+  if (__builtin_expect(((a | b) >> 32) == 0, 1)) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return divide_long(a, b);
+}
+
+// Reads the parameters of a launch: before the dependency wait, so that what they
+// cost to come to the SM's constant cache passes beside the kernel before.
+__device__ __forceinline__ void touch(const AttnParams& p) {
+  asm volatile("" ::"l"(p.c.k), "l"(p.c.table), "r"(p.c.page.mul), "l"(p.q), "l"(p.start), "r"(p.words),
+               "l"(p.out), "r"(p.m), "r"(p.ctas), "l"(p.splits), "l"(p.part_ml));
 }
 __device__ __forceinline__ int64_t share_begin(int64_t W, int active, int cta) {
   const int64_t each = divide(W, active);

@@ -90,7 +90,7 @@ struct Tc {
   static constexpr int kSideAt = kRawAt + (kCoded ? kRaw * kRawTile : 0);
   static constexpr int kMl = kSideAt + kStages * kSide;  // float[2][128][3]
   static constexpr int kRawScaleAt = kMl + 3072;         // float[kRawScales][2][kKeys]
-  static constexpr int kSwapAt = kRawScaleAt + (kCoded ? kRawScales * 8 * kKeys : 0);  // float[2][2][16][64]
+  static constexpr int kSwapAt = kRawScaleAt + (kCoded ? kRawScales * 8 * kKeys : 0);  // float[2][2][16][64]: by group and giving half
   static constexpr int kIdsAt = kSwapAt + 16384;  // int[kIds][kKeys]
   static constexpr int kTiles = kIdsAt + kIds * kKeys * 4;
   static constexpr int kSegs = kTiles + kSlots * static_cast<int>(sizeof(Tile));
@@ -400,6 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     }
     fence_mbar_init();
   }
+  touch(p);
   // Tensor memory is taken when the kernel before has completed (it might hold
   // some), and the next one may start once it is taken here.
   griddep_wait();
@@ -1060,40 +1061,45 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         const bool whole = seg.whole;
         const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (seg.u0 == 0 ? 1 : 0);
         float* part = p.part_o + (slot * kAttnTcRows + row) * D;
-        const bool writes = real && busy && !(halves && quad >= 2);
-        constexpr int kCols = D / 2;  // each group writes half of the columns
+        // Each group writes half of the columns, and of those, where the lanes hold two
+        // halves of each row, each half a half: it gives the other its sums of the
+        // other's columns.
+        const bool writes = real && busy;
+        const int side = halves ? quad >> 1 : 0, width = halves ? D / 4 : D / 2;
+        const int first = group * (D / 2) + side * width, given = group * (D / 2) + (1 - side) * width;
+        const uint32_t swap = base + F::kSwapAt + group * 8192 + row * 4;
         const bool gated = writes && whole && p.gate;
         const T* const gates = reinterpret_cast<const T*>(p.gate + static_cast<int64_t>(seg.lo + token) * p.ldg) + head * D;
-        Vec<T, 8> gate[2];
-        if (gated) {
-          gate[0] = load_vec<T, 8>(gates + group * kCols);
-          gate[1] = load_vec<T, 8>(gates + group * kCols + 8);
-        }
+        const auto sums = [&](int c, float (&o)[16]) {
+          float o1[16];
+          tmem_ld16(tmem + lanes + F::kO + c, o);
+          if (tiles > 1) tmem_ld16(tmem + lanes + F::kO + D + c, o1);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) o[j] = tiles > 1 ? o[j] * a0 + o1[j] * a1 : o[j] * a0;
+        };
 #pragma unroll 1
-        for (int c = group * kCols; c < (group + 1) * kCols; c += 16) {
-          const Vec<T, 8> now[2] = {gate[0], gate[1]};
-          if (gated && c + 16 < (group + 1) * kCols) {
-            gate[0] = load_vec<T, 8>(gates + c + 16);
-            gate[1] = load_vec<T, 8>(gates + c + 24);
+        for (int x = 0; x < width; x += 16) {
+          const int c = first + x;
+          Vec<T, 8> gate[2];
+          if (gated) {
+            gate[0] = load_vec<T, 8>(gates + c);
+            gate[1] = load_vec<T, 8>(gates + c + 8);
           }
-          float o[16], o1[16];
-          if (busy) {
-            tmem_ld16(tmem + lanes + F::kO + c, o);
-            if (tiles > 1) tmem_ld16(tmem + lanes + F::kO + D + c, o1);
-            tmem_ld_wait();
-#pragma unroll
-            for (int j = 0; j < 16; ++j) o[j] = tiles > 1 ? o[j] * a0 + o1[j] * a1 : o[j] * a0;
-          }
+          float o[16];
           if (halves) {
-            const uint32_t swap = base + F::kSwapAt + group * 8192 + (c >> 4 & 1) * 4096 + row * 4;
-            if (quad >= 2) {
+            if (busy) {
+              sums(given + x, o);
 #pragma unroll
-              for (int j = 0; j < 16; ++j) st_shared_f(swap + j * 256, o[j]);
+              for (int j = 0; j < 16; ++j) st_shared_f(swap + side * 4096 + j * 256, o[j]);
             }
             named_bar_sync(3 + group, 128);
-            if (quad < 2) {
+          }
+          if (busy) {
+            sums(c, o);
+            if (halves) {
 #pragma unroll
-              for (int j = 0; j < 16; ++j) o[j] += ld_shared_f(swap + j * 256);
+              for (int j = 0; j < 16; ++j) o[j] += ld_shared_f(swap + (1 - side) * 4096 + j * 256);
             }
           }
           if (__builtin_expect(any_odd && writes, 0)) {
@@ -1105,15 +1111,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             for (int j = 0; j < 16; ++j) o[j] = with[j];
           }
           if (writes && whole) {
-            write_out<T>(p, static_cast<int64_t>(seg.lo + token), head * D + c, o, all, now);
+            write_out<T>(p, static_cast<int64_t>(seg.lo + token), head * D + c, o, all, gate);
           } else if (writes) {
 #pragma unroll
             for (int j = 0; j < 16; j += 4)
               *reinterpret_cast<float4*>(part + c + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
           }
+          // what was given has been read
+          if (halves && x + 16 < width) named_bar_sync(3 + group, 128);
           __syncwarp();
         }
-        if (writes && group == 0) {
+        if (writes && group == 0 && side == 0) {
           if (whole) {
             if (p.lse) p.lse[static_cast<int64_t>(seg.lo + token) * p.heads + head] = lse_of(top, all);
           } else {

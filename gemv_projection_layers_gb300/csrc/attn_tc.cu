@@ -798,11 +798,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     for (int n = 0;; ++n) {
       const int slot_of = n % kSegments;
       ok = ok && wait_bar(g_full + 8 * slot_of, n / kSegments & 1u, p.status, kStatusTimeoutEpilogue);
-      const Segment seg = s_segs[slot_of];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(g_empty + 8 * slot_of);
-      if (seg.tiles == 0) break;
+      // A wait that gave up ends the loop for all: they meet at barriers below.
+      if (named_bar_sync_or(5, 32 * kSoftWarps, !ok)) break;
+      // (stays in shared memory until its end: registers are short)
+      const Segment& seg = s_segs[slot_of];
       const int tiles = seg.tiles;
+      if (tiles == 0) break;
+      const int before_drafts = seg.start - seg.u0 * kKeys;  // keys of the segment
       // Up to 64 rows: both halves of the lanes hold them, the MMAs make their scores
       // twice at no cost, and each half takes 32 of a tile's 64 keys (of the other
       // 32 its probabilities are zero): half the softmax for a warp.
@@ -892,13 +894,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         tc_fence_after();
         if (busy) {
           // what stands beside the stage
-          const int key0 = (seg.u0 + i) * kKeys;
+          const int draft = i * kKeys - before_drafts;  // of the first key
           uint64_t seen = ~uint64_t{0};
           ok = ok && wait_bar(full + 8 * stage, phase, p.status, kStatusTimeoutEpilogue);
           const uint2 valid = ld_shared_u2(side + F::kValid);
-          const bool partial = (valid.x & valid.y) != 0xFFFFFFFFu || key0 + kKeys > seg.start;
+          const bool partial = (valid.x & valid.y) != 0xFFFFFFFFu || draft + kKeys > 0;
           if (__builtin_expect(partial, 0))
-            seen = seen_here<kFormat>(p, seg.lo, token, key0 - seg.start, valid, side + F::kOddScale, side + F::kOdd, odd);
+            seen = seen_here<kFormat>(p, seg.lo, token, draft, valid, side + F::kOddScale, side + F::kOdd, odd);
           float down = 1.f, tile_sum = 0.f;
           if constexpr (kCoded) {
             const float now = ld_shared_f(side + F::kRef);
@@ -1133,6 +1135,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       // both groups are done with the item's Q, O and sums
       named_bar_sync(1, 32 * kSoftWarps);
       tc_fence_after();
+      if (lane == 0) mbar_arrive(g_empty + 8 * slot_of);
     }
   }
   tc_fence_before();

@@ -160,10 +160,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_stream_kernel(const AttnPara
       seq = sequence_at(p, b);
     }
     const int64_t local = at - before;
-    const int64_t item = divide(local, seq.units);
+    const int64_t item = item_of(local, seq.units);
     const int u0 = static_cast<int>(local - item * seq.units);
     const int u1 = static_cast<int>(min(static_cast<int64_t>(seq.units), u0 + (share.end - at)));
-    const int head = static_cast<int>(divide(item, seq.tiles));
+    const int head = static_cast<int>(item_of(item, seq.tiles));
     const int row0 = static_cast<int>(item - static_cast<int64_t>(head) * seq.tiles) * F::kRows;
     const int all_rows = seq.rows * G;
 

@@ -4,13 +4,13 @@
 // Work is cut on the device, by the lengths that the call has: an item is a
 // sequence, a head of keys and values, and `tile_rows` of its rows (a row is a
 // drafted token and a query head of the group; row r is token r / group, head
-// r % group); it has ceil(keys / unit) units.  The items' units stand in one
-// line, and CTA c of the `active` takes units [c W / active, (c + 1) W /
-// active) of the W; there are as many as have min_units units, and no fewer than
-// items.  So every SM has the same share whatever the lengths, a CTA
-// leaves at most two items unfinished (one it did not begin, one it does not
-// end), and the partial results need room for two items a CTA and nothing that
-// grows with the batch.  A second kernel joins them in the order of their CTAs.
+// r % group); it has ceil(keys / unit) units.  The items' units stand in one line
+// of W, and CTA c takes `each` of them from c `each` on: as many as spread the line
+// over all CTAs, but 2^min_shift at least, unless there are items for more CTAs.  So
+// every SM has the same share whatever the lengths, a CTA leaves at most two items
+// unfinished (one it did not begin, one it does not end), and the partial results
+// need room for two items a CTA and nothing that grows with the batch.  A second
+// kernel joins them in the order of their CTAs.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -84,8 +84,7 @@ struct alignas(32) Split {
 
 // This CTA's share.
 struct Share {
-  int64_t units, first, end;  // W, and this CTA's range
-  int active;
+  int64_t each, first, end;  // units of a CTA, and this one's range
   int b;           // the sequence that holds `first`
   int64_t before;  // units of the sequences before b
 };
@@ -98,29 +97,23 @@ __device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
   return divide_long(a, b);
 }
 
+// The same where the quotient is often 0.
+__device__ __forceinline__ int64_t item_of(int64_t a, int64_t b) { return a < b ? 0 : divide(a, b); }
+
 // Reads the parameters of a launch: before the dependency wait, so that what they
 // cost to come to the SM's constant cache passes beside the kernel before.
 __device__ __forceinline__ void touch(const AttnParams& p) {
   asm volatile("" ::"l"(p.c.k), "l"(p.c.table), "r"(p.c.page.mul), "l"(p.q), "l"(p.start), "r"(p.words),
                "l"(p.out), "r"(p.m), "r"(p.ctas), "l"(p.splits), "l"(p.part_ml));
 }
-__device__ __forceinline__ int64_t share_begin(int64_t W, int active, int cta) {
-  const int64_t each = divide(W, active);
-  return each * cta + divide((W - each * active) * cta, active);
-}
-// The CTA that holds unit x.
-__device__ __forceinline__ int share_owner(int64_t W, int active, int64_t x) {
-  return static_cast<int>(divide((x + 1) * active - 1, W));
-}
-
 // The share's ends, once the units and items of all sequences are known.
 __device__ __forceinline__ bool share_ends(const AttnParams& p, int cta, int64_t W, int items, Share& s) {
-  s.units = W;
-  s.active = static_cast<int>(min(static_cast<int64_t>(p.ctas), max(W >> p.min_shift, static_cast<int64_t>(items))));
-  if (W == 0 || cta >= s.active) return false;
-  s.first = share_begin(W, s.active, cta);
-  s.end = share_begin(W, s.active, cta + 1);
-  return true;
+  const int64_t ctas = min(static_cast<int64_t>(p.ctas), max(W >> p.min_shift, static_cast<int64_t>(items)));
+  if (W == 0) return false;
+  s.each = divide(W + ctas - 1, ctas);
+  s.first = s.each * cta;
+  s.end = min(W, s.first + s.each);
+  return s.first < W;
 }
 // Items are counted up to what CTAs there can be.
 __device__ __forceinline__ int add_items(const AttnParams& p, int items, const Sequence& seq) {
@@ -165,6 +158,43 @@ __device__ __forceinline__ bool find_share_warp(const AttnParams& p, int cta, Sh
   s.b = __shfl_sync(0xFFFFFFFFu, b, from & 31);
   s.before = __shfl_sync(0xFFFFFFFFu, before, from & 31);
   return here != 0;
+}
+
+// The same for one warp and any number of sequences: a run of them a lane.
+__device__ __forceinline__ bool find_share_walk(const AttnParams& p, int cta, Share& s) {
+  if (p.c.sequences <= kWarpSequences) return find_share_warp(p, cta, s);
+  const int lane = threadIdx.x & 31;
+  const int per = (p.c.sequences + 31) / 32;
+  const int b0 = min(lane * per, p.c.sequences), b1 = min(b0 + per, p.c.sequences);
+  int64_t sum = 0;
+  int items = 0;
+  for (int b = b0; b < b1; ++b) {
+    const Sequence seq = sequence_at(p, b);
+    sum += units_of(p, seq);
+    items = add_items(p, items, seq);
+  }
+  int64_t inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  items = __reduce_add_sync(0xFFFFFFFFu, min(items, 1 << 16));
+  if (!share_ends(p, cta, __shfl_sync(0xFFFFFFFFu, inc, 31), items, s)) return false;
+  int64_t before = inc - sum;
+  const bool here = s.first >= before && s.first < inc;
+  int b = b0;
+  if (here) {
+    for (; b < b1 - 1; ++b) {
+      const int64_t u = units_of(p, sequence_at(p, b));
+      if (s.first < before + u) break;
+      before += u;
+    }
+  }
+  const uint32_t who = __ballot_sync(0xFFFFFFFFu, here);
+  s.b = __shfl_sync(0xFFFFFFFFu, b, (__ffs(who) - 1) & 31);
+  s.before = __shfl_sync(0xFFFFFFFFu, before, (__ffs(who) - 1) & 31);
+  return who != 0;
 }
 
 // All threads of the CTA; kThreads of them.  `cta`: whose share.  False: none.
@@ -226,14 +256,14 @@ __device__ __forceinline__ bool find_share(const AttnParams& p, int cta, Share& 
 __device__ __forceinline__ Split split_of(const AttnParams& p, const Share& s, int cta) {
   Split r = {};
   const Sequence seq = sequence_at(p, s.b);
-  const int64_t item = divide(s.first - s.before, seq.units);
+  const int64_t item = item_of(s.first - s.before, seq.units);
   const int64_t begin = s.before + item * seq.units;
   if (begin == s.first) return r;
-  r.first = share_owner(s.units, s.active, begin);
+  r.first = static_cast<int>(divide(begin, s.each));
   if (cta != r.first + 1) return r;
-  r.last = share_owner(s.units, s.active, begin + seq.units - 1);
+  r.last = static_cast<int>(divide(begin + seq.units - 1, s.each));
   r.lo = seq.lo;
-  r.head = static_cast<int>(divide(item, seq.tiles));
+  r.head = static_cast<int>(item_of(item, seq.tiles));
   r.row0 = static_cast<int>(item - static_cast<int64_t>(r.head) * seq.tiles) * p.tile_rows;
   r.rows = min(p.tile_rows, seq.rows * static_cast<int>(p.group.d) - r.row0);
   return r;

@@ -270,10 +270,10 @@ struct Walk {
       seq = sequence_at(p, share.b);
     }
     const int64_t local = at - share.before;
-    const int64_t item = divide(local, seq.units);
+    const int64_t item = item_of(local, seq.units);
     u0 = static_cast<int>(local - item * seq.units);
     u1 = static_cast<int>(min(static_cast<int64_t>(seq.units), u0 + (share.end - at)));
-    head = static_cast<int>(divide(item, seq.tiles));
+    head = static_cast<int>(item_of(item, seq.tiles));
     row0 = static_cast<int>(item - static_cast<int64_t>(head) * seq.tiles) * kAttnTcRows;
     rows = min(kAttnTcRows, seq.rows * static_cast<int>(p.group.d) - row0);
     at += u1 - u0;
@@ -414,13 +414,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   const uint32_t tmem = *tmem_slot;
   griddep_launch_dependents();
 
-  Share share;
-  const bool mine = find_share<kThreads>(p, blockIdx.x, share);
-
-  if (!mine) {
-    // nothing to do but to give the tensor memory back
-    if (threadIdx.x == 0) p.splits[blockIdx.x] = Split{};
-  } else if (warp >= kMmaWarp) {
+  // Only the walking warp looks for the CTA's share; the others learn of it from
+  // the segments and tiles that it names.
+  if (warp >= kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kMmaWarp || warp == kPvWarp) {
       // --------------------------------------------------------------- MMA
@@ -479,27 +475,31 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       }
     } else if (warp == kWalkWarp) {
       // ---------------------------------------------------- the CTA's share
+      Share share;
+      const bool mine = find_share_walk(p, blockIdx.x, share);
       Walk walk;
-      walk.begin(p, share);
+      if (mine) walk.begin(p, share);
       bool ok = true;
       int slot = 0;
       uint32_t phase = 0;
       for (int n = 0;; ++n) {
-        const bool more = ok && walk.next(p);
+        const bool more = ok && mine && walk.next(p);
         const int seg = n % kSegments;
         ok = ok && wait_bar(g_empty + 8 * seg, (n / kSegments & 1u) ^ 1u, p.status, kStatusTimeoutProducer);
         if (lane == 0) {
           Segment& s = s_segs[seg];
           s.tiles = more ? walk.u1 - walk.u0 : 0;
-          s.b = walk.share.b;
-          s.lo = walk.seq.lo;
-          s.start = walk.seq.start;
-          s.len = walk.seq.len;
-          s.head = walk.head;
-          s.row0 = walk.row0;
-          s.rows = walk.rows;
-          s.u0 = walk.u0;
-          s.whole = walk.u0 == 0 && walk.u1 == walk.seq.units;
+          if (more) {
+            s.b = walk.share.b;
+            s.lo = walk.seq.lo;
+            s.start = walk.seq.start;
+            s.len = walk.seq.len;
+            s.head = walk.head;
+            s.row0 = walk.row0;
+            s.rows = walk.rows;
+            s.u0 = walk.u0;
+            s.whole = walk.u0 == 0 && walk.u1 == walk.seq.units;
+          }
           mbar_arrive(g_full + 8 * seg);
         }
         __syncwarp();
@@ -517,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
               phase ^= 1u;
             }
           }
-          if (lane == 0) p.splits[blockIdx.x] = split_of(p, share, blockIdx.x);
+          if (lane == 0) p.splits[blockIdx.x] = mine ? split_of(p, share, blockIdx.x) : Split{};
           break;
         }
         // Page ids come through shared memory, kIds - 1 tiles ahead; lanes have keys
@@ -837,32 +837,35 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       F2 up = f2(1.f);
       if constexpr (kNarrow) {
         // bf16 to fp16: the row's largest magnitude is brought to 2^14 .. 2^15
-        uint32_t most = 0;
+        uint32_t pairs = 0;
         const uint32_t room = base + F::kMl + lane_row * 4;
         if (busy) {
 #pragma unroll
-          for (int i = 0; i < D / 4; ++i) most = max(max(most, q[i] & 0x7FFFu), q[i] >> 16 & 0x7FFFu);
-          st_shared_u(room + group * 512, most);
+          for (int i = 0; i < D / 4; ++i) pairs = __vmaxu2(pairs, q[i] & 0x7FFF7FFFu);
+          st_shared_u(room + group * 512, pairs);
         }
         named_bar_sync(1, 32 * kSoftWarps);
-        if (busy) most = max(most, ld_shared_u(room + (1 - group) * 512));
+        if (busy) pairs = __vmaxu2(pairs, ld_shared_u(room + (1 - group) * 512));
+        const uint32_t most = max(pairs & 0xFFFFu, pairs >> 16);
         int e = 0;
         if (most > 0 && most < 0x7F80u) e = min(126, 14 - ilogbf(__uint_as_float(most << 16)));
-        up = f2(scalbnf(1.f, e));
+        const float s = scalbnf(1.f, e);
+        up = f2(p.scale_log2 > 0.f ? s : p.scale_log2 < 0.f ? -s : 0.f);
         f = scalbnf(1.f, -e);
       }
       if (busy) {
-        const uint32_t keep = p.scale_log2 == 0.f || !real ? 0u : 0xFFFFFFFFu;
-        const uint32_t turned = p.scale_log2 < 0.f ? 0x80008000u : 0u;
+        if constexpr (kNarrow) {
 #pragma unroll
-        for (int i = 0; i < D / 4; ++i) {
-          if constexpr (kNarrow) {
+          for (int i = 0; i < D / 4; ++i) {
             float x, y;
             widen2(q[i], x, y, __nv_bfloat16());
             parts(mul2(f2(x, y), up), x, y);
             q[i] = pack2(x, y, __half());
           }
-          q[i] = (q[i] & keep) ^ turned;
+        } else if (p.scale_log2 <= 0.f) {
+          const uint32_t keep = p.scale_log2 == 0.f ? 0u : 0xFFFFFFFFu;
+#pragma unroll
+          for (int i = 0; i < D / 4; ++i) q[i] = (q[i] ^ 0x80008000u) & keep;
         }
 #pragma unroll
         for (int i = 0; i < D / 64; ++i)
@@ -1089,20 +1092,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             gate[1] = load_vec<T, 8>(gates + c + 8);
           }
           float o[16];
-          if (halves) {
-            if (busy) {
-              sums(given + x, o);
+#pragma unroll 1
+          for (int own = halves ? 0 : 1; own < 2; ++own) {
+            if (busy) sums(own ? c : given + x, o);
+            if (!own) {
+              if (busy) {
 #pragma unroll
-              for (int j = 0; j < 16; ++j) st_shared_f(swap + side * 4096 + j * 256, o[j]);
+                for (int j = 0; j < 16; ++j) st_shared_f(swap + side * 4096 + j * 256, o[j]);
+              }
+              named_bar_sync(3 + group, 128);
             }
-            named_bar_sync(3 + group, 128);
           }
-          if (busy) {
-            sums(c, o);
-            if (halves) {
+          if (halves && busy) {
 #pragma unroll
-              for (int j = 0; j < 16; ++j) o[j] += ld_shared_f(swap + (1 - side) * 4096 + j * 256);
-            }
+            for (int j = 0; j < 16; ++j) o[j] += ld_shared_f(swap + (1 - side) * 4096 + j * 256);
           }
           if (__builtin_expect(any_odd && writes, 0)) {
             float with[16];

@@ -40,7 +40,7 @@ struct AttnParams {
   float* lse;
   int m, heads, D;
   Divisor group;
-  int tile_rows, unit, ctas;
+  int tile_rows, unit, ctas, spread;
   int tile_shift, unit_shift, min_shift;  // logarithms; min_shift: of a share's least units
   struct Split* splits;  // [ctas]
   float* part_o;   // [2 ctas][tile_rows][D]: sums relative to 2^m

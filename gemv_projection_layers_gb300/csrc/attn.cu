@@ -1,14 +1,18 @@
 // attn.cu -- attention of drafted tokens over the cache: the calls, the kernel
 // for few rows, and the join of partial results.
 //
-// The kernel for few rows (a group's heads times a sequence's drafts up to 32)
-// is a stream over the cache.  Per key and head it reads 2 D entries and does
+// The kernel for few rows (a group's heads times a sequence's drafts up to 32, in
+// items of 8 or 16) is a stream over the cache.  Per key and head it reads 2 D entries and does
 // 4 D operations a row, so with 8 rows and 8-bit entries the cache's bytes at
 // HBM's rate leave the tensor cores of the warp-level MMA a fifth of their
 // time; what counts is that the bytes flow.  Each of a CTA's eight warps has
 // a ring of its own in shared memory, filled by 16-byte asynchronous copies,
-// and takes every eighth 16 keys of the CTA's share: nothing but the end of an
-// item is a barrier for the CTA.
+// and takes every eighth step of the CTA's share, 32 keys (16 of 16-bit entries and
+// 128 dimensions): nothing but the end of an item is a barrier for the CTA.  From
+// 16384 to 65536 keys of 16 sequences a call's time grows as the bytes at HBM's
+// measured rate do (e4m3 20 us a 20 us, 16-bit 38 a 39); below, it is the chain
+// of a call that shows: lengths, pages, first bytes, the warps' and the CTAs' sums
+// (9 us for one sequence of 8192 keys, of which the join is some 3).
 //
 // Keys are the M side of both products, rows the N side (eight at a time, so
 // nothing is padded to 16):
@@ -765,7 +769,17 @@ struct Plan {
   int64_t bytes;
 };
 
-// Rows of an item by the rows that a sequence has on average.
+// Which kernel, and rows of an item, by the rows that a sequence and a head of keys
+// and values have on average (lengths are known on the device only).  Up to 8 and
+// 16 the streaming kernel; up to 32 it too, in two items that read the cache once
+// from HBM and once from L2; beyond, tcgen05.  16 sequences of up to 32768 keys of 128
+// (8192 in brackets), eight heads on one, streamed against tcgen05, us:
+//   16 rows  e4m3 32 (22), 54 (30)    16-bit 39 (20), 45 (26)
+//   32 rows  e4m3 43 (24), 55 (31)    16-bit 50 (22), 46 (27)
+//   64 rows  e4m3 112, 60             (in two items of 32 rows)
+// A share has at least 256 keys either way: a step for each of the streaming
+// kernel's warps (one sequence of 8192 keys: 9.0 us; with 128 keys 9.4, with 512
+// 9.2), four tiles of the tcgen05 kernel (2: the same or 0.3 us slower, 8: 1-3).
 const char* make_plan(const proj_kv_cache* cache, int64_t m, int64_t heads, Plan* plan,
                       int* status) {
   if (const char* why = refuse_cache(cache, status)) return why;
@@ -780,7 +794,7 @@ const char* make_plan(const proj_kv_cache* cache, int64_t m, int64_t heads, Plan
                            ? (m + cache->sequences - 1) / cache->sequences * (heads / cache->heads)
                            : 1;
   plan->rows = rows;
-  plan->tc = rows > 16;
+  plan->tc = rows > 32;
   plan->unit = plan->tc ? kAttnTcUnit : kUnit;
   plan->tile_rows = plan->tc ? kAttnTcRows : rows <= 8 ? 8 : 16;
   plan->min_units = plan->tc ? 4 : kWarps;

@@ -9,24 +9,35 @@
 // rows of 128 bytes in the 128-byte swizzle: K-major for the first product,
 // N-major for the second, so V needs no transposition.
 //
-// Roles (19 warps): 0-3 and 4-7 are two softmax groups, a thread a row, which
+// Roles (20 warps): 0-3 and 4-7 are two softmax groups, a thread a row, which
 // take the tiles in turn and have an S, a P and an O each -- so one group's
 // exponentials run beside the other's products, and neither waits for the
 // other's sums; they meet at the item's end.  8-15 bring the cache by 16-byte
-// asynchronous copies: 16-bit entries to their stage, 8-bit codes to a ring of
-// their own, from where the thread that copied them takes them to their stage
-// as fp16, which holds them exactly.  16 issues the MMAs.  17 walks the CTA's
-// share: it looks up pages, and hands each tile's addresses to the loading warps
-// and each segment to the others, so that no other warp divides or waits for a
-// table.  18 brings the scales.
-// The loops are short on purpose: five roles share a scheduler's instruction
-// cache, and with loops unrolled over several tiles two thirds of the cycles
-// went to waiting for instructions.
+// asynchronous copies, in teams that take the tiles in turn: 16-bit entries to their
+// stage, 8-bit codes to a ring of their own, from where the thread that copied them
+// takes them to their stage as fp16, which holds them exactly.  16 and 19 issue the
+// MMAs.  17 walks the CTA's share: it looks up pages, and hands each tile's addresses
+// to the loading warps and each segment to the others, so that no other warp divides
+// or waits for a table.  18 brings the scales.
 //
 // Softmax as in the streaming kernel: a reference per row that moves only when
 // a score is well above it, whereupon O is scaled in tensor memory;
-// probabilities are fp16 (bf16 caches: bf16).  Scales of K multiply the fp32 score; those of V the probability,
-// relative to a power-of-two reference that the loading warps keep.
+// probabilities are fp16 (bf16 caches: bf16).  Scales of K multiply the fp32
+// score; those of V the probability, relative to a power-of-two reference that
+// warp 18 keeps.
+//
+// What bounds it is none of the units (issue slots 45 % used, tensor pipe 15 %,
+// HBM a fifth to two thirds) but how long a tile's chain of hand-offs takes a warp:
+// some 3100 cycles in a softmax group, half of that a tile with two groups, where
+// HBM would deliver 64 keys of e4m3 in 700.  32 sequences of 8 drafts, 64 heads on
+// 8, 16-bit: 140 us (4.9 TB/s); 16 of 8 drafts over up to 32768 keys, 8 heads on 1,
+// e4m3: 59 us, of which some 25 are a call's ends (share, pages, queries, sums and
+// their join); 32 of up to 64 drafts: 141 us (0.36 PFLOP/s).  What the steps there
+// were worth: short loops (five roles share a scheduler's instruction cache; with
+// loops unrolled over tiles two thirds of the cycles went to waiting for
+// instructions) 103 -> 74 us in the second case, no spills in any loop 82 -> 65,
+// teams of loading warps 191 -> 157 in the first, lane halves that share the item's
+// end 157 -> 141, the join's CTAs 62 -> 59 in the second.
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -53,11 +64,11 @@ template <int kFormat>
 constexpr int kTeams = kFormat == PROJ_KV_ROWS ? 4 : 2;
 constexpr int kKeys = kAttnTcUnit;
 constexpr int kTmemCols = 512;
-constexpr int kRaw = 4;       // tiles of 8-bit codes in shared memory or on their way there
-constexpr int kRawScales = 4;
-constexpr int kIds = 4;  // tiles whose page ids are known or on their way
-constexpr int kSlots = 8;     // tiles whose addresses are known
-constexpr int kSegments = 4;  // segments that are known
+constexpr int kRaw = 4;        // tiles of 8-bit codes in shared memory or on their way there
+constexpr int kRawScales = 4;  // of scales
+constexpr int kIds = 4;        // of page ids
+constexpr int kSlots = 8;      // tiles whose addresses are known
+constexpr int kSegments = 4;   // segments that are known
 
 // What the walking warp says of a tile.
 struct alignas(16) Tile {
@@ -74,6 +85,10 @@ struct alignas(16) Segment {
   int pad[2];
 };
 
+// Beside a stage: scales of K and V, the reference of V's, keys that exist; of
+// drafts: keys whose scale of V, and keys of which a value is no finite number.
+constexpr int kSide = 640, kVScale = 256, kRef = 512, kValid = 520, kOddScale = 528, kOdd = 576;
+
 template <int kFormat, int D>
 struct Tc {
   static constexpr int kHalves = D / 64;            // of 64 dimensions
@@ -83,9 +98,6 @@ struct Tc {
   static constexpr bool kCoded = kFormat != PROJ_KV_ROWS;
   static constexpr int kStages = kCoded ? (D == 128 ? 4 : 6) : (D == 128 ? 6 : 8);
   static constexpr int kRawTile = 2 * kKeys * D;  // codes of K and V
-  // beside a stage: scales of K and V, the reference of V's, keys that exist; of
-  // drafts: keys whose scale of V, and keys of which a value is no finite number
-  static constexpr int kSide = 640, kVScale = 256, kRef = 512, kValid = 520, kOddScale = 528, kOdd = 576;
   static constexpr int kRawAt = kStages * kStage;
   static constexpr int kSideAt = kRawAt + (kCoded ? kRaw * kRawTile : 0);
   static constexpr int kMl = kSideAt + kStages * kSide;  // float[2][128][3]
@@ -612,8 +624,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         const int kind = tile.kind;
         if (kind == 0) break;
         ok = ok && wait_bar(empty + 8 * stage, phase ^ 1u, p.status, kStatusTimeoutProducer);
-        const uint32_t side = base + F::kSideAt + stage * F::kSide;
-        if (lane < 2) st_shared_u(side + F::kValid + 4 * lane, tile.valid[lane]);
+        const uint32_t side = base + F::kSideAt + stage * kSide;
+        if (lane < 2) st_shared_u(side + kValid + 4 * lane, tile.valid[lane]);
         if constexpr (kCoded) {
           const uint32_t at = raw + from_slot % kRawScales * (8 * kKeys);
           if (kind & 4) ref = 0.f;
@@ -629,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             if (!fine) w[j] = kind & 2 ? 0.f : __uint_as_float(0x7FC00000u);
             if (kind & 2) {
               const uint32_t odd = __ballot_sync(0xFFFFFFFFu, !fine);
-              if (lane == 0) st_shared_u(side + F::kOddScale + 4 * j, odd);
+              if (lane == 0) st_shared_u(side + kOddScale + 4 * j, odd);
             }
           }
           const float top = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, top_bits));
@@ -640,9 +652,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             st_shared_f(side + j * 128 + lane * 4, ld_shared_f(at + j * 128));
-            st_shared_f(side + F::kVScale + j * 128 + lane * 4, w[j] * inv);
+            st_shared_f(side + kVScale + j * 128 + lane * 4, w[j] * inv);
           }
-          if (lane == 0) st_shared_f(side + F::kRef, ref);
+          if (lane == 0) st_shared_f(side + kRef, ref);
         }
         __syncwarp();
         if (lane == 0) {
@@ -704,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         odd |= o;
       }
       const uint32_t who = __ballot_sync(0xFFFFFFFFu, odd) >> (lane - piece) & ((1u << kPieces) - 1u);
-      if (piece == 0) st_shared_byte(base + F::kSideAt + stage * F::kSide + F::kOdd + key, who ? 1u : 0u);
+      if (piece == 0) st_shared_byte(base + F::kSideAt + stage * kSide + kOdd + key, who ? 1u : 0u);
     };
     static_assert(!kCoded || kTurn % 8 == 0, "a thread's rows have one place in the swizzle");
     // 8-bit codes: the second half's lanes store their two chunks in the other
@@ -892,7 +904,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         phase ^= 1u;
       }
       for (int i = group; i < tiles; i += 2) {
-        const uint32_t side = base + F::kSideAt + stage * F::kSide;
+        const uint32_t side = base + F::kSideAt + stage * kSide;
         ok = ok && wait_bar(s_full + 8 * group, turn & 1u, p.status, kStatusTimeoutEpilogue);
         tc_fence_after();
         if (busy) {
@@ -900,13 +912,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
           const int draft = i * kKeys - before_drafts;  // of the first key
           uint64_t seen = ~uint64_t{0};
           ok = ok && wait_bar(full + 8 * stage, phase, p.status, kStatusTimeoutEpilogue);
-          const uint2 valid = ld_shared_u2(side + F::kValid);
+          const uint2 valid = ld_shared_u2(side + kValid);
           const bool partial = (valid.x & valid.y) != 0xFFFFFFFFu || draft + kKeys > 0;
           if (__builtin_expect(partial, 0))
-            seen = seen_here<kFormat>(p, seg.lo, token, draft, valid, side + F::kOddScale, side + F::kOdd, odd);
+            seen = seen_here<kFormat>(p, seg.lo, token, draft, valid, side + kOddScale, side + kOdd, odd);
           float down = 1.f, tile_sum = 0.f;
           if constexpr (kCoded) {
-            const float now = ld_shared_f(side + F::kRef);
+            const float now = ld_shared_f(side + kRef);
             if (now != v_ref) {
               down = v_ref / now;  // both powers of two, or v_ref 0 and nothing summed yet
               v_ref = now;
@@ -974,7 +986,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
               float4 vs[4];
               if constexpr (kCoded) {
 #pragma unroll
-                for (int x = 0; x < 4; ++x) vs[x] = ld_shared_f4(side + F::kVScale + c * 128 + (j + 4 * x) * 4);
+                for (int x = 0; x < 4; ++x) vs[x] = ld_shared_f4(side + kVScale + c * 128 + (j + 4 * x) * 4);
               }
               float e[16];
 #pragma unroll

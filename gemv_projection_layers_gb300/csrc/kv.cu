@@ -4,7 +4,10 @@
 // Writing quantises: a row's largest magnitude, the scale and its reciprocal
 // (rounded to nearest each), a multiplication and a rounding an entry.  Reading multiplies code by scale and rounds.  Moving
 // copies bytes.  All three are bound by the bytes they move, and by one chain
-// of dependent loads (offsets, start, table, entry) where there are few rows.
+// of dependent loads (offsets, start, table, entry) where there are few rows
+// (2.2 us).  139000 rows of 8 heads of 128 back from e4m3: 178 us (5.8 TB/s); 8192
+// rows of 8 heads to int8: 12.9 us (3.9 TB/s; the chain is a third of it); 256 paths
+// of 32 rows of 8 heads, 16-bit: 11.6 us (3.6 TB/s).
 //
 // A warp takes a row of the call: it finds the row's sequence once (a search
 // in `offsets` that halves the range five times a step: 32 lanes look at 32

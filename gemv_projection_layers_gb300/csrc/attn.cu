@@ -834,7 +834,9 @@ extern "C" int proj_attn(const proj_attn_args* args, proj_stream stream) {
   const int64_t width = a.heads * c.D;
   if (a.gate_act != PROJ_GATE_LINEAR && a.gate_act != PROJ_GATE_SIGMOID)
     return kv_refuse(PROJ_EINVAL, call, "unknown gate_act");
-  if (!std::isfinite(a.scale)) return kv_refuse(PROJ_EINVAL, call, "scale is no finite number");
+  const float scale_log2 = static_cast<float>(a.scale * 1.4426950408889634);
+  if (!std::isfinite(scale_log2))
+    return kv_refuse(PROJ_EINVAL, call, "scale, or scale log2(e), is no finite number");
   if (a.m > 0 && c.sequences > 0 && (!a.q || !a.out || !a.offsets || !a.start))
     return kv_refuse(PROJ_EINVAL, call, "q, out, offsets or start is NULL");
   if (a.ldq < width || a.ldo < width || (a.gate && a.ldg < width))
@@ -866,7 +868,7 @@ extern "C" int proj_attn(const proj_attn_args* args, proj_stream stream) {
   p.mask = a.mask;
   p.ldm = a.ldm;
   p.words = static_cast<int>(a.words);
-  p.scale_log2 = static_cast<float>(a.scale * 1.4426950408889634);
+  p.scale_log2 = scale_log2;
   p.gate = static_cast<const uint8_t*>(a.gate);
   p.ldg = a.ldg * 2;
   p.sigmoid = a.gate_act == PROJ_GATE_SIGMOID;

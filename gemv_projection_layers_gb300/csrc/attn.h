@@ -69,11 +69,11 @@ __device__ __forceinline__ Sequence sequence_at(const AttnParams& p, int b) {
   return s;
 }
 
-// Units of a sequence; no more than 2^35 are worked on, so that sums and
-// products below stay within 64 bits whatever stands in offsets and start.
+// Units of a sequence; no more than 2^46 (years of work) are counted, so that sums
+// and products below stay within 64 bits whatever stands in offsets and start.
 __device__ __forceinline__ int64_t units_of(const AttnParams& p, const Sequence& s) {
   const int64_t all = static_cast<int64_t>(s.tiles) * s.units;
-  return min(all < (int64_t{1} << 45) ? all * p.c.heads : all, int64_t{1} << 35);
+  return min(all < (int64_t{1} << 45) ? all * p.c.heads : all, int64_t{1} << 46);
 }
 
 // What a CTA leaves to be joined: the item in which its share begins, if that

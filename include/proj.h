@@ -727,8 +727,9 @@ typedef struct proj_kv_cache {
 
 /*
  * Write rows k and v (m rows of heads D values, dtype; 16-byte aligned, strides
- * multiples of 8) to their positions.  Two rows of one position: one of them
- * is kept.
+ * multiples of 8) to their positions; m < 2^30.  No two rows of a call may
+ * stand in one place (of a page that the table names twice): what it holds
+ * afterwards is not defined.
  */
 int proj_kv_write(const proj_kv_cache *cache, const int32_t *offsets, const int32_t *start,
                   int64_t m, const void *k, int64_t ldk, const void *v, int64_t ldv,
@@ -762,23 +763,25 @@ int proj_kv_move(const proj_kv_cache *cache, const int32_t *start, const int32_t
  *     out = (softmax(scale q k^T over what the row sees) v) act(gate)
  *
  * A row that sees nothing gets zeros, and lse = -infinity.  What a row does not
- * see does not reach it, NaN and infinities included.  Scores, their maximum
- * and sums are fp32; the products of 8-bit caches and of fp16 are computed in
- * fp16 with codes and queries exact in it (a row of bf16 queries is brought
- * to its range by a power of two; what is 2^-29 below the row's largest loses
- * digits) and probabilities rounded to it; those of bf16 caches in bf16.
+ * see does not reach it, NaN and infinities included; where it sees a value that
+ * is no finite number, that column of it is none either (an infinity or NaN).
+ * Scores, their maximum and sums are fp32; the products of 8-bit caches and of
+ * fp16 are computed in fp16 with codes and queries exact in it (a row of bf16
+ * queries is brought to its range by a power of two; what is 2^-29 below the
+ * row's largest loses digits) and probabilities rounded to it; those of bf16
+ * caches in bf16.
  * The gate is applied in fp32 and the result rounded once.
  */
 typedef struct proj_attn_args {
     const proj_kv_cache *cache;
-    int64_t m, heads;        /* rows of q; query heads, a multiple of the cache's, at most 1024 */
+    int64_t m, heads;        /* rows of q, at most 2^20; query heads, a multiple of the cache's, at most 1024 */
     const void *q;           /* [m, heads D], dtype; 16-byte aligned, strides multiples of 8 */
     int64_t ldq;
     const int32_t *offsets;  /* device [sequences + 1] */
     const int32_t *start;    /* device [sequences] */
     const uint32_t *mask;    /* device [m, words], row stride ldm, or NULL */
     int64_t ldm, words;      /* words: 1 .. 1024 */
-    float scale;             /* finite */
+    float scale;             /* finite, and scale log2(e) too */
     int gate_act;            /* enum proj_gate_act */
     const void *gate;        /* [m, heads D], dtype, as q; NULL: none */
     int64_t ldg;

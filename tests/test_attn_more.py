@@ -1,5 +1,6 @@
 """More of the attention over the cache: rows around the kernels' tiles, references that move, long caches, calls with
 offsets and starts that are out of range.  Bounds as in test_attn.py."""
+import ctypes
 import math
 
 import numpy as np
@@ -82,7 +83,7 @@ def test_a_cache_beyond_32_bits(T):
     ref = c.cache.get("k", 0, 0, n).reshape(n, -1)
     assert bool(((back.cpu().double() - ref).abs() <= (2.0 ** -8 + 2.0 ** -24) * ref.abs() + 2.0 ** -30).all())
     args = c.args()
-    args.cache = __import__("ctypes").addressof(far)
+    args.cache = ctypes.addressof(far)
     B.proj_attn(args)
     c.check()
     if T > 1:
@@ -151,3 +152,13 @@ def test_one_page_for_many_sequences(T):
     c.cache.d_table.copy_(c.cache.table)
     c.run()
     c.check()
+
+
+def test_scale_out_of_range_refused():
+    """A scale whose product with log2(e) leaves fp32: the exponents are computed in base 2."""
+    cache = B.kv_cache(format=B.PROJ_KV_ROWS, dtype=B.PROJ_BF16, pages=1, page=16, heads=1, D=64, k=4096, v=8192,
+                       page_stride=1024, head_stride=1024, token_stride=64, table=4096, ldt=1, width=1, sequences=1)
+    args = B.attn_args(cache, m=1, heads=1, q=4096, ldq=64, offsets=4096, start=4096, scale=3e38, out=8192, ldo=64,
+                       workspace=4096, workspace_bytes=1 << 30)
+    assert B.load().proj_attn(ctypes.byref(args), None) == B.PROJ_EINVAL
+    assert "scale" in B.last_cuda_error()

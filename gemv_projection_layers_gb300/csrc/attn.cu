@@ -1,11 +1,11 @@
 // attn.cu -- attention of drafted tokens over the cache: the calls, the kernel
 // for few rows, and the join of partial results.
 //
-// The kernel for few rows (a group's heads times a sequence's drafts up to 32, in
-// items of 8 or 16) is a stream over the cache.  Per key and head it reads 2 D entries and does
-// 4 D operations a row, so with 8 rows and 8-bit entries the cache's bytes at
-// HBM's rate leave the tensor cores of the warp-level MMA a fifth of their
-// time; what counts is that the bytes flow.  Each of a CTA's eight warps has
+// The kernel for few rows (a group's heads times a sequence's drafts up to 32, and
+// more of a short cache; items of 8 or 16) is a stream over the cache.  Per key and
+// head it reads 2 D entries and does 4 D operations a row, so with 8 rows and 8-bit
+// entries the cache's bytes at HBM's rate leave the tensor cores of the warp-level MMA
+// a fifth of their time; what counts is that the bytes flow.  Each of a CTA's eight warps has
 // a ring of its own in shared memory, filled by 16-byte asynchronous copies,
 // and takes every eighth step of the CTA's share, 32 keys (16 of 16-bit entries and
 // 128 dimensions): nothing but the end of an item is a barrier for the CTA.  From
@@ -769,14 +769,23 @@ struct Plan {
   int64_t bytes;
 };
 
-// Which kernel, and rows of an item, by the rows that a sequence and a head of keys
-// and values have on average (lengths are known on the device only).  Up to 8 and
-// 16 the streaming kernel; up to 32 it too, in two items that read the cache once
-// from HBM and once from L2; beyond, tcgen05.  16 sequences of up to 32768 keys of 128
-// (8192 in brackets), eight heads on one, streamed against tcgen05, us:
-//   16 rows  e4m3 32 (22), 54 (30)    16-bit 39 (20), 45 (26)
-//   32 rows  e4m3 43 (24), 55 (31)    16-bit 50 (22), 46 (27)
-//   64 rows  e4m3 112, 60             (in two items of 32 rows)
+// Which kernel, and rows of an item.  Numbers of rows and lengths are known on the
+// device only: the plan goes by the rows that a sequence and a head of keys and
+// values have on average, and by the table's width.  Up to 32 rows are streamed, in
+// items of 8 or 16, of which the second reads the cache from L2.  More are streamed
+// as well while there is little to do: an item of 16 rows costs the streaming kernel
+// some 0.13 us by itself and 1 us for every 1100 units, while a tcgen05 call is not
+// under 15 to 30 us (128 units a CTA, with 64 for each item, is where they meet).
+// Keys of 128, eight heads on one, streamed against tcgen05, us:
+//                              e4m3      16-bit
+//   16 sequences x  32768 keys,  16 rows  32  54   39  45
+//   16 x 32768,  32 rows         43  55   50  46
+//    1 x  4096,  64 rows         15  20   13  17
+//   16 x  4096,  64 rows         25  31   24  29
+//   16 x 32768,  64 rows         69  60    -   -   (tcgen05)
+//   32 x  4000,  64 rows         41  36   38  32   (tcgen05)
+//    8 x  1900, 256 rows         33  34   28  30
+//    1 x  1000, 512 rows         16  30   14  26
 // A share has at least 256 keys either way: a step for each of the streaming
 // kernel's warps (one sequence of 8192 keys: 9.0 us; with 128 keys 9.4, with 512
 // 9.2), four tiles of the tcgen05 kernel (2: the same or 0.3 us slower, 8: 1-3).
@@ -793,15 +802,18 @@ const char* make_plan(const proj_kv_cache* cache, int64_t m, int64_t heads, Plan
   const int64_t rows = cache->sequences
                            ? (m + cache->sequences - 1) / cache->sequences * (heads / cache->heads)
                            : 1;
-  plan->rows = rows;
-  plan->tc = rows > 32;
-  plan->unit = plan->tc ? kAttnTcUnit : kUnit;
-  plan->tile_rows = plan->tc ? kAttnTcRows : rows <= 8 ? 8 : 16;
-  plan->min_units = plan->tc ? 4 : kWarps;
   int sms = 0, dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
     sms = 152;
+  // the streaming kernel's items and, at most, their units
+  const int64_t items = (rows + 15) / 16 * cache->sequences * cache->heads;
+  const int64_t units = items * ((cache->width * cache->page + kUnit - 1) / kUnit);
+  plan->rows = rows;
+  plan->tc = rows > 32 && units + 64 * items > 128 * static_cast<int64_t>(sms);
+  plan->unit = plan->tc ? kAttnTcUnit : kUnit;
+  plan->tile_rows = plan->tc ? kAttnTcRows : rows <= 8 ? 8 : 16;
+  plan->min_units = plan->tc ? 4 : kWarps;
   plan->ctas = sms;
   plan->bytes = int64_t{2} * plan->ctas * plan->tile_rows * (cache->D + 2) * 4 +
                 plan->ctas * static_cast<int64_t>(sizeof(Split));

@@ -1,5 +1,6 @@
 // attn_tc.cu -- attention of drafted tokens over the cache on tcgen05, for
-// items of many rows (a group's heads times a sequence's drafts above 32).
+// items of many rows (a group's heads times a sequence's drafts above 32) over long
+// caches.
 //
 // Rows are the M side of both products, a row in each of 128 lanes of tensor
 // memory; a tile is 64 keys:

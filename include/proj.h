@@ -771,6 +771,10 @@ int proj_kv_move(const proj_kv_cache *cache, const int32_t *start, const int32_t
  * row's largest loses digits) and probabilities rounded to it; those of bf16
  * caches in bf16.
  * The gate is applied in fp32 and the result rounded once.
+ *
+ * How many rows and positions a sequence has is read on the device.  Which kernel
+ * runs goes by m, sequences and heads, and by the table's width as the most that
+ * a sequence can hold (proj_attn_describe): the results are good either way.
  */
 typedef struct proj_attn_args {
     const proj_kv_cache *cache;

@@ -28,11 +28,13 @@ def quantise(x, fmt):
 
 
 class Cache:
+    more = 0  # positions for which every table has room beyond what its sequences need
+
     def __init__(self, fmt, dtype, lens, kv, D, page, layout="head", seed=0, spare=2):
         self.fmt, self.dtype, self.kv, self.D, self.page = fmt, dtype, kv, D, page
         self.gen = torch.Generator().manual_seed(seed)
         need = [-(-n // page) for n in lens]
-        self.width = max(need + [1]) + 1
+        self.width = max(need + [1]) + 1 + -(-self.more // page)
         self.pages = sum(need) + spare
         deal = torch.randperm(self.pages, generator=self.gen).to(torch.int32)
         self.table = torch.full((max(len(lens), 1), self.width), -1, dtype=torch.int32)

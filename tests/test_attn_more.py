@@ -70,9 +70,11 @@ def test_a_cache_beyond_32_bits(T):
     k, v = (torch.zeros(pages, kv, page, D, dtype=torch.int8, device="cuda") for _ in range(2))
     ks, vs = (torch.full((pages, kv, page), math.nan, device="cuda") for _ in range(2))
     c = Call("int8", "bf16", [T], [100], kv, G, D, page, None, seed=19)
-    table = torch.tensor([[pages - 1, pages - 2, pages // 2 + 3, -1]], dtype=torch.int32, device="cuda")
+    width = 4 + Cache.more // page
+    table = torch.full((1, width), -1, dtype=torch.int32, device="cuda")
+    table[0, :3] = int32([pages - 1, pages - 2, pages // 2 + 3])
     far = B.kv_cache(format=B.PROJ_KV_INT8, dtype=B.PROJ_BF16, pages=pages, page=page, heads=kv, D=D, k=k, v=v, k_scale=ks, v_scale=vs,
-                     page_stride=kv * page * D, head_stride=page * D, token_stride=D, table=table, ldt=4, width=4, sequences=1)
+                     page_stride=kv * page * D, head_stride=page * D, token_stride=D, table=table, ldt=width, width=width, sequences=1)
     n = 100 + T
     rows_k = torch.randn(n, kv * D, device="cuda").bfloat16()
     rows_v = torch.randn(n, kv * D, device="cuda").bfloat16()

@@ -5,10 +5,11 @@
 // more of a short cache; items of 8 or 16) is a stream over the cache.  Per key and
 // head it reads 2 D entries and does 4 D operations a row, so with 8 rows and 8-bit
 // entries the cache's bytes at HBM's rate leave the tensor cores of the warp-level MMA
-// a fifth of their time; what counts is that the bytes flow.  Each of a CTA's eight warps has
-// a ring of its own in shared memory, filled by 16-byte asynchronous copies,
+// a fifth of their time; what counts is that the bytes flow.  Each of a CTA's eight
+// warps has a ring of its own in shared memory, filled by 16-byte asynchronous copies,
 // and takes every eighth step of the CTA's share, 32 keys (16 of 16-bit entries and
-// 128 dimensions): nothing but the end of an item is a barrier for the CTA.  From
+// 128 dimensions): nothing but the end of an item is a barrier for the CTA.  Where
+// there are many items, each warp has a share of its own and no barrier at all.  From
 // 16384 to 65536 keys of 16 sequences a call's time grows as the bytes at HBM's
 // measured rate do (e4m3 20 us a 20 us, 16-bit 38 a 39); below, it is the chain
 // of a call that shows: lengths, pages, first bytes, the warps' and the CTAs' sums
@@ -126,7 +127,9 @@ __device__ __forceinline__ bool odd_pair(uint32_t w, __nv_bfloat16) {
   return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
 }
 
-template <typename T, int kFormat, int D, int NT>
+// kSolo: each warp has a share of its own, and the sums of an item's part are its
+// alone; nothing in the kernel is a barrier for the CTA.
+template <typename T, int kFormat, int D, int NT, bool kSolo>
 __global__ void __launch_bounds__(kThreads, 1) attn_stream_kernel(const AttnParams p) {
   using F = Stream<kFormat, D, NT>;
   constexpr bool kCoded = kFormat != PROJ_KV_ROWS;
@@ -140,15 +143,24 @@ __global__ void __launch_bounds__(kThreads, 1) attn_stream_kernel(const AttnPara
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, c4 = lane & 3;
   const uint32_t ring = smem_u32(smem) + warp * F::kRing;
-  float* const merge = reinterpret_cast<float*>(smem);
-  float* const s_ml = reinterpret_cast<float*>(smem + F::kSmem - F::kMl);
+  constexpr int kTeam = kSolo ? 1 : kWarps;  // warps to a share
+  const int member = kSolo ? 0 : warp, tid = kSolo ? lane : threadIdx.x;
+  const int worker = kSolo ? blockIdx.x * kWarps + warp : blockIdx.x;
+  const auto team_sync = [] {
+    if constexpr (kSolo)
+      __syncwarp();
+    else
+      __syncthreads();
+  };
+  float* const merge = reinterpret_cast<float*>(smem + (kSolo ? warp * F::kRing : 0));
+  float* const s_ml = reinterpret_cast<float*>(smem + F::kSmem - F::kMl) + (kSolo ? warp * F::kRows * 2 : 0);
 
   touch(p);
   griddep_launch_dependents();
   griddep_wait();
   Share share;
-  if (!find_share<kThreads>(p, blockIdx.x, share)) {
-    if (threadIdx.x == 0) p.splits[blockIdx.x] = Split{};
+  if (!find_share<kThreads, kSolo>(p, kSolo ? blockIdx.x * kWarps : blockIdx.x, share)) {
+    if (tid == 0) p.splits[worker] = Split{};
     return;
   }
 
@@ -173,8 +185,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_stream_kernel(const AttnPara
 
     // --------------------------------------------------------------- ring --
     const int all_steps = (u1 - u0) * kUnitSteps;
-    const int steps = all_steps > warp ? (all_steps - warp + kWarps - 1) / kWarps : 0;
-    const auto first_key = [&](int i) { return u0 * kUnit + (warp + i * kWarps) * kStep; };
+    const int steps = all_steps > member ? (all_steps - member + kTeam - 1) / kTeam : 0;
+    const auto first_key = [&](int i) { return u0 * kUnit + (member + i * kTeam) * kStep; };
     const int32_t* const table = p.c.table + b * p.c.ldt;
     const int64_t head_at = head * p.c.head_stride, head_scale = static_cast<int64_t>(head) * p.c.page.d;
     // the page of key `lane` (< kStep) of step i, or -1
@@ -550,20 +562,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_stream_kernel(const AttnPara
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 
     // --------------------------------------------- the warps' sums joined --
-    // A thread has kOuts rows, four columns of each; their gate is read meanwhile.
+    // A thread has kOuts rows, four columns of each; their gate is read meanwhile
+    // (by a warp that has all rows, one at a time: other warps are at work).
     const bool whole = u0 == 0 && u1 == seq.units;
-    constexpr int kOuts = F::kRows * (D / 4) / kThreads > 0 ? F::kRows * (D / 4) / kThreads : 1;
-    const int quad = threadIdx.x % (D / 4);
-    const auto out_row = [&](int n) { return static_cast<int>(threadIdx.x) / (D / 4) + n * (kThreads / (D / 4)); };
-    Vec<T, 4> gate[kOuts][1] = {};
-    if (whole && p.gate) {
+    constexpr int kTeamThreads = 32 * kTeam;
+    constexpr int kOuts = F::kRows * (D / 4) / kTeamThreads > 0 ? F::kRows * (D / 4) / kTeamThreads : 1;
+    const int quad = tid % (D / 4);
+    const auto out_row = [&](int n) { return tid / (D / 4) + n * (kTeamThreads / (D / 4)); };
+    Vec<T, 4> gate[kSolo ? 1 : kOuts][1] = {};
+    const auto read_gate = [&](int n, Vec<T, 4>& to) {
+      const int r = row0 + out_row(n), t = quotient(r, p.group);
+      if (whole && p.gate && r < all_rows && out_row(n) < F::kRows)
+        to = load_vec<T, 4>(reinterpret_cast<const T*>(p.gate + static_cast<int64_t>(seq.lo + t) * p.ldg) +
+                            (head * G + r - t * G) * D + quad * 4);
+    };
+    if constexpr (!kSolo) {
 #pragma unroll
-      for (int n = 0; n < kOuts; ++n) {
-        const int r = row0 + out_row(n), t = quotient(r, p.group);
-        if (r < all_rows && out_row(n) < F::kRows)
-          gate[n][0] = load_vec<T, 4>(reinterpret_cast<const T*>(p.gate + static_cast<int64_t>(seq.lo + t) * p.ldg) +
-                                      (head * G + r - t * G) * D + quad * 4);
-      }
+      for (int n = 0; n < kOuts; ++n) read_gate(n, gate[n][0]);
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -571,9 +586,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_stream_kernel(const AttnPara
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) sum[nt][i] += __shfl_xor_sync(0xFFFFFFFFu, sum[nt][i], x);
-    if (!told && threadIdx.x == kThreads - 1) p.splits[blockIdx.x] = split_of(p, share, blockIdx.x);
+    if (!told && tid == kTeamThreads - 1) p.splits[worker] = split_of(p, share, worker);
     told = true;
-    __syncthreads();  // every warp is done with its ring
+    team_sync();  // every warp is done with its ring
     const float up = kCoded ? v_ref : 1.f;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -581,10 +596,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_stream_kernel(const AttnPara
       for (int i = 0; i < 2; ++i) {
         const int r = nt * 8 + c4 * 2 + i;
         if (g == 0) {
-          s_ml[(warp * F::kRows + r) * 2] = ref[nt][i] - kLift;
-          s_ml[(warp * F::kRows + r) * 2 + 1] = sum[nt][i];
+          s_ml[(member * F::kRows + r) * 2] = ref[nt][i] - kLift;
+          s_ml[(member * F::kRows + r) * 2 + 1] = sum[nt][i];
         }
-        float* to = merge + (warp * F::kRows + r) * F::kPitch;
+        float* to = merge + (member * F::kRows + r) * F::kPitch;
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk) {
           if constexpr (kCoded) {
@@ -597,17 +612,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_stream_kernel(const AttnPara
         }
       }
     }
-    __syncthreads();
-#pragma unroll
+    team_sync();
+#pragma unroll(kSolo ? 1 : kOuts)
     for (int n = 0; n < kOuts; ++n) {
       const int r = out_row(n);
       if (row0 + r >= all_rows || r >= F::kRows) continue;
+      Vec<T, 4>(&its_gate)[1] = gate[kSolo ? 0 : n];
+      if constexpr (kSolo) read_gate(n, its_gate[0]);
       float top = s_ml[r * 2];
 #pragma unroll
-      for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_ml[(w * F::kRows + r) * 2]);
+      for (int w = 1; w < kTeam; ++w) top = fmaxf(top, s_ml[(w * F::kRows + r) * 2]);
       float l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
+      for (int w = 0; w < kTeam; ++w) {
         const float f = exp2_fast(s_ml[(w * F::kRows + r) * 2] - top);
         l += f * s_ml[(w * F::kRows + r) * 2 + 1];
         const float4 v = *reinterpret_cast<const float4*>(merge + (w * F::kRows + r) * F::kPitch + quad * 4);
@@ -619,10 +636,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_stream_kernel(const AttnPara
       if (whole) {
         const int t = quotient(row0 + r, p.group);
         const int j = head * G + row0 + r - t * G;
-        write_out<T>(p, static_cast<int64_t>(seq.lo + t), j * D + quad * 4, acc, l, gate[n]);
+        write_out<T>(p, static_cast<int64_t>(seq.lo + t), j * D + quad * 4, acc, l, its_gate);
         if (p.lse && quad == 0) p.lse[static_cast<int64_t>(seq.lo + t) * p.heads + j] = lse_of(top, l);
       } else {
-        const int part = 2 * static_cast<int>(blockIdx.x) + (u0 == 0 ? 1 : 0);
+        const int part = 2 * worker + (u0 == 0 ? 1 : 0);
         float* to = p.part_o + (static_cast<int64_t>(part) * F::kRows + r) * D + quad * 4;
         *reinterpret_cast<float4*>(to) = make_float4(acc[0], acc[1], acc[2], acc[3]);
         if (quad == 0)
@@ -630,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_stream_kernel(const AttnPara
               make_float2(top, l);
       }
     }
-    __syncthreads();  // the ring is free again
+    team_sync();  // the ring is free again
     at += u1 - u0;
   }
 }
@@ -741,18 +758,20 @@ cudaError_t launch(void (*kernel)(P), dim3 grid, size_t smem, const P& p, cudaSt
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-template <typename T, int kFormat, int D, int NT>
+template <typename T, int kFormat, int D, int NT, bool kSolo>
 cudaError_t stream_launch(const AttnParams& p, cudaStream_t s) {
   using F = Stream<kFormat, D, NT>;
-  const auto kernel = attn_stream_kernel<T, kFormat, D, NT>;
+  const auto kernel = attn_stream_kernel<T, kFormat, D, NT, kSolo>;
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), F::kSmem, done);
-  return e == cudaSuccess ? launch(kernel, dim3(p.ctas), F::kSmem, p, s) : e;
+  return e == cudaSuccess ? launch(kernel, dim3(p.ctas / (kSolo ? kWarps : 1)), F::kSmem, p, s) : e;
 }
 
 template <typename T, int kFormat, int D>
 cudaError_t stream_rows(const AttnParams& p, cudaStream_t s) {
-  return p.tile_rows == 8 ? stream_launch<T, kFormat, D, 1>(p, s) : stream_launch<T, kFormat, D, 2>(p, s);
+  if (p.solo)
+    return p.tile_rows == 8 ? stream_launch<T, kFormat, D, 1, true>(p, s) : stream_launch<T, kFormat, D, 2, true>(p, s);
+  return p.tile_rows == 8 ? stream_launch<T, kFormat, D, 1, false>(p, s) : stream_launch<T, kFormat, D, 2, false>(p, s);
 }
 
 template <typename T, int D>
@@ -763,9 +782,9 @@ cudaError_t stream_format(int format, const AttnParams& p, cudaStream_t s) {
 }
 
 struct Plan {
-  bool tc;
+  bool tc, solo;
   int64_t rows;  // of a sequence and a head of keys and values, on average
-  int tile_rows, unit, ctas, min_units;
+  int tile_rows, unit, sms, ctas, min_units;  // ctas: shares
   int64_t bytes;
 };
 
@@ -786,9 +805,21 @@ struct Plan {
 //   32 x  4000,  64 rows         41  36   38  32   (tcgen05)
 //    8 x  1900, 256 rows         33  34   28  30
 //    1 x  1000, 512 rows         16  30   14  26
-// A share has at least 256 keys either way: a step for each of the streaming
-// kernel's warps (one sequence of 8192 keys: 9.0 us; with 128 keys 9.4, with 512
-// 9.2), four tiles of the tcgen05 kernel (2: the same or 0.3 us slower, 8: 1-3).
+// More than two items an SM are streamed by warps with a share each: an item's ends
+// (its lengths, first pages, queries, and the sums that a CTA's warps join) then pass
+// beside other warps' items.  8 heads on 8 caches' heads of 128, by CTAs against by
+// warps, us:
+//    16 sequences x 2000 keys  e4m3  24  30   16-bit  26  33   (by CTAs)
+//    64 x  300                       43  28           38  29
+//    64 x 4000                       86  68          116 112
+//   256 x 1000                      132  98          136 130
+//   64 x 4000, 16 rows              121  80          129 122
+//   (512 sequences x 300 with one head, where a CTA's search for its shares is long:
+//   32 and 33, 31 and 32)
+// A share has at least 256 keys of a CTA: a step for each of the streaming kernel's
+// warps (one sequence of 8192 keys: 9.0 us; with 128 keys 9.4, with 512 9.2), four
+// tiles of the tcgen05 kernel (2: the same or 0.3 us slower, 8: 1-3); and 128 of a
+// warp.
 const char* make_plan(const proj_kv_cache* cache, int64_t m, int64_t heads, Plan* plan,
                       int* status) {
   if (const char* why = refuse_cache(cache, status)) return why;
@@ -813,10 +844,14 @@ const char* make_plan(const proj_kv_cache* cache, int64_t m, int64_t heads, Plan
   plan->tc = rows > 32 && units + 64 * items > 128 * static_cast<int64_t>(sms);
   plan->unit = plan->tc ? kAttnTcUnit : kUnit;
   plan->tile_rows = plan->tc ? kAttnTcRows : rows <= 8 ? 8 : 16;
-  plan->min_units = plan->tc ? 4 : kWarps;
-  plan->ctas = sms;
+  const int64_t parts = (rows + plan->tile_rows - 1) / plan->tile_rows * cache->sequences * cache->heads;
+  plan->solo = !plan->tc && parts > 2 * static_cast<int64_t>(sms);
+  plan->min_units = plan->tc || plan->solo ? 4 : kWarps;
+  plan->sms = sms;
+  plan->ctas = plan->solo ? kWarps * sms : sms;
+  // never less for more rows: the most shares there are, whatever the kernel
   plan->bytes = int64_t{2} * plan->ctas * plan->tile_rows * (cache->D + 2) * 4 +
-                plan->ctas * static_cast<int64_t>(sizeof(Split));
+                int64_t{kWarps} * sms * static_cast<int64_t>(sizeof(Split));
   return nullptr;
 }
 
@@ -894,6 +929,7 @@ extern "C" int proj_attn(const proj_attn_args* args, proj_stream stream) {
   p.tile_rows = plan.tile_rows;
   p.unit = plan.unit;
   p.ctas = plan.ctas;
+  p.solo = plan.solo;
   while ((1 << p.min_shift) < plan.min_units) ++p.min_shift;
   while ((1 << p.tile_shift) < p.tile_rows) ++p.tile_shift;
   while ((1 << p.unit_shift) < p.unit) ++p.unit_shift;
@@ -902,7 +938,7 @@ extern "C" int proj_attn(const proj_attn_args* args, proj_stream stream) {
   if (e != cudaSuccess) return record_cuda(e, call);
   p.status = static_cast<uint32_t*>(status_word);
   p.splits = static_cast<Split*>(a.workspace);
-  p.part_o = reinterpret_cast<float*>(p.splits + plan.ctas);
+  p.part_o = reinterpret_cast<float*>(p.splits + kWarps * plan.sms);
   p.part_ml = p.part_o + int64_t{2} * plan.ctas * plan.tile_rows * c.D;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (plan.tc)
@@ -920,7 +956,7 @@ extern "C" int proj_attn(const proj_attn_args* args, proj_stream stream) {
   const int64_t x = std::min<int64_t>(items, plan.ctas);
   // 16 CTAs an SM (16 items of 8 rows in 10 parts each: the call
   // 24.7 us with a set a row, 19.9 with a CTA)
-  p.spread = x * rows <= 16 * plan.ctas;
+  p.spread = x * rows <= 16 * plan.sms;
   const int64_t y = p.spread ? rows : (rows + sets - 1) / sets;
   const dim3 grid(static_cast<unsigned>(x), static_cast<unsigned>(std::max<int64_t>(1, y)));
   if (c.dtype == PROJ_BF16)
@@ -939,8 +975,8 @@ extern "C" int proj_attn_describe(const proj_kv_cache* cache, int64_t m, int64_t
   int status = PROJ_OK;
   if (const char* why = make_plan(cache, m, heads, &plan, &status)) return kv_refuse(status, call, why);
   if (!buf || cap == 0) return kv_refuse(PROJ_EINVAL, call, "buf is NULL or cap 0");
-  std::snprintf(buf, cap, "attn %s, items of %d rows, units of %d keys, up to %d CTAs, join",
-                plan.tc ? "tcgen05" : "stream", plan.tile_rows, plan.unit, plan.ctas);
+  std::snprintf(buf, cap, "attn %s, items of %d rows, units of %d keys, up to %d %s, join",
+                plan.tc ? "tcgen05" : "stream", plan.tile_rows, plan.unit, plan.ctas, plan.solo ? "warps" : "CTAs");
   return PROJ_OK;
 }
 

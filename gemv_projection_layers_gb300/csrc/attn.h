@@ -10,7 +10,8 @@
 // every SM has the same share whatever the lengths, a CTA leaves at most two items
 // unfinished (one it did not begin, one it does not end), and the partial results
 // need room for two items a CTA and nothing that grows with the batch.  A second
-// kernel joins them in the order of their CTAs.
+// kernel joins them in the order of their CTAs.  (In batches of many items the
+// streaming kernel gives shares to warps: "CTA" is a warp then.)
 #pragma once
 
 #include <cuda_bf16.h>
@@ -40,7 +41,7 @@ struct AttnParams {
   float* lse;
   int m, heads, D;
   Divisor group;
-  int tile_rows, unit, ctas, spread;
+  int tile_rows, unit, ctas, spread, solo;
   int tile_shift, unit_shift, min_shift;  // logarithms; min_shift: of a share's least units
   struct Split* splits;  // [ctas]
   float* part_o;   // [2 ctas][tile_rows][D]: sums relative to 2^m
@@ -197,14 +198,17 @@ __device__ __forceinline__ bool find_share_walk(const AttnParams& p, int cta, Sh
   return who != 0;
 }
 
-// All threads of the CTA; kThreads of them.  `cta`: whose share.  False: none.
-template <int kThreads>
+// All threads of the CTA; kThreads of them.  `cta`: whose share (kSolo: the first
+// warp's; each has its own).  False: none.
+template <int kThreads, bool kSolo>
 __device__ __forceinline__ bool find_share(const AttnParams& p, int cta, Share& s) {
-  if (p.c.sequences <= kWarpSequences) return find_share_warp(p, cta, s);
+  constexpr int kShares = kSolo ? kThreads / 32 : 1;
+  const int mine = kSolo ? threadIdx.x >> 5 : 0;
+  if (p.c.sequences <= kWarpSequences) return find_share_warp(p, cta + mine, s);
   __shared__ int64_t warp_sum[kThreads / 32];
   __shared__ int warp_items[kThreads / 32];
-  __shared__ int found_b;
-  __shared__ int64_t found_before;
+  __shared__ int found_b[kShares];
+  __shared__ int64_t found_before[kShares];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.c.sequences + kThreads - 1) / kThreads;
   const int b0 = min(tid * per, p.c.sequences), b1 = min(b0 + per, p.c.sequences);
@@ -226,7 +230,7 @@ __device__ __forceinline__ bool find_share(const AttnParams& p, int cta, Share& 
     warp_sum[warp] = inc;
     warp_items[warp] = items;
   }
-  if (tid == 0) found_b = -1;
+  if (tid < kShares) found_b[tid] = -1;
   __syncthreads();
   int64_t before = inc - sum, W = 0;
   items = 0;
@@ -236,21 +240,27 @@ __device__ __forceinline__ bool find_share(const AttnParams& p, int cta, Share& 
     W += warp_sum[w];
     items += warp_items[w];
   }
-  if (!share_ends(p, cta, W, items, s)) return false;
-  if (s.first >= before && s.first < before + sum) {
-    int b = b0;
-    for (; b < b1 - 1; ++b) {
-      const int64_t u = units_of(p, sequence_at(p, b));
-      if (s.first < before + u) break;
-      before += u;
+  if (W == 0) return false;
+  const bool some = share_ends(p, cta + mine, W, items, s);
+  const int64_t end = before + sum;
+  int64_t at = s.each * cta;
+  int i = 0;
+  for (; i < kShares && at < before; ++i) at += s.each;
+  // the shares that begin in this thread's sequences
+  for (int b = b0; i < kShares && at < end;) {
+    const int64_t u = units_of(p, sequence_at(p, b));
+    for (; i < kShares && at < before + u; ++i) {
+      found_b[i] = b;
+      found_before[i] = before;
+      at += s.each;
     }
-    found_b = b;
-    found_before = before;
+    before += u;
+    ++b;
   }
   __syncthreads();
-  s.b = found_b;
-  s.before = found_before;
-  return s.b >= 0;
+  s.b = found_b[mine];
+  s.before = found_before[mine];
+  return some && s.b >= 0;
 }
 
 __device__ __forceinline__ Split split_of(const AttnParams& p, const Share& s, int cta) {

@@ -796,7 +796,8 @@ typedef struct proj_attn_args {
     int64_t workspace_bytes;
 } proj_attn_args;
 
-/* Bytes of workspace of proj_attn on this device; -1 for arguments it refuses.
+/* Bytes of workspace of proj_attn on this device, no less for more rows of the
+ * same cache; -1 for arguments it refuses.
  * A workspace holds nothing between calls, and calls that may overlap need one
  * each. */
 int64_t proj_attn_workspace(const proj_kv_cache *cache, int64_t m, int64_t heads);

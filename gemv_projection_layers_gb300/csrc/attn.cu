@@ -790,32 +790,38 @@ struct Plan {
 
 // Which kernel, and rows of an item.  Numbers of rows and lengths are known on the
 // device only: the plan goes by the rows that a sequence and a head of keys and
-// values have on average, and by the table's width.  Up to 32 rows are streamed, in
-// items of 8 or 16, of which the second reads the cache from L2.  More are streamed
-// as well while there is little to do: an item of 16 rows costs the streaming kernel
-// some 0.13 us by itself and 1 us for every 1100 units, while a tcgen05 call is not
-// under 15 to 30 us (128 units a CTA, with 64 for each item, is where they meet).
-// Keys of 128, eight heads on one, streamed against tcgen05, us:
-//                              e4m3      16-bit
-//   16 sequences x  32768 keys,  16 rows  32  54   39  45
-//   16 x 32768,  32 rows         43  55   50  46
-//    1 x  4096,  64 rows         15  20   13  17
-//   16 x  4096,  64 rows         25  31   24  29
-//   16 x 32768,  64 rows         69  60    -   -   (tcgen05)
-//   32 x  4000,  64 rows         41  36   38  32   (tcgen05)
-//    8 x  1900, 256 rows         33  34   28  30
-//    1 x  1000, 512 rows         16  30   14  26
-// More than two items an SM are streamed by warps with a share each: an item's ends
-// (its lengths, first pages, queries, and the sums that a CTA's warps join) then pass
-// beside other warps' items.  8 heads on 8 caches' heads of 128, by CTAs against by
-// warps, us:
-//    16 sequences x 2000 keys  e4m3  24  30   16-bit  26  33   (by CTAs)
-//    64 x  300                       43  28           38  29
-//    64 x 4000                       86  68          116 112
-//   256 x 1000                      132  98          136 130
-//   64 x 4000, 16 rows              121  80          129 122
-//   (512 sequences x 300 with one head, where a CTA's search for its shares is long:
-//   32 and 33, 31 and 32)
+// values have on average, and by the table's width.
+//
+// Up to 16 rows are streamed, in items of 8 or 16.  Up to 32 too, in two items, of
+// which the second reads the cache from L2; not so 16-bit entries of 128 dimensions
+// in a cache of twice the L2 (2^19 tokens and heads).  More than 32 are streamed
+// while there is little to do: an item of 16 rows costs the streaming kernel some
+// 0.13 us by itself and 1 us for every 1100 units, while a tcgen05 call is not under
+// 15 to 30 us (128 units a CTA, with 64 for each item, is where they meet).
+// D = 128, eight query heads on each, streamed against tcgen05, us:
+//                                        e4m3      16-bit
+//    16 sequences x 32768 keys, 16 rows   32  54    39  45
+//    32 x  2000, 8 heads,       32 rows   54  88    60  68
+//    32 x  8000, 8 heads,       32 rows  121 183   200 134  (16-bit: tcgen05)
+//     1 x  4096,                64 rows   15  20    13  17
+//    16 x  4096,                64 rows   25  31    24  29
+//    16 x 32768,                64 rows   69  60     -   -  (tcgen05)
+//    32 x  4000,                64 rows   41  36    38  32  (tcgen05)
+//   256 x   300,                64 rows   59  46    58  40  (tcgen05)
+//     8 x  1900,               256 rows   33  34    28  30
+//     1 x  1000,               512 rows   16  30    14  26
+//
+// More than three items to two SMs are streamed by warps with a share each: an
+// item's ends (its lengths, first pages, queries, and the sums that a CTA's warps
+// join) then pass beside other warps' items.  By CTAs against by warps, us:
+//    16 x 2000, 8 heads,  8 rows   e4m3  24  30   16-bit  26  33  (by CTAs)
+//    32 x 2000, 8 heads, 16 rows         57  40           52  46
+//    64 x  300, 8 heads,  8 rows         43  28           38  29
+//    64 x 4000, 8 heads,  8 rows         86  68          116 112
+//    64 x 4000, 8 heads, 16 rows        121  80          129 122
+//   256 x 1000, 8 heads,  8 rows        132  98          136 130
+//   256 x  300, 1 head,  16 rows         37  45           30  41  (where a CTA's
+//   256 x 2000, 1 head,  16 rows         50  40           48  46   search is long)
 // A share has at least 256 keys of a CTA: a step for each of the streaming kernel's
 // warps (one sequence of 8192 keys: 9.0 us; with 128 keys 9.4, with 512 9.2), four
 // tiles of the tcgen05 kernel (2: the same or 0.3 us slower, 8: 1-3); and 128 of a
@@ -839,13 +845,18 @@ const char* make_plan(const proj_kv_cache* cache, int64_t m, int64_t heads, Plan
     sms = 152;
   // the streaming kernel's items and, at most, their units
   const int64_t items = (rows + 15) / 16 * cache->sequences * cache->heads;
-  const int64_t units = items * ((cache->width * cache->page + kUnit - 1) / kUnit);
+  const int64_t capacity = cache->width * cache->page;
+  const int64_t units = items * ((capacity + kUnit - 1) / kUnit);
+  const bool wide = cache->format == PROJ_KV_ROWS && cache->D == 128;
   plan->rows = rows;
-  plan->tc = rows > 32 && units + 64 * items > 128 * static_cast<int64_t>(sms);
+  if (rows > 32)
+    plan->tc = units + 64 * items > 128 * static_cast<int64_t>(sms);
+  else
+    plan->tc = rows > 16 && wide && cache->sequences * cache->heads * capacity > (int64_t{1} << 19);
   plan->unit = plan->tc ? kAttnTcUnit : kUnit;
   plan->tile_rows = plan->tc ? kAttnTcRows : rows <= 8 ? 8 : 16;
   const int64_t parts = (rows + plan->tile_rows - 1) / plan->tile_rows * cache->sequences * cache->heads;
-  plan->solo = !plan->tc && parts > 2 * static_cast<int64_t>(sms);
+  plan->solo = !plan->tc && 2 * parts > 3 * static_cast<int64_t>(sms);
   plan->min_units = plan->tc || plan->solo ? 4 : kWarps;
   plan->sms = sms;
   plan->ctas = plan->solo ? kWarps * sms : sms;

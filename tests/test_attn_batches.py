@@ -1,4 +1,4 @@
-"""Attention of batches: more than two items an SM, which are streamed by warps with a share each.  Bounds as in test_attn.py."""
+"""Attention of batches: more than three items to two SMs, which are streamed by warps with a share each.  Bounds as in test_attn.py."""
 import math
 
 import numpy as np
@@ -115,7 +115,7 @@ def test_many_short_sequences(T):
 
 
 def test_workspace_never_shrinks_with_more_rows():
-    for sequences, kv, width in ((1, 1, 64), (40, 8, 4), (64, 1, 300), (700, 1, 2)):
+    for sequences, kv, width in ((1, 1, 64), (40, 8, 4), (64, 1, 300), (700, 1, 2), (16, 1, 2100)):
         cache = B.kv_cache(format=B.PROJ_KV_ROWS, dtype=B.PROJ_FP16, pages=1, page=16, heads=kv, D=128, k=4096, v=8192, page_stride=1 << 20,
                            head_stride=2048, token_stride=128, table=4096, ldt=width, width=width, sequences=sequences)
         sizes = [B.proj_attn_workspace(cache, m, 4 * kv) for m in range(0, 40 * sequences, max(1, sequences // 2))]

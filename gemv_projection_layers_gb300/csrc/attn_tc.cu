@@ -27,8 +27,8 @@
 // score; those of V the probability, relative to a power-of-two reference that
 // warp 18 keeps.
 //
-// What bounds it is none of the units (issue slots 45 % used, tensor pipe 15 %,
-// HBM a fifth to two thirds) but how long a tile's chain of hand-offs takes a warp:
+// What bounds it is none of the units (issue slots 39-44 % used, tensor pipe 20-31 %,
+// HBM a tenth to three quarters) but how long a tile's chain of hand-offs takes a warp:
 // some 3100 cycles in a softmax group, half of that a tile with two groups, where
 // HBM would deliver 64 keys of e4m3 in 700.  32 sequences of 8 drafts, 64 heads on
 // 8, 16-bit: 140 us (4.9 TB/s); 16 of 8 drafts over up to 32768 keys, 8 heads on 1,

@@ -769,7 +769,8 @@ int proj_kv_move(const proj_kv_cache *cache, const int32_t *start, const int32_t
  * fp16 are computed in fp16 with codes and queries exact in it (a row of bf16
  * queries is brought to its range by a power of two; what is 2^-29 below the
  * row's largest loses digits) and probabilities rounded to it; those of bf16
- * caches in bf16.
+ * caches in bf16, to which probabilities are rounded as well.  (The streaming
+ * kernel rounds them to a sum of two numbers of a 16-bit cache's type.)
  * The gate is applied in fp32 and the result rounded once.
  *
  * How many rows and positions a sequence has is read on the device.  Which kernel

@@ -112,6 +112,7 @@ class Call:
         width, D = self.heads * self.D, self.D
         u = DT[self.dtype][2]
         r = 2.0 ** -8 if self.fmt == "rows" and self.dtype == "bf16" else 2.0 ** -11
+        r = getattr(self, "r", r)
         at = 0
         for b, n in enumerate(self.counts):
             if n == 0:

@@ -156,6 +156,19 @@ def test_one_page_for_many_sequences(T):
     c.check()
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,G,D", [(1, 8, 128), (2, 8, 128), (1, 3, 64), (4, 4, 64)])
+@pytest.mark.parametrize("dtype,r", [("bf16", 2.0 ** -16), ("fp16", 2.0 ** -22)])
+def test_few_rows_of_a_16_bit_cache(T, G, D, dtype, r):
+    """Streamed, a probability is the sum of two numbers: off by half a step of what half a step of the first one left."""
+    for counts, starts in (([T, T], [500, 40]), ([T] * 250, [(7 * b) % 60 for b in range(250)])):
+        c = Call("rows", dtype, counts, starts, 1, G, D, 16, None, seed=25)
+        assert "stream" in B.proj_attn_describe(c.cache.c, c.m, c.heads)
+        c.r = r
+        c.run()
+        c.check()
+
+
 def test_scale_out_of_range_refused():
     """A scale whose product with log2(e) leaves fp32: the exponents are computed in base 2."""
     cache = B.kv_cache(format=B.PROJ_KV_ROWS, dtype=B.PROJ_BF16, pages=1, page=16, heads=1, D=64, k=4096, v=8192,

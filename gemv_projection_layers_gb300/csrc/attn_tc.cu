@@ -102,7 +102,7 @@ struct Tc {
   static constexpr int kRawAt = kStages * kStage;
   static constexpr int kSideAt = kRawAt + (kCoded ? kRaw * kRawTile : 0);
   static constexpr int kMl = kSideAt + kStages * kSide;  // float[2][128][3]
-  static constexpr int kRawScaleAt = kMl + 3072;         // float[kRawScales][2][kKeys]
+  static constexpr int kRawScaleAt = kMl + 2 * 128 * 12;  // float[kRawScales][2][kKeys]
   static constexpr int kSwapAt = kRawScaleAt + (kCoded ? kRawScales * 8 * kKeys : 0);  // float[2][2][16][64]: by group and giving half
   static constexpr int kIdsAt = kSwapAt + 16384;  // int[kIds][kKeys]
   static constexpr int kTiles = kIdsAt + kIds * kKeys * 4;

@@ -341,16 +341,19 @@ __device__ __noinline__ uint64_t seen_here(const AttnParams& p, int lo, int toke
   return seen;
 }
 
-// The values of V at columns c .. c + 15 that are no finite numbers, of the
-// segment's drafts that the row sees, added to o.
+// The values of V at columns c .. c + 15 that are no finite numbers, of keys that
+// the row sees in the segment's tiles of drafts, added to o.  The first of these
+// tiles begins with the last keys before the drafts (d < 0), which every row sees.
 template <typename T, int kFormat>
 __device__ __noinline__ void add_odd(const AttnParams& p, const Segment& seg, int token, int c, float* o) {
-  const int d0 = max(0, seg.u0 * kKeys - seg.start);
+  const int d0 = max(seg.start / kKeys, seg.u0) * kKeys - seg.start;
   const int d1 = min(seg.len - seg.start, (seg.u0 + seg.tiles) * kKeys - seg.start);
 #pragma unroll 1
   for (int d = d0; d < d1; ++d) {
-    const bool sees = p.mask ? (d >> 5) < p.words && (p.mask[static_cast<int64_t>(seg.lo + token) * p.ldm + (d >> 5)] >> (d & 31) & 1)
-                             : d <= token;
+    bool sees = d < 0;
+    if (!sees)
+      sees = p.mask ? (d >> 5) < p.words && (p.mask[static_cast<int64_t>(seg.lo + token) * p.ldm + (d >> 5)] >> (d & 31) & 1)
+                    : d <= token;
     int id, spot;
     if (!sees || !page_of(p.c, seg.b, seg.start + d, id, spot)) continue;
     const Entry e = entry_at(p.c, id, spot, seg.head);

@@ -27,7 +27,8 @@
 //
 // Softmax, one pass: each warp holds for its rows a reference m and sums
 // relative to 2^m, and a score well above m moves it (a vote; no shuffles
-// otherwise).  Scales of V multiply p, relative to the largest one seen.
+// otherwise).  Scales of V multiply p, relative to the largest one met (kRoom in
+// attn.h: what that means for rows that do not see it).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -398,16 +399,83 @@ __global__ void __launch_bounds__(kThreads, 1) attn_stream_kernel(const AttnPara
                 s[mt][nt][j] = -INFINITY;
             }
       }
+      if constexpr (kCoded) {
+        // scales that are no finite number do not enter the reference: they make
+        // p NaN for the rows that see the key, and only for those
+        float top = 0.f;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (!(fabsf(vs[mt][h]) < INFINITY)) vs[mt][h] = __uint_as_float(0x7FC00000u);
+            top = fmaxf(top, fabsf(vs[mt][h]));  // the finite ones
+          }
+        if (__any_sync(0xFFFFFFFFu, top > 2.f * v_ref)) {
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
+          // a power of two not above the largest one: its reciprocal is exact
+          top = fmaxf(__uint_as_float(__float_as_uint(top) & 0x7F800000u), fmaxf(v_ref, 1.17549435e-38f));
+          const float down = v_ref / top;
+          const int rise = v_ref > 0.f ? exponent_of(top) - exponent_of(v_ref) : 0;
+          v_ref = top;
+          v_inv = 1.f / top;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i2 = 0; i2 < 2; ++i2) {
+              float its_down = down;
+              if (partial && rise > 0) {
+                // not every row sees the key: the rows' references go down instead, and
+                // come up again below for those that do
+                float most = sum[nt][i2];
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, x));
+                const int low = lowered(most, rise);
+                ref[nt][i2] -= static_cast<float>(low);
+                sum[nt][i2] *= power_of_two(low);
+                its_down *= power_of_two(low);
+              }
+#pragma unroll
+              for (int kk = 0; kk < KK; ++kk) {
+                o[kk][nt][i2] *= its_down;
+                o[kk][nt][2 + i2] *= its_down;
+              }
+            }
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          vs[mt][0] *= v_inv;
+          vs[mt][1] *= v_inv;
+        }
+      }
       bool beyond = false;
       float tops[NT][2];
+      const auto find_tops = [&](auto by_scale) {
+        float lv[MT][2];  // logarithms of V's scales
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) lv[mt][h] = by_scale ? fmaxf(__log2f(fabsf(vs[mt][h])), -kRoom) : 0.f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i2 = 0; i2 < 2; ++i2) {
+            tops[nt][i2] = -INFINITY;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                tops[nt][i2] = fmaxf(tops[nt][i2], by_scale ? s[mt][nt][2 * h + i2] + lv[mt][h] : s[mt][nt][2 * h + i2]);
+          }
+      };
+      if (kCoded && __builtin_expect(partial, 0))
+        find_tops(std::true_type());
+      else
+        find_tops(std::false_type());
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int i2 = 0; i2 < 2; ++i2) {
-          tops[nt][i2] = fmaxf(s[0][nt][i2], s[0][nt][2 + i2]);
-          if (MT == 2) tops[nt][i2] = fmaxf(tops[nt][i2], fmaxf(s[MT - 1][nt][i2], s[MT - 1][nt][2 + i2]));
-          beyond |= tops[nt][i2] > ref[nt][i2] + kSlack;
-        }
+        for (int i2 = 0; i2 < 2; ++i2) beyond |= tops[nt][i2] > ref[nt][i2] + kSlack;
       if (__any_sync(0xFFFFFFFFu, beyond)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -426,37 +494,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_stream_kernel(const AttnPara
               o[kk][nt][2 + i2] *= down;
             }
           }
-      }
-      if constexpr (kCoded) {
-        // scales that are no finite number do not enter the reference: they make
-        // p NaN for the rows that see the key, and only for those
-        float top = 0.f;
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (!(fabsf(vs[mt][h]) < INFINITY)) vs[mt][h] = __uint_as_float(0x7FC00000u);
-            top = fmaxf(top, fabsf(vs[mt][h]));  // the finite ones
-          }
-        if (__any_sync(0xFFFFFFFFu, top > 2.f * v_ref)) {
-#pragma unroll
-          for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
-          top = fmaxf(fmaxf(top, v_ref), 1.17549435e-38f);  // its reciprocal is finite
-          const float down = v_ref / top;
-          v_ref = top;
-          v_inv = 1.f / top;
-#pragma unroll
-          for (int kk = 0; kk < KK; ++kk)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) o[kk][nt][j] *= down;
-        }
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          vs[mt][0] *= v_inv;
-          vs[mt][1] *= v_inv;
-        }
       }
       // 16-bit caches: what the rounding leaves is a second factor (no time: 32 tokens
       // over up to 16384 34.9 us with it, 35.2 without; the error against 64 bits is

@@ -291,6 +291,25 @@ __device__ __forceinline__ float exp2_fast(float x) {
 // the reference is where fp16 ends (65504 and 2^-24).
 constexpr float kSlack = 10.f, kLift = 4.f;
 
+// V's scales come relative to a reference that all rows of an item share, a power
+// of two near the largest one met, and p times that is rounded to fp16.  Before the
+// drafts every row sees every key, and what is lost is 2^-29 of the largest value
+// seen, for each key.  A draft's scale is met by rows that do not see it too.  So
+// where keys are masked, a raise of the shared reference lowers the rows' own (what
+// is summed of V stays as it is, p grows), while a row's sum stays below 2^kSumBits;
+// and a row's own reference is then the largest score plus the logarithm of V's
+// scale, down to 2^-kRoom, of what it sees.  So p times the scale is 2^kLift there,
+// whatever stands in other drafts, and p alone at most 2^(kRoom + kSlack + kLift),
+// far from where its sums leave fp32.
+constexpr float kRoom = 64.f;
+constexpr int kSumBits = 96;
+__device__ __forceinline__ int exponent_of(float x) { return static_cast<int>(__float_as_uint(x) >> 23 & 255u) - 127; }
+__device__ __forceinline__ float power_of_two(int n) { return __uint_as_float(static_cast<uint32_t>(n + 127) << 23); }
+// By how many powers of two a row's reference goes down, of `rise`: 0 .. 120.
+__device__ __forceinline__ int lowered(float sum, int rise) {
+  return max(0, min(min(rise, 120), kSumBits - exponent_of(sum)));
+}
+
 // The reference of a row that has seen nothing yet.
 constexpr float kNoScore = -3e38f;
 

@@ -25,7 +25,8 @@
 // a score is well above it, whereupon O is scaled in tensor memory;
 // probabilities are fp16 (bf16 caches: bf16).  Scales of K multiply the fp32
 // score; those of V the probability, relative to a power-of-two reference that
-// warp 18 keeps.
+// warp 18 keeps (and that tiles of drafts turn into one of each row's own: attn.h,
+// kRoom; by the largest scale and the largest score that the row sees of 32 keys).
 //
 // What bounds it is none of the units (issue slots 39-44 % used, tensor pipe 20-31 %,
 // HBM a tenth to three quarters) but how long a tile's chain of hand-offs takes a warp:
@@ -924,7 +925,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
           if constexpr (kCoded) {
             const float now = ld_shared_f(side + kRef);
             if (now != v_ref) {
-              down = v_ref / now;  // both powers of two, or v_ref 0 and nothing summed yet
+              down = v_ref / now;  // both powers of two, or v_ref 0 and nothing of V summed yet
+              if (partial && v_ref > 0.f) {
+                // not every row sees the key: this row's reference goes down instead
+                const int low = lowered(sum, exponent_of(now) - exponent_of(v_ref));
+                ref -= static_cast<float>(low);
+                sum *= power_of_two(low);
+                down *= power_of_two(low);
+              }
               v_ref = now;
             }
           }
@@ -953,16 +961,29 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                 }
               }
             }
+            float by_scale = 0.f;  // of what is seen here, logarithm of V's largest scale
             if (__builtin_expect(partial, 0)) {
               const uint32_t here = static_cast<uint32_t>(c ? seen >> 32 : seen);
+              float most = 0.f;
 #pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (!(here >> j & 1)) f[j] = -INFINITY;
+              for (int j = 0; j < 32; j += 4) {
+                float4 vs = make_float4(0.f, 0.f, 0.f, 0.f);
+                if constexpr (kCoded) vs = ld_shared_f4(side + kVScale + c * 128 + j * 4);
+                const float v[4] = {vs.x, vs.y, vs.z, vs.w};
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                  if (here >> (j + x) & 1)
+                    most = fmaxf(most, fabsf(v[x]));
+                  else
+                    f[j + x] = -INFINITY;
+                }
+              }
+              if constexpr (kCoded) by_scale = fmaxf(__log2f(most), -kRoom);
             }
             float tops[4] = {f[0], f[1], f[2], f[3]};
 #pragma unroll
             for (int j = 4; j < 32; ++j) tops[j & 3] = fmaxf(tops[j & 3], f[j]);
-            const float top = fq * fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+            const float top = fmaf(fq, fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])), by_scale);
             if (__builtin_expect(__any_sync(0xFFFFFFFFu, top > ref + kSlack), 0)) {
               if (top > ref + kSlack) {
                 const float step = exp2_fast(ref - top);

@@ -765,12 +765,16 @@ int proj_kv_move(const proj_kv_cache *cache, const int32_t *start, const int32_t
  * A row that sees nothing gets zeros, and lse = -infinity.  What a row does not
  * see does not reach it, NaN and infinities included; where it sees a value that
  * is no finite number, that column of it is none either (an infinity or NaN).
- * Scores, their maximum and sums are fp32; the products of 8-bit caches and of
- * fp16 are computed in fp16 with codes and queries exact in it (a row of bf16
- * queries is brought to its range by a power of two; what is 2^-29 below the
- * row's largest loses digits) and probabilities rounded to it; those of bf16
- * caches in bf16, to which probabilities are rounded as well.  (The streaming
- * kernel rounds them to a sum of two numbers of a 16-bit cache's type.)
+ * Scores, their maximum and sums are fp32 (|v| below 2^90 keeps those of V there);
+ * the products of 8-bit caches and of fp16 are computed in fp16 with codes and
+ * queries exact in it (a row of bf16 queries is brought to its range by a power of
+ * two; what is 2^-29 below the row's largest loses digits) and probabilities rounded
+ * to it; those of bf16 caches in bf16, to which probabilities are rounded as well.
+ * (The streaming kernel rounds them to a sum of two numbers of a 16-bit cache's
+ * type.)  With 8-bit caches it is the product of probability and V's scale that is
+ * rounded, to 2^-11 of itself or 2^-29 of the largest |v| that the row sees, whichever
+ * is more; drafts that it does not see count for nothing in that as long as their
+ * values are not beyond 2^60 times those that it does.
  * The gate is applied in fp32 and the result rounded once.
  *
  * How many rows and positions a sequence has is read on the device.  Which kernel

@@ -78,10 +78,13 @@ __device__ __forceinline__ int64_t units_of(const AttnParams& p, const Sequence&
 }
 
 // What a CTA leaves to be joined: the item in which its share begins, if that
-// began before and this is its second CTA (rows 0: nothing).
-struct alignas(32) Split {
+// began before and this is its second CTA (rows 0: nothing).  The list stands at the
+// workspace's start, which is aligned to 16 bytes and no more.
+struct alignas(16) Split {
   int rows, lo, row0, head, first, last;  // first, last: the item's CTAs
+  int pad[2];
 };
+static_assert(sizeof(Split) == 32 && alignof(Split) == 16, "an entry of the workspace");
 
 // This CTA's share.
 struct Share {

@@ -739,8 +739,8 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(const AttnParams p)
   if (it.rows == 0) return;
   const int G = static_cast<int>(p.group.d);
   const int set = threadIdx.x / kLanes, quad = threadIdx.x % kLanes;
-  const bool few = !p.spread;
-  const int y0 = few ? blockIdx.y * kSets + set : blockIdx.y, dy = few ? gridDim.y * kSets : gridDim.y;
+  const bool alone = !p.spread;  // a set has a row to itself: then no barrier below is reached
+  const int y0 = alone ? blockIdx.y * kSets + set : blockIdx.y, dy = alone ? gridDim.y * kSets : gridDim.y;
   for (int r = y0; r < it.rows; r += dy) {
     float top = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
     const int t = quotient(it.row0 + r, p.group);
@@ -748,7 +748,7 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(const AttnParams p)
     Vec<T, 4> gate[1] = {};
     if (p.gate) gate[0] = load_vec<T, 4>(reinterpret_cast<const T*>(p.gate + static_cast<int64_t>(it.lo + t) * p.ldg) + j * D + quad * 4);
 #pragma unroll 8
-    for (int c = it.first + (few ? 0 : set); c <= it.last; c += few ? 1 : kSets) {
+    for (int c = it.first + (alone ? 0 : set); c <= it.last; c += alone ? 1 : kSets) {
       const int64_t slot = 2ll * c + (c == it.first ? 1 : 0);
       const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (slot * p.tile_rows + r) * 2);
       const float4 v = *reinterpret_cast<const float4*>(p.part_o + (slot * p.tile_rows + r) * D + quad * 4);
@@ -761,7 +761,7 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(const AttnParams p)
       acc[2] = acc[2] * a + v.z * f;
       acc[3] = acc[3] * a + v.w * f;
     }
-    if (!few) {
+    if (!alone) {
       *reinterpret_cast<float4*>(&s_o[set][quad * 4]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
       if (quad == 0) {
         s_ml[set][0] = top;
@@ -785,7 +785,7 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(const AttnParams p)
       }
       __syncthreads();
     }
-    if (few || set == 0) {
+    if (alone || set == 0) {
       write_out<T>(p, static_cast<int64_t>(it.lo + t), j * D + quad * 4, acc, l, gate);
       if (p.lse && quad == 0) p.lse[static_cast<int64_t>(it.lo + t) * p.heads + j] = lse_of(top, l);
     }

@@ -762,7 +762,8 @@ int proj_kv_move(const proj_kv_cache *cache, const int32_t *start, const int32_t
  *
  *     out = (softmax(scale q k^T over what the row sees) v) act(gate)
  *
- * A row that sees nothing gets zeros, and lse = -infinity.  What a row does not
+ * A row that sees nothing, or only keys whose score is -infinity, gets zeros and
+ * lse = -infinity.  What a row does not
  * see does not reach it, NaN and infinities included; where it sees a value that
  * is no finite number, that column of it is none either (an infinity or NaN).
  * Scores, their maximum and sums are fp32 (|v| below 2^90 keeps those of V there);

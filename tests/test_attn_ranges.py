@@ -120,3 +120,27 @@ def test_extreme_queries(T, G, fmt, scale, table):
     # the infinity is the first head's alone
     assert c.out[T - 1, 64:].isfinite().all()
     part(c, 0, 0, T - 1, 50, 50 + T, chain(T - 1, 50, 50 + T)).check()
+
+
+@pytest.mark.parametrize("T,G", [(2, 4), (9, 8), (40, 4)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_scores_of_minus_infinity(T, G, dtype, table):
+    """A row of which every score is -infinity gets zeros, as one that sees nothing; beside other keys such a score counts for nothing."""
+    c = A.Call("rows", dtype, [T, T], [0, 20], 1, G, 64, 16, None, seed=85)
+    for b, s in enumerate(c.starts):
+        k, v = torch.zeros(1, 1, 64), torch.ones(1, 1, 64)
+        k[0, 0, 0] = -math.inf
+        c.cache.put(b, s, k.to(c.q.dtype), v.to(c.q.dtype))
+    c.q[:, 0::64] = 1.0  # each head's first dimension: the key's score is -infinity for every row
+    c.run()
+    torch.cuda.synchronize()
+    assert bool((c.out[0] == 0).all()) and bool((c.lse[0] == -math.inf).all())
+    # without that key
+    for b, (s, at) in enumerate(zip(c.starts, (0, T))):
+        sees = chain(T, s, s + T)
+        sees[:, s] = False
+        d = part(c, b, at, at + T, s, s + T, sees)
+        k = c.cache.get("k", b, 0, s + T)
+        k[s] = 0
+        d.cache = type("Kept", (), {"get": staticmethod(lambda n, _, first, count, k=k, b=b: k if n == "k" else c.cache.get(n, b, first, count))})
+        d.check()

@@ -497,7 +497,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_stream_kernel(const AttnPara
       }
       // 16-bit caches: what the rounding leaves is a second factor (no time: 32 tokens
       // over up to 16384 34.9 us with it, 35.2 without; the error against 64 bits is
-      // the output's own rounding then)
+      // the output's own rounding then).  With 8-bit caches, where decoding already
+      // takes the issue slots, it would cost 32 rows 11 % (32 x 8000, 8 heads 123 us,
+      // 137 with it), 16 rows 5 to 11 and 8 rows 1 to 3, and p stays one fp16 number:
+      // error 0.0003 in fp16 for 0.0002, in bf16 no more than the output's rounding.
       uint32_t pb[MT][NT][2], rest[MT][NT][2];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
@@ -871,8 +874,11 @@ struct Plan {
 //    64 x 4000, 8 heads,  8 rows         86  68          116 112
 //    64 x 4000, 8 heads, 16 rows        121  80          129 122
 //   256 x 1000, 8 heads,  8 rows        132  98          136 130
-//   256 x  300, 1 head,  16 rows         37  45           30  41  (where a CTA's
-//   256 x 2000, 1 head,  16 rows         50  40           48  46   search is long)
+//   256 x  300, 1 head,  16 rows         37  45           30  41  (warps all the same)
+//   256 x 2000, 1 head,  16 rows         50  40           48  46
+// So of many short sequences with one head the rule takes the slower form.  (Both
+// tables are of before V's scales had a reference by row where keys are masked: over
+// 8-bit caches the streaming kernel takes 1 to 3 % more since, tcgen05 0 to 1.)
 // A share has at least 256 keys of a CTA: a step for each of the streaming kernel's
 // warps (one sequence of 8192 keys: 9.0 us; with 128 keys 9.4, with 512 9.2), four
 // tiles of the tcgen05 kernel (2: the same or 0.3 us slower, 8: 1-3); and 128 of a

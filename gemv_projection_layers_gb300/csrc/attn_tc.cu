@@ -1,6 +1,6 @@
 // attn_tc.cu -- attention of drafted tokens over the cache on tcgen05, for
-// items of many rows (a group's heads times a sequence's drafts above 32) over long
-// caches.
+// items of many rows (a group's heads times a sequence's drafts above 32; 17 to 32 of
+// 16-bit entries too, attn.cu's make_plan) over long caches.
 //
 // Rows are the M side of both products, a row in each of 128 lanes of tensor
 // memory; a tile is 64 keys:
@@ -23,7 +23,11 @@
 //
 // Softmax as in the streaming kernel: a reference per row that moves only when
 // a score is well above it, whereupon O is scaled in tensor memory;
-// probabilities are fp16 (bf16 caches: bf16).  Scales of K multiply the fp32
+// probabilities are fp16 (bf16 caches: bf16, since V may leave fp16's range).  A
+// second number for what that rounding leaves has no room: with 128 dimensions Q, two
+// S, two P and two O fill all 512 columns.  (Error against 64 bits 0.0003 in fp16,
+// where the output's own rounding is 0.0002; 0.0017 in bf16, as that rounding alone;
+// 0.0023 over a bf16 cache.)  Scales of K multiply the fp32
 // score; those of V the probability, relative to a power-of-two reference that
 // warp 18 keeps (and that tiles of drafts turn into one of each row's own: attn.h,
 // kRoom; by the largest scale and the largest score that the row sees of 32 keys).
@@ -33,7 +37,7 @@
 // some 3100 cycles in a softmax group, half of that a tile with two groups, where
 // HBM would deliver 64 keys of e4m3 in 700.  32 sequences of 8 drafts, 64 heads on
 // 8, 16-bit: 140 us (4.9 TB/s); 16 of 8 drafts over up to 32768 keys, 8 heads on 1,
-// e4m3: 59 us, of which some 25 are a call's ends (share, pages, queries, sums and
+// e4m3: 60 us, of which some 25 are a call's ends (share, pages, queries, sums and
 // their join); 32 of up to 64 drafts: 141 us (0.36 PFLOP/s).  What the steps there
 // were worth: short loops (five roles share a scheduler's instruction cache; with
 // loops unrolled over tiles two thirds of the cycles went to waiting for
@@ -56,8 +60,9 @@ constexpr int kSoftWarps = 8, kLoadWarp = 8, kLoadWarps = 8, kMmaWarp = 16, kWal
               kPvWarp = 19;
 constexpr int kThreads = 32 * 20;
 // Registers a thread: at launch, and of the three kinds of warpgroups (two of
-// softmax, two of loading, one of the others).  Nothing may spill in a loop:
-// beside this much shared memory L1 does not hold what 640 threads spill.
+// softmax, two of loading, one of the others).  Spills cost: beside this much shared
+// memory L1 does not hold those of 640 threads.  16-bit and int8 instances have up to
+// 16 bytes of them, e4m3's 48 to 64.
 constexpr int kRegs = 96, kSoftRegs = 160, kLoadRegs = 48, kOtherRegs = 64;
 static_assert(2 * kSoftRegs + 2 * kLoadRegs + kOtherRegs <= 5 * kRegs && 5 * kRegs * 128 <= 65536, "registers");
 // The loading warps are teams that take the tiles in turn: what one warp does for a

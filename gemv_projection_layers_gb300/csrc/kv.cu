@@ -7,7 +7,7 @@
 // of dependent loads (offsets, start, table, entry) where there are few rows
 // (2.2 us).  139000 rows of 8 heads of 128 back from e4m3: 178 us (5.8 TB/s); 8192
 // rows of 8 heads to int8: 12.9 us (3.9 TB/s; the chain is a third of it); 256 paths
-// of 32 rows of 8 heads, 16-bit: 11.6 us (3.6 TB/s).
+// of 32 rows of 8 heads, 16-bit: 11.7 us (3.6 TB/s).
 //
 // A warp takes a row of the call: it finds the row's sequence once (a search
 // in `offsets` that halves the range five times a step: 32 lanes look at 32
@@ -208,8 +208,8 @@ struct MoveParams {
 // ascends and find the places of an entry each, and the warps take the entries in
 // turn.  All loads of a run come before its first store: a target can be another
 // entry's source, of the same run or an earlier one, but not of a later one, whose
-// sources lie behind.  (Runs of 64 hold twice as much in registers; 256 paths of 32 x
-// 16 heads' rows then went in seven rounds of CTAs instead of four, 19.5 us.)
+// sources lie behind.  (Runs of 64 hold twice as much in registers, for fewer CTAs an
+// SM: 256 paths of 32 x 16 heads' rows took 19.5 us, 11.7 so, in 2.7 rounds of CTAs.)
 constexpr int kRun = 32;
 
 __global__ void __launch_bounds__(kThreads, 5) kv_move_kernel(const MoveParams p) {
